@@ -258,6 +258,116 @@ gdn_status gdn_decode(const void* Q, const void* K, const void* V, int32_t qkv_d
                       void* O, int32_t o_dtype, int32_t B, int32_t H, int32_t n,
                       int32_t d_k, int32_t d_v, float scale, void* stream);
 
+/* ---- linear attention with a decay for each head ---------------------------------
+ * The gated recurrence without the delta correction, per sequence and value head, tokens
+ * in order, state S [d_k][d_v] fp32:
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T        o_t = scale S_t^T q_t
+ * with one log-decay per token, or one per head for all tokens (g_per_head != 0).  Queries
+ * and keys may be shared: H_qk divides H, and value head h reads query and key head
+ * h / (H / H_qk).
+ *
+ * offsets == NULL: B sequences of T tokens each; Q, K [B][H_qk][T][d_k], V, O
+ *   [B][H][T][d_v], g [B][H][T] (or [H]).
+ * offsets != NULL: B packed sequences in T tokens, sequence s at tokens offsets[s] ..
+ *   offsets[s+1] - 1 (DEVICE int32 [B+1], 0 <= offsets[s] <= offsets[s+1] <= T; empty
+ *   sequences are valid); Q, K [H_qk][T][d_k], V, O [H][T][d_v], g [H][T] (or [H]).  Rows of
+ *   no sequence are neither read into a result nor written.  Offsets that break the rule
+ *   are clamped: no access leaves the tensors, the results are unspecified.
+ * States are [B][H][d_k][d_v] fp32 either way.  T is any length up to 2^31 - 65; T == 0 and
+ * empty sequences return the given states unchanged (or zeros).  g <= 0 is expected, -inf
+ * included (the state is forgotten before the token); log-decays below -354 count as
+ * -inf. */
+typedef struct gdn_lin_shape {
+  int64_t T;
+  const int32_t* offsets;
+  int32_t B, H, H_qk;
+  int32_t d_k, d_v;
+  int32_t g_per_head;
+  float scale;
+} gdn_lin_shape;
+
+/* Device workspace in bytes of gdn_lin_chunk_fwd and gdn_lin_chunk_bwd (0 for arguments
+ * they reject; offsets only selects the layout and is not read).  The forward pass needs
+ * some where sequences and heads are too few to fill the GPU and the tokens are divided. */
+size_t gdn_lin_chunk_fwd_workspace_bytes(const gdn_lin_shape* shape);
+size_t gdn_lin_chunk_bwd_workspace_bytes(const gdn_lin_shape* shape);
+
+/* O and S_out of whole sequences, chunk by chunk.  qkv_dtype GDN_BF16; o_dtype GDN_BF16 or
+ * GDN_F32; S0 NULL = zeros; S_out NULL = not wanted.  d_k in {64, 128}, d_v a multiple of
+ * 32, at most 256 (GDN_ERR_UNSUPPORTED otherwise).  workspace: 16-byte aligned scratch of at
+ * least the query's bytes, not to be shared by two calls in flight (GDN_ERR_WORKSPACE if it
+ * is needed and NULL or smaller). */
+gdn_status gdn_lin_chunk_fwd(const gdn_lin_shape* shape, const void* Q, const void* K, const void* V,
+                             int32_t qkv_dtype, const float* g, const float* S0, void* O,
+                             int32_t o_dtype, float* S_out, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* Its backward pass: gradients of a loss from dO (GDN_BF16, as O) and dS (gradient of S_out;
+ * NULL = zeros).  dQ, dK, dV as Q, K, V in grad_dtype (GDN_BF16 or GDN_F32; shared heads get
+ * the sum over their group), dg fp32 as g (per head: the sum over all its tokens; NULL = not
+ * wanted), dS0 [B][H][d_k][d_v] fp32 (NULL = not wanted).  d_k and d_v in {64, 128}.  The
+ * call reads no output of the forward pass.  The same call gives the same bits. */
+gdn_status gdn_lin_chunk_bwd(const gdn_lin_shape* shape, const void* Q, const void* K, const void* V,
+                             int32_t qkv_dtype, const float* g, const float* S0, const void* dO,
+                             const float* dS, void* dQ, void* dK, void* dV, int32_t grad_dtype,
+                             float* dg, float* dS0, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* The recurrence one token at a time (decode), T = the tokens of the call (offsets must be
+ * NULL: GDN_ERR_UNSUPPORTED otherwise).  The state is read and written once per call and
+ * S_out MAY equal S_in, as in gdn_decode.  qkv_dtype and o_dtype GDN_BF16 or GDN_F32; d_k in
+ * {64, 128}, d_v a multiple of 32, at most 256. */
+gdn_status gdn_lin_decode(const gdn_lin_shape* shape, const void* Q, const void* K, const void* V,
+                          int32_t qkv_dtype, const float* g, const float* S_in, float* S_out, void* O,
+                          int32_t o_dtype, void* stream);
+
+/* ---- the norms around the token mixer ------------------------------------------------ */
+
+/* activation of the gate: z / (1 + exp(-z)), or 1 / (1 + exp(-z)) */
+typedef enum gdn_gate_act { GDN_GATE_SILU = 0, GDN_GATE_SIGMOID = 1 } gdn_gate_act;
+
+/* The gated norm of the head outputs, as the output projection reads them:
+ *   Y[b][t][h] = O[b][h][t] / sqrt(mean(O[b][h][t]^2) + eps) * w * act(Z[b][t][h])
+ * over the d values of a row.  O [B][H][T][d] as the entry points above and gdn_chunk_fwd /
+ * gdn_decode write it, Z [B][T] rows of H * d values, z_stride values apart (a part of a
+ * wider projection; a multiple of 8, >= H * d), Y [B][T][H][d]; dtype GDN_BF16 or GDN_F32 for
+ * all three; w fp32 [d], NULL = ones.  d a multiple of 32, at most 256. */
+gdn_status gdn_gate_norm_fwd(const void* O, const void* Z, int64_t z_stride, const float* w, void* Y,
+                             int32_t dtype, int32_t B, int32_t H, int64_t T, int32_t d, int32_t act,
+                             float eps, void* stream);
+
+/* Its backward pass: dO [B][H][T][d] and dZ [B][T][H][d] in dtype, dw fp32 [d] (NULL = not
+ * wanted).  workspace as for gdn_lin_chunk_bwd, needed for dw.  The same call gives the same
+ * bits. */
+size_t gdn_gate_norm_bwd_workspace_bytes(int32_t B, int32_t H, int64_t T, int32_t d);
+gdn_status gdn_gate_norm_bwd(const void* dY, const void* O, const void* Z, int64_t z_stride,
+                             const float* w, void* dO, void* dZ, float* dw, int32_t dtype, int32_t B,
+                             int32_t H, int64_t T, int32_t d, int32_t act, float eps, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* The residual sum around a block, with the norm after the block and the norm before the
+ * next one, rms(x) = x / sqrt(mean(x^2) + eps) over a row of D values:
+ *   R = X + alpha s * (rms(Y) * w_post)        N = rms(R) * w_pre
+ * X, R [rows][D] in x_dtype, Y, N [rows][D] in y_dtype (GDN_BF16 or GDN_F32 each); w_post, s,
+ * w_pre fp32 [D].  w_post NULL: no norm after (Y itself); s NULL: ones; w_pre NULL: ones;
+ * N NULL: not wanted.  N is formed from the sum before its rounding.  R MAY equal X.  D a
+ * multiple of 8, at most 16384. */
+gdn_status gdn_residual_norm_fwd(const void* X, int32_t x_dtype, const void* Y, int32_t y_dtype,
+                                 const float* w_post, const float* s, float alpha, const float* w_pre,
+                                 void* R, void* N, int64_t rows, int32_t D, float eps, void* stream);
+
+/* Its backward pass from dN (y_dtype; NULL = zeros, and R is then not read) and dR (x_dtype;
+ * NULL = zeros), with R as the forward pass wrote it: dX (x_dtype), dY (y_dtype), dw_pre,
+ * dw_post, ds fp32 [D] (each NULL = not wanted; dw_post and ds need w_post and s).  dX MAY
+ * equal dR.  workspace as for gdn_lin_chunk_bwd, needed for the fp32 gradients.  The same
+ * call gives the same bits. */
+size_t gdn_residual_norm_bwd_workspace_bytes(int64_t rows, int32_t D);
+gdn_status gdn_residual_norm_bwd(const void* dN, const void* dR, const void* R, int32_t x_dtype,
+                                 const void* Y, int32_t y_dtype, const float* w_post, const float* s,
+                                 float alpha, const float* w_pre, void* dX, void* dY, float* dw_pre,
+                                 float* dw_post, float* ds, int64_t rows, int32_t D, float eps,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

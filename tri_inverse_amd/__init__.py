@@ -27,6 +27,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 # dtype and mode codes (gdn.h)
 GDN_F32, GDN_BF16, GDN_FP8_E4M3, GDN_INT8, GDN_INT16 = 0, 1, 2, 3, 4
 GDN_INV_NEUMANN, GDN_INV_EXACT, GDN_INV_NEUMANN_PRODUCTS = 0, 1, 2
+GDN_GATE_SILU, GDN_GATE_SIGMOID = 0, 1
 GDN_OK = 0
 GDN_ERR_UNSUPPORTED, GDN_ERR_WORKSPACE, GDN_ERR_HIP = 5, 6, 7
 FP8_STATS_FIELDS = ("nonfinite", "sat_dynamic", "sat_static", "underflow")
@@ -46,6 +47,12 @@ class gdn_blocks(ctypes.Structure):
 class gdn_inverse_cfg(ctypes.Structure):
     _fields_ = [("mode", ctypes.c_int32), ("N", ctypes.c_int32), ("mask", ctypes.c_int32),
                 ("compute", ctypes.c_int32)]
+
+
+class gdn_lin_shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("offsets", ctypes.c_void_p), ("B", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("H_qk", ctypes.c_int32), ("d_k", ctypes.c_int32),
+                ("d_v", ctypes.c_int32), ("g_per_head", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 _vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
@@ -78,10 +85,40 @@ _lib.gdn_chunk_fwd_noalloc.argtypes = [_vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, 
 _lib.gdn_decode.restype = _i32
 _lib.gdn_decode.argtypes = [_vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
                             _i32, _i32, _f32, _vp]
+_sz = ctypes.c_size_t
+_lib.gdn_lin_chunk_fwd_workspace_bytes.restype = _sz
+_lib.gdn_lin_chunk_fwd_workspace_bytes.argtypes = [_P(gdn_lin_shape)]
+_lib.gdn_lin_chunk_bwd_workspace_bytes.restype = _sz
+_lib.gdn_lin_chunk_bwd_workspace_bytes.argtypes = [_P(gdn_lin_shape)]
+_lib.gdn_lin_chunk_fwd.restype = _i32
+_lib.gdn_lin_chunk_fwd.argtypes = [_P(gdn_lin_shape), _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _sz, _vp]
+_lib.gdn_lin_chunk_bwd.restype = _i32
+_lib.gdn_lin_chunk_bwd.argtypes = [_P(gdn_lin_shape), _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
+                                   _vp, _vp, _vp, _sz, _vp]
+_lib.gdn_lin_decode.restype = _i32
+_lib.gdn_lin_decode.argtypes = [_P(gdn_lin_shape), _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp]
+_lib.gdn_gate_norm_fwd.restype = _i32
+_lib.gdn_gate_norm_fwd.argtypes = [_vp, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i64, _i32, _i32, _f32, _vp]
+_lib.gdn_gate_norm_bwd_workspace_bytes.restype = _sz
+_lib.gdn_gate_norm_bwd_workspace_bytes.argtypes = [_i32, _i32, _i64, _i32]
+_lib.gdn_gate_norm_bwd.restype = _i32
+_lib.gdn_gate_norm_bwd.argtypes = [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i64, _i32, _i32, _f32,
+                                   _vp, _sz, _vp]
+_lib.gdn_residual_norm_fwd.restype = _i32
+_lib.gdn_residual_norm_fwd.argtypes = [_vp, _i32, _vp, _i32, _vp, _vp, _f32, _vp, _vp, _vp, _i64, _i32, _f32, _vp]
+_lib.gdn_residual_norm_bwd_workspace_bytes.restype = _sz
+_lib.gdn_residual_norm_bwd_workspace_bytes.argtypes = [_i64, _i32]
+_lib.gdn_residual_norm_bwd.restype = _i32
+_lib.gdn_residual_norm_bwd.argtypes = [_vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                       _i64, _i32, _f32, _vp, _sz, _vp]
 
 EXPORTED = ("gdn_abi_version", "gdn_status_string", "gdn_build_A", "gdn_tri_inverse_neumann",
             "gdn_tri_inverse_exact", "gdn_tri_inverse_residual", "gdn_tri_inverse_fs", "gdn_wy",
-            "gdn_chunk_fwd_workspace_bytes", "gdn_chunk_fwd", "gdn_chunk_fwd_noalloc", "gdn_decode")
+            "gdn_chunk_fwd_workspace_bytes", "gdn_chunk_fwd", "gdn_chunk_fwd_noalloc", "gdn_decode",
+            "gdn_lin_chunk_fwd_workspace_bytes", "gdn_lin_chunk_bwd_workspace_bytes", "gdn_lin_chunk_fwd",
+            "gdn_lin_chunk_bwd", "gdn_lin_decode", "gdn_gate_norm_fwd", "gdn_gate_norm_bwd_workspace_bytes",
+            "gdn_gate_norm_bwd", "gdn_residual_norm_fwd", "gdn_residual_norm_bwd_workspace_bytes",
+            "gdn_residual_norm_bwd")
 GDN_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -406,3 +443,294 @@ def gdn_decode(Q, K, V, beta, g, S=None, scale: float | None = None, S_out=None,
                          float(scale), _stream(stream))
     _check(st, "gdn_decode")
     return O, S_out
+
+
+# ---- linear attention with a decay for each head, and the norms around it -------------------
+# Launches run on the tensors' device, whichever device is current.  With an explicit stream
+# everything allocated here belongs to that stream, so that no other stream's work can be
+# given a workspace that is still in use.
+
+_BF16, _FLOAT = (torch.bfloat16,), (torch.float32, torch.bfloat16)
+_ACT = {"silu": GDN_GATE_SILU, "sigmoid": GDN_GATE_SIGMOID}
+
+
+class _Here:
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE_SCOPE = _Here()
+
+
+def _scope(dev, stream):
+    """Context in which dev is the current device and, if given, stream the current stream."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, dev))
+        return torch.cuda.stream(stream)
+    return _HERE_SCOPE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _arg(t, name, dtypes, shape, dev):
+    """A required tensor: on dev (None: any GPU), contiguous, of one of dtypes, of this shape."""
+    _dev(t, name, dtypes)
+    if t is None:
+        raise TypeError("%s is required" % name)
+    if dev is not None and t.device != dev:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    return t
+
+
+def _out(t, name, dtypes, shape, dev, dtype):
+    """An output: the caller's tensor after its checks, or a new one."""
+    if t is None:
+        return torch.empty(shape, device=dev, dtype=dtype)
+    return _arg(t, name, dtypes, shape, dev)
+
+
+def _scratch(workspace, need, dev):
+    if workspace is None:
+        return (torch.empty(need, device=dev, dtype=torch.uint8), need) if need else (None, 0)
+    _dev(workspace, "workspace")
+    if workspace.device != dev:
+        raise ValueError("workspace is on %s, expected %s" % (workspace.device, dev))
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _lin_shape(Q, K, V, g, scale, offsets, dtypes):
+    """The gdn_lin_shape of a call after the inputs' checks; returns (shape, sequences, device)."""
+    if K is None or K.dim() != 4 or V is None or V.dim() != 4:
+        raise ValueError("Q and K must be [B, H_qk, T, d_k], V [B, H, T, d_v]")
+    B, Hk, T, dk = K.shape
+    H, dv = V.shape[1], V.shape[3]
+    dev = K.device
+    _arg(K, "K", dtypes, (B, Hk, T, dk), None)
+    _arg(Q, "Q", (K.dtype,), (B, Hk, T, dk), dev)
+    _arg(V, "V", (K.dtype,), (B, H, T, dv), dev)
+    if Hk == 0 or H % Hk != 0:
+        raise ValueError("the %d heads of V cannot share the %d heads of Q and K" % (H, Hk))
+    per_head = g is not None and g.dim() == 1
+    _arg(g, "g", (torch.float32,), (H,) if per_head else (B, H, T), dev)
+    n = B
+    if offsets is not None:
+        if B != 1:
+            raise ValueError("packed sequences lie in one row: B must be 1, got %d" % B)
+        if offsets.dim() != 1 or offsets.numel() < 1:
+            raise ValueError("offsets must be [sequences + 1]")
+        n = offsets.numel() - 1
+        _arg(offsets, "offsets", (torch.int32,), (n + 1,), dev)
+    sh = gdn_lin_shape()
+    sh.T, sh.B, sh.H, sh.H_qk, sh.d_k, sh.d_v = T, n, H, Hk, dk, dv
+    sh.offsets = None if offsets is None else offsets.data_ptr()
+    sh.g_per_head = int(per_head)
+    sh.scale = dk ** -0.5 if scale is None else float(scale)
+    return sh, n, dev
+
+
+def _plain_shape(B, H, H_qk, T, d_k, d_v, packed):
+    sh = gdn_lin_shape()
+    sh.T, sh.B, sh.H, sh.H_qk, sh.d_k, sh.d_v = int(T), int(B), int(H), int(H_qk), int(d_k), int(d_v)
+    sh.offsets = 16 if packed else None  # only its presence counts
+    sh.g_per_head, sh.scale = 1, 1.0
+    return sh
+
+
+def gdn_lin_chunk_fwd_workspace_bytes(B: int, H: int, T: int, d_k: int, d_v: int, H_qk: int | None = None,
+                                      packed: bool = False) -> int:
+    """Device workspace (bytes) gdn_lin_chunk_fwd needs for B sequences (0: none)."""
+    return int(_lib.gdn_lin_chunk_fwd_workspace_bytes(
+        ctypes.byref(_plain_shape(B, H, H if H_qk is None else H_qk, T, d_k, d_v, packed))))
+
+
+def gdn_lin_chunk_bwd_workspace_bytes(B: int, H: int, T: int, d_k: int, d_v: int, H_qk: int | None = None,
+                                      packed: bool = False) -> int:
+    """Device workspace (bytes) gdn_lin_chunk_bwd needs for B sequences."""
+    return int(_lib.gdn_lin_chunk_bwd_workspace_bytes(
+        ctypes.byref(_plain_shape(B, H, H if H_qk is None else H_qk, T, d_k, d_v, packed))))
+
+
+def gdn_lin_chunk_fwd(Q, K, V, g, scale: float | None = None, S0=None, offsets=None, o_dtype=torch.bfloat16,
+                      O=None, S_out=None, workspace=None, stream=None):
+    """Linear attention with a decay for each head, whole sequences:
+    S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.
+
+    Q, K [B,H_qk,T,d_k], V [B,H,T,d_v] bf16 (H_qk divides H); g fp32, [B,H,T] log-decays or
+    [H] for one decay per head.  offsets: int32 [n+1] for n packed sequences in B = 1 rows of
+    T tokens.  S0 [B or n,H,d_k,d_v] fp32 or None (zeros).  Any T.  workspace: a uint8 tensor
+    of gdn_lin_chunk_fwd_workspace_bytes(...) bytes, or None to have one allocated here.
+    Returns (O [B,H,T,d_v], S_out [B or n,H,d_k,d_v] fp32)."""
+    sh, n, dev = _lin_shape(Q, K, V, g, scale, offsets, _BF16)
+    state = (n, sh.H, sh.d_k, sh.d_v)
+    if S0 is not None:
+        _arg(S0, "S0", (torch.float32,), state, dev)
+    with _scope(dev, stream):
+        O = _out(O, "O", _FLOAT, V.shape, dev, o_dtype)
+        S_out = _out(S_out, "S_out", (torch.float32,), state, dev, torch.float32)
+        ws, ws_bytes = _scratch(workspace, _lib.gdn_lin_chunk_fwd_workspace_bytes(ctypes.byref(sh)), dev)
+        st = _lib.gdn_lin_chunk_fwd(ctypes.byref(sh), _ptr(Q), _ptr(K), _ptr(V), GDN_BF16, _ptr(g), _ptr(S0), _ptr(O),
+                                    _TORCH_DTYPE[O.dtype], _ptr(S_out), _ptr(ws), ws_bytes, _stream(None))
+    _check(st, "gdn_lin_chunk_fwd")
+    return O, S_out
+
+
+def gdn_lin_chunk_bwd(Q, K, V, g, dO, scale: float | None = None, S0=None, dS=None, offsets=None,
+                      grad_dtype=torch.bfloat16, want_dg: bool = True, workspace=None, stream=None):
+    """Backward pass of gdn_lin_chunk_fwd from dO [B,H,T,d_v] (bf16) and dS (gradient of
+    S_out, or None).  Returns (dQ, dK, dV in grad_dtype, dg fp32 as g or None, dS0 fp32, or
+    None without S0)."""
+    sh, n, dev = _lin_shape(Q, K, V, g, scale, offsets, _BF16)
+    state = (n, sh.H, sh.d_k, sh.d_v)
+    _arg(dO, "dO", _BF16, V.shape, dev)
+    for t, name in ((S0, "S0"), (dS, "dS")):
+        if t is not None:
+            _arg(t, name, (torch.float32,), state, dev)
+    if grad_dtype not in _FLOAT:
+        raise TypeError("grad_dtype is %s, expected one of %s" % (grad_dtype, _FLOAT))
+    with _scope(dev, stream):
+        # rows of no packed sequence get no gradient
+        new = torch.empty if offsets is None else torch.zeros
+        dQ, dK, dV = (new(t.shape, device=dev, dtype=grad_dtype) for t in (Q, K, V))
+        dg = new(g.shape, device=dev, dtype=torch.float32) if want_dg else None
+        dS0 = None if S0 is None else torch.empty(state, device=dev, dtype=torch.float32)
+        ws, ws_bytes = _scratch(workspace, _lib.gdn_lin_chunk_bwd_workspace_bytes(ctypes.byref(sh)), dev)
+        st = _lib.gdn_lin_chunk_bwd(ctypes.byref(sh), _ptr(Q), _ptr(K), _ptr(V), GDN_BF16, _ptr(g), _ptr(S0), _ptr(dO),
+                                    _ptr(dS), _ptr(dQ), _ptr(dK), _ptr(dV), _TORCH_DTYPE[grad_dtype], _ptr(dg),
+                                    _ptr(dS0), _ptr(ws), ws_bytes, _stream(None))
+    _check(st, "gdn_lin_chunk_bwd")
+    return dQ, dK, dV, dg, dS0
+
+
+def gdn_lin_decode(Q, K, V, g, S=None, scale: float | None = None, S_out=None, O=None, o_dtype=torch.bfloat16,
+                   stream=None):
+    """The recurrence of gdn_lin_chunk_fwd token by token with the state kept on chip.
+    Q, K [B,H_qk,n,d_k], V [B,H,n,d_v] (bf16 or fp32, one dtype), g [B,H,n] or [H] fp32,
+    S [B,H,d_k,d_v] fp32 or None (zeros).  Pass S_out=S to update the state in place.
+    Returns (O [B,H,n,d_v], S_out)."""
+    sh, n, dev = _lin_shape(Q, K, V, g, scale, None, _FLOAT)
+    state = (n, sh.H, sh.d_k, sh.d_v)
+    if S is not None:
+        _arg(S, "S", (torch.float32,), state, dev)
+    with _scope(dev, stream):
+        O = _out(O, "O", _FLOAT, V.shape, dev, o_dtype)
+        S_out = _out(S_out, "S_out", (torch.float32,), state, dev, torch.float32)
+        st = _lib.gdn_lin_decode(ctypes.byref(sh), _ptr(Q), _ptr(K), _ptr(V), _TORCH_DTYPE[K.dtype], _ptr(g), _ptr(S),
+                                 _ptr(S_out), _ptr(O), _TORCH_DTYPE[O.dtype], _stream(None))
+    _check(st, "gdn_lin_decode")
+    return O, S_out
+
+
+def _gate_args(O, Z, w, act):
+    """Checks of the gated norm's inputs; returns (B, H, T, d, Z's token stride, device)."""
+    if O is None or O.dim() != 4:
+        raise ValueError("O must be [B, H, T, d]")
+    B, H, T, d = O.shape
+    dev = O.device
+    _arg(O, "O", _FLOAT, (B, H, T, d), None)
+    if not isinstance(Z, torch.Tensor) or not Z.is_cuda or Z.dtype != O.dtype:
+        raise TypeError("Z must be a CUDA (HIP) tensor of O's dtype")
+    if Z.device != dev:
+        raise ValueError("Z is on %s, expected %s" % (Z.device, dev))
+    if tuple(Z.shape) != (B, T, H, d):
+        raise ValueError("Z must be %s, got %s" % ((B, T, H, d), tuple(Z.shape)))
+    # tokens at any stride (a part of a wider projection), the values of a token together
+    step = Z.stride(1) if T > 1 else Z.stride(0) if B > 1 else H * d
+    if Z.numel() and ((d > 1 and Z.stride(3) != 1) or (H > 1 and Z.stride(2) != d) or
+                      (B > 1 and T > 1 and Z.stride(0) != T * step) or step < H * d):
+        raise ValueError("Z's heads must be contiguous within a token and its tokens at one stride")
+    if not Z.numel():
+        step = H * d
+    if w is not None:
+        _arg(w, "w", (torch.float32,), (d,), dev)
+    if act not in _ACT:
+        raise ValueError("act must be one of %s" % (tuple(_ACT),))
+    return B, H, T, d, step, dev
+
+
+def gdn_gate_norm_fwd(O, Z, w=None, eps: float = 1e-6, act: str = "silu", Y=None, stream=None):
+    """Gated norm of the head outputs: O [B,H,T,d] (as gdn_lin_chunk_fwd, gdn_chunk_fwd and the
+    decode entry points return it), Z [B,T,H,d] (its tokens at any stride), w [d] fp32 or None
+    -> Y [B,T,H,d] = O / rms(O) * w * act(Z), act "silu" or "sigmoid"; O, Z, Y bf16 or fp32."""
+    B, H, T, d, step, dev = _gate_args(O, Z, w, act)
+    with _scope(dev, stream):
+        Y = _out(Y, "Y", (O.dtype,), (B, T, H, d), dev, O.dtype)
+        st = _lib.gdn_gate_norm_fwd(_ptr(O), _ptr(Z), step, _ptr(w), _ptr(Y), _TORCH_DTYPE[O.dtype], B, H, T, d,
+                                    _ACT[act], float(eps), _stream(None))
+    _check(st, "gdn_gate_norm_fwd")
+    return Y
+
+
+def gdn_gate_norm_bwd(dY, O, Z, w=None, eps: float = 1e-6, act: str = "silu", workspace=None, stream=None):
+    """Backward pass of gdn_gate_norm_fwd from dY [B,T,H,d].  Returns (dO [B,H,T,d],
+    dZ [B,T,H,d], dw [d] fp32, or None without w)."""
+    B, H, T, d, step, dev = _gate_args(O, Z, w, act)
+    _arg(dY, "dY", (O.dtype,), (B, T, H, d), dev)
+    with _scope(dev, stream):
+        dO = torch.empty_like(O)
+        dZ = torch.empty((B, T, H, d), device=dev, dtype=O.dtype)
+        dw = None if w is None else torch.empty((d,), device=dev, dtype=torch.float32)
+        ws, ws_bytes = (None, 0) if dw is None else _scratch(
+            workspace, _lib.gdn_gate_norm_bwd_workspace_bytes(B, H, T, d), dev)
+        st = _lib.gdn_gate_norm_bwd(_ptr(dY), _ptr(O), _ptr(Z), step, _ptr(w), _ptr(dO), _ptr(dZ), _ptr(dw),
+                                    _TORCH_DTYPE[O.dtype], B, H, T, d, _ACT[act], float(eps), _ptr(ws), ws_bytes,
+                                    _stream(None))
+    _check(st, "gdn_gate_norm_bwd")
+    return dO, dZ, dw
+
+
+def _res_args(X, Y, w_post, s, w_pre, x_name):
+    """Checks of the residual norm's inputs; returns (rows, D, device)."""
+    if X is None or X.dim() < 1:
+        raise ValueError("%s must be [.., D]" % x_name)
+    dev, D = X.device, X.shape[-1]
+    _arg(X, x_name, _FLOAT, X.shape, None)
+    _arg(Y, "Y", _FLOAT, X.shape, dev)
+    for t, name in ((w_post, "w_post"), (s, "s"), (w_pre, "w_pre")):
+        if t is not None:
+            _arg(t, name, (torch.float32,), (D,), dev)
+    return (X.numel() // D if D else 0), D, dev
+
+
+def gdn_residual_norm_fwd(X, Y, w_post=None, s=None, alpha: float = 1.0, w_pre=None, eps: float = 1e-6,
+                          want_norm: bool = True, R=None, N=None, stream=None):
+    """Residual sum with the norms around it: R = X + alpha s * (rms(Y) * w_post) and
+    N = rms(R) * w_pre, over rows of D (X, Y [.., D], bf16 or fp32 each; R as X, N as Y).
+    w_post None: Y is not normed; s, w_pre None: ones; want_norm=False: N is None.  R may be X.
+    Returns (R, N)."""
+    rows, D, dev = _res_args(X, Y, w_post, s, w_pre, "X")
+    with _scope(dev, stream):
+        R = _out(R, "R", (X.dtype,), X.shape, dev, X.dtype)
+        N = _out(N, "N", (Y.dtype,), Y.shape, dev, Y.dtype) if want_norm else None
+        st = _lib.gdn_residual_norm_fwd(_ptr(X), _TORCH_DTYPE[X.dtype], _ptr(Y), _TORCH_DTYPE[Y.dtype], _ptr(w_post),
+                                        _ptr(s), float(alpha), _ptr(w_pre), _ptr(R), _ptr(N), rows, D, float(eps),
+                                        _stream(None))
+    _check(st, "gdn_residual_norm_fwd")
+    return R, N
+
+
+def gdn_residual_norm_bwd(dN, dR, R, Y, w_post=None, s=None, alpha: float = 1.0, w_pre=None, eps: float = 1e-6,
+                          workspace=None, stream=None):
+    """Backward pass of gdn_residual_norm_fwd from dN (as Y) and dR (as R), either None for
+    zeros, with the R that the forward pass returned.  Returns (dX, dY, dw_pre, dw_post, ds),
+    the last three fp32 [D], each None without its factor (dw_pre also without dN)."""
+    rows, D, dev = _res_args(R, Y, w_post, s, w_pre, "R")
+    if dN is not None:
+        _arg(dN, "dN", (Y.dtype,), Y.shape, dev)
+    if dR is not None:
+        _arg(dR, "dR", (R.dtype,), R.shape, dev)
+    with _scope(dev, stream):
+        dX, dY = torch.empty_like(R), torch.empty_like(Y)
+        vec = lambda t: None if t is None else torch.empty((D,), device=dev, dtype=torch.float32)  # noqa: E731
+        dw_pre, dw_post, ds = vec(w_pre if dN is not None else None), vec(w_post), vec(s)
+        ws, ws_bytes = (None, 0) if dw_pre is dw_post is ds is None else _scratch(
+            workspace, _lib.gdn_residual_norm_bwd_workspace_bytes(rows, D), dev)
+        st = _lib.gdn_residual_norm_bwd(_ptr(dN), _ptr(dR), _ptr(R), _TORCH_DTYPE[R.dtype], _ptr(Y),
+                                        _TORCH_DTYPE[Y.dtype], _ptr(w_post), _ptr(s), float(alpha), _ptr(w_pre),
+                                        _ptr(dX), _ptr(dY), _ptr(dw_pre), _ptr(dw_post), _ptr(ds), rows, D, float(eps),
+                                        _ptr(ws), ws_bytes, _stream(None))
+    _check(st, "gdn_residual_norm_bwd")
+    return dX, dY, dw_pre, dw_post, ds

@@ -6,6 +6,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <initializer_list>
+
 #include "gdn_kernels.hpp"
 
 namespace {
@@ -329,6 +331,293 @@ gdn_status gdn_decode(const void* Q, const void* K, const void* V, int32_t qkv_d
   p.o_bf16 = o_dtype == GDN_BF16;
   p.scale = scale;
   return launch_result(gdn::launch_decode(p, as_stream(stream)));
+}
+
+// ---- linear attention with a decay for each head --------------------------------------
+
+// sizes of a gdn_lin_shape (pointers are the entry points' matter)
+static gdn_status check_lin(const gdn_lin_shape* s, bool bwd) {
+  if (!s) return GDN_ERR_NULL_POINTER;
+  if (s->B < 0 || s->H < 0 || s->H_qk < 0 || s->T < 0 || s->d_k <= 0 || s->d_v <= 0) return GDN_ERR_BAD_SHAPE;
+  if (s->H > 0 && (s->H_qk == 0 || s->H % s->H_qk != 0)) return GDN_ERR_BAD_SHAPE;
+  if (s->g_per_head != 0 && s->g_per_head != 1) return GDN_ERR_BAD_SHAPE;
+  if (!(s->d_k == 64 || s->d_k == 128)) return GDN_ERR_UNSUPPORTED;
+  if (bwd ? !(s->d_v == 64 || s->d_v == 128) : (s->d_v % 32 != 0 || s->d_v > 256)) return GDN_ERR_UNSUPPORTED;
+  if (s->T > INT32_MAX - 64) return GDN_ERR_UNSUPPORTED;  // token indices within a sequence are 32 bits
+  if ((int64_t)s->B * s->H > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+static gdn::LinLaunch lin_launch(const gdn_lin_shape* s) {
+  gdn::LinLaunch p{};
+  p.offsets = s->offsets;
+  p.scale = s->scale;
+  p.g_per_head = s->g_per_head;
+  p.n_seq = s->B;
+  p.H = s->H;
+  p.H_qk = s->H_qk;
+  p.d_k = s->d_k;
+  p.d_v = s->d_v;
+  p.T = s->T;
+  return p;
+}
+
+static gdn_status check_workspace(size_t need, const void* workspace, size_t bytes) {
+  if (need == 0) return GDN_OK;
+  if (!workspace || bytes < need) return GDN_ERR_WORKSPACE;
+  return aligned16(workspace) ? GDN_OK : GDN_ERR_BAD_ALIGNMENT;
+}
+
+static bool all_aligned16(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!aligned16(p)) return false;
+  return true;
+}
+
+size_t gdn_lin_chunk_fwd_workspace_bytes(const gdn_lin_shape* s) {
+  if (check_lin(s, false) != GDN_OK || s->B == 0 || s->H == 0) return 0;
+  return gdn::lin_workspace(lin_launch(s), false);
+}
+
+size_t gdn_lin_chunk_bwd_workspace_bytes(const gdn_lin_shape* s) {
+  if (check_lin(s, true) != GDN_OK || s->B == 0 || s->H == 0) return 0;
+  return gdn::lin_workspace(lin_launch(s), true);
+}
+
+gdn_status gdn_lin_chunk_fwd(const gdn_lin_shape* s, const void* Q, const void* K, const void* V,
+                             int32_t qkv_dtype, const float* g, const float* S0, void* O, int32_t o_dtype,
+                             float* S_out, void* workspace, size_t workspace_bytes, void* stream) {
+  gdn_status st = check_lin(s, false);
+  if (st != GDN_OK) return st;
+  if (qkv_dtype != GDN_BF16) return qkv_dtype == GDN_F32 ? GDN_ERR_UNSUPPORTED : GDN_ERR_BAD_DTYPE;
+  if (o_dtype != GDN_F32 && o_dtype != GDN_BF16) return GDN_ERR_BAD_DTYPE;
+  if (s->B == 0 || s->H == 0) return GDN_OK;
+  if (s->T > 0 && (!Q || !K || !V || !g || !O)) return GDN_ERR_NULL_POINTER;
+  if (!all_aligned16({Q, K, V, g, S0, O, S_out, s->offsets})) return GDN_ERR_BAD_ALIGNMENT;
+  gdn::LinLaunch p = lin_launch(s);
+  if (!gdn::lin_grid_ok(p, false)) return GDN_ERR_UNSUPPORTED;
+  st = check_workspace(gdn::lin_workspace(p, false), workspace, workspace_bytes);
+  if (st != GDN_OK) return st;
+  p.Q = Q;
+  p.K = K;
+  p.V = V;
+  p.g = g;
+  p.S0 = S0;
+  p.O = O;
+  p.o_bf16 = o_dtype == GDN_BF16;
+  p.S_out = S_out;
+  return launch_result(gdn::launch_lin_fwd(p, workspace, as_stream(stream)));
+}
+
+gdn_status gdn_lin_chunk_bwd(const gdn_lin_shape* s, const void* Q, const void* K, const void* V,
+                             int32_t qkv_dtype, const float* g, const float* S0, const void* dO,
+                             const float* dS, void* dQ, void* dK, void* dV, int32_t grad_dtype, float* dg,
+                             float* dS0, void* workspace, size_t workspace_bytes, void* stream) {
+  gdn_status st = check_lin(s, true);
+  if (st != GDN_OK) return st;
+  if (qkv_dtype != GDN_BF16) return qkv_dtype == GDN_F32 ? GDN_ERR_UNSUPPORTED : GDN_ERR_BAD_DTYPE;
+  if (grad_dtype != GDN_F32 && grad_dtype != GDN_BF16) return GDN_ERR_BAD_DTYPE;
+  if (s->B == 0 || s->H == 0) return GDN_OK;
+  if (s->T > 0 && (!Q || !K || !V || !g || !dO || !dQ || !dK || !dV)) return GDN_ERR_NULL_POINTER;
+  if (!all_aligned16({Q, K, V, g, S0, dO, dS, dQ, dK, dV, dg, dS0, s->offsets})) return GDN_ERR_BAD_ALIGNMENT;
+  gdn::LinLaunch p = lin_launch(s);
+  if (!gdn::lin_grid_ok(p, true)) return GDN_ERR_UNSUPPORTED;
+  st = check_workspace(gdn::lin_workspace(p, true), workspace, workspace_bytes);
+  if (st != GDN_OK) return st;
+  p.Q = Q;
+  p.K = K;
+  p.V = V;
+  p.g = g;
+  p.S0 = S0;
+  p.dO = dO;
+  p.dS = dS;
+  p.dQ = dQ;
+  p.dK = dK;
+  p.dV = dV;
+  p.grad_bf16 = grad_dtype == GDN_BF16;
+  p.dg = dg;
+  p.dS0 = dS0;
+  return launch_result(gdn::launch_lin_bwd(p, workspace, as_stream(stream)));
+}
+
+gdn_status gdn_lin_decode(const gdn_lin_shape* s, const void* Q, const void* K, const void* V, int32_t qkv_dtype,
+                          const float* g, const float* S_in, float* S_out, void* O, int32_t o_dtype,
+                          void* stream) {
+  gdn_status st = check_lin(s, false);
+  if (st != GDN_OK) return st;
+  if (qkv_dtype != GDN_BF16 && qkv_dtype != GDN_F32) return GDN_ERR_BAD_DTYPE;
+  if (o_dtype != GDN_F32 && o_dtype != GDN_BF16) return GDN_ERR_BAD_DTYPE;
+  if (s->offsets) return GDN_ERR_UNSUPPORTED;
+  if (s->B == 0 || s->H == 0) return GDN_OK;
+  if (!S_out || (s->T > 0 && (!Q || !K || !V || !g || !O))) return GDN_ERR_NULL_POINTER;
+  if (!all_aligned16({Q, K, V, g, S_in, S_out, O})) return GDN_ERR_BAD_ALIGNMENT;
+  gdn::LinDecodeLaunch p{};
+  p.Q = Q;
+  p.K = K;
+  p.V = V;
+  p.g = g;
+  p.S_in = S_in;
+  p.S_out = S_out;
+  p.O = O;
+  p.g_per_head = s->g_per_head;
+  p.B = s->B;
+  p.H = s->H;
+  p.H_qk = s->H_qk;
+  p.n = (int)s->T;
+  p.d_k = s->d_k;
+  p.d_v = s->d_v;
+  p.in_bf16 = qkv_dtype == GDN_BF16;
+  p.o_bf16 = o_dtype == GDN_BF16;
+  p.scale = s->scale;
+  return launch_result(gdn::launch_lin_decode(p, as_stream(stream)));
+}
+
+// ---- the norms around the token mixer ---------------------------------------------------
+
+static bool float_dtype(int32_t t) { return t == GDN_F32 || t == GDN_BF16; }
+
+static gdn_status check_gate(int32_t dtype, int32_t B, int32_t H, int64_t T, int32_t d, int64_t z_stride, int32_t act,
+                             float eps) {
+  if (B < 0 || H < 0 || T < 0 || d <= 0 || !(eps >= 0.f)) return GDN_ERR_BAD_SHAPE;
+  if (!float_dtype(dtype)) return GDN_ERR_BAD_DTYPE;
+  if (act != GDN_GATE_SILU && act != GDN_GATE_SIGMOID) return GDN_ERR_BAD_SHAPE;
+  if (z_stride < (int64_t)H * d) return GDN_ERR_BAD_SHAPE;
+  if (z_stride % 8 != 0) return GDN_ERR_BAD_ALIGNMENT;
+  if (d % 32 != 0 || d > 256) return GDN_ERR_UNSUPPORTED;
+  // row indices are 32 bits
+  if (H > 0 && B > 0 && T > INT32_MAX / ((int64_t)B * H)) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+static gdn::GateNormLaunch gate_launch(int32_t dtype, int32_t B, int32_t H, int64_t T, int32_t d) {
+  gdn::GateNormLaunch p{};
+  p.bf16 = dtype == GDN_BF16;
+  p.B = B;
+  p.H = H;
+  p.T = T;
+  p.d = d;
+  return p;
+}
+
+gdn_status gdn_gate_norm_fwd(const void* O, const void* Z, int64_t z_stride, const float* w, void* Y, int32_t dtype,
+                             int32_t B, int32_t H, int64_t T, int32_t d, int32_t act, float eps, void* stream) {
+  const gdn_status st = check_gate(dtype, B, H, T, d, z_stride, act, eps);
+  if (st != GDN_OK) return st;
+  if (B == 0 || H == 0 || T == 0) return GDN_OK;
+  if (!O || !Z || !Y) return GDN_ERR_NULL_POINTER;
+  if (!all_aligned16({O, Z, w, Y})) return GDN_ERR_BAD_ALIGNMENT;
+  gdn::GateNormLaunch p = gate_launch(dtype, B, H, T, d);
+  p.O = O;
+  p.Z = Z;
+  p.z_stride = z_stride;
+  p.w = w;
+  p.Y = Y;
+  p.act = act;
+  p.eps = eps;
+  return launch_result(gdn::launch_gate_norm(p, as_stream(stream)));
+}
+
+size_t gdn_gate_norm_bwd_workspace_bytes(int32_t B, int32_t H, int64_t T, int32_t d) {
+  if (H < 0 || d <= 0 || check_gate(GDN_BF16, B, H, T, d, (int64_t)H * d, GDN_GATE_SILU, 0.f) != GDN_OK) return 0;
+  return gdn::gate_norm_bwd_workspace(gate_launch(GDN_BF16, B, H, T, d));
+}
+
+gdn_status gdn_gate_norm_bwd(const void* dY, const void* O, const void* Z, int64_t z_stride, const float* w, void* dO,
+                             void* dZ, float* dw, int32_t dtype, int32_t B, int32_t H, int64_t T, int32_t d,
+                             int32_t act, float eps, void* workspace, size_t workspace_bytes, void* stream) {
+  gdn_status st = check_gate(dtype, B, H, T, d, z_stride, act, eps);
+  if (st != GDN_OK) return st;
+  gdn::GateNormLaunch p = gate_launch(dtype, B, H, T, d);
+  const bool empty = B == 0 || H == 0 || T == 0;
+  if (empty && !dw) return GDN_OK;
+  if (!empty && (!dY || !O || !Z || !dO || !dZ)) return GDN_ERR_NULL_POINTER;
+  if (!all_aligned16({dY, O, Z, w, dO, dZ, dw})) return GDN_ERR_BAD_ALIGNMENT;
+  st = check_workspace(dw ? gdn::gate_norm_bwd_workspace(p) : 0, workspace, workspace_bytes);
+  if (st != GDN_OK) return st;
+  p.dY = dY;
+  p.O = O;
+  p.Z = Z;
+  p.z_stride = z_stride;
+  p.w = w;
+  p.dO = dO;
+  p.dZ = dZ;
+  p.dw = dw;
+  p.act = act;
+  p.eps = eps;
+  return launch_result(gdn::launch_gate_norm_bwd(p, workspace, as_stream(stream)));
+}
+
+static gdn_status check_res(int32_t x_dtype, int32_t y_dtype, int64_t rows, int32_t D, float eps) {
+  if (rows < 0 || D <= 0 || !(eps >= 0.f)) return GDN_ERR_BAD_SHAPE;
+  if (!float_dtype(x_dtype) || !float_dtype(y_dtype)) return GDN_ERR_BAD_DTYPE;
+  if (D % 8 != 0 || D > 16384) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+static gdn::ResNormLaunch res_launch(int32_t x_dtype, int32_t y_dtype, int64_t rows, int32_t D, float alpha,
+                                     float eps) {
+  gdn::ResNormLaunch p{};
+  p.x_bf16 = x_dtype == GDN_BF16;
+  p.y_bf16 = y_dtype == GDN_BF16;
+  p.rows = rows;
+  p.D = D;
+  p.alpha = alpha;
+  p.eps = eps;
+  return p;
+}
+
+gdn_status gdn_residual_norm_fwd(const void* X, int32_t x_dtype, const void* Y, int32_t y_dtype, const float* w_post,
+                                 const float* s, float alpha, const float* w_pre, void* R, void* N, int64_t rows,
+                                 int32_t D, float eps, void* stream) {
+  const gdn_status st = check_res(x_dtype, y_dtype, rows, D, eps);
+  if (st != GDN_OK) return st;
+  if (rows == 0) return GDN_OK;
+  if (!X || !Y || !R) return GDN_ERR_NULL_POINTER;
+  if (!all_aligned16({X, Y, w_post, s, w_pre, R, N})) return GDN_ERR_BAD_ALIGNMENT;
+  gdn::ResNormLaunch p = res_launch(x_dtype, y_dtype, rows, D, alpha, eps);
+  p.X = X;
+  p.Y = Y;
+  p.w_post = w_post;
+  p.s = s;
+  p.w_pre = w_pre;
+  p.R = R;
+  p.N = N;
+  return launch_result(gdn::launch_res_norm(p, as_stream(stream)));
+}
+
+size_t gdn_residual_norm_bwd_workspace_bytes(int64_t rows, int32_t D) {
+  if (check_res(GDN_F32, GDN_F32, rows, D, 0.f) != GDN_OK) return 0;
+  return gdn::res_norm_bwd_workspace(res_launch(GDN_F32, GDN_F32, rows, D, 0.f, 0.f));
+}
+
+gdn_status gdn_residual_norm_bwd(const void* dN, const void* dR, const void* R, int32_t x_dtype, const void* Y,
+                                 int32_t y_dtype, const float* w_post, const float* s, float alpha,
+                                 const float* w_pre, void* dX, void* dY, float* dw_pre, float* dw_post, float* ds,
+                                 int64_t rows, int32_t D, float eps, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  gdn_status st = check_res(x_dtype, y_dtype, rows, D, eps);
+  if (st != GDN_OK) return st;
+  if ((dw_post && !w_post) || (ds && !s)) return GDN_ERR_NULL_POINTER;
+  const bool sums = dw_pre || dw_post || ds;
+  if (rows == 0 && !sums) return GDN_OK;
+  if (rows > 0 && (!dX || !dY || (dN && !R) || ((w_post || ds) && !Y))) return GDN_ERR_NULL_POINTER;
+  if (!all_aligned16({dN, dR, R, Y, w_post, s, w_pre, dX, dY, dw_pre, dw_post, ds})) return GDN_ERR_BAD_ALIGNMENT;
+  gdn::ResNormLaunch p = res_launch(x_dtype, y_dtype, rows, D, alpha, eps);
+  st = check_workspace(sums ? gdn::res_norm_bwd_workspace(p) : 0, workspace, workspace_bytes);
+  if (st != GDN_OK) return st;
+  p.dN = dN;
+  p.dR = dR;
+  p.X = R;
+  p.Y = Y;
+  p.w_post = w_post;
+  p.s = s;
+  p.w_pre = w_pre;
+  p.dX = dX;
+  p.dY = dY;
+  p.dw_pre = dw_pre;
+  p.dw_post = dw_post;
+  p.ds = ds;
+  return launch_result(gdn::launch_res_norm_bwd(p, workspace, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -120,4 +120,97 @@ struct DecodeLaunch {
 // gated delta rule token by token with the state resident on chip for all n tokens;
 // d_k in {64, 128}, d_v a multiple of 32 up to 256
 int launch_decode(const DecodeLaunch& p, hipStream_t s);
+
+// linear attention with a decay for each head (offsets: packed sequences, n_seq of them in
+// T tokens; NULL: n_seq sequences of T tokens each); d_k in {64, 128}, d_v a multiple of 32
+// up to 256 (backward: in {64, 128})
+struct LinLaunch {
+  const void* Q;
+  const void* K;
+  const void* V;
+  const float* g;
+  const float* S0;  // NULL = zeros
+  const int32_t* offsets;
+  float scale;
+  int g_per_head;
+  int n_seq, H, H_qk, d_k, d_v;
+  int64_t T;
+  // forward
+  void* O;
+  int o_bf16;
+  float* S_out;  // NULL = not wanted
+  // backward
+  const void* dO;
+  const float* dS;  // NULL = zeros
+  void* dQ;
+  void* dK;
+  void* dV;
+  int grad_bf16;
+  float* dg;
+  float* dS0;  // NULL = not wanted
+};
+size_t lin_workspace(const LinLaunch& p, bool bwd);
+bool lin_grid_ok(const LinLaunch& p, bool bwd);  // the launches' grids stay within their limits
+int launch_lin_fwd(const LinLaunch& p, void* workspace, hipStream_t s);
+int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s);
+
+struct LinDecodeLaunch {
+  const void* Q;
+  const void* K;
+  const void* V;
+  const float* g;
+  const float* S_in;  // NULL = zeros; may equal S_out
+  float* S_out;
+  void* O;
+  int g_per_head, B, H, H_qk, n, d_k, d_v;
+  int in_bf16, o_bf16;
+  float scale;
+};
+int launch_lin_decode(const LinDecodeLaunch& p, hipStream_t s);
+
+// gated norm of head outputs: O [B][H][T][d], Z and dZ [B][T] rows of H * d (Z's at stride
+// z_stride), Y and dY [B][T][H][d]; d a multiple of 32 up to 256
+struct GateNormLaunch {
+  const void* O;
+  const void* Z;
+  const float* w;  // NULL = ones
+  void* Y;
+  const void* dY;
+  void* dO;
+  void* dZ;
+  float* dw;  // NULL = not wanted
+  int bf16;
+  int act;
+  int B, H, d;
+  int64_t T, z_stride;
+  float eps;
+};
+size_t gate_norm_bwd_workspace(const GateNormLaunch& p);
+int launch_gate_norm(const GateNormLaunch& p, hipStream_t s);
+int launch_gate_norm_bwd(const GateNormLaunch& p, void* workspace, hipStream_t s);
+
+// residual sum with the norms before and after: [rows][D], D a multiple of 8 up to 16384
+struct ResNormLaunch {
+  const void* X;  // backward: R
+  const void* Y;
+  const float* w_post;
+  const float* s;
+  const float* w_pre;
+  void* R;
+  void* N;
+  const void* dN;
+  const void* dR;
+  void* dX;
+  void* dY;
+  float* dw_pre;
+  float* dw_post;
+  float* ds;
+  int x_bf16, y_bf16;
+  int64_t rows;
+  int D;
+  float alpha, eps;
+};
+size_t res_norm_bwd_workspace(const ResNormLaunch& p);
+int launch_res_norm(const ResNormLaunch& p, hipStream_t s);
+int launch_res_norm_bwd(const ResNormLaunch& p, void* workspace, hipStream_t s);
 }  // namespace gdn

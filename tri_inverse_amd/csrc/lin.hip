@@ -1,0 +1,904 @@
+// lin.hip -- linear attention with a decay for each head, chunk-wise: forward and backward.
+//
+// Per sequence and value head, tokens in order, g_t the log-decays, S [d_k][d_v] fp32:
+//   S_t = e^{g_t} S_{t-1} + k_t v_t^T,     o_t = scale S_t^T q_t
+// (the gated recurrence without the delta correction).  In chunks of 64 tokens, with G the
+// in-chunk cumulative sum of g, S the state before the chunk and D the gradient of the loss
+// with respect to the state after it:
+//   O_i  = scale (sum_{j<=i} e^{G_i-G_j} (q_i . k_j)  v_j  + e^{G_i} q_i S)
+//   dQ_i = scale (sum_{j<=i} e^{G_i-G_j} (do_i . v_j) k_j  + e^{G_i} do_i S^T)
+//   dV_i = scale sum_{j>=i} e^{G_j-G_i} (k_i . q_j)  do_j + e^{G_C-G_i} k_i D
+//   dK_i = scale sum_{j>=i} e^{G_j-G_i} (v_i . do_j) q_j  + e^{G_C-G_i} v_i D^T
+//   S   <- e^{G_C} S + sum_j e^{G_C-G_j} k_j v_j^T
+//   D   <- e^{G_C} D + scale sum_j e^{G_j} q_j do_j^T          (chunks from last to first)
+// All four are one scan over row operands a, column operands b and values c,
+//   out_i = sum_j w_ij (a_i . b_j) c_j + row_i a_i X,   X <- e^{G_C} X + sum_j col_j b_j c_j^T,
+// run forwards for O and dQ and backwards for dV and dK; one kernel serves them all.
+//
+// Gradient of the log-decays: with r_t = q_t . dq_t - k_t . dk_t, dg_t = sum_{s>=t} r_s over
+// the rest of the sequence + <dS_out, S_out>.  Summed over a whole long sequence the
+// differences r_s would lose digits, so the sum runs within a segment of at most 1024 tokens
+// and starts from <D, S> at the segment's end, formed from the two states there.
+//
+// Precision: a, b and c are bf16 as given, so a . b is exact up to the fp32 sums of the
+// MFMA.  The fp32 factor of every other product enters as a sum of bf16 parts: w (a . b) and
+// X (outputs) as two, col c (the state) as three, which keeps all 24 bits of the state that
+// is carried from chunk to chunk and returned in fp32.  G is summed in fp64 and handed over
+// as two floats: the exponent of w is a difference of two sums that can both be large.
+//
+// Work split: one workgroup per (segment, head, 32 columns of c), eight waves.
+//   waves 0..3  state waves (column half h, contraction half kh): each keeps its DK/2 x 16
+//               part of X in registers, adds a X to the chunk's output (partial over kh,
+//               through LDS) and updates X.
+//   waves 4..7  output waves, one 16-row tile each, one chunk behind: w (a . b), its product
+//               with c, the sum with the state waves' part, the store.
+// Rows of b and c and the decay factors pass through a ring of three LDS slots; a comes
+// straight from memory in operand order (16 contiguous bytes per lane).  One barrier per
+// chunk.  A segment is a run of chunks of one sequence: where sequences and heads alone fill
+// the machine a segment is a whole sequence; else each segment's own state is formed first
+// (the same kernel without outputs), the segments are joined in order, and every segment
+// then starts from its state.
+#include "gdn_kernels.hpp"
+#include "gdn_device.hpp"
+
+namespace gdn {
+
+namespace {
+
+constexpr int LC = 64;     // tokens of a chunk
+constexpr int LNT = 4;     // 16-row tiles of a chunk
+constexpr int LDC = 32;    // columns of c per workgroup
+constexpr int LPAD = 16;   // bf16 padding of the LDS rows of b (bank spread)
+constexpr int LWAVES = 8;
+constexpr double LOG2E = 1.4426950408889634;
+
+struct ScanArgs {
+  const __bf16* a;
+  const __bf16* b;
+  const __bf16* c;
+  const float* g;
+  const float* init;   // states given per sequence (NULL: zeros)
+  float* fin;          // states returned per sequence (NULL: not wanted)
+  float* slot;         // states of the segments (workspace); written without OUT, read with
+  float* slot_decay;   // [segment][head] decay over the segment, written without OUT
+  void* out;
+  const __bf16* dotw;  // rows whose product with the output rows goes to dots (NULL: none)
+  float* dots;         // [slice][head row]
+  const int32_t* offsets;
+  int64_t T;
+  int64_t heads_T;     // rows of all heads, B * H * T
+  int n_seq, H, group_a, group_b, group_c, dc;
+  int seg_chunks, n_seg, segs_per_seq;
+  int g_per_head, out_bf16, skip_end;
+  int64_t st_row, st_col;  // strides of the states in this scan's (row, column) order
+  float s_intra, s_inter, s_state;
+};
+
+template <int DK>
+struct alignas(16) LinIn {
+  __bf16 b[LC][DK + LPAD];
+  __bf16 c[LC][LDC];
+};
+
+struct alignas(16) LinGates {
+  float hi[LC], lo[LC];  // G in units of log 2, as a sum of two floats
+  float row[LC];         // factor of a_i X
+  float col[LC];         // factor of b_j c_j^T
+  float end;             // e^{G_C}
+};
+
+// one segment: tokens [tok0 + 64 c0, ...) of a sequence of len tokens starting at tok0
+struct Span {
+  int64_t tok0;
+  int len, seq, c0, nc;
+  bool first, last;
+};
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+__device__ __forceinline__ int wave_scan_int(int v) {
+#pragma unroll
+  for (int d = 1; d < WAVE; d <<= 1) {
+    const int o = __shfl_up(v, d);
+    if (lane_id() >= d) v += o;
+  }
+  return v;
+}
+
+// offsets outside [0, T] or out of order are clamped, so that no access leaves the tensors
+__device__ __forceinline__ void seq_bounds(const int32_t* off, int s, int64_t T, int& o0, int& o1) {
+  const int t = (int)T;
+  o0 = min(max(off[s], 0), t);
+  o1 = min(max(off[s + 1], o0), t);
+}
+
+__device__ __forceinline__ int seg_count(int len, int seg_chunks) {
+  const int nch = (len + LC - 1) / LC;
+  return max(1, (nch + seg_chunks - 1) / seg_chunks);
+}
+
+__device__ __forceinline__ void cut_span(int k, int ns, int seg_chunks, Span& sp) {
+  const int nch = (sp.len + LC - 1) / LC;
+  sp.c0 = k * seg_chunks;
+  sp.nc = min(seg_chunks, nch - sp.c0);
+  sp.first = k == 0;
+  sp.last = k == ns - 1;
+}
+
+// the segment of index seg; false: there are fewer (packed sequences: the grid is an upper bound)
+__device__ __forceinline__ bool find_segment(const int32_t* off, int n_seq, int64_t T, int seg_chunks,
+                                             int segs_per_seq, int seg, Span& sp) {
+  if (!off) {
+    sp.seq = seg / segs_per_seq;
+    sp.tok0 = 0;
+    sp.len = (int)T;
+    cut_span(seg % segs_per_seq, segs_per_seq, seg_chunks, sp);
+    return true;
+  }
+  int base = 0;
+  for (int s0 = 0; s0 < n_seq; s0 += WAVE) {
+    const int s = s0 + lane_id();
+    int o0 = 0, o1 = 0, n = 0;
+    if (s < n_seq) {
+      seq_bounds(off, s, T, o0, o1);
+      n = seg_count(o1 - o0, seg_chunks);
+    }
+    const int inc = wave_scan_int(n);
+    const uint64_t m = __builtin_amdgcn_ballot_w64(base + inc > seg);
+    if (m) {
+      const int src = __builtin_ctzll(m);
+      const int a0 = __builtin_amdgcn_readlane(o0, src), a1 = __builtin_amdgcn_readlane(o1, src);
+      const int ns = __builtin_amdgcn_readlane(n, src), i1 = __builtin_amdgcn_readlane(inc, src);
+      sp.seq = s0 + src;
+      sp.tok0 = a0;
+      sp.len = a1 - a0;
+      cut_span(seg - (base + i1 - ns), ns, seg_chunks, sp);
+      return true;
+    }
+    base += __builtin_amdgcn_readlane(inc, WAVE - 1);
+  }
+  return false;
+}
+
+// index of a sequence's first segment, and how many it has
+__device__ __forceinline__ int first_segment(const int32_t* off, int64_t T, int seg_chunks, int segs_per_seq,
+                                             int seq, int& ns) {
+  if (!off) {
+    ns = segs_per_seq;
+    return seq * segs_per_seq;
+  }
+  int base = 0;
+  for (int s0 = 0; s0 < seq; s0 += WAVE) {
+    const int s = s0 + lane_id();
+    int n = 0, o0, o1;
+    if (s < seq) {
+      seq_bounds(off, s, T, o0, o1);
+      n = seg_count(o1 - o0, seg_chunks);
+    }
+    base += __builtin_amdgcn_readlane(wave_scan_int(n), WAVE - 1);
+  }
+  int o0, o1;
+  seq_bounds(off, seq, T, o0, o1);
+  ns = seg_count(o1 - o0, seg_chunks);
+  return base;
+}
+
+__device__ __forceinline__ double wave_scan_f64(double v) {
+#pragma unroll
+  for (int d = 1; d < WAVE; d <<= 1) {
+    const double o = __shfl_up(v, d);
+    if (lane_id() >= d) v += o;
+  }
+  return v;
+}
+
+// log-decays below 2^-512 are e^g = 0 in every product: clamped, so that -inf (a state that is
+// forgotten) keeps the differences of G finite.  A NaN stays one.
+__device__ __forceinline__ double clamp_log2(double x) { return x < -512.0 ? -512.0 : x; }
+
+__device__ __forceinline__ float exp2_f32(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ f32x4 lo4(const bf16x8& v) { return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]}; }
+__device__ __forceinline__ f32x4 hi4(const bf16x8& v) { return f32x4{(float)v[4], (float)v[5], (float)v[6], (float)v[7]}; }
+
+// x as the sum of two (three) bf16 operands
+__device__ __forceinline__ void split2(const f32x4& a, const f32x4& b, bf16x8 (&s)[2]) {
+  s[0] = pack8(a, b);
+  s[1] = pack8(a - lo4(s[0]), b - hi4(s[0]));
+}
+__device__ __forceinline__ void split3(const f32x4& a, const f32x4& b, bf16x8 (&s)[3]) {
+  s[0] = pack8(a, b);
+  const f32x4 ra = a - lo4(s[0]), rb = b - hi4(s[0]);
+  s[1] = pack8(ra, rb);
+  s[2] = pack8(ra - lo4(s[1]), rb - hi4(s[1]));
+}
+
+// d of the state tile's row 4g + r: two tiles 2p, 2p + 1 of a lane are then the natural-order
+// operand (slot t <-> d = 32p + 8g + t)
+__device__ __forceinline__ int state_dim(int a, int g, int r) { return 32 * (a >> 1) + 8 * g + 4 * (a & 1) + r; }
+
+__device__ __forceinline__ void lds_handover() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+}  // namespace
+
+template <int DK, bool REV, bool OUT>
+__global__ __launch_bounds__(LWAVES * WAVE, 1) void lin_scan_kernel(ScanArgs A) {
+  __shared__ LinIn<DK> in[3];
+  __shared__ LinGates gates[3];
+  __shared__ f32x4 part[2][2][2][LNT][WAVE];  // [chunk parity][kh][h][row tile]: a X over half the contraction
+  constexpr int NP = DK / 32;   // 32-wide steps of the contraction
+  constexpr int NH = NP / 2;    // of one state wave
+  constexpr int NA = DK / 32;   // 16-row state tiles of one state wave
+  constexpr int SEG = DK / 8;   // 16-byte pieces of a row of b
+  constexpr int NB = LC * SEG / (LWAVES * WAVE);
+
+  // workgroup -> (segment, head, slice): the slices of a head, and the heads that share rows,
+  // are consecutive indices within one XCD (workgroups are dealt round-robin over the 8 XCDs)
+  const int n_slices = A.dc / LDC;
+  const int total = A.n_seg * A.H * n_slices;
+  const int per = (total + 7) / 8;
+  const int idx = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
+  if (idx >= total) return;
+  const int slice = idx % n_slices, head = (idx / n_slices) % A.H, seg = idx / (n_slices * A.H);
+  Span sp;
+  if (!find_segment(A.offsets, A.n_seq, A.T, A.seg_chunks, A.segs_per_seq, seg, sp)) return;
+  if (!OUT && A.skip_end && (REV ? sp.first : sp.last)) return;
+
+  const int wave = uniform(threadIdx.x / WAVE);
+  const int l = lane_id(), g = l >> 4, c = l & 15;
+  const int n = sp.nc, len = sp.len;
+  // first row of the sequence in each tensor ([B][heads][T][.], or [heads][T][.] packed)
+  const int64_t batch = A.offsets ? 0 : sp.seq;
+  auto row_of = [&](int group) {
+    const int heads = A.H / group;
+    return (batch * heads + head / group) * A.T + sp.tok0;
+  };
+  const __bf16* ap = A.a + row_of(A.group_a) * DK;
+  const __bf16* bp = A.b + row_of(A.group_b) * DK;
+  const int64_t crow = row_of(A.group_c);
+  const __bf16* cp = A.c + crow * A.dc + slice * LDC;
+  const int64_t orow = row_of(1);
+  auto chunk_of = [&](int j) { return REV ? sp.c0 + n - 1 - j : sp.c0 + j; };
+
+  // ---- staging: every thread loads NB pieces of b, the first 256 one piece of c --------
+  struct Staged {
+    bf16x8 b[NB];
+    bf16x8 c;
+    float g;
+  } st;
+  const int tid = threadIdx.x;
+  const bool has_c = wave < 4;
+  constexpr int GATE_TILE = REV ? LNT - 1 : 0;  // the output wave with the fewest products
+  const bool has_g = wave == 4 + GATE_TILE;
+  auto load = [&](int j) {
+    const int t0 = LC * chunk_of(min(j, n - 1));
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int e = i * LWAVES * WAVE + tid;
+      const int t = min(t0 + e / SEG, len - 1);
+      st.b[i] = *reinterpret_cast<const bf16x8*>(bp + (int64_t)t * DK + 8 * (e % SEG));
+    }
+    if (has_c) {
+      const int t = min(t0 + (tid >> 2), len - 1);
+      st.c = *reinterpret_cast<const bf16x8*>(cp + (int64_t)t * A.dc + 8 * (tid & 3));
+    }
+    if (has_g) st.g = A.g_per_head ? A.g[head] : A.g[orow + min(t0 + l, len - 1)];
+  };
+  double decay = 0.0;  // sum of G_C over the segment (gate wave, without OUT)
+  // rows past the sequence's end become zero rows with no decay
+  auto store = [&](int j, LinIn<DK>& S, LinGates& GT) {
+    const int t0 = LC * chunk_of(j);
+    const bf16x8 z = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int e = i * LWAVES * WAVE + tid;
+      *reinterpret_cast<bf16x8*>(&S.b[e / SEG][8 * (e % SEG)]) = t0 + e / SEG < len ? st.b[i] : z;
+    }
+    if (has_c) *reinterpret_cast<bf16x8*>(&S.c[tid >> 2][8 * (tid & 3)]) = t0 + (tid >> 2) < len ? st.c : z;
+    if (has_g) {
+      const double gl = t0 + l < len ? clamp_log2((double)st.g * LOG2E) : 0.0;
+      const double G = wave_scan_f64(gl), GC = __shfl(G, WAVE - 1);
+      const float hi = (float)G;
+      GT.hi[l] = hi;
+      GT.lo[l] = (float)(G - (double)hi);
+      const float eG = exp2_f32((float)G), eR = exp2_f32((float)(GC - G));
+      GT.row[l] = (REV ? eR : eG) * A.s_inter;
+      GT.col[l] = (REV ? eG : eR) * A.s_state;
+      if (l == 0) GT.end = exp2_f32((float)GC);
+      decay += GC;
+    }
+  };
+
+  const int64_t head_state = (int64_t)DK * A.dc;
+  const float* from = nullptr;  // the state this segment starts from (NULL: zeros)
+  if (OUT) {
+    if (REV ? sp.last : sp.first)
+      from = A.init ? A.init + ((int64_t)sp.seq * A.H + head) * head_state : nullptr;
+    else
+      from = A.slot + ((int64_t)(REV ? min(seg + 1, A.n_seg - 1) : seg - 1) * A.H + head) * head_state;
+  }
+  float* to = nullptr;
+  if (!OUT)
+    to = A.slot + ((int64_t)seg * A.H + head) * head_state;
+  else if ((REV ? sp.first : sp.last) && A.fin)
+    to = A.fin + ((int64_t)sp.seq * A.H + head) * head_state;
+
+  if (n > 0) {
+    load(0);
+    store(0, in[0], gates[0]);
+    load(1);
+    lds_handover();
+  }
+
+  if (wave < 4) {
+    // ---- state waves -----------------------------------------------------------------
+    const int h = wave & 1, kh = wave >> 1;
+    const int d0 = kh * (DK / 2);
+    const int64_t col = slice * LDC + 16 * h + c;
+    f32x4 X[NA];
+#pragma unroll
+    for (int t = 0; t < NA; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        X[t][r] = from ? from[(d0 + state_dim(t, g, r)) * A.st_row + col * A.st_col] : 0.f;
+    bf16x8 af[LNT][NH];
+    auto load_a = [&](int j) {
+      const int t0 = LC * chunk_of(min(j, n - 1));
+#pragma unroll
+      for (int I = 0; I < LNT; ++I) {
+        const int t = min(t0 + 16 * I + c, len - 1);
+#pragma unroll
+        for (int p = 0; p < NH; ++p)
+          af[I][p] = *reinterpret_cast<const bf16x8*>(ap + (int64_t)t * DK + d0 + 32 * p + 8 * g);
+      }
+    };
+    if (OUT && n > 0) load_a(0);
+    for (int it = 0; it < n; ++it) {
+      if (it + 1 < n) store(it + 1, in[(it + 1) % 3], gates[(it + 1) % 3]);
+      load(it + 2);
+      const LinIn<DK>& S = in[it % 3];
+      const LinGates& GT = gates[it % 3];
+      if constexpr (OUT) {
+        f32x4 x[LNT];
+#pragma unroll
+        for (int I = 0; I < LNT; ++I) x[I] = zero4();
+#pragma unroll
+        for (int p = 0; p < NH; ++p) {
+          bf16x8 s[2];
+          split2(X[2 * p], X[2 * p + 1], s);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int I = 0; I < LNT; ++I) x[I] = mma_bf16(s[k], af[I][p], x[I]);
+        }
+        load_a(it + 1);
+#pragma unroll
+        for (int I = 0; I < LNT; ++I) part[it & 1][kh][h][I][l] = x[I];
+      }
+      const float end = GT.end;
+#pragma unroll
+      for (int t = 0; t < NA; ++t) X[t] = X[t] * end;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const bf16x4 c0 = lds_read_tr4(&S.c[32 * p + 4 * g + (c >> 2)][16 * h + 4 * (c & 3)]);
+        const bf16x4 c1 = lds_read_tr4(&S.c[32 * p + 16 + 4 * g + (c >> 2)][16 * h + 4 * (c & 3)]);
+        const f32x4 w0 = *reinterpret_cast<const f32x4*>(&GT.col[32 * p + 4 * g]);
+        const f32x4 w1 = *reinterpret_cast<const f32x4*>(&GT.col[32 * p + 16 + 4 * g]);
+        bf16x8 u[3];
+        split3(unpack4(c0) * w0, unpack4(c1) * w1, u);
+        bf16x8 bt[NA];
+#pragma unroll
+        for (int t = 0; t < NA; ++t) {
+          const int d = d0 + state_dim(t, c & 3, 0);
+          bt[t] = join8(lds_read_tr4(&S.b[32 * p + 4 * g + (c >> 2)][d]),
+                        lds_read_tr4(&S.b[32 * p + 16 + 4 * g + (c >> 2)][d]));
+        }
+#pragma unroll
+        for (int k = 2; k >= 0; --k)
+#pragma unroll
+          for (int t = 0; t < NA; ++t) X[t] = mma_bf16(bt[t], u[k], X[t]);
+      }
+      lds_handover();
+    }
+    if (OUT && n > 0) lds_handover();
+    if (to) {
+#pragma unroll
+      for (int t = 0; t < NA; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) to[(d0 + state_dim(t, g, r)) * A.st_row + col * A.st_col] = X[t][r];
+    }
+    return;
+  }
+
+  // ---- output waves: row tile I of the chunk before the state waves' --------------------
+  if constexpr (!OUT) {
+    for (int it = 0; it < n; ++it) {
+      if (it + 1 < n) store(it + 1, in[(it + 1) % 3], gates[(it + 1) % 3]);
+      load(it + 2);
+      lds_handover();
+    }
+    if (has_g && slice == 0 && l == 0) A.slot_decay[(int64_t)seg * A.H + head] = exp2_f32((float)decay);
+    return;
+  } else {
+    if (n <= 0) return;
+    auto rows = [&](auto tile) {
+      constexpr int I = tile.value;
+      constexpr int J0 = REV ? I : 0, J1 = REV ? LNT - 1 : I;  // tiles of b with a non-zero weight
+      bf16x8 af[NP];
+      auto load_a = [&](int j) {
+        const int t = min(LC * chunk_of(min(j, n - 1)) + 16 * I + c, len - 1);
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+          af[p] = *reinterpret_cast<const bf16x8*>(ap + (int64_t)t * DK + 32 * p + 8 * g);
+      };
+      load_a(0);
+      for (int it = 0; it <= n; ++it) {
+        if (it + 1 < n) store(it + 1, in[(it + 1) % 3], gates[(it + 1) % 3]);
+        if (it < n) load(it + 2);
+        if (it > 0) {
+          const int j = it - 1;
+          const LinIn<DK>& S = in[j % 3];
+          const LinGates& GT = gates[j % 3];
+          // P_ij = w_ij (a_i . b_j): lane (g, c) holds row i = 16I + c, columns 16J + 4g + r
+          f32x4 P[LNT];
+#pragma unroll
+          for (int J = 0; J < LNT; ++J) {
+            P[J] = zero4();
+            if (J < J0 || J > J1) continue;
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+              P[J] = mma_bf16(*reinterpret_cast<const bf16x8*>(&S.b[16 * J + c][32 * p + 8 * g]), af[p], P[J]);
+          }
+          load_a(it);
+          const float hi = GT.hi[16 * I + c], lo = GT.lo[16 * I + c];
+#pragma unroll
+          for (int J = J0; J <= J1; ++J) {
+            const f32x4 hj = *reinterpret_cast<const f32x4*>(&GT.hi[16 * J + 4 * g]);
+            const f32x4 lj = *reinterpret_cast<const f32x4*>(&GT.lo[16 * J + 4 * g]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float e = REV ? (hj[r] - hi) + (lj[r] - lo) : (hi - hj[r]) + (lo - lj[r]);
+              const float w = exp2_f32(e) * A.s_intra;
+              const bool keep = J != I || (REV ? 4 * g + r >= c : 4 * g + r <= c);
+              P[J][r] = keep ? P[J][r] * w : 0.f;
+            }
+          }
+          f32x4 o[2] = {zero4(), zero4()};
+#pragma unroll
+          for (int p = J0 / 2; p <= J1 / 2; ++p) {
+            bf16x8 s[2];
+            split2(P[2 * p], P[2 * p + 1], s);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const bf16x8 cf = join8(lds_read_tr4(&S.c[32 * p + 4 * g + (c >> 2)][16 * h + 4 * (c & 3)]),
+                                      lds_read_tr4(&S.c[32 * p + 16 + 4 * g + (c >> 2)][16 * h + 4 * (c & 3)]));
+              o[h] = mma_bf16(cf, s[1], o[h]);
+              o[h] = mma_bf16(cf, s[0], o[h]);
+            }
+          }
+          const float rw = GT.row[16 * I + c];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            o[h] = o[h] + (part[j & 1][0][h][I][l] + part[j & 1][1][h][I][l]) * rw;
+          const int t = LC * chunk_of(j) + 16 * I + c;
+          const int64_t row = orow + t;
+          if (A.dotw) {
+            const __bf16* wp = A.dotw + (crow + min(t, len - 1)) * A.dc + slice * LDC + 4 * g;
+            float s = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const f32x4 x = unpack4(*reinterpret_cast<const bf16x4*>(wp + 16 * h));
+#pragma unroll
+              for (int r = 0; r < 4; ++r) s = fmaf(x[r], o[h][r], s);
+            }
+            float s0, s1;
+            self_swap_f<16>(s, s0, s1);
+            s = s0 + s1;
+            self_swap_f<32>(s, s0, s1);
+            s = s0 + s1;
+            if (g == 0 && t < len) A.dots[(int64_t)slice * A.heads_T + row] = s;
+          }
+          if (A.out_bf16) {
+            // all lanes take part in the exchange inside; rows past the end are not stored
+            const bf16x4 h0 = pack4(o[0]), h1 = pack4(o[1]);
+            const u32x2 w0 = __builtin_bit_cast(u32x2, h0), w1 = __builtin_bit_cast(u32x2, h1);
+            u32x4 v;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const unsigned x0 = w0[k], x1 = w1[k];
+              const auto sw = __builtin_amdgcn_permlane16_swap(x0, x1, false, false);
+              const unsigned y0 = sw[0], y1 = sw[1];
+              v[k] = y0;
+              v[2 + k] = y1;
+            }
+            if (t < len)
+              *reinterpret_cast<u32x4*>(reinterpret_cast<__bf16*>(A.out) + row * A.dc + slice * LDC +
+                                        16 * (g & 1) + 8 * (g >> 1)) = v;
+          } else if (t < len) {
+            float* op = reinterpret_cast<float*>(A.out) + row * A.dc + slice * LDC + 4 * g;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) *reinterpret_cast<f32x4*>(op + 16 * h) = o[h];
+          }
+        }
+        lds_handover();
+      }
+    };
+    switch (wave) {
+      case 4: rows(std::integral_constant<int, 0>{}); break;
+      case 5: rows(std::integral_constant<int, 1>{}); break;
+      case 6: rows(std::integral_constant<int, 2>{}); break;
+      default: rows(std::integral_constant<int, 3>{}); break;
+    }
+  }
+}
+
+// The segments' own states joined in order: slot[k] becomes the state after segment k
+// (before it, REV), from the states given per sequence.  One thread per four state values.
+template <bool REV>
+__global__ __launch_bounds__(256) void lin_join_kernel(float* slot, const float* slot_decay, const float* init,
+                                                       const int32_t* offsets, int64_t T, int n_seg, int H, int size,
+                                                       int seg_chunks, int segs_per_seq, int skip_end) {
+  const int per = (size / 4 + 255) / 256;  // workgroups of one state
+  const int head = (int)(blockIdx.x / per) % H, seq = (int)(blockIdx.x / per) / H;
+  int ns;
+  const int s0 = first_segment(offsets, T, seg_chunks, segs_per_seq, seq, ns);
+  if (s0 + ns > n_seg) return;  // offsets out of order: more segments than there can be
+  const int n = ns - skip_end;
+  const int e = 4 * (int)((blockIdx.x % per) * 256 + threadIdx.x);
+  if (e >= size) return;
+  f32x4 x = init ? *reinterpret_cast<const f32x4*>(init + ((int64_t)seq * H + head) * size + e) : zero4();
+  for (int i = 0; i < n; ++i) {
+    const int64_t sh = (int64_t)(REV ? s0 + ns - 1 - i : s0 + i) * H + head;
+    f32x4* p = reinterpret_cast<f32x4*>(slot + sh * size + e);
+    x = x * slot_decay[sh] + *p;
+    *p = x;
+  }
+}
+
+// dg of one (segment, head): from the segment's end backwards, dg_t = <D, S> at the end +
+// sum_{s>=t} (q_s . dq_s - k_s . dk_s), the sums in fp64.  Per-head decays: the segment's sum.
+__global__ __launch_bounds__(256) void lin_dgate_kernel(const float* dot_q, const float* dot_k, int nq, int nk,
+                                                        const float* slot_s, const float* slot_d, const float* dS,
+                                                        float* dg, double* dg_seg, const int32_t* offsets, int64_t T,
+                                                        int64_t heads_T, int n_seq, int n_seg, int H, int size,
+                                                        int seg_chunks, int segs_per_seq) {
+  __shared__ double red[4];
+  const int seg = (int)blockIdx.x / H, head = (int)blockIdx.x % H;
+  const int l = lane_id(), wave = threadIdx.x / WAVE;
+  Span sp;
+  if (!find_segment(offsets, n_seq, T, seg_chunks, segs_per_seq, seg, sp)) return;
+  auto block_sum = [&](double x) {
+#pragma unroll
+    for (int d = 1; d < WAVE; d <<= 1) x += __shfl_xor(x, d);
+    __syncthreads();
+    if (l == 0) red[wave] = x;
+    __syncthreads();
+    return (red[0] + red[1]) + (red[2] + red[3]);
+  };
+  // the states at the segment's end; none given there: their product is zero
+  double run = 0.0;
+  const float* D = sp.last ? (dS ? dS + ((int64_t)sp.seq * H + head) * size : nullptr)
+                           : slot_d + ((int64_t)(seg + 1) * H + head) * size;
+  if (D && seg + (sp.last ? 0 : 1) < n_seg) {
+    const float* S = slot_s + ((int64_t)seg * H + head) * size;
+    double x = 0.0;
+    for (int e = threadIdx.x; e < size; e += 256) x += (double)D[e] * (double)S[e];
+    run = block_sum(x);
+  }
+  const int64_t row0 = ((offsets ? 0 : (int64_t)sp.seq * H) + head) * T + sp.tok0;
+  const int t0 = sp.c0 * LC, t1 = min(sp.len, (sp.c0 + sp.nc) * LC);
+  double sum = 0.0;
+  // 256 tokens a time from the end; thread i holds token hi - 1 - i
+  for (int hi = t1; hi > t0; hi -= 256) {
+    const int t = hi - 1 - (int)threadIdx.x;
+    const bool in = t >= t0;
+    double r = 0.0;
+    if (in) {
+      const int64_t row = row0 + t;
+      for (int s = 0; s < nq; ++s) r += (double)dot_q[s * heads_T + row];
+      for (int s = 0; s < nk; ++s) r -= (double)dot_k[s * heads_T + row];
+    }
+    r = wave_scan_f64(r);
+    __syncthreads();
+    if (l == WAVE - 1) red[wave] = r;
+    __syncthreads();
+    double before = run;
+    for (int w = 0; w < 4; ++w) {
+      if (w < wave) before += red[w];
+      run += red[w];
+    }
+    if (in) {
+      if (dg) dg[row0 + t] = (float)(before + r);
+      sum += before + r;
+    }
+  }
+  if (dg_seg) {
+    sum = block_sum(sum);
+    if (threadIdx.x == 0) dg_seg[(int64_t)seg * H + head] = sum;
+  }
+}
+
+// per-head decays: the segments' sums in order
+__global__ __launch_bounds__(64) void lin_dgate_head_kernel(const double* dg_seg, float* dg, const int32_t* offsets,
+                                                            int64_t T, int n_seq, int n_seg, int H, int seg_chunks,
+                                                            int segs_per_seq) {
+  int ns;
+  const int n = min(n_seg, first_segment(offsets, T, seg_chunks, segs_per_seq, n_seq - 1, ns) + ns);
+  double x = 0.0;
+  for (int s = lane_id(); s < n; s += WAVE) x += dg_seg[(int64_t)s * H + blockIdx.x];
+#pragma unroll
+  for (int d = 1; d < WAVE; d <<= 1) x += __shfl_xor(x, d);
+  if (lane_id() == 0) dg[blockIdx.x] = (float)x;
+}
+
+// gradients of shared heads: the group's fp32 parts summed in order and rounded once; rows
+// before the first and behind the last packed sequence are left as they are
+__global__ __launch_bounds__(256) void lin_group_sum_kernel(const float* part, void* out, int out_bf16, int64_t n,
+                                                            int64_t head_size, int d, int group,
+                                                            const int32_t* offsets, int n_seq) {
+  const int64_t e = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+  if (e >= n) return;
+  const int64_t hd = e / head_size, in = e % head_size;
+  if (offsets && (in < (int64_t)offsets[0] * d || in >= (int64_t)offsets[n_seq] * d)) return;
+  f32x4 x = zero4();
+  for (int i = 0; i < group; ++i)
+    x = x + *reinterpret_cast<const f32x4*>(part + (hd * group + i) * head_size + in);
+  if (out_bf16)
+    *reinterpret_cast<bf16x4*>(reinterpret_cast<__bf16*>(out) + e) = pack4(x);
+  else
+    *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(out) + e) = x;
+}
+
+// ---- host side -----------------------------------------------------------------------
+
+namespace {
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// segments of a call and where its workspace holds what
+struct LinPlan {
+  int seg_chunks, segs_per_seq;
+  int64_t n_seg;
+  bool split;
+  size_t slot_s, slot_d, decay_s, decay_d, dot_q, dot_k, dg_seg, part_q, part_k, bytes;
+};
+
+constexpr int64_t BWD_SEG_CHUNKS = 16;  // at most 1024 tokens are summed into dg from one pair of states
+
+LinPlan make_plan(const LinLaunch& p, bool bwd) {
+  LinPlan q{};
+  const int64_t nch = (p.T + LC - 1) / LC;
+  const int64_t all = p.offsets ? nch + p.n_seq : nch * p.n_seq;  // chunks, at most
+  const int cols = bwd && p.d_k < p.d_v ? p.d_k : p.d_v;
+  const int64_t items = (int64_t)p.H * (cols / LDC);             // workgroups per segment
+  // segments long enough that 512 workgroups share the chunks (two for each CU), at least
+  // 8 chunks: a segment's state costs about half of what its outputs do
+  int64_t seg = (all * items + 511) / 512;
+  seg = seg < 8 ? 8 : seg;
+  if (!bwd && !p.offsets && (p.n_seq * items >= 256 || nch <= 2 * seg)) seg = nch > 0 ? nch : 1;
+  if (bwd && seg > BWD_SEG_CHUNKS) seg = BWD_SEG_CHUNKS;
+  if (seg > nch) seg = nch > 0 ? nch : 1;
+  q.seg_chunks = (int)seg;
+  const int64_t per = nch > 0 ? (nch + seg - 1) / seg : 1;
+  q.segs_per_seq = (int)per;
+  q.n_seg = p.offsets ? nch / seg + p.n_seq : per * p.n_seq;
+  q.split = per > 1;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t x = at;
+    at += up256(n);
+    return x;
+  };
+  const size_t state = (size_t)p.d_k * p.d_v * 4, sh = (size_t)q.n_seg * p.H;
+  const size_t rows = (size_t)(p.offsets ? 1 : p.n_seq) * p.H * p.T;
+  if (q.split || bwd) {
+    q.slot_s = take(sh * state);
+    q.decay_s = take(sh * 4);
+  }
+  if (bwd) {
+    q.slot_d = take(sh * state);
+    q.decay_d = take(sh * 4);
+    q.dot_q = take(rows * (p.d_k / LDC) * 4);
+    q.dot_k = take(rows * (p.d_k / LDC) * 4);
+    if (p.g_per_head) q.dg_seg = take(sh * 8);
+    if (p.H != p.H_qk) {
+      q.part_q = take(rows * p.d_k * 4);
+      q.part_k = take(rows * p.d_k * 4);
+    }
+  }
+  q.bytes = at;
+  return q;
+}
+
+template <bool REV, bool OUT>
+int scan(int dk, const ScanArgs& a, hipStream_t s) {
+  const int64_t total = (int64_t)a.n_seg * a.H * (a.dc / LDC);
+  const dim3 grid((unsigned)(8 * ((total + 7) / 8))), block(LWAVES * WAVE);
+  if (dk == 64)
+    hipLaunchKernelGGL((lin_scan_kernel<64, REV, OUT>), grid, block, 0, s, a);
+  else if (dk == 128)
+    hipLaunchKernelGGL((lin_scan_kernel<128, REV, OUT>), grid, block, 0, s, a);
+  else
+    return -1;
+  return 0;
+}
+
+ScanArgs base_args(const LinLaunch& p, const LinPlan& q) {
+  ScanArgs a{};
+  a.g = p.g;
+  a.offsets = p.offsets;
+  a.T = p.T;
+  a.heads_T = (int64_t)(p.offsets ? 1 : p.n_seq) * p.H * p.T;
+  a.n_seq = p.n_seq;
+  a.H = p.H;
+  a.seg_chunks = q.seg_chunks;
+  a.n_seg = (int)q.n_seg;
+  a.segs_per_seq = q.segs_per_seq;
+  a.g_per_head = p.g_per_head;
+  return a;
+}
+
+void join(bool rev, float* slot, const float* decay, const float* init, const LinLaunch& p, const LinPlan& q,
+          int skip_end, hipStream_t s) {
+  const int size = p.d_k * p.d_v;
+  const dim3 grid((unsigned)((size / 4 + 255) / 256 * p.H * p.n_seq)), block(256);
+  if (rev)
+    hipLaunchKernelGGL((lin_join_kernel<true>), grid, block, 0, s, slot, decay, init, p.offsets, p.T, (int)q.n_seg,
+                       p.H, size, q.seg_chunks, q.segs_per_seq, skip_end);
+  else
+    hipLaunchKernelGGL((lin_join_kernel<false>), grid, block, 0, s, slot, decay, init, p.offsets, p.T, (int)q.n_seg,
+                       p.H, size, q.seg_chunks, q.segs_per_seq, skip_end);
+}
+
+const __bf16* bf(const void* p) { return reinterpret_cast<const __bf16*>(p); }
+
+}  // namespace
+
+size_t lin_workspace(const LinLaunch& p, bool bwd) { return make_plan(p, bwd).bytes; }
+
+bool lin_grid_ok(const LinLaunch& p, bool bwd) {
+  const LinPlan q = make_plan(p, bwd);
+  const int64_t cols = p.d_k > p.d_v ? p.d_k : p.d_v;
+  return q.n_seg * p.H * (cols / LDC) < ((int64_t)1 << 31) - 8;
+}
+
+int launch_lin_fwd(const LinLaunch& p, void* workspace, hipStream_t s) {
+  const LinPlan q = make_plan(p, false);
+  char* ws = reinterpret_cast<char*>(workspace);
+  const int group = p.H / p.H_qk;
+  ScanArgs a = base_args(p, q);
+  a.a = bf(p.Q);
+  a.b = bf(p.K);
+  a.c = bf(p.V);
+  a.group_a = a.group_b = group;
+  a.group_c = 1;
+  a.dc = p.d_v;
+  a.st_row = p.d_v;
+  a.st_col = 1;
+  a.init = p.S0;
+  a.fin = p.S_out;
+  a.out = p.O;
+  a.out_bf16 = p.o_bf16;
+  a.s_intra = a.s_inter = p.scale;
+  a.s_state = 1.f;
+  if (q.split) {
+    a.slot = reinterpret_cast<float*>(ws + q.slot_s);
+    a.slot_decay = reinterpret_cast<float*>(ws + q.decay_s);
+    a.skip_end = 1;
+    int rc = scan<false, false>(p.d_k, a, s);
+    if (rc) return rc;
+    join(false, a.slot, a.slot_decay, p.S0, p, q, 1, s);
+  }
+  return scan<false, true>(p.d_k, a, s);
+}
+
+int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
+  const LinPlan q = make_plan(p, true);
+  char* ws = reinterpret_cast<char*>(workspace);
+  const int group = p.H / p.H_qk;
+  const int end = p.dS != nullptr && p.dg != nullptr;  // <dS, S> at the sequences' ends is wanted
+  float* slot_s = reinterpret_cast<float*>(ws + q.slot_s);
+  float* slot_d = reinterpret_cast<float*>(ws + q.slot_d);
+  ScanArgs f = base_args(p, q), r;
+  f.st_row = p.d_v;
+  f.st_col = 1;
+  r = f;
+  // states before the segments, and gradients of the states after them
+  f.b = bf(p.K);
+  f.c = bf(p.V);
+  f.a = f.b;
+  f.group_a = f.group_b = group;
+  f.group_c = 1;
+  f.dc = p.d_v;
+  f.s_state = 1.f;
+  f.slot = slot_s;
+  f.slot_decay = reinterpret_cast<float*>(ws + q.decay_s);
+  f.skip_end = !end;
+  int rc = 0;
+  if (q.split || end) {
+    rc = scan<false, false>(p.d_k, f, s);
+    if (rc) return rc;
+    join(false, f.slot, f.slot_decay, p.S0, p, q, !end, s);
+  }
+  r.a = r.b = bf(p.Q);
+  r.c = bf(p.dO);
+  r.group_a = r.group_b = group;
+  r.group_c = 1;
+  r.dc = p.d_v;
+  r.s_state = p.scale;
+  r.slot = slot_d;
+  r.slot_decay = reinterpret_cast<float*>(ws + q.decay_d);
+  r.skip_end = 1;
+  if (q.split) {
+    rc = scan<true, false>(p.d_k, r, s);
+    if (rc) return rc;
+    join(true, r.slot, r.slot_decay, p.dS, p, q, 1, s);
+  }
+  // dV, and the gradient of the states given
+  r.a = bf(p.K);
+  r.init = p.dS;
+  r.fin = p.dS0;
+  r.out = p.dV;
+  r.out_bf16 = p.grad_bf16;
+  r.s_intra = p.scale;
+  r.s_inter = 1.f;
+  rc = scan<true, true>(p.d_k, r, s);
+  if (rc) return rc;
+  // dK and dQ: the transposed states, contraction over d_v
+  ScanArgs k = base_args(p, q);
+  k.st_row = 1;
+  k.st_col = p.d_v;
+  k.dc = p.d_k;
+  k.a = bf(p.V);
+  k.b = bf(p.dO);
+  k.c = bf(p.Q);
+  k.group_a = k.group_b = 1;
+  k.group_c = group;
+  k.init = p.dS;
+  k.slot = slot_d;
+  k.dotw = p.dg ? bf(p.K) : nullptr;
+  k.dots = reinterpret_cast<float*>(ws + q.dot_k);
+  k.out = group > 1 ? (void*)(ws + q.part_k) : p.dK;
+  k.out_bf16 = group > 1 ? 0 : p.grad_bf16;
+  k.s_intra = k.s_state = p.scale;
+  k.s_inter = 1.f;
+  rc = scan<true, true>(p.d_v, k, s);
+  if (rc) return rc;
+  k.a = bf(p.dO);
+  k.b = bf(p.V);
+  k.c = bf(p.K);
+  k.init = p.S0;
+  k.slot = slot_s;
+  k.dotw = p.dg ? bf(p.Q) : nullptr;
+  k.dots = reinterpret_cast<float*>(ws + q.dot_q);
+  k.out = group > 1 ? (void*)(ws + q.part_q) : p.dQ;
+  k.s_intra = k.s_inter = p.scale;
+  k.s_state = 1.f;
+  rc = scan<false, true>(p.d_v, k, s);
+  if (rc) return rc;
+  if (group > 1 && p.T > 0) {
+    const int64_t n = (int64_t)(p.offsets ? 1 : p.n_seq) * p.H_qk * p.T * p.d_k;
+    const dim3 grid((unsigned)((n / 4 + 255) / 256)), block(256);
+    hipLaunchKernelGGL(lin_group_sum_kernel, grid, block, 0, s, reinterpret_cast<const float*>(ws + q.part_k), p.dK,
+                       p.grad_bf16, n, p.T * p.d_k, p.d_k, group, p.offsets, p.n_seq);
+    hipLaunchKernelGGL(lin_group_sum_kernel, grid, block, 0, s, reinterpret_cast<const float*>(ws + q.part_q), p.dQ,
+                       p.grad_bf16, n, p.T * p.d_k, p.d_k, group, p.offsets, p.n_seq);
+  }
+  if (!p.dg) return 0;
+  const int nsl = p.d_k / LDC;
+  double* dg_seg = p.g_per_head ? reinterpret_cast<double*>(ws + q.dg_seg) : nullptr;
+  hipLaunchKernelGGL(lin_dgate_kernel, dim3((unsigned)(p.H * q.n_seg)), dim3(256), 0, s,
+                     reinterpret_cast<const float*>(ws + q.dot_q), reinterpret_cast<const float*>(ws + q.dot_k), nsl,
+                     nsl, slot_s, slot_d, p.dS, p.g_per_head ? nullptr : p.dg, dg_seg, p.offsets, p.T, f.heads_T,
+                     p.n_seq, (int)q.n_seg, p.H, p.d_k * p.d_v, q.seg_chunks, q.segs_per_seq);
+  if (p.g_per_head)
+    hipLaunchKernelGGL(lin_dgate_head_kernel, dim3((unsigned)p.H), dim3(64), 0, s, dg_seg, p.dg, p.offsets, p.T,
+                       p.n_seq, (int)q.n_seg, p.H, q.seg_chunks, q.segs_per_seq);
+  return 0;
+}
+
+}  // namespace gdn
