@@ -48,8 +48,7 @@ namespace {
 constexpr int LC = 64;     // tokens of a chunk
 constexpr int LNT = 4;     // 16-row tiles of a chunk
 constexpr int LDC = 32;    // columns of c per workgroup
-constexpr int LPAD = 16;   // bf16 padding of the LDS rows of b (bank spread)
-constexpr int LWAVES = 8;
+constexpr int AHEAD = 5;   // chunks from memory to L2 ahead of their use
 constexpr double LOG2E = 1.4426950408889634;
 
 struct ScanArgs {
@@ -62,29 +61,53 @@ struct ScanArgs {
   float* slot;         // states of the segments (workspace); written without OUT, read with
   float* slot_decay;   // [segment][head] decay over the segment, written without OUT
   void* out;
-  const __bf16* dotw;  // rows whose product with the output rows goes to dots (NULL: none)
+  const __bf16* dotw;  // rows whose product with the output rows goes to dots,
   float* dots;         // [slice][head row]
   const int32_t* offsets;
   int64_t T;
   int64_t heads_T;     // rows of all heads, B * H * T
   int n_seq, H, group_a, group_b, group_c, dc;
   int seg_chunks, n_seg, segs_per_seq;
-  int g_per_head, out_bf16, skip_end;
+  int g_per_head, skip_end;
   int64_t st_row, st_col;  // strides of the states in this scan's (row, column) order
   float s_intra, s_inter, s_state;
 };
 
+// 64 rows of b in LDS, without padding (they arrive by direct loads, 1 KB an instruction in
+// lane order).  The 16-byte pieces of row r are permuted by r so that both readers spread over
+// the banks: 16 consecutive rows at one piece, and 4 rows x 4 pieces by the transpose read.
 template <int DK>
-struct alignas(16) LinIn {
-  __bf16 b[LC][DK + LPAD];
-  __bf16 c[LC][LDC];
+struct alignas(16) LinRows {
+  __bf16 v[LC * DK];
+  static __device__ __forceinline__ int mix(int r) {
+    return DK == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+  }
+  // where element d of row r lies (d a multiple of 4: the rest of its piece follows)
+  static __device__ __forceinline__ int at(int r, int d) { return r * DK + 8 * ((d >> 3) ^ mix(r)) + (d & 7); }
+  // byte offset in memory of what lane l of load i brings
+  static __device__ __forceinline__ int source(int i, int l) {
+    const int e = i * 512 + l * 8, r = e / DK, piece = (e % DK) / 8;
+    return (r * DK + 8 * (piece ^ mix(r))) * 2;
+  }
+};
+
+// this workgroup's 32 columns of c, and col c as the sum of three bf16 parts
+// (rows 4..7 of each 8 hold their two 16-column halves swapped: the transpose reads of four row
+// groups then use all banks)
+template <bool OUT>
+struct alignas(16) LinValues {
+  __bf16 u[3][LC][LDC];
+  __bf16 c[OUT ? LC : 1][LDC];
+  static __device__ __forceinline__ int at(int row, int col) { return row * LDC + (col ^ (4 * (row & 4))); }
 };
 
 struct alignas(16) LinGates {
-  float hi[LC], lo[LC];  // G in units of log 2, as a sum of two floats
-  float row[LC];         // factor of a_i X
-  float col[LC];         // factor of b_j c_j^T
-  float end;             // e^{G_C}
+  float hi[LC], lo[LC];         // G in units of log 2, as a sum of two floats
+  float row[LC];                // factor of a_i X
+  float col[LC];                // factor of b_j c_j^T
+  float from[LNT - 1][LC];      // w of j to the boundary of a tile,
+  float to[LC];                 // and from the row's boundary to the row, with the scale
+  float end;                    // e^{G_C}
 };
 
 // one segment: tokens [tok0 + 64 c0, ...) of a sequence of len tokens starting at tok0
@@ -183,13 +206,28 @@ __device__ __forceinline__ int first_segment(const int32_t* off, int64_t T, int 
   return base;
 }
 
+template <int CTRL>
+__device__ __forceinline__ double dpp_d(double x) {
+  const u32x2 w = __builtin_bit_cast(u32x2, x);
+  const unsigned lo = w[0], hi = w[1];
+  return __builtin_bit_cast(double, u32x2{dpp_u<CTRL>(lo), dpp_u<CTRL>(hi)});
+}
+__device__ __forceinline__ double readlane_d(double x, int lane) {
+  const u32x2 w = __builtin_bit_cast(u32x2, x);
+  const int lo = (int)w[0], hi = (int)w[1];
+  return __builtin_bit_cast(double, u32x2{(unsigned)__builtin_amdgcn_readlane(lo, lane),
+                                          (unsigned)__builtin_amdgcn_readlane(hi, lane)});
+}
+// inclusive prefix sum over the 64 lanes: shifts within each row of 16 (lanes that would read
+// across its start add 0), then the totals of the rows before
 __device__ __forceinline__ double wave_scan_f64(double v) {
-#pragma unroll
-  for (int d = 1; d < WAVE; d <<= 1) {
-    const double o = __shfl_up(v, d);
-    if (lane_id() >= d) v += o;
-  }
-  return v;
+  v += dpp_d<0x111>(v);
+  v += dpp_d<0x112>(v);
+  v += dpp_d<0x114>(v);
+  v += dpp_d<0x118>(v);
+  const double t0 = readlane_d(v, 15), t1 = readlane_d(v, 31), t2 = readlane_d(v, 47);
+  const int row = lane_id() >> 4;
+  return v + ((row >= 1 ? t0 : 0.0) + (row >= 2 ? t1 : 0.0) + (row >= 3 ? t2 : 0.0));
 }
 
 // log-decays below 2^-512 are e^g = 0 in every product: clamped, so that -inf (a state that is
@@ -201,16 +239,84 @@ __device__ __forceinline__ float exp2_f32(float x) { return __builtin_amdgcn_exp
 __device__ __forceinline__ f32x4 lo4(const bf16x8& v) { return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]}; }
 __device__ __forceinline__ f32x4 hi4(const bf16x8& v) { return f32x4{(float)v[4], (float)v[5], (float)v[6], (float)v[7]}; }
 
-// x as the sum of two (three) bf16 operands
-__device__ __forceinline__ void split2(const f32x4& a, const f32x4& b, bf16x8 (&s)[2]) {
-  s[0] = pack8(a, b);
-  s[1] = pack8(a - lo4(s[0]), b - hi4(s[0]));
+// two tiles as the sum of N bf16 operands
+template <int N>
+__device__ __forceinline__ void split(f32x4 a, f32x4 b, bf16x8 (&s)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    s[k] = pack8(a, b);
+    if (k + 1 < N) {
+      a = a - lo4(s[k]);
+      b = b - hi4(s[k]);
+    }
+  }
 }
-__device__ __forceinline__ void split3(const f32x4& a, const f32x4& b, bf16x8 (&s)[3]) {
-  s[0] = pack8(a, b);
-  const f32x4 ra = a - lo4(s[0]), rb = b - hi4(s[0]);
-  s[1] = pack8(ra, rb);
-  s[2] = pack8(ra - lo4(s[1]), rb - hi4(s[1]));
+
+// x as the sum of three bf16 values, exactly: each part is the upper half of what is left (no
+// rounding, so 8 + 8 + 8 bits hold all 24), and one byte permute packs the parts of two values
+__device__ __forceinline__ void split3_exact(const float (&x)[8], bf16x8 (&s)[3]) {
+  uint32_t w[3][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = x[2 * i], b = x[2 * i + 1];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const uint32_t ua = __builtin_bit_cast(uint32_t, a), ub = __builtin_bit_cast(uint32_t, b);
+      w[k][i] = __builtin_amdgcn_perm(ub, ua, 0x07060302);
+      a -= __builtin_bit_cast(float, ua & 0xffff0000u);
+      b -= __builtin_bit_cast(float, ub & 0xffff0000u);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) s[k] = __builtin_bit_cast(bf16x8, u32x4{w[k][0], w[k][1], w[k][2], w[k][3]});
+}
+
+// A run of rows as a buffer: loads past its end give 0 and stores there do nothing, so the
+// last, shorter chunk of a sequence needs no code of its own.  base and bytes are uniform.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const void* base, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00020000);
+}
+__device__ __forceinline__ bf16x8 load16(__amdgpu_buffer_rsrc_t r, int off) {
+  return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+__device__ __forceinline__ bf16x4 load8b(__amdgpu_buffer_rsrc_t r, int off) {
+  return __builtin_bit_cast(bf16x4, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+}
+__device__ __forceinline__ float load4(__amdgpu_buffer_rsrc_t r, int off) {
+  const unsigned x = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+  return __builtin_bit_cast(float, x);
+}
+__device__ __forceinline__ void store16b(__amdgpu_buffer_rsrc_t r, int off, const u32x4& x) {
+  __builtin_amdgcn_raw_buffer_store_b128(x, r, off, 0, 0);
+}
+__device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t r, int off, float x) {
+  __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, x), r, off, 0, 0);
+}
+// 16 bytes a lane straight to LDS, at p + 16 bytes x lane (p uniform)
+__device__ __forceinline__ void load16_lds(__amdgpu_buffer_rsrc_t r, __bf16* p, int off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)p, 16, off, 0, 0, 0);
+}
+// until at most N of this wave's vector memory operations are in flight
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// two adjacent 16-column tiles of a row as bf16, 16 contiguous bytes per lane: group g then
+// holds columns 16(g % 2) + 8(g / 2) .. + 7
+__device__ __forceinline__ u32x4 pair_bf16(const f32x4& a0, const f32x4& a1) {
+  const bf16x4 h0 = pack4(a0), h1 = pack4(a1);
+  const u32x2 w0 = __builtin_bit_cast(u32x2, h0), w1 = __builtin_bit_cast(u32x2, h1);
+  u32x4 v;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const unsigned x0 = w0[k], x1 = w1[k];  // vector elements to scalars before any bit cast
+    const auto sw = __builtin_amdgcn_permlane16_swap(x0, x1, false, false);
+    const unsigned y0 = sw[0], y1 = sw[1];
+    v[k] = y0;
+    v[2 + k] = y1;
+  }
+  return v;
 }
 
 // d of the state tile's row 4g + r: two tiles 2p, 2p + 1 of a lane are then the natural-order
@@ -225,16 +331,15 @@ __device__ __forceinline__ void lds_handover() {
 
 }  // namespace
 
-template <int DK, bool REV, bool OUT>
-__global__ __launch_bounds__(LWAVES * WAVE, 1) void lin_scan_kernel(ScanArgs A) {
-  __shared__ LinIn<DK> in[3];
+// roles of the waves (wave w runs on SIMD w % 4)
+constexpr int scan_waves(bool out) { return out ? 9 : 7; }
+
+template <int DK, bool REV, bool OUT, int PARTS, bool DOTS, class TO>
+__global__ __launch_bounds__(scan_waves(OUT) * WAVE, 1) void lin_scan_kernel(ScanArgs A) {
+  __shared__ LinRows<DK> rows_a[OUT ? 3 : 1], rows_b[3];
+  __shared__ LinValues<OUT> vals[2];
   __shared__ LinGates gates[3];
-  __shared__ f32x4 part[2][2][2][LNT][WAVE];  // [chunk parity][kh][h][row tile]: a X over half the contraction
-  constexpr int NP = DK / 32;   // 32-wide steps of the contraction
-  constexpr int NH = NP / 2;    // of one state wave
-  constexpr int NA = DK / 32;   // 16-row state tiles of one state wave
-  constexpr int SEG = DK / 8;   // 16-byte pieces of a row of b
-  constexpr int NB = LC * SEG / (LWAVES * WAVE);
+  __shared__ f32x4 part[OUT ? 2 : 1][2][LNT][WAVE];  // [chunk parity][column half][row tile]: a X
 
   // workgroup -> (segment, head, slice): the slices of a head, and the heads that share rows,
   // are consecutive indices within one XCD (workgroups are dealt round-robin over the 8 XCDs)
@@ -250,289 +355,441 @@ __global__ __launch_bounds__(LWAVES * WAVE, 1) void lin_scan_kernel(ScanArgs A) 
 
   const int wave = uniform(threadIdx.x / WAVE);
   const int l = lane_id(), g = l >> 4, c = l & 15;
-  const int n = sp.nc, len = sp.len;
+  const int n = sp.nc;
   // first row of the sequence in each tensor ([B][heads][T][.], or [heads][T][.] packed)
   const int64_t batch = A.offsets ? 0 : sp.seq;
   auto row_of = [&](int group) {
     const int heads = A.H / group;
     return (batch * heads + head / group) * A.T + sp.tok0;
   };
-  const __bf16* ap = A.a + row_of(A.group_a) * DK;
-  const __bf16* bp = A.b + row_of(A.group_b) * DK;
-  const int64_t crow = row_of(A.group_c);
-  const __bf16* cp = A.c + crow * A.dc + slice * LDC;
-  const int64_t orow = row_of(1);
-  auto chunk_of = [&](int j) { return REV ? sp.c0 + n - 1 - j : sp.c0 + j; };
-
-  // ---- staging: every thread loads NB pieces of b, the first 256 one piece of c --------
-  struct Staged {
-    bf16x8 b[NB];
-    bf16x8 c;
-    float g;
-  } st;
-  const int tid = threadIdx.x;
-  const bool has_c = wave < 4;
-  constexpr int GATE_TILE = REV ? LNT - 1 : 0;  // the output wave with the fewest products
-  const bool has_g = wave == 4 + GATE_TILE;
-  auto load = [&](int j) {
-    const int t0 = LC * chunk_of(min(j, n - 1));
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int e = i * LWAVES * WAVE + tid;
-      const int t = min(t0 + e / SEG, len - 1);
-      st.b[i] = *reinterpret_cast<const bf16x8*>(bp + (int64_t)t * DK + 8 * (e % SEG));
-    }
-    if (has_c) {
-      const int t = min(t0 + (tid >> 2), len - 1);
-      st.c = *reinterpret_cast<const bf16x8*>(cp + (int64_t)t * A.dc + 8 * (tid & 3));
-    }
-    if (has_g) st.g = A.g_per_head ? A.g[head] : A.g[orow + min(t0 + l, len - 1)];
+  // chunk j of the scan: its first token, clamped to the segment, and the rows it has
+  auto token_of = [&](int j) {
+    j = min(j, n - 1);
+    return LC * (REV ? sp.c0 + n - 1 - j : sp.c0 + j);
   };
-  double decay = 0.0;  // sum of G_C over the segment (gate wave, without OUT)
-  // rows past the sequence's end become zero rows with no decay
-  auto store = [&](int j, LinIn<DK>& S, LinGates& GT) {
-    const int t0 = LC * chunk_of(j);
-    const bf16x8 z = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int e = i * LWAVES * WAVE + tid;
-      *reinterpret_cast<bf16x8*>(&S.b[e / SEG][8 * (e % SEG)]) = t0 + e / SEG < len ? st.b[i] : z;
-    }
-    if (has_c) *reinterpret_cast<bf16x8*>(&S.c[tid >> 2][8 * (tid & 3)]) = t0 + (tid >> 2) < len ? st.c : z;
-    if (has_g) {
-      const double gl = t0 + l < len ? clamp_log2((double)st.g * LOG2E) : 0.0;
-      const double G = wave_scan_f64(gl), GC = __shfl(G, WAVE - 1);
-      const float hi = (float)G;
-      GT.hi[l] = hi;
-      GT.lo[l] = (float)(G - (double)hi);
-      const float eG = exp2_f32((float)G), eR = exp2_f32((float)(GC - G));
-      GT.row[l] = (REV ? eR : eG) * A.s_inter;
-      GT.col[l] = (REV ? eG : eR) * A.s_state;
-      if (l == 0) GT.end = exp2_f32((float)GC);
-      decay += GC;
-    }
+  auto chunk_rows = [&](const void* base, int64_t row0, int j, int row_bytes) {
+    const int t0 = token_of(j);
+    return row_buffer(reinterpret_cast<const char*>(base) + (row0 + t0) * row_bytes, min(LC, sp.len - t0) * row_bytes);
   };
 
   const int64_t head_state = (int64_t)DK * A.dc;
-  const float* from = nullptr;  // the state this segment starts from (NULL: zeros)
-  if (OUT) {
-    if (REV ? sp.last : sp.first)
-      from = A.init ? A.init + ((int64_t)sp.seq * A.H + head) * head_state : nullptr;
-    else
-      from = A.slot + ((int64_t)(REV ? min(seg + 1, A.n_seg - 1) : seg - 1) * A.H + head) * head_state;
-  }
-  float* to = nullptr;
-  if (!OUT)
-    to = A.slot + ((int64_t)seg * A.H + head) * head_state;
-  else if ((REV ? sp.first : sp.last) && A.fin)
-    to = A.fin + ((int64_t)sp.seq * A.H + head) * head_state;
+  const int64_t brow = row_of(A.group_b), crow = row_of(A.group_c), orow = row_of(1);
 
-  if (n > 0) {
-    load(0);
-    store(0, in[0], gates[0]);
-    load(1);
-    lds_handover();
-  }
+  constexpr int W_SPLIT = OUT ? 4 : 2, W_GATES = W_SPLIT + 2, W_ROWS = W_SPLIT + 3, W_AHEAD = W_SPLIT + 4;
 
-  if (wave < 4) {
-    // ---- state waves -----------------------------------------------------------------
-    const int h = wave & 1, kh = wave >> 1;
-    const int d0 = kh * (DK / 2);
+  if (wave < 2) {
+    // ---- state waves: 16 columns of X each ---------------------------------------------
+    constexpr int NA = DK / 16;  // 16-row state tiles
+    constexpr int NP = DK / 32;  // 32-wide steps of the contraction
+    const int h = wave;
     const int64_t col = slice * LDC + 16 * h + c;
+    const float* from = nullptr;  // the state this segment starts from (NULL: zeros)
+    float* to = nullptr;
+    if (!OUT) {
+      to = A.slot + ((int64_t)seg * A.H + head) * head_state;
+    } else {
+      if (!(REV ? sp.last : sp.first))
+        from = A.slot + ((int64_t)(REV ? min(seg + 1, A.n_seg - 1) : seg - 1) * A.H + head) * head_state;
+      else if (A.init)
+        from = A.init + ((int64_t)sp.seq * A.H + head) * head_state;
+      if ((REV ? sp.first : sp.last) && A.fin) to = A.fin + ((int64_t)sp.seq * A.H + head) * head_state;
+    }
     f32x4 X[NA];
 #pragma unroll
     for (int t = 0; t < NA; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        X[t][r] = from ? from[(d0 + state_dim(t, g, r)) * A.st_row + col * A.st_col] : 0.f;
-    bf16x8 af[LNT][NH];
-    auto load_a = [&](int j) {
-      const int t0 = LC * chunk_of(min(j, n - 1));
+      for (int r = 0; r < 4; ++r) X[t][r] = from ? from[state_dim(t, g, r) * A.st_row + col * A.st_col] : 0.f;
+    if (n > 0) {
+      // rows of a as operands: lane (g, c) reads row 16I + c, 16 bytes at 32p + 8g
+      int a_at[NP];
 #pragma unroll
-      for (int I = 0; I < LNT; ++I) {
-        const int t = min(t0 + 16 * I + c, len - 1);
+      for (int p = 0; p < NP; ++p) a_at[p] = LinRows<DK>::at(c, 32 * p + 8 * g);
+      // transposed rows of b: lane addresses of state tiles (t, t + 1) for even t
+      const int bt_row = 4 * g + (c >> 2);
+      int bt_at[NA / 2];
 #pragma unroll
-        for (int p = 0; p < NH; ++p)
-          af[I][p] = *reinterpret_cast<const bf16x8*>(ap + (int64_t)t * DK + d0 + 32 * p + 8 * g);
-      }
-    };
-    if (OUT && n > 0) load_a(0);
-    for (int it = 0; it < n; ++it) {
-      if (it + 1 < n) store(it + 1, in[(it + 1) % 3], gates[(it + 1) % 3]);
-      load(it + 2);
-      const LinIn<DK>& S = in[it % 3];
-      const LinGates& GT = gates[it % 3];
-      if constexpr (OUT) {
-        f32x4 x[LNT];
-#pragma unroll
-        for (int I = 0; I < LNT; ++I) x[I] = zero4();
-#pragma unroll
-        for (int p = 0; p < NH; ++p) {
-          bf16x8 s[2];
-          split2(X[2 * p], X[2 * p + 1], s);
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int I = 0; I < LNT; ++I) x[I] = mma_bf16(s[k], af[I][p], x[I]);
-        }
-        load_a(it + 1);
-#pragma unroll
-        for (int I = 0; I < LNT; ++I) part[it & 1][kh][h][I][l] = x[I];
-      }
-      const float end = GT.end;
-#pragma unroll
-      for (int t = 0; t < NA; ++t) X[t] = X[t] * end;
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const bf16x4 c0 = lds_read_tr4(&S.c[32 * p + 4 * g + (c >> 2)][16 * h + 4 * (c & 3)]);
-        const bf16x4 c1 = lds_read_tr4(&S.c[32 * p + 16 + 4 * g + (c >> 2)][16 * h + 4 * (c & 3)]);
-        const f32x4 w0 = *reinterpret_cast<const f32x4*>(&GT.col[32 * p + 4 * g]);
-        const f32x4 w1 = *reinterpret_cast<const f32x4*>(&GT.col[32 * p + 16 + 4 * g]);
-        bf16x8 u[3];
-        split3(unpack4(c0) * w0, unpack4(c1) * w1, u);
-        bf16x8 bt[NA];
-#pragma unroll
-        for (int t = 0; t < NA; ++t) {
-          const int d = d0 + state_dim(t, c & 3, 0);
-          bt[t] = join8(lds_read_tr4(&S.b[32 * p + 4 * g + (c >> 2)][d]),
-                        lds_read_tr4(&S.b[32 * p + 16 + 4 * g + (c >> 2)][d]));
-        }
-#pragma unroll
-        for (int k = 2; k >= 0; --k)
-#pragma unroll
-          for (int t = 0; t < NA; ++t) X[t] = mma_bf16(bt[t], u[k], X[t]);
-      }
+      for (int t = 0; t < NA / 2; ++t) bt_at[t] = LinRows<DK>::at(bt_row, 32 * t + 8 * (c & 3));
+      const int ct_at = LinValues<OUT>::at(4 * g + (c >> 2), 16 * h + 4 * (c & 3));
       lds_handover();
+      lds_handover();
+      int slot3 = 0;
+      for (int it = 0; it < n; ++it) {
+        const __bf16* bs = rows_b[slot3].v;
+        const LinGates& GT = gates[slot3];
+        const LinValues<OUT>& U = vals[it & 1];
+        if constexpr (OUT) {
+          const __bf16* as = rows_a[slot3].v;
+          f32x4 x[LNT];
+#pragma unroll
+          for (int I = 0; I < LNT; ++I) x[I] = zero4();
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            bf16x8 s[PARTS];
+            split<PARTS>(X[2 * p], X[2 * p + 1], s);
+#pragma unroll
+            for (int I = 0; I < LNT; ++I) {
+              const bf16x8 af = *reinterpret_cast<const bf16x8*>(as + a_at[p] + 16 * I * DK);
+#pragma unroll
+              for (int k = PARTS - 1; k >= 0; --k) x[I] = mma_bf16(s[k], af, x[I]);
+            }
+          }
+#pragma unroll
+          for (int I = 0; I < LNT; ++I) part[it & 1][h][I][l] = x[I];
+        }
+        const float end = GT.end;
+#pragma unroll
+        for (int t = 0; t < NA; ++t) X[t] = X[t] * end;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          bf16x8 u[3];
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            const __bf16* q = &U.u[k][0][0] + ct_at + 32 * p * LDC;
+            u[k] = join8(lds_read_tr4(q), lds_read_tr4(q + 16 * LDC));
+          }
+#pragma unroll
+          for (int t = 0; t < NA; ++t) {
+            const __bf16* q = bs + bt_at[t / 2] + 32 * p * DK + 4 * (t & 1);
+            const bf16x8 bt = join8(lds_read_tr4(q), lds_read_tr4(q + 16 * DK));
+#pragma unroll
+            for (int k = 2; k >= 0; --k) X[t] = mma_bf16(bt, u[k], X[t]);
+          }
+        }
+        slot3 = slot3 == 2 ? 0 : slot3 + 1;
+        lds_handover();
+      }
+      if (OUT) lds_handover();
     }
-    if (OUT && n > 0) lds_handover();
     if (to) {
 #pragma unroll
       for (int t = 0; t < NA; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) to[(d0 + state_dim(t, g, r)) * A.st_row + col * A.st_col] = X[t][r];
+        for (int r = 0; r < 4; ++r) to[state_dim(t, g, r) * A.st_row + col * A.st_col] = X[t][r];
     }
     return;
   }
-
-  // ---- output waves: row tile I of the chunk before the state waves' --------------------
-  if constexpr (!OUT) {
-    for (int it = 0; it < n; ++it) {
-      if (it + 1 < n) store(it + 1, in[(it + 1) % 3], gates[(it + 1) % 3]);
-      load(it + 2);
-      lds_handover();
-    }
-    if (has_g && slice == 0 && l == 0) A.slot_decay[(int64_t)seg * A.H + head] = exp2_f32((float)decay);
-    return;
-  } else {
+  const int iters = OUT ? n + 1 : n;  // barriers of the loop
+  if (wave >= W_SPLIT && wave < W_GATES) {
+    // ---- c, and col c in three parts, one chunk ahead: 32 rows a wave, 8 columns a lane ---
     if (n <= 0) return;
-    auto rows = [&](auto tile) {
-      constexpr int I = tile.value;
-      constexpr int J0 = REV ? I : 0, J1 = REV ? LNT - 1 : I;  // tiles of b with a non-zero weight
-      bf16x8 af[NP];
-      auto load_a = [&](int j) {
-        const int t = min(LC * chunk_of(min(j, n - 1)) + 16 * I + c, len - 1);
+    const int row = 32 * (wave - W_SPLIT) + (l >> 2), c0 = 8 * (l & 3);
+    const int coff = (row * A.dc + slice * LDC + c0) * 2;
+    bf16x8 x[2];
+    auto load = [&](int j) {
+      const auto r = chunk_rows(A.c, crow, j, 2 * A.dc);
+      x[0] = load16(r, coff);
+      x[1] = load16(r, coff + 32 * A.dc);
+    };
+    auto store = [&](LinValues<OUT>& V, const LinGates& GT) {
 #pragma unroll
-        for (int p = 0; p < NP; ++p)
-          af[p] = *reinterpret_cast<const bf16x8*>(ap + (int64_t)t * DK + 32 * p + 8 * g);
-      };
-      load_a(0);
-      for (int it = 0; it <= n; ++it) {
-        if (it + 1 < n) store(it + 1, in[(it + 1) % 3], gates[(it + 1) % 3]);
-        if (it < n) load(it + 2);
-        if (it > 0) {
-          const int j = it - 1;
-          const LinIn<DK>& S = in[j % 3];
-          const LinGates& GT = gates[j % 3];
-          // P_ij = w_ij (a_i . b_j): lane (g, c) holds row i = 16I + c, columns 16J + 4g + r
-          f32x4 P[LNT];
+      for (int i = 0; i < 2; ++i) {
+        const float w = GT.col[row + 16 * i];
+        float y[8];
 #pragma unroll
-          for (int J = 0; J < LNT; ++J) {
-            P[J] = zero4();
-            if (J < J0 || J > J1) continue;
+        for (int e = 0; e < 8; ++e) y[e] = (float)x[i][e] * w;
+        bf16x8 u[3];
+        split3_exact(y, u);
+        const int at = LinValues<OUT>::at(row + 16 * i, c0);
+        if (OUT) *reinterpret_cast<bf16x8*>(&V.c[0][0] + at) = x[i];
 #pragma unroll
-            for (int p = 0; p < NP; ++p)
-              P[J] = mma_bf16(*reinterpret_cast<const bf16x8*>(&S.b[16 * J + c][32 * p + 8 * g]), af[p], P[J]);
-          }
-          load_a(it);
-          const float hi = GT.hi[16 * I + c], lo = GT.lo[16 * I + c];
-#pragma unroll
-          for (int J = J0; J <= J1; ++J) {
-            const f32x4 hj = *reinterpret_cast<const f32x4*>(&GT.hi[16 * J + 4 * g]);
-            const f32x4 lj = *reinterpret_cast<const f32x4*>(&GT.lo[16 * J + 4 * g]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float e = REV ? (hj[r] - hi) + (lj[r] - lo) : (hi - hj[r]) + (lo - lj[r]);
-              const float w = exp2_f32(e) * A.s_intra;
-              const bool keep = J != I || (REV ? 4 * g + r >= c : 4 * g + r <= c);
-              P[J][r] = keep ? P[J][r] * w : 0.f;
-            }
-          }
-          f32x4 o[2] = {zero4(), zero4()};
-#pragma unroll
-          for (int p = J0 / 2; p <= J1 / 2; ++p) {
-            bf16x8 s[2];
-            split2(P[2 * p], P[2 * p + 1], s);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const bf16x8 cf = join8(lds_read_tr4(&S.c[32 * p + 4 * g + (c >> 2)][16 * h + 4 * (c & 3)]),
-                                      lds_read_tr4(&S.c[32 * p + 16 + 4 * g + (c >> 2)][16 * h + 4 * (c & 3)]));
-              o[h] = mma_bf16(cf, s[1], o[h]);
-              o[h] = mma_bf16(cf, s[0], o[h]);
-            }
-          }
-          const float rw = GT.row[16 * I + c];
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            o[h] = o[h] + (part[j & 1][0][h][I][l] + part[j & 1][1][h][I][l]) * rw;
-          const int t = LC * chunk_of(j) + 16 * I + c;
-          const int64_t row = orow + t;
-          if (A.dotw) {
-            const __bf16* wp = A.dotw + (crow + min(t, len - 1)) * A.dc + slice * LDC + 4 * g;
-            float s = 0.f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const f32x4 x = unpack4(*reinterpret_cast<const bf16x4*>(wp + 16 * h));
-#pragma unroll
-              for (int r = 0; r < 4; ++r) s = fmaf(x[r], o[h][r], s);
-            }
-            float s0, s1;
-            self_swap_f<16>(s, s0, s1);
-            s = s0 + s1;
-            self_swap_f<32>(s, s0, s1);
-            s = s0 + s1;
-            if (g == 0 && t < len) A.dots[(int64_t)slice * A.heads_T + row] = s;
-          }
-          if (A.out_bf16) {
-            // all lanes take part in the exchange inside; rows past the end are not stored
-            const bf16x4 h0 = pack4(o[0]), h1 = pack4(o[1]);
-            const u32x2 w0 = __builtin_bit_cast(u32x2, h0), w1 = __builtin_bit_cast(u32x2, h1);
-            u32x4 v;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const unsigned x0 = w0[k], x1 = w1[k];
-              const auto sw = __builtin_amdgcn_permlane16_swap(x0, x1, false, false);
-              const unsigned y0 = sw[0], y1 = sw[1];
-              v[k] = y0;
-              v[2 + k] = y1;
-            }
-            if (t < len)
-              *reinterpret_cast<u32x4*>(reinterpret_cast<__bf16*>(A.out) + row * A.dc + slice * LDC +
-                                        16 * (g & 1) + 8 * (g >> 1)) = v;
-          } else if (t < len) {
-            float* op = reinterpret_cast<float*>(A.out) + row * A.dc + slice * LDC + 4 * g;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) *reinterpret_cast<f32x4*>(op + 16 * h) = o[h];
-          }
-        }
-        lds_handover();
+        for (int k = 0; k < 3; ++k) *reinterpret_cast<bf16x8*>(&V.u[k][0][0] + at) = u[k];
       }
     };
-    switch (wave) {
-      case 4: rows(std::integral_constant<int, 0>{}); break;
-      case 5: rows(std::integral_constant<int, 1>{}); break;
-      case 6: rows(std::integral_constant<int, 2>{}); break;
-      default: rows(std::integral_constant<int, 3>{}); break;
+    load(0);
+    lds_handover();
+    store(vals[0], gates[0]);
+    load(1);
+    lds_handover();
+    int slot3 = 1;
+    for (int it = 0; it < iters; ++it) {
+      if (it + 1 < n) {
+        store(vals[(it + 1) & 1], gates[slot3]);
+        load(it + 2);
+      }
+      slot3 = slot3 == 2 ? 0 : slot3 + 1;
+      lds_handover();
     }
+    return;
+  }
+  if (wave == W_GATES) {
+    // ---- decay factors, two chunks ahead (lane = token) --------------------------------
+    double decay = 0.0;  // sum of G_C over the segment
+    const float g_head = A.g_per_head ? A.g[head] : 0.f;
+    auto load = [&](int j) {
+      const int t0 = token_of(j);
+      if (A.g_per_head) return t0 + l < sp.len ? g_head : 0.f;
+      return load4(row_buffer(A.g + orow + t0, min(LC, sp.len - t0) * 4), 4 * l);  // 0 past the end
+    };
+    auto store = [&](float gl, LinGates& GT) {
+      const double G = wave_scan_f64(clamp_log2((double)gl * LOG2E)), GC = readlane_d(G, WAVE - 1);
+      const float hi = (float)G;
+      const float eG = exp2_f32(hi), eR = exp2_f32((float)(GC - G));
+      GT.col[l] = (REV ? eG : eR) * A.s_state;
+      if (l == 0) GT.end = exp2_f32((float)GC);
+      if constexpr (OUT) {
+        GT.hi[l] = hi;
+        GT.lo[l] = (float)(G - (double)hi);
+        GT.row[l] = (REV ? eR : eG) * A.s_inter;
+        // between tiles w factors at the boundary next to the row's tile: forwards G at the end
+        // of tile I - 1, backwards at the end of tile I; both exponents are <= 0 there
+#pragma unroll
+        for (int B = 0; B < LNT - 1; ++B) {
+          const double Gb = readlane_d(G, 16 * B + 15);
+          const float e = exp2_f32((float)(REV ? G - Gb : Gb - G));
+          if (REV ? l > 16 * B + 15 : l <= 16 * B + 15) GT.from[B][l] = e;
+          if ((l >> 4) == (REV ? B : B + 1)) GT.to[l] = exp2_f32((float)(REV ? Gb - G : G - Gb)) * A.s_intra;
+        }
+      }
+      decay += GC;
+    };
+    if (n > 0) {
+      store(load(0), gates[0]);
+      if (n > 1) store(load(1), gates[1]);
+      float gl = load(2);
+      lds_handover();
+      lds_handover();
+      int slot3 = 2;
+      for (int it = 0; it < iters; ++it) {
+        if (it + 2 < n) {
+          store(gl, gates[slot3]);
+          gl = load(it + 3);
+        }
+        slot3 = slot3 == 2 ? 0 : slot3 + 1;
+        lds_handover();
+      }
+    }
+    if (!OUT && slice == 0 && l == 0) A.slot_decay[(int64_t)seg * A.H + head] = exp2_f32((float)decay);
+    return;
+  }
+  if (wave == W_ROWS) {
+    // ---- rows of a and b straight into LDS, two chunks ahead ------------------------------
+    if (n <= 0) return;
+    constexpr int NB = LC * DK * 2 / 1024;  // 1 KB an instruction
+    const int64_t arow = row_of(A.group_a);
+    int off[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) off[i] = LinRows<DK>::source(i, l);
+    auto load = [&](int j, int slot) {
+      const auto rb = chunk_rows(A.b, brow, j, 2 * DK);
+#pragma unroll
+      for (int i = 0; i < NB; ++i) load16_lds(rb, rows_b[slot].v + 512 * i, off[i]);
+      if constexpr (OUT) {
+        const auto ra = chunk_rows(A.a, arow, j, 2 * DK);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) load16_lds(ra, rows_a[slot].v + 512 * i, off[i]);
+      }
+    };
+    load(0, 0);
+    load(1, 1);
+    lds_handover();
+    wait_loads<OUT ? 2 * NB : NB>();
+    lds_handover();
+    int slot3 = 2;
+    for (int it = 0; it < iters; ++it) {
+      // chunk it + 1 has to be there after this barrier, chunk it + 2 stays in flight
+      if (it + 2 < n) {
+        load(it + 2, slot3);
+        wait_loads<OUT ? 2 * NB : NB>();
+      } else {
+        wait_loads<0>();
+      }
+      slot3 = slot3 == 2 ? 0 : slot3 + 1;
+      lds_handover();
+    }
+    return;
+  }
+  if (wave == W_AHEAD) {
+    // ---- memory to L2, AHEAD chunks ahead -------------------------------------------------
+    // Loads whose values nobody needs: the other waves' loads, one chunk ahead, then find their
+    // lines in L2.  The slices of a head divide the rows of a and b among them: one 16-byte
+    // piece of each 128-byte line a lane.
+    if (n <= 0) return;
+    constexpr int LINES = LC * DK * 2 / 128;  // of a chunk of a or b
+    const int64_t arow = row_of(A.group_a);
+    const int share = (LINES + n_slices - 1) / n_slices;
+    const int line = slice * share + l;
+    const int off = l < share && line < LINES ? 128 * line : INT32_MAX;  // past the end: no access
+    const int coff = (l * A.dc + slice * LDC) * 2;
+    unsigned x[4] = {0, 0, 0, 0};
+    auto touch = [&](int j) {
+      asm volatile("" ::"v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]));  // the loads before have arrived
+      x[0] = __builtin_amdgcn_raw_buffer_load_b32(chunk_rows(A.b, brow, j, 2 * DK), off, 0, 0);
+      x[1] = __builtin_amdgcn_raw_buffer_load_b32(chunk_rows(A.c, crow, j, 2 * A.dc), coff, 0, 0);
+      if (!A.g_per_head) {
+        const int t0 = token_of(j);
+        x[2] = __builtin_amdgcn_raw_buffer_load_b32(row_buffer(A.g + orow + t0, min(LC, sp.len - t0) * 4), 4 * l, 0, 0);
+      }
+      if (OUT) x[3] = __builtin_amdgcn_raw_buffer_load_b32(chunk_rows(A.a, arow, j, 2 * DK), off, 0, 0);
+    };
+    for (int j = 2; j < min(AHEAD, n); ++j) touch(j);
+    lds_handover();
+    lds_handover();
+    for (int it = 0; it < iters; ++it) {
+      if (it + AHEAD < n) touch(it + AHEAD);
+      lds_handover();
+    }
+    asm volatile("" ::"v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]));
+    return;
+  }
+  if constexpr (OUT) {
+    // ---- output waves: row tiles 0 and 3, or 1 and 2 (equal numbers of products) ----------
+    if (n <= 0) return;
+    auto out_rows = [&](auto tile0, auto tile1) {
+      constexpr int TI[2] = {tile0.value, tile1.value};
+      constexpr int NP = DK / 32;
+      constexpr bool OBF = sizeof(TO) == 2;
+      // tiles J of b that have a weight for row tile I
+      constexpr auto used = [](int I, int J) { return REV ? J >= I : J <= I; };
+      int row_at[NP];  // row c of a tile, 16 bytes at 32p + 8g
+#pragma unroll
+      for (int p = 0; p < NP; ++p) row_at[p] = LinRows<DK>::at(c, 32 * p + 8 * g);
+      const int ct_at[2] = {LinValues<OUT>::at(4 * g + (c >> 2), 4 * (c & 3)),
+                            LinValues<OUT>::at(4 * g + (c >> 2), 16 + 4 * (c & 3))};
+      const int ooff = (c * A.dc + slice * LDC + (OBF ? 16 * (g & 1) + 8 * (g >> 1) : 4 * g)) * (int)sizeof(TO);
+      const int woff = (c * A.dc + slice * LDC + 4 * g) * 2;
+      lds_handover();
+      lds_handover();
+      f32x4 o[2][2];  // [tile][column half]: w (a . b) c of the chunk before
+      float rw[2];
+      bf16x4 wv[2][2];
+      int slot3 = 0;
+      // one iteration: products of chunk it (NEW), outputs of chunk it - 1 (OLD), whose products
+      // with the state are there now.  One block of code, so that the finishing arithmetic runs
+      // beside the new products.
+      auto step = [&](int it, auto old_, auto new_) {
+        constexpr bool OLD = old_.value, NEW = new_.value;
+        f32x4 x[2][2], P[2][LNT];
+        const LinGates& GT = gates[slot3];
+        if constexpr (OLD) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) x[i][h] = part[(it - 1) & 1][h][TI[i]][l];
+        }
+        if constexpr (NEW) {
+          const __bf16* as = rows_a[slot3].v;
+          const __bf16* bs = rows_b[slot3].v;
+          // P_ij = w_ij (a_i . b_j): lane (g, c) holds row i = 16I + c, columns 16J + 4g + r
+          bf16x8 af[2][NP];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+              af[i][p] = *reinterpret_cast<const bf16x8*>(as + row_at[p] + 16 * TI[i] * DK);
+#pragma unroll
+          for (int J = 0; J < LNT; ++J) {
+            P[0][J] = P[1][J] = zero4();
+            if (!used(TI[0], J) && !used(TI[1], J)) continue;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+              const bf16x8 bf = *reinterpret_cast<const bf16x8*>(bs + row_at[p] + 16 * J * DK);
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (used(TI[i], J)) P[i][J] = mma_bf16(bf, af[i][p], P[i][J]);
+            }
+          }
+        }
+        if constexpr (OLD) {
+          const int j = it - 1;
+          const auto r = chunk_rows(A.out, orow, j, (int)sizeof(TO) * A.dc);  // rows past the end are not stored
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) o[i][h][q] = fmaf(x[i][h][q], rw[i], o[i][h][q]);
+            if constexpr (DOTS) {
+              float s = 0.f;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const f32x4 w = unpack4(wv[i][h]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) s = fmaf(w[q], o[i][h][q], s);
+              }
+              float s0, s1;
+              self_swap_f<16>(s, s0, s1);
+              s = s0 + s1;
+              self_swap_f<32>(s, s0, s1);
+              s = s0 + s1;
+              const auto d = chunk_rows(A.dots + slice * A.heads_T, orow, j, 4);
+              if (g == 0) store4(d, 4 * (16 * TI[i] + c), s);
+            }
+            const int at = ooff + 16 * TI[i] * A.dc * (int)sizeof(TO);
+            if constexpr (OBF) {
+              store16b(r, at, pair_bf16(o[i][0], o[i][1]));
+            } else {
+              store16b(r, at, __builtin_bit_cast(u32x4, o[i][0]));
+              store16b(r, at + 64, __builtin_bit_cast(u32x4, o[i][1]));
+            }
+          }
+        }
+        if constexpr (NEW) {
+          if constexpr (DOTS) {
+            const auto r = chunk_rows(A.dotw, crow, it, 2 * A.dc);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) wv[i][h] = load8b(r, woff + 16 * TI[i] * A.dc * 2 + 32 * h);
+          }
+          const __bf16* cs = &vals[it & 1].c[0][0];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int I = TI[i];
+            rw[i] = GT.row[16 * I + c];
+            const float to = GT.to[16 * I + c];
+#pragma unroll
+            for (int J = 0; J < LNT; ++J) {
+              if (!used(I, J)) continue;
+              if (J != I) {
+                const f32x4 f = *reinterpret_cast<const f32x4*>(&GT.from[REV ? I : I - 1][16 * J + 4 * g]);
+                P[i][J] = P[i][J] * (f * to);
+              } else {
+                const float hi = GT.hi[16 * I + c], lo = GT.lo[16 * I + c];
+                const f32x4 hj = *reinterpret_cast<const f32x4*>(&GT.hi[16 * J + 4 * g]);
+                const f32x4 lj = *reinterpret_cast<const f32x4*>(&GT.lo[16 * J + 4 * g]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const float e = REV ? (hj[q] - hi) + (lj[q] - lo) : (hi - hj[q]) + (lo - lj[q]);
+                  const bool keep = REV ? 4 * g + q >= c : 4 * g + q <= c;
+                  P[i][J][q] = keep ? P[i][J][q] * (exp2_f32(e) * A.s_intra) : 0.f;
+                }
+              }
+            }
+            o[i][0] = o[i][1] = zero4();
+          }
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            bf16x8 cf[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const __bf16* q = cs + ct_at[h] + 32 * p * LDC;
+              cf[h] = join8(lds_read_tr4(q), lds_read_tr4(q + 16 * LDC));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (!used(TI[i], 2 * p) && !used(TI[i], 2 * p + 1)) continue;
+              bf16x8 s[PARTS];
+              split<PARTS>(P[i][2 * p], P[i][2 * p + 1], s);
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = PARTS - 1; k >= 0; --k) o[i][h] = mma_bf16(cf[h], s[k], o[i][h]);
+            }
+          }
+        }
+        slot3 = slot3 == 2 ? 0 : slot3 + 1;
+        lds_handover();
+      };
+      using std::bool_constant;
+      step(0, bool_constant<false>{}, bool_constant<true>{});
+      for (int it = 1; it < n; ++it) step(it, bool_constant<true>{}, bool_constant<true>{});
+      step(n, bool_constant<true>{}, bool_constant<false>{});
+    };
+    using std::integral_constant;
+    if (wave == 2)
+      out_rows(integral_constant<int, 0>{}, integral_constant<int, 3>{});
+    else
+      out_rows(integral_constant<int, 1>{}, integral_constant<int, 2>{});
   }
 }
 
@@ -714,14 +971,14 @@ LinPlan make_plan(const LinLaunch& p, bool bwd) {
   return q;
 }
 
-template <bool REV, bool OUT>
+template <bool REV, bool OUT, int PARTS, bool DOTS, class TO>
 int scan(int dk, const ScanArgs& a, hipStream_t s) {
   const int64_t total = (int64_t)a.n_seg * a.H * (a.dc / LDC);
-  const dim3 grid((unsigned)(8 * ((total + 7) / 8))), block(LWAVES * WAVE);
+  const dim3 grid((unsigned)(8 * ((total + 7) / 8))), block(scan_waves(OUT) * WAVE);
   if (dk == 64)
-    hipLaunchKernelGGL((lin_scan_kernel<64, REV, OUT>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((lin_scan_kernel<64, REV, OUT, PARTS, DOTS, TO>), grid, block, 0, s, a);
   else if (dk == 128)
-    hipLaunchKernelGGL((lin_scan_kernel<128, REV, OUT>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((lin_scan_kernel<128, REV, OUT, PARTS, DOTS, TO>), grid, block, 0, s, a);
   else
     return -1;
   return 0;
@@ -782,18 +1039,17 @@ int launch_lin_fwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   a.init = p.S0;
   a.fin = p.S_out;
   a.out = p.O;
-  a.out_bf16 = p.o_bf16;
   a.s_intra = a.s_inter = p.scale;
   a.s_state = 1.f;
   if (q.split) {
     a.slot = reinterpret_cast<float*>(ws + q.slot_s);
     a.slot_decay = reinterpret_cast<float*>(ws + q.decay_s);
     a.skip_end = 1;
-    int rc = scan<false, false>(p.d_k, a, s);
+    int rc = scan<false, false, 1, false, float>(p.d_k, a, s);
     if (rc) return rc;
     join(false, a.slot, a.slot_decay, p.S0, p, q, 1, s);
   }
-  return scan<false, true>(p.d_k, a, s);
+  return p.o_bf16 ? scan<false, true, 1, false, __bf16>(p.d_k, a, s) : scan<false, true, 3, false, float>(p.d_k, a, s);
 }
 
 int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
@@ -820,7 +1076,7 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   f.skip_end = !end;
   int rc = 0;
   if (q.split || end) {
-    rc = scan<false, false>(p.d_k, f, s);
+    rc = scan<false, false, 1, false, float>(p.d_k, f, s);
     if (rc) return rc;
     join(false, f.slot, f.slot_decay, p.S0, p, q, !end, s);
   }
@@ -834,7 +1090,7 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   r.slot_decay = reinterpret_cast<float*>(ws + q.decay_d);
   r.skip_end = 1;
   if (q.split) {
-    rc = scan<true, false>(p.d_k, r, s);
+    rc = scan<true, false, 1, false, float>(p.d_k, r, s);
     if (rc) return rc;
     join(true, r.slot, r.slot_decay, p.dS, p, q, 1, s);
   }
@@ -843,10 +1099,9 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   r.init = p.dS;
   r.fin = p.dS0;
   r.out = p.dV;
-  r.out_bf16 = p.grad_bf16;
   r.s_intra = p.scale;
   r.s_inter = 1.f;
-  rc = scan<true, true>(p.d_k, r, s);
+  rc = p.grad_bf16 ? scan<true, true, 1, false, __bf16>(p.d_k, r, s) : scan<true, true, 3, false, float>(p.d_k, r, s);
   if (rc) return rc;
   // dK and dQ: the transposed states, contraction over d_v
   ScanArgs k = base_args(p, q);
@@ -860,25 +1115,25 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   k.group_c = group;
   k.init = p.dS;
   k.slot = slot_d;
-  k.dotw = p.dg ? bf(p.K) : nullptr;
+  k.dotw = bf(p.K);
   k.dots = reinterpret_cast<float*>(ws + q.dot_k);
   k.out = group > 1 ? (void*)(ws + q.part_k) : p.dK;
-  k.out_bf16 = group > 1 ? 0 : p.grad_bf16;
+  const bool part_bf16 = group == 1 && p.grad_bf16;
   k.s_intra = k.s_state = p.scale;
   k.s_inter = 1.f;
-  rc = scan<true, true>(p.d_v, k, s);
+  rc = part_bf16 ? scan<true, true, 3, true, __bf16>(p.d_v, k, s) : scan<true, true, 3, true, float>(p.d_v, k, s);
   if (rc) return rc;
   k.a = bf(p.dO);
   k.b = bf(p.V);
   k.c = bf(p.K);
   k.init = p.S0;
   k.slot = slot_s;
-  k.dotw = p.dg ? bf(p.Q) : nullptr;
+  k.dotw = bf(p.Q);
   k.dots = reinterpret_cast<float*>(ws + q.dot_q);
   k.out = group > 1 ? (void*)(ws + q.part_q) : p.dQ;
   k.s_intra = k.s_inter = p.scale;
   k.s_state = 1.f;
-  rc = scan<false, true>(p.d_v, k, s);
+  rc = part_bf16 ? scan<false, true, 3, true, __bf16>(p.d_v, k, s) : scan<false, true, 3, true, float>(p.d_v, k, s);
   if (rc) return rc;
   if (group > 1 && p.T > 0) {
     const int64_t n = (int64_t)(p.offsets ? 1 : p.n_seq) * p.H_qk * p.T * p.d_k;
