@@ -47,8 +47,6 @@ namespace {
 
 constexpr int LC = 64;     // tokens of a chunk
 constexpr int LNT = 4;     // 16-row tiles of a chunk
-constexpr int LDC = 32;    // columns of c per workgroup
-constexpr int AHEAD = 5;   // chunks from memory to L2 ahead of their use
 constexpr double LOG2E = 1.4426950408889634;
 
 struct ScanArgs {
@@ -73,32 +71,22 @@ struct ScanArgs {
   float s_intra, s_inter, s_state;
 };
 
-// 64 rows of b in LDS, without padding (they arrive by direct loads, 1 KB an instruction in
-// lane order).  The 16-byte pieces of row r are permuted by r so that both readers spread over
+// 64 rows of D values in LDS, without padding (they arrive by direct loads, 1 KB an instruction
+// in lane order).  The 16-byte pieces of row r are permuted by r so that the readers spread over
 // the banks: 16 consecutive rows at one piece, and 4 rows x 4 pieces by the transpose read.
-template <int DK>
+template <int D>
 struct alignas(16) LinRows {
-  __bf16 v[LC * DK];
+  __bf16 v[LC * D];
   static __device__ __forceinline__ int mix(int r) {
-    return DK == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+    return D == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : D == 64 ? (((r >> 1) & 1) << 2) | ((r >> 2) & 3) : (r >> 1) & 2;
   }
   // where element d of row r lies (d a multiple of 4: the rest of its piece follows)
-  static __device__ __forceinline__ int at(int r, int d) { return r * DK + 8 * ((d >> 3) ^ mix(r)) + (d & 7); }
-  // byte offset in memory of what lane l of load i brings
-  static __device__ __forceinline__ int source(int i, int l) {
-    const int e = i * 512 + l * 8, r = e / DK, piece = (e % DK) / 8;
-    return (r * DK + 8 * (piece ^ mix(r))) * 2;
+  static __device__ __forceinline__ int at(int r, int d) { return r * D + 8 * ((d >> 3) ^ mix(r)) + (d & 7); }
+  // byte offset in memory of what lane l of load i brings, rows being stride values apart
+  static __device__ __forceinline__ int source(int i, int l, int stride) {
+    const int e = i * 512 + l * 8, r = e / D, piece = (e % D) / 8;
+    return (r * stride + 8 * (piece ^ mix(r))) * 2;
   }
-};
-
-// this workgroup's 32 columns of c, and col c as the sum of three bf16 parts
-// (rows 4..7 of each 8 hold their two 16-column halves swapped: the transpose reads of four row
-// groups then use all banks)
-template <bool OUT>
-struct alignas(16) LinValues {
-  __bf16 u[3][LC][LDC];
-  __bf16 c[OUT ? LC : 1][LDC];
-  static __device__ __forceinline__ int at(int row, int col) { return row * LDC + (col ^ (4 * (row & 4))); }
 };
 
 struct alignas(16) LinGates {
@@ -276,18 +264,15 @@ __device__ __forceinline__ void split3_exact(const float (&x)[8], bf16x8 (&s)[3]
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const void* base, int bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00020000);
 }
-__device__ __forceinline__ bf16x8 load16(__amdgpu_buffer_rsrc_t r, int off) {
-  return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
-}
-__device__ __forceinline__ bf16x4 load8b(__amdgpu_buffer_rsrc_t r, int off) {
-  return __builtin_bit_cast(bf16x4, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
-}
 __device__ __forceinline__ float load4(__amdgpu_buffer_rsrc_t r, int off) {
   const unsigned x = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
   return __builtin_bit_cast(float, x);
 }
 __device__ __forceinline__ void store16b(__amdgpu_buffer_rsrc_t r, int off, const u32x4& x) {
   __builtin_amdgcn_raw_buffer_store_b128(x, r, off, 0, 0);
+}
+__device__ __forceinline__ void store8b(__amdgpu_buffer_rsrc_t r, int off, const bf16x4& x) {
+  __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, x), r, off, 0, 0);
 }
 __device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t r, int off, float x) {
   __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, x), r, off, 0, 0);
@@ -302,23 +287,6 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// two adjacent 16-column tiles of a row as bf16, 16 contiguous bytes per lane: group g then
-// holds columns 16(g % 2) + 8(g / 2) .. + 7
-__device__ __forceinline__ u32x4 pair_bf16(const f32x4& a0, const f32x4& a1) {
-  const bf16x4 h0 = pack4(a0), h1 = pack4(a1);
-  const u32x2 w0 = __builtin_bit_cast(u32x2, h0), w1 = __builtin_bit_cast(u32x2, h1);
-  u32x4 v;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const unsigned x0 = w0[k], x1 = w1[k];  // vector elements to scalars before any bit cast
-    const auto sw = __builtin_amdgcn_permlane16_swap(x0, x1, false, false);
-    const unsigned y0 = sw[0], y1 = sw[1];
-    v[k] = y0;
-    v[2 + k] = y1;
-  }
-  return v;
-}
-
 // d of the state tile's row 4g + r: two tiles 2p, 2p + 1 of a lane are then the natural-order
 // operand (slot t <-> d = 32p + 8g + t)
 __device__ __forceinline__ int state_dim(int a, int g, int r) { return 32 * (a >> 1) + 8 * g + 4 * (a & 1) + r; }
@@ -331,19 +299,23 @@ __device__ __forceinline__ void lds_handover() {
 
 }  // namespace
 
-// roles of the waves (wave w runs on SIMD w % 4)
-constexpr int scan_waves(bool out) { return out ? 9 : 7; }
+// waves of a workgroup of W columns: W / 16 column waves, two that form w (a . b) (with
+// outputs), one for the decay factors, one for the loads
+constexpr int scan_waves(int W, bool out) { return W / 16 + (out ? 4 : 2); }
 
-template <int DK, bool REV, bool OUT, int PARTS, bool DOTS, class TO>
-__global__ __launch_bounds__(scan_waves(OUT) * WAVE, 1) void lin_scan_kernel(ScanArgs A) {
-  __shared__ LinRows<DK> rows_a[OUT ? 3 : 1], rows_b[3];
-  __shared__ LinValues<OUT> vals[2];
-  __shared__ LinGates gates[3];
-  __shared__ f32x4 part[OUT ? 2 : 1][2][LNT][WAVE];  // [chunk parity][column half][row tile]: a X
+template <int DK, int W, bool REV, bool OUT, int PARTS, bool DOTS, class TO>
+__global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, 1) void lin_scan_kernel(ScanArgs A) {
+  __shared__ LinRows<DK> rows_a[OUT ? 2 : 1], rows_b[2];
+  __shared__ LinRows<W> rows_c[2], rows_w[DOTS ? 2 : 1];
+  __shared__ LinGates gates[2];
+  __shared__ bf16x8 weights[OUT ? PARTS : 1][LNT][2][WAVE];  // w (a . b) as operands: [part][row tile][32-wide step]
+  __shared__ float dot_part[DOTS ? W / 16 : 1][LC];
+  constexpr int COLS = W / 16, NP = DK / 32;
+  constexpr int W_GATES = COLS + (OUT ? 2 : 0), W_ROWS = W_GATES + 1;
 
   // workgroup -> (segment, head, slice): the slices of a head, and the heads that share rows,
   // are consecutive indices within one XCD (workgroups are dealt round-robin over the 8 XCDs)
-  const int n_slices = A.dc / LDC;
+  const int n_slices = A.dc / W;
   const int total = A.n_seg * A.H * n_slices;
   const int per = (total + 7) / 8;
   const int idx = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
@@ -371,18 +343,13 @@ __global__ __launch_bounds__(scan_waves(OUT) * WAVE, 1) void lin_scan_kernel(Sca
     const int t0 = token_of(j);
     return row_buffer(reinterpret_cast<const char*>(base) + (row0 + t0) * row_bytes, min(LC, sp.len - t0) * row_bytes);
   };
-
   const int64_t head_state = (int64_t)DK * A.dc;
-  const int64_t brow = row_of(A.group_b), crow = row_of(A.group_c), orow = row_of(1);
+  const int64_t crow = row_of(A.group_c), orow = row_of(1);
 
-  constexpr int W_SPLIT = OUT ? 4 : 2, W_GATES = W_SPLIT + 2, W_ROWS = W_SPLIT + 3, W_AHEAD = W_SPLIT + 4;
-
-  if (wave < 2) {
-    // ---- state waves: 16 columns of X each ---------------------------------------------
+  if (wave < COLS) {
+    // ---- column waves: 16 columns of X, in registers from the segment's start to its end --
     constexpr int NA = DK / 16;  // 16-row state tiles
-    constexpr int NP = DK / 32;  // 32-wide steps of the contraction
-    const int h = wave;
-    const int64_t col = slice * LDC + 16 * h + c;
+    const int64_t col = slice * W + 16 * wave + c;
     const float* from = nullptr;  // the state this segment starts from (NULL: zeros)
     float* to = nullptr;
     if (!OUT) {
@@ -404,24 +371,25 @@ __global__ __launch_bounds__(scan_waves(OUT) * WAVE, 1) void lin_scan_kernel(Sca
       int a_at[NP];
 #pragma unroll
       for (int p = 0; p < NP; ++p) a_at[p] = LinRows<DK>::at(c, 32 * p + 8 * g);
-      // transposed rows of b: lane addresses of state tiles (t, t + 1) for even t
-      const int bt_row = 4 * g + (c >> 2);
+      // transposed rows of b: lane addresses of state tiles (t, t + 1) for even t; of c
+      const int tr_row = 4 * g + (c >> 2);
       int bt_at[NA / 2];
 #pragma unroll
-      for (int t = 0; t < NA / 2; ++t) bt_at[t] = LinRows<DK>::at(bt_row, 32 * t + 8 * (c & 3));
-      const int ct_at = LinValues<OUT>::at(4 * g + (c >> 2), 16 * h + 4 * (c & 3));
+      for (int t = 0; t < NA / 2; ++t) bt_at[t] = LinRows<DK>::at(tr_row, 32 * t + 8 * (c & 3));
+      const int ct_at = LinRows<W>::at(tr_row, 16 * wave + 4 * (c & 3));
+      const int w_at = LinRows<W>::at(c, 16 * wave + 4 * g);
+      const int ooff = (c * A.dc + slice * W + 16 * wave + 4 * g) * (int)sizeof(TO);
       lds_handover();
-      lds_handover();
-      int slot3 = 0;
       for (int it = 0; it < n; ++it) {
-        const __bf16* bs = rows_b[slot3].v;
-        const LinGates& GT = gates[slot3];
-        const LinValues<OUT>& U = vals[it & 1];
+        const LinGates& GT = gates[it & 1];
+        const __bf16* bs = rows_b[it & 1].v;
+        const __bf16* cs = rows_c[it & 1].v;
+        // a X: lane (g, c) holds row 16I + c, columns 4g + r
+        f32x4 o[LNT];
         if constexpr (OUT) {
-          const __bf16* as = rows_a[slot3].v;
-          f32x4 x[LNT];
+          const __bf16* as = rows_a[it & 1].v;
 #pragma unroll
-          for (int I = 0; I < LNT; ++I) x[I] = zero4();
+          for (int I = 0; I < LNT; ++I) o[I] = zero4();
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
             bf16x8 s[PARTS];
@@ -430,23 +398,25 @@ __global__ __launch_bounds__(scan_waves(OUT) * WAVE, 1) void lin_scan_kernel(Sca
             for (int I = 0; I < LNT; ++I) {
               const bf16x8 af = *reinterpret_cast<const bf16x8*>(as + a_at[p] + 16 * I * DK);
 #pragma unroll
-              for (int k = PARTS - 1; k >= 0; --k) x[I] = mma_bf16(s[k], af, x[I]);
+              for (int k = PARTS - 1; k >= 0; --k) o[I] = mma_bf16(s[k], af, o[I]);
             }
           }
-#pragma unroll
-          for (int I = 0; I < LNT; ++I) part[it & 1][h][I][l] = x[I];
         }
+        // X <- e^{G_C} X + b^T (col c), col c as three parts
         const float end = GT.end;
 #pragma unroll
         for (int t = 0; t < NA; ++t) X[t] = X[t] * end;
+        bf16x8 cf[2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
+          const bf16x4 c0 = lds_read_tr4(cs + ct_at + 32 * p * W), c1 = lds_read_tr4(cs + ct_at + (32 * p + 16) * W);
+          cf[p] = join8(c0, c1);
+          const f32x4 w0 = *reinterpret_cast<const f32x4*>(&GT.col[32 * p + 4 * g]);
+          const f32x4 w1 = *reinterpret_cast<const f32x4*>(&GT.col[32 * p + 16 + 4 * g]);
+          const f32x4 y0 = unpack4(c0) * w0, y1 = unpack4(c1) * w1;
+          const float y[8] = {y0[0], y0[1], y0[2], y0[3], y1[0], y1[1], y1[2], y1[3]};
           bf16x8 u[3];
-#pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const __bf16* q = &U.u[k][0][0] + ct_at + 32 * p * LDC;
-            u[k] = join8(lds_read_tr4(q), lds_read_tr4(q + 16 * LDC));
-          }
+          split3_exact(y, u);
 #pragma unroll
           for (int t = 0; t < NA; ++t) {
             const __bf16* q = bs + bt_at[t / 2] + 32 * p * DK + 4 * (t & 1);
@@ -455,10 +425,39 @@ __global__ __launch_bounds__(scan_waves(OUT) * WAVE, 1) void lin_scan_kernel(Sca
             for (int k = 2; k >= 0; --k) X[t] = mma_bf16(bt, u[k], X[t]);
           }
         }
-        slot3 = slot3 == 2 ? 0 : slot3 + 1;
+        if constexpr (OUT) {
+#pragma unroll
+          for (int I = 0; I < LNT; ++I) o[I] = o[I] * GT.row[16 * I + c];
+          lds_handover();  // the weights are there
+#pragma unroll
+          for (int I = 0; I < LNT; ++I)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              if (REV ? 2 * p + 1 < I : 2 * p > I) continue;
+#pragma unroll
+              for (int k = PARTS - 1; k >= 0; --k) o[I] = mma_bf16(cf[p], weights[k][I][p][l], o[I]);
+            }
+          const auto r = chunk_rows(A.out, orow, it, (int)sizeof(TO) * A.dc);  // rows past the end are not stored
+#pragma unroll
+          for (int I = 0; I < LNT; ++I) {
+            if constexpr (DOTS) {
+              const f32x4 w = unpack4(*reinterpret_cast<const bf16x4*>(rows_w[it & 1].v + w_at + 16 * I * W));
+              float s = 0.f, s0, s1;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) s = fmaf(w[q], o[I][q], s);
+              self_swap_f<16>(s, s0, s1);
+              s = s0 + s1;
+              self_swap_f<32>(s, s0, s1);
+              if (g == 0) dot_part[wave][16 * I + c] = s0 + s1;
+            }
+            if constexpr (sizeof(TO) == 2)
+              store8b(r, ooff + 16 * I * A.dc * 2, pack4(o[I]));
+            else
+              store16b(r, ooff + 16 * I * A.dc * 4, __builtin_bit_cast(u32x4, o[I]));
+          }
+        }
         lds_handover();
       }
-      if (OUT) lds_handover();
     }
     if (to) {
 #pragma unroll
@@ -468,51 +467,8 @@ __global__ __launch_bounds__(scan_waves(OUT) * WAVE, 1) void lin_scan_kernel(Sca
     }
     return;
   }
-  const int iters = OUT ? n + 1 : n;  // barriers of the loop
-  if (wave >= W_SPLIT && wave < W_GATES) {
-    // ---- c, and col c in three parts, one chunk ahead: 32 rows a wave, 8 columns a lane ---
-    if (n <= 0) return;
-    const int row = 32 * (wave - W_SPLIT) + (l >> 2), c0 = 8 * (l & 3);
-    const int coff = (row * A.dc + slice * LDC + c0) * 2;
-    bf16x8 x[2];
-    auto load = [&](int j) {
-      const auto r = chunk_rows(A.c, crow, j, 2 * A.dc);
-      x[0] = load16(r, coff);
-      x[1] = load16(r, coff + 32 * A.dc);
-    };
-    auto store = [&](LinValues<OUT>& V, const LinGates& GT) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float w = GT.col[row + 16 * i];
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = (float)x[i][e] * w;
-        bf16x8 u[3];
-        split3_exact(y, u);
-        const int at = LinValues<OUT>::at(row + 16 * i, c0);
-        if (OUT) *reinterpret_cast<bf16x8*>(&V.c[0][0] + at) = x[i];
-#pragma unroll
-        for (int k = 0; k < 3; ++k) *reinterpret_cast<bf16x8*>(&V.u[k][0][0] + at) = u[k];
-      }
-    };
-    load(0);
-    lds_handover();
-    store(vals[0], gates[0]);
-    load(1);
-    lds_handover();
-    int slot3 = 1;
-    for (int it = 0; it < iters; ++it) {
-      if (it + 1 < n) {
-        store(vals[(it + 1) & 1], gates[slot3]);
-        load(it + 2);
-      }
-      slot3 = slot3 == 2 ? 0 : slot3 + 1;
-      lds_handover();
-    }
-    return;
-  }
   if (wave == W_GATES) {
-    // ---- decay factors, two chunks ahead (lane = token) --------------------------------
+    // ---- decay factors, one chunk ahead (lane = token) ----------------------------------
     double decay = 0.0;  // sum of G_C over the segment
     const float g_head = A.g_per_head ? A.g[head] : 0.f;
     auto load = [&](int j) {
@@ -542,254 +498,148 @@ __global__ __launch_bounds__(scan_waves(OUT) * WAVE, 1) void lin_scan_kernel(Sca
       }
       decay += GC;
     };
+    // products of a chunk's output rows with those of dotw: the column waves' parts in order
+    auto sum_dots = [&](int j) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < COLS; ++w) s += dot_part[w][l];
+      store4(chunk_rows(A.dots + slice * A.heads_T, orow, j, 4), 4 * l, s);
+    };
     if (n > 0) {
       store(load(0), gates[0]);
-      if (n > 1) store(load(1), gates[1]);
-      float gl = load(2);
+      float gl = load(1);
       lds_handover();
-      lds_handover();
-      int slot3 = 2;
-      for (int it = 0; it < iters; ++it) {
-        if (it + 2 < n) {
-          store(gl, gates[slot3]);
-          gl = load(it + 3);
+      for (int it = 0; it < n; ++it) {
+        if constexpr (DOTS) {
+          if (it > 0) sum_dots(it - 1);  // the column waves write the next ones after the coming barrier
         }
-        slot3 = slot3 == 2 ? 0 : slot3 + 1;
+        if (it + 1 < n) {
+          store(gl, gates[(it + 1) & 1]);
+          gl = load(it + 2);
+        }
+        if (OUT) lds_handover();
         lds_handover();
       }
+      if constexpr (DOTS) sum_dots(n - 1);
     }
     if (!OUT && slice == 0 && l == 0) A.slot_decay[(int64_t)seg * A.H + head] = exp2_f32((float)decay);
     return;
   }
   if (wave == W_ROWS) {
-    // ---- rows of a and b straight into LDS, two chunks ahead ------------------------------
+    // ---- rows of a, b, c straight into LDS, one chunk ahead ------------------------------
     if (n <= 0) return;
-    constexpr int NB = LC * DK * 2 / 1024;  // 1 KB an instruction
-    const int64_t arow = row_of(A.group_a);
-    int off[NB];
+    constexpr int NB = LC * DK * 2 / 1024, NC = LC * W * 2 / 1024;  // 1 KB an instruction
+    const int64_t arow = row_of(A.group_a), brow = row_of(A.group_b);
+    int boff[NB], coff[NC];
 #pragma unroll
-    for (int i = 0; i < NB; ++i) off[i] = LinRows<DK>::source(i, l);
-    auto load = [&](int j, int slot) {
+    for (int i = 0; i < NB; ++i) boff[i] = LinRows<DK>::source(i, l, DK);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) coff[i] = LinRows<W>::source(i, l, A.dc) + slice * W * 2;
+    auto load = [&](int j) {
+      const int s = j & 1;
       const auto rb = chunk_rows(A.b, brow, j, 2 * DK);
 #pragma unroll
-      for (int i = 0; i < NB; ++i) load16_lds(rb, rows_b[slot].v + 512 * i, off[i]);
+      for (int i = 0; i < NB; ++i) load16_lds(rb, rows_b[s].v + 512 * i, boff[i]);
+      const auto rc = chunk_rows(A.c, crow, j, 2 * A.dc);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) load16_lds(rc, rows_c[s].v + 512 * i, coff[i]);
       if constexpr (OUT) {
         const auto ra = chunk_rows(A.a, arow, j, 2 * DK);
 #pragma unroll
-        for (int i = 0; i < NB; ++i) load16_lds(ra, rows_a[slot].v + 512 * i, off[i]);
+        for (int i = 0; i < NB; ++i) load16_lds(ra, rows_a[s].v + 512 * i, boff[i]);
+      }
+      if constexpr (DOTS) {
+        const auto rw = chunk_rows(A.dotw, crow, j, 2 * A.dc);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) load16_lds(rw, rows_w[s].v + 512 * i, coff[i]);
       }
     };
-    load(0, 0);
-    load(1, 1);
+    load(0);
+    wait_loads<0>();
     lds_handover();
-    wait_loads<OUT ? 2 * NB : NB>();
-    lds_handover();
-    int slot3 = 2;
-    for (int it = 0; it < iters; ++it) {
-      // chunk it + 1 has to be there after this barrier, chunk it + 2 stays in flight
-      if (it + 2 < n) {
-        load(it + 2, slot3);
-        wait_loads<OUT ? 2 * NB : NB>();
-      } else {
-        wait_loads<0>();
-      }
-      slot3 = slot3 == 2 ? 0 : slot3 + 1;
+    for (int it = 0; it < n; ++it) {
+      if (it + 1 < n) load(it + 1);
+      if (OUT) lds_handover();
+      wait_loads<0>();
       lds_handover();
     }
-    return;
-  }
-  if (wave == W_AHEAD) {
-    // ---- memory to L2, AHEAD chunks ahead -------------------------------------------------
-    // Loads whose values nobody needs: the other waves' loads, one chunk ahead, then find their
-    // lines in L2.  The slices of a head divide the rows of a and b among them: one 16-byte
-    // piece of each 128-byte line a lane.
-    if (n <= 0) return;
-    constexpr int LINES = LC * DK * 2 / 128;  // of a chunk of a or b
-    const int64_t arow = row_of(A.group_a);
-    const int share = (LINES + n_slices - 1) / n_slices;
-    const int line = slice * share + l;
-    const int off = l < share && line < LINES ? 128 * line : INT32_MAX;  // past the end: no access
-    const int coff = (l * A.dc + slice * LDC) * 2;
-    unsigned x[4] = {0, 0, 0, 0};
-    auto touch = [&](int j) {
-      asm volatile("" ::"v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]));  // the loads before have arrived
-      x[0] = __builtin_amdgcn_raw_buffer_load_b32(chunk_rows(A.b, brow, j, 2 * DK), off, 0, 0);
-      x[1] = __builtin_amdgcn_raw_buffer_load_b32(chunk_rows(A.c, crow, j, 2 * A.dc), coff, 0, 0);
-      if (!A.g_per_head) {
-        const int t0 = token_of(j);
-        x[2] = __builtin_amdgcn_raw_buffer_load_b32(row_buffer(A.g + orow + t0, min(LC, sp.len - t0) * 4), 4 * l, 0, 0);
-      }
-      if (OUT) x[3] = __builtin_amdgcn_raw_buffer_load_b32(chunk_rows(A.a, arow, j, 2 * DK), off, 0, 0);
-    };
-    for (int j = 2; j < min(AHEAD, n); ++j) touch(j);
-    lds_handover();
-    lds_handover();
-    for (int it = 0; it < iters; ++it) {
-      if (it + AHEAD < n) touch(it + AHEAD);
-      lds_handover();
-    }
-    asm volatile("" ::"v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]));
     return;
   }
   if constexpr (OUT) {
-    // ---- output waves: row tiles 0 and 3, or 1 and 2 (equal numbers of products) ----------
+    // ---- weight waves: row tiles 0 and 3, or 1 and 2 (equal numbers of products) ----------
     if (n <= 0) return;
-    auto out_rows = [&](auto tile0, auto tile1) {
+    auto weigh = [&](auto tile0, auto tile1) {
       constexpr int TI[2] = {tile0.value, tile1.value};
-      constexpr int NP = DK / 32;
-      constexpr bool OBF = sizeof(TO) == 2;
       // tiles J of b that have a weight for row tile I
       constexpr auto used = [](int I, int J) { return REV ? J >= I : J <= I; };
       int row_at[NP];  // row c of a tile, 16 bytes at 32p + 8g
 #pragma unroll
       for (int p = 0; p < NP; ++p) row_at[p] = LinRows<DK>::at(c, 32 * p + 8 * g);
-      const int ct_at[2] = {LinValues<OUT>::at(4 * g + (c >> 2), 4 * (c & 3)),
-                            LinValues<OUT>::at(4 * g + (c >> 2), 16 + 4 * (c & 3))};
-      const int ooff = (c * A.dc + slice * LDC + (OBF ? 16 * (g & 1) + 8 * (g >> 1) : 4 * g)) * (int)sizeof(TO);
-      const int woff = (c * A.dc + slice * LDC + 4 * g) * 2;
       lds_handover();
-      lds_handover();
-      f32x4 o[2][2];  // [tile][column half]: w (a . b) c of the chunk before
-      float rw[2];
-      bf16x4 wv[2][2];
-      int slot3 = 0;
-      // one iteration: products of chunk it (NEW), outputs of chunk it - 1 (OLD), whose products
-      // with the state are there now.  One block of code, so that the finishing arithmetic runs
-      // beside the new products.
-      auto step = [&](int it, auto old_, auto new_) {
-        constexpr bool OLD = old_.value, NEW = new_.value;
-        f32x4 x[2][2], P[2][LNT];
-        const LinGates& GT = gates[slot3];
-        if constexpr (OLD) {
+      for (int it = 0; it < n; ++it) {
+        const LinGates& GT = gates[it & 1];
+        const __bf16* as = rows_a[it & 1].v;
+        const __bf16* bs = rows_b[it & 1].v;
+        // P_ij = w_ij (a_i . b_j): lane (g, c) holds row i = 16I + c, columns 16J + 4g + r
+        f32x4 P[2][LNT];
+        bf16x8 af[2][NP];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) x[i][h] = part[(it - 1) & 1][h][TI[i]][l];
-        }
-        if constexpr (NEW) {
-          const __bf16* as = rows_a[slot3].v;
-          const __bf16* bs = rows_b[slot3].v;
-          // P_ij = w_ij (a_i . b_j): lane (g, c) holds row i = 16I + c, columns 16J + 4g + r
-          bf16x8 af[2][NP];
+          for (int p = 0; p < NP; ++p)
+            af[i][p] = *reinterpret_cast<const bf16x8*>(as + row_at[p] + 16 * TI[i] * DK);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+        for (int J = 0; J < LNT; ++J) {
+          P[0][J] = P[1][J] = zero4();
+          if (!used(TI[0], J) && !used(TI[1], J)) continue;
 #pragma unroll
-            for (int p = 0; p < NP; ++p)
-              af[i][p] = *reinterpret_cast<const bf16x8*>(as + row_at[p] + 16 * TI[i] * DK);
-#pragma unroll
-          for (int J = 0; J < LNT; ++J) {
-            P[0][J] = P[1][J] = zero4();
-            if (!used(TI[0], J) && !used(TI[1], J)) continue;
-#pragma unroll
-            for (int p = 0; p < NP; ++p) {
-              const bf16x8 bf = *reinterpret_cast<const bf16x8*>(bs + row_at[p] + 16 * J * DK);
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                if (used(TI[i], J)) P[i][J] = mma_bf16(bf, af[i][p], P[i][J]);
-            }
-          }
-        }
-        if constexpr (OLD) {
-          const int j = it - 1;
-          const auto r = chunk_rows(A.out, orow, j, (int)sizeof(TO) * A.dc);  // rows past the end are not stored
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int q = 0; q < 4; ++q) o[i][h][q] = fmaf(x[i][h][q], rw[i], o[i][h][q]);
-            if constexpr (DOTS) {
-              float s = 0.f;
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const f32x4 w = unpack4(wv[i][h]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) s = fmaf(w[q], o[i][h][q], s);
-              }
-              float s0, s1;
-              self_swap_f<16>(s, s0, s1);
-              s = s0 + s1;
-              self_swap_f<32>(s, s0, s1);
-              s = s0 + s1;
-              const auto d = chunk_rows(A.dots + slice * A.heads_T, orow, j, 4);
-              if (g == 0) store4(d, 4 * (16 * TI[i] + c), s);
-            }
-            const int at = ooff + 16 * TI[i] * A.dc * (int)sizeof(TO);
-            if constexpr (OBF) {
-              store16b(r, at, pair_bf16(o[i][0], o[i][1]));
-            } else {
-              store16b(r, at, __builtin_bit_cast(u32x4, o[i][0]));
-              store16b(r, at + 64, __builtin_bit_cast(u32x4, o[i][1]));
-            }
-          }
-        }
-        if constexpr (NEW) {
-          if constexpr (DOTS) {
-            const auto r = chunk_rows(A.dotw, crow, it, 2 * A.dc);
+          for (int p = 0; p < NP; ++p) {
+            const bf16x8 bf = *reinterpret_cast<const bf16x8*>(bs + row_at[p] + 16 * J * DK);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) wv[i][h] = load8b(r, woff + 16 * TI[i] * A.dc * 2 + 32 * h);
+              if (used(TI[i], J)) P[i][J] = mma_bf16(bf, af[i][p], P[i][J]);
           }
-          const __bf16* cs = &vals[it & 1].c[0][0];
+        }
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int I = TI[i];
-            rw[i] = GT.row[16 * I + c];
-            const float to = GT.to[16 * I + c];
+        for (int i = 0; i < 2; ++i) {
+          const int I = TI[i];
+          const float to = GT.to[16 * I + c];
 #pragma unroll
-            for (int J = 0; J < LNT; ++J) {
-              if (!used(I, J)) continue;
-              if (J != I) {
-                const f32x4 f = *reinterpret_cast<const f32x4*>(&GT.from[REV ? I : I - 1][16 * J + 4 * g]);
-                P[i][J] = P[i][J] * (f * to);
-              } else {
-                const float hi = GT.hi[16 * I + c], lo = GT.lo[16 * I + c];
-                const f32x4 hj = *reinterpret_cast<const f32x4*>(&GT.hi[16 * J + 4 * g]);
-                const f32x4 lj = *reinterpret_cast<const f32x4*>(&GT.lo[16 * J + 4 * g]);
+          for (int J = 0; J < LNT; ++J) {
+            if (!used(I, J)) continue;
+            if (J != I) {
+              const f32x4 f = *reinterpret_cast<const f32x4*>(&GT.from[REV ? I : I - 1][16 * J + 4 * g]);
+              P[i][J] = P[i][J] * (f * to);
+            } else {
+              const float hi = GT.hi[16 * I + c], lo = GT.lo[16 * I + c];
+              const f32x4 hj = *reinterpret_cast<const f32x4*>(&GT.hi[16 * J + 4 * g]);
+              const f32x4 lj = *reinterpret_cast<const f32x4*>(&GT.lo[16 * J + 4 * g]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const float e = REV ? (hj[q] - hi) + (lj[q] - lo) : (hi - hj[q]) + (lo - lj[q]);
-                  const bool keep = REV ? 4 * g + q >= c : 4 * g + q <= c;
-                  P[i][J][q] = keep ? P[i][J][q] * (exp2_f32(e) * A.s_intra) : 0.f;
-                }
+              for (int q = 0; q < 4; ++q) {
+                const float e = REV ? (hj[q] - hi) + (lj[q] - lo) : (hi - hj[q]) + (lo - lj[q]);
+                const bool keep = REV ? 4 * g + q >= c : 4 * g + q <= c;
+                P[i][J][q] = keep ? P[i][J][q] * (exp2_f32(e) * A.s_intra) : 0.f;
               }
             }
-            o[i][0] = o[i][1] = zero4();
           }
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            bf16x8 cf[2];
+            if (REV ? 2 * p + 1 < I : 2 * p > I) continue;
+            bf16x8 s[PARTS];
+            split<PARTS>(P[i][2 * p], P[i][2 * p + 1], s);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const __bf16* q = cs + ct_at[h] + 32 * p * LDC;
-              cf[h] = join8(lds_read_tr4(q), lds_read_tr4(q + 16 * LDC));
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (!used(TI[i], 2 * p) && !used(TI[i], 2 * p + 1)) continue;
-              bf16x8 s[PARTS];
-              split<PARTS>(P[i][2 * p], P[i][2 * p + 1], s);
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int k = PARTS - 1; k >= 0; --k) o[i][h] = mma_bf16(cf[h], s[k], o[i][h]);
-            }
+            for (int k = 0; k < PARTS; ++k) weights[k][I][p][l] = s[k];
           }
         }
-        slot3 = slot3 == 2 ? 0 : slot3 + 1;
         lds_handover();
-      };
-      using std::bool_constant;
-      step(0, bool_constant<false>{}, bool_constant<true>{});
-      for (int it = 1; it < n; ++it) step(it, bool_constant<true>{}, bool_constant<true>{});
-      step(n, bool_constant<true>{}, bool_constant<false>{});
+        lds_handover();
+      }
     };
     using std::integral_constant;
-    if (wave == 2)
-      out_rows(integral_constant<int, 0>{}, integral_constant<int, 3>{});
+    if (wave == COLS)
+      weigh(integral_constant<int, 0>{}, integral_constant<int, 3>{});
     else
-      out_rows(integral_constant<int, 1>{}, integral_constant<int, 2>{});
+      weigh(integral_constant<int, 1>{}, integral_constant<int, 2>{});
   }
 }
 
@@ -916,6 +766,9 @@ namespace {
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// columns of c per workgroup: the more, the fewer times w (a . b) is formed
+int scan_width(int dc) { return dc % 128 == 0 ? 128 : dc % 64 == 0 ? 64 : 32; }
+
 // segments of a call and where its workspace holds what
 struct LinPlan {
   int seg_chunks, segs_per_seq;
@@ -930,15 +783,24 @@ LinPlan make_plan(const LinLaunch& p, bool bwd) {
   LinPlan q{};
   const int64_t nch = (p.T + LC - 1) / LC;
   const int64_t all = p.offsets ? nch + p.n_seq : nch * p.n_seq;  // chunks, at most
-  const int cols = bwd && p.d_k < p.d_v ? p.d_k : p.d_v;
-  const int64_t items = (int64_t)p.H * (cols / LDC);             // workgroups per segment
-  // segments long enough that 512 workgroups share the chunks (two for each CU), at least
-  // 8 chunks: a segment's state costs about half of what its outputs do
-  int64_t seg = (all * items + 511) / 512;
-  seg = seg < 8 ? 8 : seg;
-  if (!bwd && !p.offsets && (p.n_seq * items >= 256 || nch <= 2 * seg)) seg = nch > 0 ? nch : 1;
+  const int64_t items = (int64_t)p.H * (p.d_v / scan_width(p.d_v));  // workgroups per segment
+  // Segment length by what the launches cost in chunks: a round of outputs has a workgroup on
+  // each of 256 CUs; a segment's own state takes about half of that with two on each; the
+  // launches and the joining add a few.
+  int64_t seg = nch > 0 ? nch : 1, best = INT64_MAX;
+  const int64_t longest = nch > 0 ? nch : 1;
+  for (int64_t ns = 1; ns <= 256 && ns <= longest; ++ns) {
+    const int64_t len = (longest + ns - 1) / ns;
+    const int64_t n = p.offsets ? (all + len - 1) / len : p.n_seq * ((longest + len - 1) / len);
+    const int64_t rounds = (n * items + 255) / 256;
+    const int64_t before = ((n - (p.offsets ? 1 : p.n_seq)) * items + 511) / 512;
+    const int64_t cost = 4 * rounds * len + (ns > 1 ? 2 * before * len + 20 : 0);
+    if (cost < best) {
+      best = cost;
+      seg = len;
+    }
+  }
   if (bwd && seg > BWD_SEG_CHUNKS) seg = BWD_SEG_CHUNKS;
-  if (seg > nch) seg = nch > 0 ? nch : 1;
   q.seg_chunks = (int)seg;
   const int64_t per = nch > 0 ? (nch + seg - 1) / seg : 1;
   q.segs_per_seq = (int)per;
@@ -959,8 +821,8 @@ LinPlan make_plan(const LinLaunch& p, bool bwd) {
   if (bwd) {
     q.slot_d = take(sh * state);
     q.decay_d = take(sh * 4);
-    q.dot_q = take(rows * (p.d_k / LDC) * 4);
-    q.dot_k = take(rows * (p.d_k / LDC) * 4);
+    q.dot_q = take(rows * (p.d_k / scan_width(p.d_k)) * 4);
+    q.dot_k = take(rows * (p.d_k / scan_width(p.d_k)) * 4);
     if (p.g_per_head) q.dg_seg = take(sh * 8);
     if (p.H != p.H_qk) {
       q.part_q = take(rows * p.d_k * 4);
@@ -973,15 +835,25 @@ LinPlan make_plan(const LinLaunch& p, bool bwd) {
 
 template <bool REV, bool OUT, int PARTS, bool DOTS, class TO>
 int scan(int dk, const ScanArgs& a, hipStream_t s) {
-  const int64_t total = (int64_t)a.n_seg * a.H * (a.dc / LDC);
-  const dim3 grid((unsigned)(8 * ((total + 7) / 8))), block(scan_waves(OUT) * WAVE);
-  if (dk == 64)
-    hipLaunchKernelGGL((lin_scan_kernel<64, REV, OUT, PARTS, DOTS, TO>), grid, block, 0, s, a);
-  else if (dk == 128)
-    hipLaunchKernelGGL((lin_scan_kernel<128, REV, OUT, PARTS, DOTS, TO>), grid, block, 0, s, a);
-  else
+  const int width = scan_width(a.dc);
+  const int64_t total = (int64_t)a.n_seg * a.H * (a.dc / width);
+  const dim3 grid((unsigned)(8 * ((total + 7) / 8)));
+  auto go = [&](auto d, auto w) {
+    hipLaunchKernelGGL((lin_scan_kernel<d.value, w.value, REV, OUT, PARTS, DOTS, TO>), grid,
+                       dim3(scan_waves(w.value, OUT) * WAVE), 0, s, a);
+    return 0;
+  };
+  using std::integral_constant;
+  auto by_width = [&](auto d) {
+    if (width == 128) return go(d, integral_constant<int, 128>{});
+    if (width == 64) return go(d, integral_constant<int, 64>{});
+    // the backward pass has d_k and d_v of 64 and 128 only
+    if constexpr (!REV && !DOTS) return go(d, integral_constant<int, 32>{});
     return -1;
-  return 0;
+  };
+  if (dk == 64) return by_width(integral_constant<int, 64>{});
+  if (dk == 128) return by_width(integral_constant<int, 128>{});
+  return -1;
 }
 
 ScanArgs base_args(const LinLaunch& p, const LinPlan& q) {
@@ -1020,7 +892,7 @@ size_t lin_workspace(const LinLaunch& p, bool bwd) { return make_plan(p, bwd).by
 bool lin_grid_ok(const LinLaunch& p, bool bwd) {
   const LinPlan q = make_plan(p, bwd);
   const int64_t cols = p.d_k > p.d_v ? p.d_k : p.d_v;
-  return q.n_seg * p.H * (cols / LDC) < ((int64_t)1 << 31) - 8;
+  return q.n_seg * p.H * (cols / 32) < ((int64_t)1 << 31) - 8;
 }
 
 int launch_lin_fwd(const LinLaunch& p, void* workspace, hipStream_t s) {
@@ -1144,7 +1016,7 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
                        p.grad_bf16, n, p.T * p.d_k, p.d_k, group, p.offsets, p.n_seq);
   }
   if (!p.dg) return 0;
-  const int nsl = p.d_k / LDC;
+  const int nsl = p.d_k / scan_width(p.d_k);
   double* dg_seg = p.g_per_head ? reinterpret_cast<double*>(ws + q.dg_seg) : nullptr;
   hipLaunchKernelGGL(lin_dgate_kernel, dim3((unsigned)(p.H * q.n_seg)), dim3(256), 0, s,
                      reinterpret_cast<const float*>(ws + q.dot_q), reinterpret_cast<const float*>(ws + q.dot_k), nsl,
