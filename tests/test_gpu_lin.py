@@ -436,7 +436,7 @@ def test_c_refusals():
 
 def test_workspace_queries():
     fwd, bwd = tri.gdn_lin_chunk_fwd_workspace_bytes, tri.gdn_lin_chunk_bwd_workspace_bytes
-    assert fwd(4, 16, 8192, 128, 128) == 0          # heads and sequences fill the GPU
+    assert fwd(32, 16, 8192, 128, 128) == 0         # heads and sequences fill the GPU
     assert fwd(1, 2, 64, 64, 64) == 0               # nothing to divide
     assert fwd(1, 2, 100000, 64, 64) >= 2 * 64 * 64 * 4
     assert fwd(1, 3, 100, 96, 64) == 0 and bwd(1, 3, 100, 64, 32) == 0  # refused arguments

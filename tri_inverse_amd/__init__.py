@@ -471,11 +471,24 @@ def _scope(dev, stream):
         if stream.device != dev:
             raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, dev))
         return torch.cuda.stream(stream)
-    return _HERE_SCOPE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    return _HERE_SCOPE if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
+
+
+def _current(dev):
+    """The current stream of dev as the library takes it (without building a Stream object: the
+    calls of a decode step cost more on the host than their kernels take)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _arg(t, name, dtypes, shape, dev):
     """A required tensor: on dev (None: any GPU), contiguous, of one of dtypes, of this shape."""
+    if (type(t) is torch.Tensor and t.is_cuda and t.dtype in dtypes and t.shape == shape and t.is_contiguous()
+            and (dev is None or t.device == dev)):
+        return t
     _dev(t, name, dtypes)
     if t is None:
         raise TypeError("%s is required" % name)
@@ -572,8 +585,8 @@ def gdn_lin_chunk_fwd(Q, K, V, g, scale: float | None = None, S0=None, offsets=N
         O = _out(O, "O", _FLOAT, V.shape, dev, o_dtype)
         S_out = _out(S_out, "S_out", (torch.float32,), state, dev, torch.float32)
         ws, ws_bytes = _scratch(workspace, _lib.gdn_lin_chunk_fwd_workspace_bytes(ctypes.byref(sh)), dev)
-        st = _lib.gdn_lin_chunk_fwd(ctypes.byref(sh), _ptr(Q), _ptr(K), _ptr(V), GDN_BF16, _ptr(g), _ptr(S0), _ptr(O),
-                                    _TORCH_DTYPE[O.dtype], _ptr(S_out), _ptr(ws), ws_bytes, _stream(None))
+        st = _lib.gdn_lin_chunk_fwd(ctypes.byref(sh), _at(Q), _at(K), _at(V), GDN_BF16, _at(g), _at(S0), _at(O),
+                                    _TORCH_DTYPE[O.dtype], _at(S_out), _at(ws), ws_bytes, _current(dev))
     _check(st, "gdn_lin_chunk_fwd")
     return O, S_out
 
@@ -598,9 +611,9 @@ def gdn_lin_chunk_bwd(Q, K, V, g, dO, scale: float | None = None, S0=None, dS=No
         dg = new(g.shape, device=dev, dtype=torch.float32) if want_dg else None
         dS0 = None if S0 is None else torch.empty(state, device=dev, dtype=torch.float32)
         ws, ws_bytes = _scratch(workspace, _lib.gdn_lin_chunk_bwd_workspace_bytes(ctypes.byref(sh)), dev)
-        st = _lib.gdn_lin_chunk_bwd(ctypes.byref(sh), _ptr(Q), _ptr(K), _ptr(V), GDN_BF16, _ptr(g), _ptr(S0), _ptr(dO),
-                                    _ptr(dS), _ptr(dQ), _ptr(dK), _ptr(dV), _TORCH_DTYPE[grad_dtype], _ptr(dg),
-                                    _ptr(dS0), _ptr(ws), ws_bytes, _stream(None))
+        st = _lib.gdn_lin_chunk_bwd(ctypes.byref(sh), _at(Q), _at(K), _at(V), GDN_BF16, _at(g), _at(S0), _at(dO),
+                                    _at(dS), _at(dQ), _at(dK), _at(dV), _TORCH_DTYPE[grad_dtype], _at(dg),
+                                    _at(dS0), _at(ws), ws_bytes, _current(dev))
     _check(st, "gdn_lin_chunk_bwd")
     return dQ, dK, dV, dg, dS0
 
@@ -618,8 +631,8 @@ def gdn_lin_decode(Q, K, V, g, S=None, scale: float | None = None, S_out=None, O
     with _scope(dev, stream):
         O = _out(O, "O", _FLOAT, V.shape, dev, o_dtype)
         S_out = _out(S_out, "S_out", (torch.float32,), state, dev, torch.float32)
-        st = _lib.gdn_lin_decode(ctypes.byref(sh), _ptr(Q), _ptr(K), _ptr(V), _TORCH_DTYPE[K.dtype], _ptr(g), _ptr(S),
-                                 _ptr(S_out), _ptr(O), _TORCH_DTYPE[O.dtype], _stream(None))
+        st = _lib.gdn_lin_decode(ctypes.byref(sh), _at(Q), _at(K), _at(V), _TORCH_DTYPE[K.dtype], _at(g), _at(S),
+                                 _at(S_out), _at(O), _TORCH_DTYPE[O.dtype], _current(dev))
     _check(st, "gdn_lin_decode")
     return O, S_out
 
@@ -658,8 +671,8 @@ def gdn_gate_norm_fwd(O, Z, w=None, eps: float = 1e-6, act: str = "silu", Y=None
     B, H, T, d, step, dev = _gate_args(O, Z, w, act)
     with _scope(dev, stream):
         Y = _out(Y, "Y", (O.dtype,), (B, T, H, d), dev, O.dtype)
-        st = _lib.gdn_gate_norm_fwd(_ptr(O), _ptr(Z), step, _ptr(w), _ptr(Y), _TORCH_DTYPE[O.dtype], B, H, T, d,
-                                    _ACT[act], float(eps), _stream(None))
+        st = _lib.gdn_gate_norm_fwd(_at(O), _at(Z), step, _at(w), _at(Y), _TORCH_DTYPE[O.dtype], B, H, T, d,
+                                    _ACT[act], float(eps), _current(dev))
     _check(st, "gdn_gate_norm_fwd")
     return Y
 
@@ -675,9 +688,9 @@ def gdn_gate_norm_bwd(dY, O, Z, w=None, eps: float = 1e-6, act: str = "silu", wo
         dw = None if w is None else torch.empty((d,), device=dev, dtype=torch.float32)
         ws, ws_bytes = (None, 0) if dw is None else _scratch(
             workspace, _lib.gdn_gate_norm_bwd_workspace_bytes(B, H, T, d), dev)
-        st = _lib.gdn_gate_norm_bwd(_ptr(dY), _ptr(O), _ptr(Z), step, _ptr(w), _ptr(dO), _ptr(dZ), _ptr(dw),
-                                    _TORCH_DTYPE[O.dtype], B, H, T, d, _ACT[act], float(eps), _ptr(ws), ws_bytes,
-                                    _stream(None))
+        st = _lib.gdn_gate_norm_bwd(_at(dY), _at(O), _at(Z), step, _at(w), _at(dO), _at(dZ), _at(dw),
+                                    _TORCH_DTYPE[O.dtype], B, H, T, d, _ACT[act], float(eps), _at(ws), ws_bytes,
+                                    _current(dev))
     _check(st, "gdn_gate_norm_bwd")
     return dO, dZ, dw
 
@@ -705,9 +718,9 @@ def gdn_residual_norm_fwd(X, Y, w_post=None, s=None, alpha: float = 1.0, w_pre=N
     with _scope(dev, stream):
         R = _out(R, "R", (X.dtype,), X.shape, dev, X.dtype)
         N = _out(N, "N", (Y.dtype,), Y.shape, dev, Y.dtype) if want_norm else None
-        st = _lib.gdn_residual_norm_fwd(_ptr(X), _TORCH_DTYPE[X.dtype], _ptr(Y), _TORCH_DTYPE[Y.dtype], _ptr(w_post),
-                                        _ptr(s), float(alpha), _ptr(w_pre), _ptr(R), _ptr(N), rows, D, float(eps),
-                                        _stream(None))
+        st = _lib.gdn_residual_norm_fwd(_at(X), _TORCH_DTYPE[X.dtype], _at(Y), _TORCH_DTYPE[Y.dtype], _at(w_post),
+                                        _at(s), float(alpha), _at(w_pre), _at(R), _at(N), rows, D, float(eps),
+                                        _current(dev))
     _check(st, "gdn_residual_norm_fwd")
     return R, N
 
@@ -728,9 +741,9 @@ def gdn_residual_norm_bwd(dN, dR, R, Y, w_post=None, s=None, alpha: float = 1.0,
         dw_pre, dw_post, ds = vec(w_pre if dN is not None else None), vec(w_post), vec(s)
         ws, ws_bytes = (None, 0) if dw_pre is dw_post is ds is None else _scratch(
             workspace, _lib.gdn_residual_norm_bwd_workspace_bytes(rows, D), dev)
-        st = _lib.gdn_residual_norm_bwd(_ptr(dN), _ptr(dR), _ptr(R), _TORCH_DTYPE[R.dtype], _ptr(Y),
-                                        _TORCH_DTYPE[Y.dtype], _ptr(w_post), _ptr(s), float(alpha), _ptr(w_pre),
-                                        _ptr(dX), _ptr(dY), _ptr(dw_pre), _ptr(dw_post), _ptr(ds), rows, D, float(eps),
-                                        _ptr(ws), ws_bytes, _stream(None))
+        st = _lib.gdn_residual_norm_bwd(_at(dN), _at(dR), _at(R), _TORCH_DTYPE[R.dtype], _at(Y),
+                                        _TORCH_DTYPE[Y.dtype], _at(w_post), _at(s), float(alpha), _at(w_pre),
+                                        _at(dX), _at(dY), _at(dw_pre), _at(dw_post), _at(ds), rows, D, float(eps),
+                                        _at(ws), ws_bytes, _current(dev))
     _check(st, "gdn_residual_norm_bwd")
     return dX, dY, dw_pre, dw_post, ds

@@ -47,6 +47,7 @@ namespace {
 
 constexpr int LC = 64;     // tokens of a chunk
 constexpr int LNT = 4;     // 16-row tiles of a chunk
+constexpr int BWD_SEG_CHUNKS = 16;  // at most 1024 tokens are summed into dg from one pair of states
 constexpr double LOG2E = 1.4426950408889634;
 
 struct ScanArgs {
@@ -658,17 +659,32 @@ __global__ __launch_bounds__(256) void lin_join_kernel(float* slot, const float*
   const int e = 4 * (int)((blockIdx.x % per) * 256 + threadIdx.x);
   if (e >= size) return;
   f32x4 x = init ? *reinterpret_cast<const f32x4*>(init + ((int64_t)seq * H + head) * size + e) : zero4();
-  for (int i = 0; i < n; ++i) {
-    const int64_t sh = (int64_t)(REV ? s0 + ns - 1 - i : s0 + i) * H + head;
-    f32x4* p = reinterpret_cast<f32x4*>(slot + sh * size + e);
-    x = x * slot_decay[sh] + *p;
-    *p = x;
+  // eight segments' values asked for together: the loads do not wait for the sums
+  constexpr int N = 8;
+  for (int i0 = 0; i0 < n; i0 += N) {
+    f32x4* at[N];
+    f32x4 v[N];
+    float d[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = min(i0 + k, n - 1);
+      const int64_t sh = (int64_t)(REV ? s0 + ns - 1 - i : s0 + i) * H + head;
+      at[k] = reinterpret_cast<f32x4*>(slot + sh * size + e);
+      v[k] = *at[k];
+      d[k] = slot_decay[sh];
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (i0 + k < n) {
+        x = x * d[k] + v[k];
+        *at[k] = x;
+      }
   }
 }
 
 // dg of one (segment, head): from the segment's end backwards, dg_t = <D, S> at the end +
 // sum_{s>=t} (q_s . dq_s - k_s . dk_s), the sums in fp64.  Per-head decays: the segment's sum.
-__global__ __launch_bounds__(256) void lin_dgate_kernel(const float* dot_q, const float* dot_k, int nq, int nk,
+__global__ __launch_bounds__(256) void lin_dgate_kernel(const float* dot_q, const float* dot_k, int n_dots,
                                                         const float* slot_s, const float* slot_d, const float* dS,
                                                         float* dg, double* dg_seg, const int32_t* offsets, int64_t T,
                                                         int64_t heads_T, int n_seq, int n_seg, int H, int size,
@@ -686,6 +702,20 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(const float* dot_q, cons
     __syncthreads();
     return (red[0] + red[1]) + (red[2] + red[3]);
   };
+  // thread i holds tokens t1 - 1 - i - 256 k: all are asked for before anything is summed
+  constexpr int RUNS = (int)BWD_SEG_CHUNKS * LC / 256;
+  const int64_t row0 = ((offsets ? 0 : (int64_t)sp.seq * H) + head) * T + sp.tok0;
+  const int t0 = sp.c0 * LC, t1 = min(sp.len, (sp.c0 + sp.nc) * LC);
+  float rq[RUNS][2], rk[RUNS][2];
+#pragma unroll
+  for (int k = 0; k < RUNS; ++k) {
+    const int t = t1 - 1 - (int)threadIdx.x - 256 * k;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      rq[k][s] = s < n_dots && t >= t0 ? dot_q[s * heads_T + row0 + t] : 0.f;
+      rk[k][s] = s < n_dots && t >= t0 ? dot_k[s * heads_T + row0 + t] : 0.f;
+    }
+  }
   // the states at the segment's end; none given there: their product is zero
   double run = 0.0;
   const float* D = sp.last ? (dS ? dS + ((int64_t)sp.seq * H + head) * size : nullptr)
@@ -693,23 +723,20 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(const float* dot_q, cons
   if (D && seg + (sp.last ? 0 : 1) < n_seg) {
     const float* S = slot_s + ((int64_t)seg * H + head) * size;
     double x = 0.0;
-    for (int e = threadIdx.x; e < size; e += 256) x += (double)D[e] * (double)S[e];
+#pragma unroll 4
+    for (int e = 4 * (int)threadIdx.x; e < size; e += 1024) {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(D + e), b = *reinterpret_cast<const f32x4*>(S + e);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x = fma((double)a[r], (double)b[r], x);
+    }
     run = block_sum(x);
   }
-  const int64_t row0 = ((offsets ? 0 : (int64_t)sp.seq * H) + head) * T + sp.tok0;
-  const int t0 = sp.c0 * LC, t1 = min(sp.len, (sp.c0 + sp.nc) * LC);
   double sum = 0.0;
-  // 256 tokens a time from the end; thread i holds token hi - 1 - i
-  for (int hi = t1; hi > t0; hi -= 256) {
-    const int t = hi - 1 - (int)threadIdx.x;
-    const bool in = t >= t0;
-    double r = 0.0;
-    if (in) {
-      const int64_t row = row0 + t;
-      for (int s = 0; s < nq; ++s) r += (double)dot_q[s * heads_T + row];
-      for (int s = 0; s < nk; ++s) r -= (double)dot_k[s * heads_T + row];
-    }
-    r = wave_scan_f64(r);
+#pragma unroll
+  for (int k = 0; k < RUNS; ++k) {
+    if (t1 - 256 * k <= t0) break;
+    const int t = t1 - 1 - (int)threadIdx.x - 256 * k;
+    const double r = wave_scan_f64(((double)rq[k][0] - (double)rk[k][0]) + ((double)rq[k][1] - (double)rk[k][1]));
     __syncthreads();
     if (l == WAVE - 1) red[wave] = r;
     __syncthreads();
@@ -718,7 +745,7 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(const float* dot_q, cons
       if (w < wave) before += red[w];
       run += red[w];
     }
-    if (in) {
+    if (t >= t0) {
       if (dg) dg[row0 + t] = (float)(before + r);
       sum += before + r;
     }
@@ -777,7 +804,6 @@ struct LinPlan {
   size_t slot_s, slot_d, decay_s, decay_d, dot_q, dot_k, dg_seg, part_q, part_k, bytes;
 };
 
-constexpr int64_t BWD_SEG_CHUNKS = 16;  // at most 1024 tokens are summed into dg from one pair of states
 
 LinPlan make_plan(const LinLaunch& p, bool bwd) {
   LinPlan q{};
@@ -1020,7 +1046,7 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   double* dg_seg = p.g_per_head ? reinterpret_cast<double*>(ws + q.dg_seg) : nullptr;
   hipLaunchKernelGGL(lin_dgate_kernel, dim3((unsigned)(p.H * q.n_seg)), dim3(256), 0, s,
                      reinterpret_cast<const float*>(ws + q.dot_q), reinterpret_cast<const float*>(ws + q.dot_k), nsl,
-                     nsl, slot_s, slot_d, p.dS, p.g_per_head ? nullptr : p.dg, dg_seg, p.offsets, p.T, f.heads_T,
+                     slot_s, slot_d, p.dS, p.g_per_head ? nullptr : p.dg, dg_seg, p.offsets, p.T, f.heads_T,
                      p.n_seq, (int)q.n_seg, p.H, p.d_k * p.d_v, q.seg_chunks, q.segs_per_seq);
   if (p.g_per_head)
     hipLaunchKernelGGL(lin_dgate_head_kernel, dim3((unsigned)p.H), dim3(64), 0, s, dg_seg, p.dg, p.offsets, p.T,

@@ -176,25 +176,33 @@ __global__ __launch_bounds__(256) void gate_norm_bwd_kernel(GateNormLaunch a, ui
   }
 }
 
-// out[j][i] = sum over k < n of part[k][j][i], in order: 16 columns a workgroup, 16 threads a
+// out[j][i] = sum over k < n of part[k][j][i], in order: 16 columns a workgroup, 64 threads a
 // column (each a fixed run of k), joined in order
-__global__ __launch_bounds__(256) void column_sum_kernel(const float* part, int n, int D, int n_out, float* out0,
-                                                         float* out1, float* out2) {
-  __shared__ double red[16][17];
-  const int i = blockIdx.x * 16 + threadIdx.x % 16, k0 = threadIdx.x / 16;
+__global__ __launch_bounds__(1024) void column_sum_kernel(const float* part, int n, int D, int n_out, float* out0,
+                                                          float* out1, float* out2) {
+  constexpr int RUNS = 64;
+  __shared__ double red[RUNS][17];
+  const int c = threadIdx.x % 16, k0 = threadIdx.x / 16, i = blockIdx.x * 16 + c;
   const int j = blockIdx.y;
   float* out = j == 0 ? out0 : j == 1 ? out1 : out2;
   if (!out) return;
-  const int run = (n + 15) / 16;
+  const int run = (n + RUNS - 1) / RUNS, k1 = min(n, (k0 + 1) * run);
   double x = 0.0;
   if (i < D)
-    for (int k = k0 * run; k < min(n, (k0 + 1) * run); ++k) x += (double)part[((int64_t)k * n_out + j) * D + i];
-  red[k0][threadIdx.x % 16] = x;
+#pragma unroll 8
+    for (int k = k0 * run; k < k1; ++k) x += (double)part[((int64_t)k * n_out + j) * D + i];
+  red[k0][c] = x;
   __syncthreads();
-  if (k0 == 0 && i < D) {
-    for (int k = 1; k < 16; ++k) x += red[k][threadIdx.x % 16];
-    out[i] = (float)x;
+  // 16 neighbouring runs, then those four sums
+  if (k0 < 4) {
+    x = 0.0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x += red[16 * k0 + k][c];
   }
+  __syncthreads();
+  if (k0 < 4) red[k0][c] = x;
+  __syncthreads();
+  if (k0 == 0 && i < D) out[i] = (float)((red[0][c] + red[1][c]) + (red[2][c] + red[3][c]));
 }
 
 // ---- residual norm ----------------------------------------------------------------------
@@ -463,7 +471,7 @@ int64_t res_groups(const ResNormLaunch& p, int64_t most) {
 constexpr int64_t RES_FWD_GROUPS = 2048, RES_BWD_GROUPS = 512;
 
 void column_sum(const float* part, int64_t n, int D, int n_out, float* o0, float* o1, float* o2, hipStream_t s) {
-  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((D + 15) / 16), (unsigned)n_out), dim3(256), 0, s, part, (int)n,
+  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((D + 15) / 16), (unsigned)n_out), dim3(1024), 0, s, part, (int)n,
                      D, n_out, o0, o1, o2);
 }
 
