@@ -83,7 +83,7 @@ def test_forward_heads_widths_decays(H, Hk, dk, dv, decay, strong):
 
 
 @gpu
-@pytest.mark.parametrize("T,decay", [(1100, "token"), (2500, "head"), (1029, "head")])
+@pytest.mark.parametrize("T,decay", [(4100, "token"), (6500, "head"), (4159, "head")])
 def test_forward_divided_tokens(T, decay):
     """Few heads and many tokens: segments are formed apart and joined."""
     say(f"lin forward divided T={T} {decay}")
@@ -96,7 +96,8 @@ def test_forward_divided_tokens(T, decay):
     close(S, want[1], mag[1], TOL_S, "S")
 
 
-PACKS = [[1], [64, 64], [0, 70, 0, 1, 129, 63, 0], [5] * 70 + [0] * 3 + [200], [1300, 3, 600], [0, 0, 0]]
+PACKS = [[1], [64, 64], [0, 70, 0, 1, 129, 63, 0], [5] * 70 + [0] * 3 + [200], [1300, 3, 600], [0, 0, 0],
+         [4400, 3, 0, 700]]
 
 
 @gpu
@@ -108,6 +109,8 @@ def test_forward_packed(lens, decay):
     H, Hk, dk, dv, first, behind = 4, 2, 64, 64, 3, 5
     T = first + sum(lens) + behind
     say(f"lin forward packed {len(lens)} sequences, {T} tokens, {decay}")
+    if max(lens) > 4000:  # divided: segments are formed apart and joined
+        assert tri.gdn_lin_chunk_fwd_workspace_bytes(len(lens), H, T, dk, dv, H_qk=Hk, packed=True) > 0
     x = ref.lin_inputs(11, 1, H, Hk, T, dk, dv, decay, n_state=len(lens))
     bad = dict(x)
     inside = slice(first, T - behind)
@@ -319,7 +322,7 @@ def test_captured_and_on_another_stream():
     """A captured call replayed between eager ones, and a call on a stream of its own, give the
     eager call's bits."""
     say("lin captured and streamed")
-    T = 1500
+    T = 5000
     c = {k: cuda(t) for k, t in ref.lin_inputs(51, 1, 4, 2, T, 64, 64).items()}
     args = (c["Q"], c["K"], c["V"], c["g"])
 
@@ -351,9 +354,9 @@ def test_captured_and_on_another_stream():
 @gpu
 def test_caller_tensors_and_workspace():
     say("lin caller workspace")
-    x = {k: cuda(t) for k, t in ref.lin_inputs(61, 1, 2, 2, 1200, 64, 64).items()}
-    need = tri.gdn_lin_chunk_fwd_workspace_bytes(1, 2, 1200, 64, 64)
-    O = torch.empty((1, 2, 1200, 64), device="cuda", dtype=torch.bfloat16)
+    x = {k: cuda(t) for k, t in ref.lin_inputs(61, 1, 2, 2, 5000, 64, 64).items()}
+    need = tri.gdn_lin_chunk_fwd_workspace_bytes(1, 2, 5000, 64, 64)
+    O = torch.empty((1, 2, 5000, 64), device="cuda", dtype=torch.bfloat16)
     S = torch.empty((1, 2, 64, 64), device="cuda")
     ws = torch.empty(need, device="cuda", dtype=torch.uint8)
     o, s = tri.gdn_lin_chunk_fwd(x["Q"], x["K"], x["V"], x["g"], O=O, S_out=S, workspace=ws)

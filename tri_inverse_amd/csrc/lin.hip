@@ -50,6 +50,16 @@ constexpr int LNT = 4;     // 16-row tiles of a chunk
 constexpr int BWD_SEG_CHUNKS = 16;  // at most 1024 tokens are summed into dg from one pair of states
 constexpr double LOG2E = 1.4426950408889634;
 
+// How sequences are cut into segments, runs of chunks that one workgroup (for some columns) walks
+struct Cut {
+  const int32_t* offsets;  // packed sequences
+  int64_t T;
+  int n_seq;
+  int chunks;    // of a segment
+  int segments;  // of a sequence (packed: at most, not used)
+  int n_seg;     // of all sequences (packed: at most)
+};
+
 struct ScanArgs {
   const __bf16* a;
   const __bf16* b;
@@ -62,12 +72,11 @@ struct ScanArgs {
   void* out;
   const __bf16* dotw;  // rows whose product with the output rows goes to dots,
   float* dots;         // [slice][head row]
-  const int32_t* offsets;
-  int64_t T;
   int64_t heads_T;     // rows of all heads, B * H * T
-  int n_seq, H, group_a, group_b, group_c, dc;
-  int seg_chunks, n_seg, segs_per_seq;
-  int g_per_head, skip_end;
+  int H, group_a, group_b, group_c, dc;
+  Cut cut;
+  int g_per_head;
+  int skip;            // without OUT: a sequence's end segment is not wanted
   int64_t st_row, st_col;  // strides of the states in this scan's (row, column) order
   float s_intra, s_inter, s_state;
 };
@@ -99,7 +108,7 @@ struct alignas(16) LinGates {
   float end;                    // e^{G_C}
 };
 
-// one segment: tokens [tok0 + 64 c0, ...) of a sequence of len tokens starting at tok0
+// one segment: nc chunks from chunk c0 on of a sequence of len tokens from token tok0 on
 struct Span {
   int64_t tok0;
   int len, seq, c0, nc;
@@ -124,48 +133,48 @@ __device__ __forceinline__ void seq_bounds(const int32_t* off, int s, int64_t T,
   o1 = min(max(off[s + 1], o0), t);
 }
 
-__device__ __forceinline__ int seg_count(int len, int seg_chunks) {
+__device__ __forceinline__ int segment_count(int len, int chunks) {
   const int nch = (len + LC - 1) / LC;
-  return max(1, (nch + seg_chunks - 1) / seg_chunks);
+  return max(1, (nch + chunks - 1) / chunks);
 }
 
-__device__ __forceinline__ void cut_span(int k, int ns, int seg_chunks, Span& sp) {
+__device__ __forceinline__ void cut_span(const Cut& c, int k, int n, Span& sp) {
   const int nch = (sp.len + LC - 1) / LC;
-  sp.c0 = k * seg_chunks;
-  sp.nc = min(seg_chunks, nch - sp.c0);
+  sp.c0 = k * c.chunks;
+  sp.nc = min(c.chunks, nch - sp.c0);
   sp.first = k == 0;
-  sp.last = k == ns - 1;
+  sp.last = k == n - 1;
 }
 
-// the segment of index seg; false: there are fewer (packed sequences: the grid is an upper bound)
-__device__ __forceinline__ bool find_segment(const int32_t* off, int n_seq, int64_t T, int seg_chunks,
-                                             int segs_per_seq, int seg, Span& sp) {
-  if (!off) {
-    sp.seq = seg / segs_per_seq;
+// the segment of index seg; false: there are fewer (packed sequences: the grid is an upper
+// bound), or offsets out of order make more than there can be
+__device__ __forceinline__ bool find_segment(const Cut& c, int seg, Span& sp) {
+  if (!c.offsets) {
+    sp.seq = seg / c.segments;
     sp.tok0 = 0;
-    sp.len = (int)T;
-    cut_span(seg % segs_per_seq, segs_per_seq, seg_chunks, sp);
+    sp.len = (int)c.T;
+    cut_span(c, seg % c.segments, c.segments, sp);
     return true;
   }
   int base = 0;
-  for (int s0 = 0; s0 < n_seq; s0 += WAVE) {
+  for (int s0 = 0; s0 < c.n_seq; s0 += WAVE) {
     const int s = s0 + lane_id();
     int o0 = 0, o1 = 0, n = 0;
-    if (s < n_seq) {
-      seq_bounds(off, s, T, o0, o1);
-      n = seg_count(o1 - o0, seg_chunks);
+    if (s < c.n_seq) {
+      seq_bounds(c.offsets, s, c.T, o0, o1);
+      n = segment_count(o1 - o0, c.chunks);
     }
     const int inc = wave_scan_int(n);
     const uint64_t m = __builtin_amdgcn_ballot_w64(base + inc > seg);
     if (m) {
       const int src = __builtin_ctzll(m);
       const int a0 = __builtin_amdgcn_readlane(o0, src), a1 = __builtin_amdgcn_readlane(o1, src);
-      const int ns = __builtin_amdgcn_readlane(n, src), i1 = __builtin_amdgcn_readlane(inc, src);
+      const int ns = __builtin_amdgcn_readlane(n, src), end = base + __builtin_amdgcn_readlane(inc, src);
       sp.seq = s0 + src;
       sp.tok0 = a0;
       sp.len = a1 - a0;
-      cut_span(seg - (base + i1 - ns), ns, seg_chunks, sp);
-      return true;
+      cut_span(c, seg - (end - ns), ns, sp);
+      return end <= c.n_seg;
     }
     base += __builtin_amdgcn_readlane(inc, WAVE - 1);
   }
@@ -173,25 +182,24 @@ __device__ __forceinline__ bool find_segment(const int32_t* off, int n_seq, int6
 }
 
 // index of a sequence's first segment, and how many it has
-__device__ __forceinline__ int first_segment(const int32_t* off, int64_t T, int seg_chunks, int segs_per_seq,
-                                             int seq, int& ns) {
-  if (!off) {
-    ns = segs_per_seq;
-    return seq * segs_per_seq;
+__device__ __forceinline__ int first_segment(const Cut& c, int seq, int& ns) {
+  if (!c.offsets) {
+    ns = c.segments;
+    return seq * c.segments;
   }
   int base = 0;
   for (int s0 = 0; s0 < seq; s0 += WAVE) {
     const int s = s0 + lane_id();
     int n = 0, o0, o1;
     if (s < seq) {
-      seq_bounds(off, s, T, o0, o1);
-      n = seg_count(o1 - o0, seg_chunks);
+      seq_bounds(c.offsets, s, c.T, o0, o1);
+      n = segment_count(o1 - o0, c.chunks);
     }
     base += __builtin_amdgcn_readlane(wave_scan_int(n), WAVE - 1);
   }
   int o0, o1;
-  seq_bounds(off, seq, T, o0, o1);
-  ns = seg_count(o1 - o0, seg_chunks);
+  seq_bounds(c.offsets, seq, c.T, o0, o1);
+  ns = segment_count(o1 - o0, c.chunks);
   return base;
 }
 
@@ -303,37 +311,44 @@ __device__ __forceinline__ void lds_handover() {
 // waves of a workgroup of W columns: W / 16 column waves, two that form w (a . b) (with
 // outputs), one for the decay factors, one for the loads
 constexpr int scan_waves(int W, bool out) { return W / 16 + (out ? 4 : 2); }
+// waves a SIMD has to hold: those of one workgroup, of two without outputs
+constexpr int scan_per_simd(int W, bool out) { return (scan_waves(W, out) * (out ? 1 : 2) + 3) / 4; }
 
 template <int DK, int W, bool REV, bool OUT, int PARTS, bool DOTS, class TO>
-__global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, 1) void lin_scan_kernel(ScanArgs A) {
-  __shared__ LinRows<DK> rows_a[OUT ? 2 : 1], rows_b[2];
-  __shared__ LinRows<W> rows_c[2], rows_w[DOTS ? 2 : 1];
+__global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) void lin_scan_kernel(ScanArgs A) {
+  // slots of the rows: where one part of everything leaves the room, two chunks are under way
+  // beside the one in use
+  constexpr int RING = 2;
+  __shared__ LinRows<DK> rows_a[OUT ? RING : 1], rows_b[RING];
+  __shared__ LinRows<W> rows_c[RING], rows_w[DOTS ? RING : 1];
   __shared__ LinGates gates[2];
   __shared__ bf16x8 weights[OUT ? PARTS : 1][LNT][2][WAVE];  // w (a . b) as operands: [part][row tile][32-wide step]
   __shared__ float dot_part[DOTS ? W / 16 : 1][LC];
   constexpr int COLS = W / 16, NP = DK / 32;
   constexpr int W_GATES = COLS + (OUT ? 2 : 0), W_ROWS = W_GATES + 1;
 
-  // workgroup -> (segment, head, slice): the slices of a head, and the heads that share rows,
-  // are consecutive indices within one XCD (workgroups are dealt round-robin over the 8 XCDs)
+  // workgroup -> (segment, head, slice).  Workgroups are dealt round-robin over the 8 XCDs;
+  // those that share rows (the slices of a head, the heads of a group) come one after another
+  // on one XCD, so that its L2 has the rows once, and such families alternate between XCDs, so
+  // that long and short segments mix.
   const int n_slices = A.dc / W;
-  const int total = A.n_seg * A.H * n_slices;
-  const int per = (total + 7) / 8;
-  const int idx = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
-  if (idx >= total) return;
+  const int family = n_slices * (A.group_a > A.group_c ? A.group_a : A.group_c);
+  const int turn = (int)(blockIdx.x / 8);
+  const int idx = (turn / family * 8 + (int)(blockIdx.x % 8)) * family + turn % family;
+  if (idx >= A.cut.n_seg * A.H * n_slices) return;
   const int slice = idx % n_slices, head = (idx / n_slices) % A.H, seg = idx / (n_slices * A.H);
   Span sp;
-  if (!find_segment(A.offsets, A.n_seq, A.T, A.seg_chunks, A.segs_per_seq, seg, sp)) return;
-  if (!OUT && A.skip_end && (REV ? sp.first : sp.last)) return;
+  if (!find_segment(A.cut, seg, sp)) return;
+  if (!OUT && A.skip && (REV ? sp.first : sp.last)) return;
 
   const int wave = uniform(threadIdx.x / WAVE);
   const int l = lane_id(), g = l >> 4, c = l & 15;
   const int n = sp.nc;
   // first row of the sequence in each tensor ([B][heads][T][.], or [heads][T][.] packed)
-  const int64_t batch = A.offsets ? 0 : sp.seq;
+  const int64_t batch = A.cut.offsets ? 0 : sp.seq;
   auto row_of = [&](int group) {
     const int heads = A.H / group;
-    return (batch * heads + head / group) * A.T + sp.tok0;
+    return (batch * heads + head / group) * A.cut.T + sp.tok0;
   };
   // chunk j of the scan: its first token, clamped to the segment, and the rows it has
   auto token_of = [&](int j) {
@@ -357,7 +372,7 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, 1) void lin_scan_kernel(
       to = A.slot + ((int64_t)seg * A.H + head) * head_state;
     } else {
       if (!(REV ? sp.last : sp.first))
-        from = A.slot + ((int64_t)(REV ? min(seg + 1, A.n_seg - 1) : seg - 1) * A.H + head) * head_state;
+        from = A.slot + ((int64_t)(REV ? seg + 1 : seg - 1) * A.H + head) * head_state;
       else if (A.init)
         from = A.init + ((int64_t)sp.seq * A.H + head) * head_state;
       if ((REV ? sp.first : sp.last) && A.fin) to = A.fin + ((int64_t)sp.seq * A.H + head) * head_state;
@@ -381,14 +396,15 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, 1) void lin_scan_kernel(
       const int w_at = LinRows<W>::at(c, 16 * wave + 4 * g);
       const int ooff = (c * A.dc + slice * W + 16 * wave + 4 * g) * (int)sizeof(TO);
       lds_handover();
+      int slot = 0;
       for (int it = 0; it < n; ++it) {
         const LinGates& GT = gates[it & 1];
-        const __bf16* bs = rows_b[it & 1].v;
-        const __bf16* cs = rows_c[it & 1].v;
+        const __bf16* bs = rows_b[slot].v;
+        const __bf16* cs = rows_c[slot].v;
         // a X: lane (g, c) holds row 16I + c, columns 4g + r
         f32x4 o[LNT];
         if constexpr (OUT) {
-          const __bf16* as = rows_a[it & 1].v;
+          const __bf16* as = rows_a[slot].v;
 #pragma unroll
           for (int I = 0; I < LNT; ++I) o[I] = zero4();
 #pragma unroll
@@ -442,7 +458,7 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, 1) void lin_scan_kernel(
 #pragma unroll
           for (int I = 0; I < LNT; ++I) {
             if constexpr (DOTS) {
-              const f32x4 w = unpack4(*reinterpret_cast<const bf16x4*>(rows_w[it & 1].v + w_at + 16 * I * W));
+              const f32x4 w = unpack4(*reinterpret_cast<const bf16x4*>(rows_w[slot].v + w_at + 16 * I * W));
               float s = 0.f, s0, s1;
 #pragma unroll
               for (int q = 0; q < 4; ++q) s = fmaf(w[q], o[I][q], s);
@@ -457,6 +473,7 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, 1) void lin_scan_kernel(
               store16b(r, ooff + 16 * I * A.dc * 4, __builtin_bit_cast(u32x4, o[I]));
           }
         }
+        slot = slot == RING - 1 ? 0 : slot + 1;
         lds_handover();
       }
     }
@@ -527,7 +544,7 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, 1) void lin_scan_kernel(
     return;
   }
   if (wave == W_ROWS) {
-    // ---- rows of a, b, c straight into LDS, one chunk ahead ------------------------------
+    // ---- rows of a, b, c straight into LDS, RING - 1 chunks ahead ------------------------
     if (n <= 0) return;
     constexpr int NB = LC * DK * 2 / 1024, NC = LC * W * 2 / 1024;  // 1 KB an instruction
     const int64_t arow = row_of(A.group_a), brow = row_of(A.group_b);
@@ -536,8 +553,7 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, 1) void lin_scan_kernel(
     for (int i = 0; i < NB; ++i) boff[i] = LinRows<DK>::source(i, l, DK);
 #pragma unroll
     for (int i = 0; i < NC; ++i) coff[i] = LinRows<W>::source(i, l, A.dc) + slice * W * 2;
-    auto load = [&](int j) {
-      const int s = j & 1;
+    auto load = [&](int j, int s) {
       const auto rb = chunk_rows(A.b, brow, j, 2 * DK);
 #pragma unroll
       for (int i = 0; i < NB; ++i) load16_lds(rb, rows_b[s].v + 512 * i, boff[i]);
@@ -555,13 +571,22 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, 1) void lin_scan_kernel(
         for (int i = 0; i < NC; ++i) load16_lds(rw, rows_w[s].v + 512 * i, coff[i]);
       }
     };
-    load(0);
-    wait_loads<0>();
+    // all loads but those of the last RING - 2 chunks asked for have arrived
+    constexpr int LATER = (RING - 2) * (NB + NC + (OUT ? NB : 0) + (DOTS ? NC : 0));
+    static_assert(LATER < 64, "the counter of loads in flight");
+    for (int j = 0; j < RING - 1; ++j) load(j, j);
+    wait_loads<LATER>();
     lds_handover();
+    int slot = RING - 1;
     for (int it = 0; it < n; ++it) {
-      if (it + 1 < n) load(it + 1);
+      const bool more = it + RING - 1 < n;
+      if (more) load(it + RING - 1, slot);
+      slot = slot == RING - 1 ? 0 : slot + 1;
       if (OUT) lds_handover();
-      wait_loads<0>();
+      if (more)
+        wait_loads<LATER>();
+      else
+        wait_loads<0>();
       lds_handover();
     }
     return;
@@ -577,10 +602,11 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, 1) void lin_scan_kernel(
 #pragma unroll
       for (int p = 0; p < NP; ++p) row_at[p] = LinRows<DK>::at(c, 32 * p + 8 * g);
       lds_handover();
+      int slot = 0;
       for (int it = 0; it < n; ++it) {
         const LinGates& GT = gates[it & 1];
-        const __bf16* as = rows_a[it & 1].v;
-        const __bf16* bs = rows_b[it & 1].v;
+        const __bf16* as = rows_a[slot].v;
+        const __bf16* bs = rows_b[slot].v;
         // P_ij = w_ij (a_i . b_j): lane (g, c) holds row i = 16I + c, columns 16J + 4g + r
         f32x4 P[2][LNT];
         bf16x8 af[2][NP];
@@ -632,6 +658,7 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, 1) void lin_scan_kernel(
             for (int k = 0; k < PARTS; ++k) weights[k][I][p][l] = s[k];
           }
         }
+        slot = slot == RING - 1 ? 0 : slot + 1;
         lds_handover();
         lds_handover();
       }
@@ -644,18 +671,17 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, 1) void lin_scan_kernel(
   }
 }
 
-// The segments' own states joined in order: slot[k] becomes the state after segment k
-// (before it, REV), from the states given per sequence.  One thread per four state values.
+// The segments' own states joined in order: slot[k] becomes the state after segment k (before
+// it, REV), from the states given per sequence.  One thread per four state values.
 template <bool REV>
-__global__ __launch_bounds__(256) void lin_join_kernel(float* slot, const float* slot_decay, const float* init,
-                                                       const int32_t* offsets, int64_t T, int n_seg, int H, int size,
-                                                       int seg_chunks, int segs_per_seq, int skip_end) {
+__global__ __launch_bounds__(256) void lin_join_kernel(float* slot, const float* slot_decay, const float* init, Cut cut,
+                                                       int H, int size, int skip) {
   const int per = (size / 4 + 255) / 256;  // workgroups of one state
   const int head = (int)(blockIdx.x / per) % H, seq = (int)(blockIdx.x / per) / H;
   int ns;
-  const int s0 = first_segment(offsets, T, seg_chunks, segs_per_seq, seq, ns);
-  if (s0 + ns > n_seg) return;  // offsets out of order: more segments than there can be
-  const int n = ns - skip_end;
+  const int s0 = first_segment(cut, seq, ns);
+  if (s0 + ns > cut.n_seg) return;  // offsets out of order: more segments than there can be
+  const int n = ns - skip;
   const int e = 4 * (int)((blockIdx.x % per) * 256 + threadIdx.x);
   if (e >= size) return;
   f32x4 x = init ? *reinterpret_cast<const f32x4*>(init + ((int64_t)seq * H + head) * size + e) : zero4();
@@ -686,14 +712,14 @@ __global__ __launch_bounds__(256) void lin_join_kernel(float* slot, const float*
 // sum_{s>=t} (q_s . dq_s - k_s . dk_s), the sums in fp64.  Per-head decays: the segment's sum.
 __global__ __launch_bounds__(256) void lin_dgate_kernel(const float* dot_q, const float* dot_k, int n_dots,
                                                         const float* slot_s, const float* slot_d, const float* dS,
-                                                        float* dg, double* dg_seg, const int32_t* offsets, int64_t T,
-                                                        int64_t heads_T, int n_seq, int n_seg, int H, int size,
-                                                        int seg_chunks, int segs_per_seq) {
+                                                        float* dg, double* dg_seg, Cut cut, int64_t heads_T, int H,
+                                                        int size) {
   __shared__ double red[4];
-  const int seg = (int)blockIdx.x / H, head = (int)blockIdx.x % H;
+  const int head = (int)blockIdx.x % H;
   const int l = lane_id(), wave = threadIdx.x / WAVE;
   Span sp;
-  if (!find_segment(offsets, n_seq, T, seg_chunks, segs_per_seq, seg, sp)) return;
+  const int64_t seg = blockIdx.x / H;
+  if (!find_segment(cut, (int)seg, sp)) return;
   auto block_sum = [&](double x) {
 #pragma unroll
     for (int d = 1; d < WAVE; d <<= 1) x += __shfl_xor(x, d);
@@ -704,7 +730,7 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(const float* dot_q, cons
   };
   // thread i holds tokens t1 - 1 - i - 256 k: all are asked for before anything is summed
   constexpr int RUNS = (int)BWD_SEG_CHUNKS * LC / 256;
-  const int64_t row0 = ((offsets ? 0 : (int64_t)sp.seq * H) + head) * T + sp.tok0;
+  const int64_t row0 = ((cut.offsets ? 0 : (int64_t)sp.seq * H) + head) * cut.T + sp.tok0;
   const int t0 = sp.c0 * LC, t1 = min(sp.len, (sp.c0 + sp.nc) * LC);
   float rq[RUNS][2], rk[RUNS][2];
 #pragma unroll
@@ -719,9 +745,9 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(const float* dot_q, cons
   // the states at the segment's end; none given there: their product is zero
   double run = 0.0;
   const float* D = sp.last ? (dS ? dS + ((int64_t)sp.seq * H + head) * size : nullptr)
-                           : slot_d + ((int64_t)(seg + 1) * H + head) * size;
-  if (D && seg + (sp.last ? 0 : 1) < n_seg) {
-    const float* S = slot_s + ((int64_t)seg * H + head) * size;
+                           : slot_d + ((seg + 1) * H + head) * size;
+  if (D) {
+    const float* S = slot_s + (seg * H + head) * size;
     double x = 0.0;
 #pragma unroll 4
     for (int e = 4 * (int)threadIdx.x; e < size; e += 1024) {
@@ -752,16 +778,14 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(const float* dot_q, cons
   }
   if (dg_seg) {
     sum = block_sum(sum);
-    if (threadIdx.x == 0) dg_seg[(int64_t)seg * H + head] = sum;
+    if (threadIdx.x == 0) dg_seg[seg * H + head] = sum;
   }
 }
 
 // per-head decays: the segments' sums in order
-__global__ __launch_bounds__(64) void lin_dgate_head_kernel(const double* dg_seg, float* dg, const int32_t* offsets,
-                                                            int64_t T, int n_seq, int n_seg, int H, int seg_chunks,
-                                                            int segs_per_seq) {
+__global__ __launch_bounds__(64) void lin_dgate_head_kernel(const double* dg_seg, float* dg, Cut cut, int H) {
   int ns;
-  const int n = min(n_seg, first_segment(offsets, T, seg_chunks, segs_per_seq, n_seq - 1, ns) + ns);
+  const int n = min(cut.n_seg, first_segment(cut, cut.n_seq - 1, ns) + ns);
   double x = 0.0;
   for (int s = lane_id(); s < n; s += WAVE) x += dg_seg[(int64_t)s * H + blockIdx.x];
 #pragma unroll
@@ -793,66 +817,99 @@ namespace {
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// columns of c per workgroup: the more, the fewer times w (a . b) is formed
-int scan_width(int dc) { return dc % 128 == 0 ? 128 : dc % 64 == 0 ? 64 : 32; }
-
-// segments of a call and where its workspace holds what
+// how a call is cut and where its workspace holds what
 struct LinPlan {
-  int seg_chunks, segs_per_seq;
-  int64_t n_seg;
-  bool split;
+  Cut cut;
+  int width;   // columns of c per workgroup, of d_v
+  bool ahead;  // the segments' states are formed ahead
   size_t slot_s, slot_d, decay_s, decay_d, dot_q, dot_k, dg_seg, part_q, part_k, bytes;
 };
 
+bool fits(int d, int width) { return d % width == 0; }
+// of d_k in the backward pass (64 or 128)
+int grad_width(int d) { return d == 128 ? 128 : 64; }
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Microseconds of one launch, after whole launches at d = 128: a workgroup of 128 / 64 / 32
+// columns takes 3.0 / 2.3 / 2.05 a chunk with outputs (one workgroup a CU) and 1.7 / 1.3 / 1.1
+// without (two), starts and ends in 8, and memory gives 4.5 MB a microsecond.
+double scan_cost(const LinLaunch& p, int width, int64_t groups, int64_t chunks, bool out, double bytes) {
+  const double chunk = (out ? (width == 128 ? 3.0 : width == 64 ? 2.3 : 2.05)
+                            : (width == 128 ? 1.7 : width == 64 ? 1.3 : 1.1)) * (p.d_k == 128 ? 1.0 : 0.7);
+  const double work = (double)ceil_div(groups, out ? 256 : 512) * ((double)chunks * chunk + 8.0);
+  const double memory = bytes / 4.5e6 + 6.0;
+  return work > memory ? work : memory;
+}
 
 LinPlan make_plan(const LinLaunch& p, bool bwd) {
   LinPlan q{};
-  const int64_t nch = (p.T + LC - 1) / LC;
-  const int64_t all = p.offsets ? nch + p.n_seq : nch * p.n_seq;  // chunks, at most
-  const int64_t items = (int64_t)p.H * (p.d_v / scan_width(p.d_v));  // workgroups per segment
-  // Segment length by what the launches cost in chunks: a round of outputs has a workgroup on
-  // each of 256 CUs; a segment's own state takes about half of that with two on each; the
-  // launches and the joining add a few.
-  int64_t seg = nch > 0 ? nch : 1, best = INT64_MAX;
-  const int64_t longest = nch > 0 ? nch : 1;
-  for (int64_t ns = 1; ns <= 256 && ns <= longest; ++ns) {
-    const int64_t len = (longest + ns - 1) / ns;
-    const int64_t n = p.offsets ? (all + len - 1) / len : p.n_seq * ((longest + len - 1) / len);
-    const int64_t rounds = (n * items + 255) / 256;
-    const int64_t before = ((n - (p.offsets ? 1 : p.n_seq)) * items + 511) / 512;
-    const int64_t cost = 4 * rounds * len + (ns > 1 ? 2 * before * len + 20 : 0);
-    if (cost < best) {
-      best = cost;
-      seg = len;
-    }
+  const int64_t nch = ceil_div(p.T, LC), longest = nch > 0 ? nch : 1;
+  const int64_t all = p.offsets ? nch + p.n_seq : longest * p.n_seq;  // chunks, at most
+  q.width = bwd ? grad_width(p.d_v) : fits(p.d_v, 128) ? 128 : fits(p.d_v, 64) ? 64 : 32;
+  int64_t chunks = longest;
+  if (bwd) {
+    // segments bound the sums of dg; shorter ones where the workgroups would be too few
+    if (chunks > BWD_SEG_CHUNKS) chunks = BWD_SEG_CHUNKS;
+    const int64_t items = (int64_t)p.H * (p.d_v / q.width);
+    while (chunks > 4 && ceil_div(all, chunks) * items < 256) chunks = (chunks + 1) / 2;
+  } else if (longest > 4) {
+    // Whole sequences, or segments that give every CU one to four workgroups: their own states
+    // cost another reading of K and V, and the launches and the joining some more.  B4 H16
+    // T8192 d128: four segments a sequence 181 us, eight 203, whole sequences in four slices
+    // of 32 columns 262; 128 heads of 4096: two slices 151, two segments about 200.
+    const double rows = (double)(p.offsets ? 1 : p.n_seq) * (double)p.T;
+    const double bytes = rows * 2.0 * ((double)p.H_qk * p.d_k + (double)p.H * p.d_v);  // K and V
+    const double state = 4.0 * p.H * p.d_k * p.d_v;
+    const int64_t seqs = p.offsets ? 1 : p.n_seq;  // packed: one may hold nearly all tokens
+    double best = 1e300;
+    const int widest = q.width;
+    for (int w = widest; w >= 32; w /= 2)
+      for (int rounds = 0; rounds <= 4; ++rounds) {
+        const int64_t items = (int64_t)p.H * (p.d_v / w);
+        int64_t len = rounds ? ceil_div(all * items, 256 * rounds) : longest;
+        len = len < 4 ? 4 : len > longest ? longest : len;
+        const int64_t per = ceil_div(longest, len), n = p.offsets ? ceil_div(all, len) : p.n_seq * per;
+        double cost = scan_cost(p, w, n * items, len, true, 2.0 * bytes);
+        if (per > 1)
+          cost += scan_cost(p, w, (n - seqs) * items, len, false, bytes * (double)(per - 1) / (double)per) + 8.0 +
+                  3.0 * (double)n * state / 4e6;
+        if (cost < best) {
+          best = cost;
+          q.width = w;
+          chunks = len;
+        }
+      }
   }
-  if (bwd && seg > BWD_SEG_CHUNKS) seg = BWD_SEG_CHUNKS;
-  q.seg_chunks = (int)seg;
-  const int64_t per = nch > 0 ? (nch + seg - 1) / seg : 1;
-  q.segs_per_seq = (int)per;
-  q.n_seg = p.offsets ? nch / seg + p.n_seq : per * p.n_seq;
-  q.split = per > 1;
+  q.cut.offsets = p.offsets;
+  q.cut.T = p.T;
+  q.cut.n_seq = p.n_seq;
+  q.cut.chunks = (int)chunks;
+  q.cut.segments = (int)ceil_div(longest, chunks);
+  // packed: sum over sequences of max(1, ceil(len / (64 chunks))) <= T / (64 chunks) + sequences
+  q.cut.n_seg = (int)(p.offsets ? nch / chunks + p.n_seq : (int64_t)q.cut.segments * p.n_seq);
+  q.ahead = q.cut.segments > 1;
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t x = at;
     at += up256(n);
     return x;
   };
-  const size_t state = (size_t)p.d_k * p.d_v * 4, sh = (size_t)q.n_seg * p.H;
-  const size_t rows = (size_t)(p.offsets ? 1 : p.n_seq) * p.H * p.T;
-  if (q.split || bwd) {
-    q.slot_s = take(sh * state);
+  const size_t one = (size_t)p.d_k * p.d_v * 4, sh = (size_t)q.cut.n_seg * p.H;
+  const size_t tokens = (size_t)(p.offsets ? 1 : p.n_seq) * p.H * p.T;
+  if (q.ahead || bwd) {
+    q.slot_s = take(sh * one);
     q.decay_s = take(sh * 4);
   }
   if (bwd) {
-    q.slot_d = take(sh * state);
+    q.slot_d = take(sh * one);
     q.decay_d = take(sh * 4);
-    q.dot_q = take(rows * (p.d_k / scan_width(p.d_k)) * 4);
-    q.dot_k = take(rows * (p.d_k / scan_width(p.d_k)) * 4);
+    q.dot_q = take(tokens * (p.d_k / grad_width(p.d_k)) * 4);
+    q.dot_k = take(tokens * (p.d_k / grad_width(p.d_k)) * 4);
     if (p.g_per_head) q.dg_seg = take(sh * 8);
     if (p.H != p.H_qk) {
-      q.part_q = take(rows * p.d_k * 4);
-      q.part_k = take(rows * p.d_k * 4);
+      q.part_q = take(tokens * p.d_k * 4);
+      q.part_k = take(tokens * p.d_k * 4);
     }
   }
   q.bytes = at;
@@ -860,10 +917,10 @@ LinPlan make_plan(const LinLaunch& p, bool bwd) {
 }
 
 template <bool REV, bool OUT, int PARTS, bool DOTS, class TO>
-int scan(int dk, const ScanArgs& a, hipStream_t s) {
-  const int width = scan_width(a.dc);
-  const int64_t total = (int64_t)a.n_seg * a.H * (a.dc / width);
-  const dim3 grid((unsigned)(8 * ((total + 7) / 8)));
+int scan(int dk, int width, const ScanArgs& a, hipStream_t s) {
+  const int64_t family = (int64_t)(a.dc / width) * (a.group_a > a.group_c ? a.group_a : a.group_c);
+  const int64_t total = (int64_t)a.cut.n_seg * a.H * (a.dc / width);
+  const dim3 grid((unsigned)(8 * family * ceil_div(total, 8 * family)));
   auto go = [&](auto d, auto w) {
     hipLaunchKernelGGL((lin_scan_kernel<d.value, w.value, REV, OUT, PARTS, DOTS, TO>), grid,
                        dim3(scan_waves(w.value, OUT) * WAVE), 0, s, a);
@@ -885,28 +942,22 @@ int scan(int dk, const ScanArgs& a, hipStream_t s) {
 ScanArgs base_args(const LinLaunch& p, const LinPlan& q) {
   ScanArgs a{};
   a.g = p.g;
-  a.offsets = p.offsets;
-  a.T = p.T;
+  a.cut = q.cut;
   a.heads_T = (int64_t)(p.offsets ? 1 : p.n_seq) * p.H * p.T;
-  a.n_seq = p.n_seq;
   a.H = p.H;
-  a.seg_chunks = q.seg_chunks;
-  a.n_seg = (int)q.n_seg;
-  a.segs_per_seq = q.segs_per_seq;
+  a.group_a = a.group_b = a.group_c = 1;
   a.g_per_head = p.g_per_head;
   return a;
 }
 
 void join(bool rev, float* slot, const float* decay, const float* init, const LinLaunch& p, const LinPlan& q,
-          int skip_end, hipStream_t s) {
+          int skip, hipStream_t s) {
   const int size = p.d_k * p.d_v;
   const dim3 grid((unsigned)((size / 4 + 255) / 256 * p.H * p.n_seq)), block(256);
   if (rev)
-    hipLaunchKernelGGL((lin_join_kernel<true>), grid, block, 0, s, slot, decay, init, p.offsets, p.T, (int)q.n_seg,
-                       p.H, size, q.seg_chunks, q.segs_per_seq, skip_end);
+    hipLaunchKernelGGL((lin_join_kernel<true>), grid, block, 0, s, slot, decay, init, q.cut, p.H, size, skip);
   else
-    hipLaunchKernelGGL((lin_join_kernel<false>), grid, block, 0, s, slot, decay, init, p.offsets, p.T, (int)q.n_seg,
-                       p.H, size, q.seg_chunks, q.segs_per_seq, skip_end);
+    hipLaunchKernelGGL((lin_join_kernel<false>), grid, block, 0, s, slot, decay, init, q.cut, p.H, size, skip);
 }
 
 const __bf16* bf(const void* p) { return reinterpret_cast<const __bf16*>(p); }
@@ -918,19 +969,18 @@ size_t lin_workspace(const LinLaunch& p, bool bwd) { return make_plan(p, bwd).by
 bool lin_grid_ok(const LinLaunch& p, bool bwd) {
   const LinPlan q = make_plan(p, bwd);
   const int64_t cols = p.d_k > p.d_v ? p.d_k : p.d_v;
-  return q.n_seg * p.H * (cols / 32) < ((int64_t)1 << 31) - 8;
+  // with the last round of families filled up
+  return ((int64_t)q.cut.n_seg + 8) * p.H * (cols / 32) < ((int64_t)1 << 31);
 }
 
 int launch_lin_fwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   const LinPlan q = make_plan(p, false);
   char* ws = reinterpret_cast<char*>(workspace);
-  const int group = p.H / p.H_qk;
   ScanArgs a = base_args(p, q);
   a.a = bf(p.Q);
   a.b = bf(p.K);
   a.c = bf(p.V);
-  a.group_a = a.group_b = group;
-  a.group_c = 1;
+  a.group_a = a.group_b = p.H / p.H_qk;
   a.dc = p.d_v;
   a.st_row = p.d_v;
   a.st_col = 1;
@@ -939,69 +989,74 @@ int launch_lin_fwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   a.out = p.O;
   a.s_intra = a.s_inter = p.scale;
   a.s_state = 1.f;
-  if (q.split) {
+  if (q.ahead) {
     a.slot = reinterpret_cast<float*>(ws + q.slot_s);
     a.slot_decay = reinterpret_cast<float*>(ws + q.decay_s);
-    a.skip_end = 1;
-    int rc = scan<false, false, 1, false, float>(p.d_k, a, s);
+    a.skip = 1;
+    const int rc = scan<false, false, 1, false, float>(p.d_k, q.width, a, s);
     if (rc) return rc;
     join(false, a.slot, a.slot_decay, p.S0, p, q, 1, s);
   }
-  return p.o_bf16 ? scan<false, true, 1, false, __bf16>(p.d_k, a, s) : scan<false, true, 3, false, float>(p.d_k, a, s);
+  // a bf16 output is formed with its fp32 factors as one bf16 part: each term is rounded once
+  // more, together as much as the output's own rounding; an fp32 output with three
+  return p.o_bf16 ? scan<false, true, 1, false, __bf16>(p.d_k, q.width, a, s)
+                  : scan<false, true, 3, false, float>(p.d_k, q.width, a, s);
 }
 
 int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   const LinPlan q = make_plan(p, true);
   char* ws = reinterpret_cast<char*>(workspace);
   const int group = p.H / p.H_qk;
-  const int end = p.dS != nullptr && p.dg != nullptr;  // <dS, S> at the sequences' ends is wanted
+  const bool end = p.dS != nullptr && p.dg != nullptr;  // <dS, S> at the sequences' ends is wanted
+  const int wk = grad_width(p.d_k);
   float* slot_s = reinterpret_cast<float*>(ws + q.slot_s);
   float* slot_d = reinterpret_cast<float*>(ws + q.slot_d);
-  ScanArgs f = base_args(p, q), r;
-  f.st_row = p.d_v;
-  f.st_col = 1;
-  r = f;
-  // states before the segments, and gradients of the states after them
-  f.b = bf(p.K);
-  f.c = bf(p.V);
-  f.a = f.b;
-  f.group_a = f.group_b = group;
-  f.group_c = 1;
-  f.dc = p.d_v;
-  f.s_state = 1.f;
-  f.slot = slot_s;
-  f.slot_decay = reinterpret_cast<float*>(ws + q.decay_s);
-  f.skip_end = !end;
   int rc = 0;
-  if (q.split || end) {
-    rc = scan<false, false, 1, false, float>(p.d_k, f, s);
+  // states after the segments
+  if (q.ahead || end) {
+    ScanArgs f = base_args(p, q);
+    f.b = bf(p.K);
+    f.c = bf(p.V);
+    f.group_a = f.group_b = group;
+    f.dc = p.d_v;
+    f.st_row = p.d_v;
+    f.st_col = 1;
+    f.s_state = 1.f;
+    f.slot = slot_s;
+    f.slot_decay = reinterpret_cast<float*>(ws + q.decay_s);
+    f.skip = end ? 0 : 1;
+    rc = scan<false, false, 1, false, float>(p.d_k, q.width, f, s);
     if (rc) return rc;
-    join(false, f.slot, f.slot_decay, p.S0, p, q, !end, s);
+    join(false, f.slot, f.slot_decay, p.S0, p, q, f.skip, s);
   }
-  r.a = r.b = bf(p.Q);
+  // gradients of the states before the segments; dV, and the gradient of the states given
+  ScanArgs r = base_args(p, q);
+  r.a = bf(p.K);
+  r.b = bf(p.Q);
   r.c = bf(p.dO);
   r.group_a = r.group_b = group;
-  r.group_c = 1;
   r.dc = p.d_v;
+  r.st_row = p.d_v;
+  r.st_col = 1;
   r.s_state = p.scale;
   r.slot = slot_d;
   r.slot_decay = reinterpret_cast<float*>(ws + q.decay_d);
-  r.skip_end = 1;
-  if (q.split) {
-    rc = scan<true, false, 1, false, float>(p.d_k, r, s);
+  r.skip = 1;
+  if (q.ahead) {
+    rc = scan<true, false, 1, false, float>(p.d_k, q.width, r, s);
     if (rc) return rc;
-    join(true, r.slot, r.slot_decay, p.dS, p, q, 1, s);
+    join(true, r.slot, r.slot_decay, p.dS, p, q, r.skip, s);
   }
-  // dV, and the gradient of the states given
-  r.a = bf(p.K);
   r.init = p.dS;
   r.fin = p.dS0;
   r.out = p.dV;
   r.s_intra = p.scale;
   r.s_inter = 1.f;
-  rc = p.grad_bf16 ? scan<true, true, 1, false, __bf16>(p.d_k, r, s) : scan<true, true, 3, false, float>(p.d_k, r, s);
+  rc = p.grad_bf16 ? scan<true, true, 1, false, __bf16>(p.d_k, q.width, r, s)
+                   : scan<true, true, 3, false, float>(p.d_k, q.width, r, s);
   if (rc) return rc;
-  // dK and dQ: the transposed states, contraction over d_v
+  // dK and dQ: the transposed states, contraction over d_v; three parts, as dg is a difference
+  // of their products
   ScanArgs k = base_args(p, q);
   k.st_row = 1;
   k.st_col = p.d_v;
@@ -1009,7 +1064,6 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   k.a = bf(p.V);
   k.b = bf(p.dO);
   k.c = bf(p.Q);
-  k.group_a = k.group_b = 1;
   k.group_c = group;
   k.init = p.dS;
   k.slot = slot_d;
@@ -1019,7 +1073,7 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   const bool part_bf16 = group == 1 && p.grad_bf16;
   k.s_intra = k.s_state = p.scale;
   k.s_inter = 1.f;
-  rc = part_bf16 ? scan<true, true, 3, true, __bf16>(p.d_v, k, s) : scan<true, true, 3, true, float>(p.d_v, k, s);
+  rc = part_bf16 ? scan<true, true, 3, true, __bf16>(p.d_v, wk, k, s) : scan<true, true, 3, true, float>(p.d_v, wk, k, s);
   if (rc) return rc;
   k.a = bf(p.dO);
   k.b = bf(p.V);
@@ -1031,26 +1085,25 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   k.out = group > 1 ? (void*)(ws + q.part_q) : p.dQ;
   k.s_intra = k.s_inter = p.scale;
   k.s_state = 1.f;
-  rc = part_bf16 ? scan<false, true, 3, true, __bf16>(p.d_v, k, s) : scan<false, true, 3, true, float>(p.d_v, k, s);
+  rc = part_bf16 ? scan<false, true, 3, true, __bf16>(p.d_v, wk, k, s)
+                 : scan<false, true, 3, true, float>(p.d_v, wk, k, s);
   if (rc) return rc;
   if (group > 1 && p.T > 0) {
     const int64_t n = (int64_t)(p.offsets ? 1 : p.n_seq) * p.H_qk * p.T * p.d_k;
-    const dim3 grid((unsigned)((n / 4 + 255) / 256)), block(256);
+    const dim3 grid((unsigned)ceil_div(n / 4, 256)), block(256);
     hipLaunchKernelGGL(lin_group_sum_kernel, grid, block, 0, s, reinterpret_cast<const float*>(ws + q.part_k), p.dK,
                        p.grad_bf16, n, p.T * p.d_k, p.d_k, group, p.offsets, p.n_seq);
     hipLaunchKernelGGL(lin_group_sum_kernel, grid, block, 0, s, reinterpret_cast<const float*>(ws + q.part_q), p.dQ,
                        p.grad_bf16, n, p.T * p.d_k, p.d_k, group, p.offsets, p.n_seq);
   }
   if (!p.dg) return 0;
-  const int nsl = p.d_k / scan_width(p.d_k);
   double* dg_seg = p.g_per_head ? reinterpret_cast<double*>(ws + q.dg_seg) : nullptr;
-  hipLaunchKernelGGL(lin_dgate_kernel, dim3((unsigned)(p.H * q.n_seg)), dim3(256), 0, s,
-                     reinterpret_cast<const float*>(ws + q.dot_q), reinterpret_cast<const float*>(ws + q.dot_k), nsl,
-                     slot_s, slot_d, p.dS, p.g_per_head ? nullptr : p.dg, dg_seg, p.offsets, p.T, f.heads_T,
-                     p.n_seq, (int)q.n_seg, p.H, p.d_k * p.d_v, q.seg_chunks, q.segs_per_seq);
+  hipLaunchKernelGGL(lin_dgate_kernel, dim3((unsigned)(p.H * q.cut.n_seg)), dim3(256), 0, s,
+                     reinterpret_cast<const float*>(ws + q.dot_q), reinterpret_cast<const float*>(ws + q.dot_k),
+                     p.d_k / wk, slot_s, slot_d, p.dS, p.g_per_head ? nullptr : p.dg, dg_seg, q.cut, k.heads_T, p.H,
+                     p.d_k * p.d_v);
   if (p.g_per_head)
-    hipLaunchKernelGGL(lin_dgate_head_kernel, dim3((unsigned)p.H), dim3(64), 0, s, dg_seg, p.dg, p.offsets, p.T,
-                       p.n_seq, (int)q.n_seg, p.H, q.seg_chunks, q.segs_per_seq);
+    hipLaunchKernelGGL(lin_dgate_head_kernel, dim3((unsigned)p.H), dim3(64), 0, s, dg_seg, p.dg, q.cut, p.H);
   return 0;
 }
 
