@@ -296,6 +296,23 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// two adjacent 16-column tiles of a row as bf16, 16 contiguous bytes per lane: group g then
+// holds columns 16(g % 2) + 8(g / 2) .. + 7
+__device__ __forceinline__ u32x4 pair_bf16(const f32x4& a0, const f32x4& a1) {
+  const bf16x4 h0 = pack4(a0), h1 = pack4(a1);
+  const u32x2 w0 = __builtin_bit_cast(u32x2, h0), w1 = __builtin_bit_cast(u32x2, h1);
+  u32x4 v;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const unsigned x0 = w0[k], x1 = w1[k];  // vector elements to scalars before any bit cast
+    const auto sw = __builtin_amdgcn_permlane16_swap(x0, x1, false, false);
+    const unsigned y0 = sw[0], y1 = sw[1];
+    v[k] = y0;
+    v[2 + k] = y1;
+  }
+  return v;
+}
+
 // d of the state tile's row 4g + r: two tiles 2p, 2p + 1 of a lane are then the natural-order
 // operand (slot t <-> d = 32p + 8g + t)
 __device__ __forceinline__ int state_dim(int a, int g, int r) { return 32 * (a >> 1) + 8 * g + 4 * (a & 1) + r; }
@@ -308,9 +325,11 @@ __device__ __forceinline__ void lds_handover() {
 
 }  // namespace
 
-// waves of a workgroup of W columns: W / 16 column waves, two that form w (a . b) (with
-// outputs), one for the decay factors, one for the loads
-constexpr int scan_waves(int W, bool out) { return W / 16 + (out ? 4 : 2); }
+// waves of a workgroup of W columns: column waves, two that form w (a . b) (with outputs), one
+// for the decay factors, one for the loads.  A column wave of 32 columns reads the rows of a
+// and b once for both 16-column tiles; below 128 columns the waves would be too few.
+constexpr int scan_tiles(int W) { return W == 128 ? 2 : 1; }
+constexpr int scan_waves(int W, bool out) { return W / (16 * scan_tiles(W)) + (out ? 4 : 2); }
 // waves a SIMD has to hold: those of one workgroup, of two without outputs
 constexpr int scan_per_simd(int W, bool out) { return (scan_waves(W, out) * (out ? 1 : 2) + 3) / 4; }
 
@@ -323,8 +342,8 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
   __shared__ LinRows<W> rows_c[RING], rows_w[DOTS ? RING : 1];
   __shared__ LinGates gates[2];
   __shared__ bf16x8 weights[OUT ? PARTS : 1][LNT][2][WAVE];  // w (a . b) as operands: [part][row tile][32-wide step]
-  __shared__ float dot_part[DOTS ? W / 16 : 1][LC];
-  constexpr int COLS = W / 16, NP = DK / 32;
+  __shared__ float dot_part[DOTS ? W / (16 * scan_tiles(W)) : 1][LC];
+  constexpr int HC = scan_tiles(W), COLS = W / (16 * HC), NP = DK / 32;
   constexpr int W_GATES = COLS + (OUT ? 2 : 0), W_ROWS = W_GATES + 1;
 
   // workgroup -> (segment, head, slice).  Workgroups are dealt round-robin over the 8 XCDs;
@@ -363,9 +382,10 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
   const int64_t crow = row_of(A.group_c), orow = row_of(1);
 
   if (wave < COLS) {
-    // ---- column waves: 16 columns of X, in registers from the segment's start to its end --
+    // ---- column waves: their columns of X, in registers from the segment's start to its end --
     constexpr int NA = DK / 16;  // 16-row state tiles
-    const int64_t col = slice * W + 16 * wave + c;
+    const int col0 = 16 * HC * wave;
+    const int64_t col = slice * W + col0 + c;
     const float* from = nullptr;  // the state this segment starts from (NULL: zeros)
     float* to = nullptr;
     if (!OUT) {
@@ -377,11 +397,14 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
         from = A.init + ((int64_t)sp.seq * A.H + head) * head_state;
       if ((REV ? sp.first : sp.last) && A.fin) to = A.fin + ((int64_t)sp.seq * A.H + head) * head_state;
     }
-    f32x4 X[NA];
+    f32x4 X[HC][NA];
 #pragma unroll
-    for (int t = 0; t < NA; ++t)
+    for (int h = 0; h < HC; ++h)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) X[t][r] = from ? from[state_dim(t, g, r) * A.st_row + col * A.st_col] : 0.f;
+      for (int t = 0; t < NA; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          X[h][t][r] = from ? from[state_dim(t, g, r) * A.st_row + (col + 16 * h) * A.st_col] : 0.f;
     if (n > 0) {
       // rows of a as operands: lane (g, c) reads row 16I + c, 16 bytes at 32p + 8g
       int a_at[NP];
@@ -389,62 +412,80 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
       for (int p = 0; p < NP; ++p) a_at[p] = LinRows<DK>::at(c, 32 * p + 8 * g);
       // transposed rows of b: lane addresses of state tiles (t, t + 1) for even t; of c
       const int tr_row = 4 * g + (c >> 2);
-      int bt_at[NA / 2];
+      int bt_at[NA / 2], ct_at[HC], w_at[HC];
 #pragma unroll
       for (int t = 0; t < NA / 2; ++t) bt_at[t] = LinRows<DK>::at(tr_row, 32 * t + 8 * (c & 3));
-      const int ct_at = LinRows<W>::at(tr_row, 16 * wave + 4 * (c & 3));
-      const int w_at = LinRows<W>::at(c, 16 * wave + 4 * g);
-      const int ooff = (c * A.dc + slice * W + 16 * wave + 4 * g) * (int)sizeof(TO);
+#pragma unroll
+      for (int h = 0; h < HC; ++h) {
+        ct_at[h] = LinRows<W>::at(tr_row, col0 + 16 * h + 4 * (c & 3));
+        w_at[h] = LinRows<W>::at(c, col0 + 16 * h + 4 * g);
+      }
+      constexpr bool PAIR = HC == 2 && sizeof(TO) == 2;  // 16 bytes a lane from two tiles
+      const int ooff = (c * A.dc + slice * W + col0 + (PAIR ? 16 * (g & 1) + 8 * (g >> 1) : 4 * g)) * (int)sizeof(TO);
       lds_handover();
       int slot = 0;
       for (int it = 0; it < n; ++it) {
         const LinGates& GT = gates[it & 1];
         const __bf16* bs = rows_b[slot].v;
         const __bf16* cs = rows_c[slot].v;
-        // a X: lane (g, c) holds row 16I + c, columns 4g + r
-        f32x4 o[LNT];
+        // a X: lane (g, c) holds row 16I + c, columns 4g + r of each tile
+        f32x4 o[HC][LNT];
         if constexpr (OUT) {
           const __bf16* as = rows_a[slot].v;
 #pragma unroll
-          for (int I = 0; I < LNT; ++I) o[I] = zero4();
+          for (int h = 0; h < HC; ++h)
+#pragma unroll
+            for (int I = 0; I < LNT; ++I) o[h][I] = zero4();
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
-            bf16x8 s[PARTS];
-            split<PARTS>(X[2 * p], X[2 * p + 1], s);
+            bf16x8 s[HC][PARTS];
+#pragma unroll
+            for (int h = 0; h < HC; ++h) split<PARTS>(X[h][2 * p], X[h][2 * p + 1], s[h]);
 #pragma unroll
             for (int I = 0; I < LNT; ++I) {
               const bf16x8 af = *reinterpret_cast<const bf16x8*>(as + a_at[p] + 16 * I * DK);
 #pragma unroll
-              for (int k = PARTS - 1; k >= 0; --k) o[I] = mma_bf16(s[k], af, o[I]);
+              for (int h = 0; h < HC; ++h)
+#pragma unroll
+                for (int k = PARTS - 1; k >= 0; --k) o[h][I] = mma_bf16(s[h][k], af, o[h][I]);
             }
           }
         }
         // X <- e^{G_C} X + b^T (col c), col c as three parts
         const float end = GT.end;
-#pragma unroll
-        for (int t = 0; t < NA; ++t) X[t] = X[t] * end;
-        bf16x8 cf[2];
+        bf16x8 cf[HC][2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const bf16x4 c0 = lds_read_tr4(cs + ct_at + 32 * p * W), c1 = lds_read_tr4(cs + ct_at + (32 * p + 16) * W);
-          cf[p] = join8(c0, c1);
           const f32x4 w0 = *reinterpret_cast<const f32x4*>(&GT.col[32 * p + 4 * g]);
           const f32x4 w1 = *reinterpret_cast<const f32x4*>(&GT.col[32 * p + 16 + 4 * g]);
-          const f32x4 y0 = unpack4(c0) * w0, y1 = unpack4(c1) * w1;
-          const float y[8] = {y0[0], y0[1], y0[2], y0[3], y1[0], y1[1], y1[2], y1[3]};
-          bf16x8 u[3];
-          split3_exact(y, u);
+          bf16x8 u[HC][3];
+#pragma unroll
+          for (int h = 0; h < HC; ++h) {
+            const bf16x4 c0 = lds_read_tr4(cs + ct_at[h] + 32 * p * W), c1 = lds_read_tr4(cs + ct_at[h] + (32 * p + 16) * W);
+            cf[h][p] = join8(c0, c1);
+            const f32x4 y0 = unpack4(c0) * w0, y1 = unpack4(c1) * w1;
+            const float y[8] = {y0[0], y0[1], y0[2], y0[3], y1[0], y1[1], y1[2], y1[3]};
+            split3_exact(y, u[h]);
+          }
 #pragma unroll
           for (int t = 0; t < NA; ++t) {
             const __bf16* q = bs + bt_at[t / 2] + 32 * p * DK + 4 * (t & 1);
             const bf16x8 bt = join8(lds_read_tr4(q), lds_read_tr4(q + 16 * DK));
 #pragma unroll
-            for (int k = 2; k >= 0; --k) X[t] = mma_bf16(bt, u[k], X[t]);
+            for (int h = 0; h < HC; ++h) {
+              if (p == 0) X[h][t] = X[h][t] * end;
+#pragma unroll
+              for (int k = 2; k >= 0; --k) X[h][t] = mma_bf16(bt, u[h][k], X[h][t]);
+            }
           }
         }
         if constexpr (OUT) {
 #pragma unroll
-          for (int I = 0; I < LNT; ++I) o[I] = o[I] * GT.row[16 * I + c];
+          for (int I = 0; I < LNT; ++I) {
+            const float rw = GT.row[16 * I + c];
+#pragma unroll
+            for (int h = 0; h < HC; ++h) o[h][I] = o[h][I] * rw;
+          }
           lds_handover();  // the weights are there
 #pragma unroll
           for (int I = 0; I < LNT; ++I)
@@ -452,25 +493,40 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
             for (int p = 0; p < 2; ++p) {
               if (REV ? 2 * p + 1 < I : 2 * p > I) continue;
 #pragma unroll
-              for (int k = PARTS - 1; k >= 0; --k) o[I] = mma_bf16(cf[p], weights[k][I][p][l], o[I]);
+              for (int k = PARTS - 1; k >= 0; --k) {
+                const bf16x8 wf = weights[k][I][p][l];
+#pragma unroll
+                for (int h = 0; h < HC; ++h) o[h][I] = mma_bf16(cf[h][p], wf, o[h][I]);
+              }
             }
           const auto r = chunk_rows(A.out, orow, it, (int)sizeof(TO) * A.dc);  // rows past the end are not stored
 #pragma unroll
           for (int I = 0; I < LNT; ++I) {
             if constexpr (DOTS) {
-              const f32x4 w = unpack4(*reinterpret_cast<const bf16x4*>(rows_w[slot].v + w_at + 16 * I * W));
               float s = 0.f, s0, s1;
 #pragma unroll
-              for (int q = 0; q < 4; ++q) s = fmaf(w[q], o[I][q], s);
+              for (int h = 0; h < HC; ++h) {
+                const f32x4 w = unpack4(*reinterpret_cast<const bf16x4*>(rows_w[slot].v + w_at[h] + 16 * I * W));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) s = fmaf(w[q], o[h][I][q], s);
+              }
               self_swap_f<16>(s, s0, s1);
               s = s0 + s1;
               self_swap_f<32>(s, s0, s1);
               if (g == 0) dot_part[wave][16 * I + c] = s0 + s1;
             }
-            if constexpr (sizeof(TO) == 2)
-              store8b(r, ooff + 16 * I * A.dc * 2, pack4(o[I]));
-            else
-              store16b(r, ooff + 16 * I * A.dc * 4, __builtin_bit_cast(u32x4, o[I]));
+            const int at = ooff + 16 * I * A.dc * (int)sizeof(TO);
+            if constexpr (PAIR) {
+              store16b(r, at, pair_bf16(o[0][I], o[HC - 1][I]));
+            } else {
+#pragma unroll
+              for (int h = 0; h < HC; ++h) {
+                if constexpr (sizeof(TO) == 2)
+                  store8b(r, at + 32 * h, pack4(o[h][I]));
+                else
+                  store16b(r, at + 64 * h, __builtin_bit_cast(u32x4, o[h][I]));
+              }
+            }
           }
         }
         slot = slot == RING - 1 ? 0 : slot + 1;
@@ -479,9 +535,12 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
     }
     if (to) {
 #pragma unroll
-      for (int t = 0; t < NA; ++t)
+      for (int h = 0; h < HC; ++h)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) to[state_dim(t, g, r) * A.st_row + col * A.st_col] = X[t][r];
+        for (int t = 0; t < NA; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            to[state_dim(t, g, r) * A.st_row + (col + 16 * h) * A.st_col] = X[h][t][r];
     }
     return;
   }
