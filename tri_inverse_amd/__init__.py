@@ -486,8 +486,8 @@ def _at(t):
 
 def _arg(t, name, dtypes, shape, dev):
     """A required tensor: on dev (None: any GPU), contiguous, of one of dtypes, of this shape."""
-    if (type(t) is torch.Tensor and t.is_cuda and t.dtype in dtypes and t.shape == shape and t.is_contiguous()
-            and (dev is None or t.device == dev)):
+    if (type(t) is torch.Tensor and t.shape == shape and t.dtype in dtypes and t.is_contiguous()
+            and (t.is_cuda if dev is None else t.get_device() == dev.index)):
         return t
     _dev(t, name, dtypes)
     if t is None:
@@ -499,9 +499,14 @@ def _arg(t, name, dtypes, shape, dev):
     return t
 
 
-def _out(t, name, dtypes, shape, dev, dtype):
-    """An output: the caller's tensor after its checks, or a new one."""
+def _out(t, name, dtypes, shape, dev, dtype, like=None):
+    """An output: the caller's tensor after its checks, or a new one (like: a contiguous tensor of
+    this shape, which makes a new one of the same type cheaper)."""
     if t is None:
+        if dtype not in dtypes:
+            raise TypeError("%s has dtype %s, expected one of %s" % (name, dtype, dtypes))
+        if like is not None and like.dtype is dtype:
+            return torch.empty_like(like)
         return torch.empty(shape, device=dev, dtype=dtype)
     return _arg(t, name, dtypes, shape, dev)
 
@@ -516,7 +521,7 @@ def _scratch(workspace, need, dev):
 
 
 def _lin_shape(Q, K, V, g, scale, offsets, dtypes):
-    """The gdn_lin_shape of a call after the inputs' checks; returns (shape, sequences, device)."""
+    """The gdn_lin_shape of a call after the inputs' checks; returns (shape, the states' shape, device)."""
     if K is None or K.dim() != 4 or V is None or V.dim() != 4:
         raise ValueError("Q and K must be [B, H_qk, T, d_k], V [B, H, T, d_v]")
     B, Hk, T, dk = K.shape
@@ -537,20 +542,13 @@ def _lin_shape(Q, K, V, g, scale, offsets, dtypes):
             raise ValueError("offsets must be [sequences + 1]")
         n = offsets.numel() - 1
         _arg(offsets, "offsets", (torch.int32,), (n + 1,), dev)
-    sh = gdn_lin_shape()
-    sh.T, sh.B, sh.H, sh.H_qk, sh.d_k, sh.d_v = T, n, H, Hk, dk, dv
-    sh.offsets = None if offsets is None else offsets.data_ptr()
-    sh.g_per_head = int(per_head)
-    sh.scale = dk ** -0.5 if scale is None else float(scale)
-    return sh, n, dev
+    sh = gdn_lin_shape(T, _at(offsets), n, H, Hk, dk, dv, per_head, dk ** -0.5 if scale is None else float(scale))
+    return sh, (n, H, dk, dv), dev
 
 
 def _plain_shape(B, H, H_qk, T, d_k, d_v, packed):
-    sh = gdn_lin_shape()
-    sh.T, sh.B, sh.H, sh.H_qk, sh.d_k, sh.d_v = int(T), int(B), int(H), int(H_qk), int(d_k), int(d_v)
-    sh.offsets = 16 if packed else None  # only its presence counts
-    sh.g_per_head, sh.scale = 1, 1.0
-    return sh
+    # of the offsets only their presence counts
+    return gdn_lin_shape(int(T), 16 if packed else None, int(B), int(H), int(H_qk), int(d_k), int(d_v), 1, 1.0)
 
 
 def gdn_lin_chunk_fwd_workspace_bytes(B: int, H: int, T: int, d_k: int, d_v: int, H_qk: int | None = None,
@@ -577,13 +575,12 @@ def gdn_lin_chunk_fwd(Q, K, V, g, scale: float | None = None, S0=None, offsets=N
     T tokens.  S0 [B or n,H,d_k,d_v] fp32 or None (zeros).  Any T.  workspace: a uint8 tensor
     of gdn_lin_chunk_fwd_workspace_bytes(...) bytes, or None to have one allocated here.
     Returns (O [B,H,T,d_v], S_out [B or n,H,d_k,d_v] fp32)."""
-    sh, n, dev = _lin_shape(Q, K, V, g, scale, offsets, _BF16)
-    state = (n, sh.H, sh.d_k, sh.d_v)
+    sh, state, dev = _lin_shape(Q, K, V, g, scale, offsets, _BF16)
     if S0 is not None:
         _arg(S0, "S0", (torch.float32,), state, dev)
     with _scope(dev, stream):
-        O = _out(O, "O", _FLOAT, V.shape, dev, o_dtype)
-        S_out = _out(S_out, "S_out", (torch.float32,), state, dev, torch.float32)
+        O = _out(O, "O", _FLOAT, V.shape, dev, o_dtype, V)
+        S_out = _out(S_out, "S_out", (torch.float32,), state, dev, torch.float32, S0)
         ws, ws_bytes = _scratch(workspace, _lib.gdn_lin_chunk_fwd_workspace_bytes(ctypes.byref(sh)), dev)
         st = _lib.gdn_lin_chunk_fwd(ctypes.byref(sh), _at(Q), _at(K), _at(V), GDN_BF16, _at(g), _at(S0), _at(O),
                                     _TORCH_DTYPE[O.dtype], _at(S_out), _at(ws), ws_bytes, _current(dev))
@@ -596,8 +593,7 @@ def gdn_lin_chunk_bwd(Q, K, V, g, dO, scale: float | None = None, S0=None, dS=No
     """Backward pass of gdn_lin_chunk_fwd from dO [B,H,T,d_v] (bf16) and dS (gradient of
     S_out, or None).  Returns (dQ, dK, dV in grad_dtype, dg fp32 as g or None, dS0 fp32, or
     None without S0)."""
-    sh, n, dev = _lin_shape(Q, K, V, g, scale, offsets, _BF16)
-    state = (n, sh.H, sh.d_k, sh.d_v)
+    sh, state, dev = _lin_shape(Q, K, V, g, scale, offsets, _BF16)
     _arg(dO, "dO", _BF16, V.shape, dev)
     for t, name in ((S0, "S0"), (dS, "dS")):
         if t is not None:
@@ -624,13 +620,12 @@ def gdn_lin_decode(Q, K, V, g, S=None, scale: float | None = None, S_out=None, O
     Q, K [B,H_qk,n,d_k], V [B,H,n,d_v] (bf16 or fp32, one dtype), g [B,H,n] or [H] fp32,
     S [B,H,d_k,d_v] fp32 or None (zeros).  Pass S_out=S to update the state in place.
     Returns (O [B,H,n,d_v], S_out)."""
-    sh, n, dev = _lin_shape(Q, K, V, g, scale, None, _FLOAT)
-    state = (n, sh.H, sh.d_k, sh.d_v)
+    sh, state, dev = _lin_shape(Q, K, V, g, scale, None, _FLOAT)
     if S is not None:
         _arg(S, "S", (torch.float32,), state, dev)
     with _scope(dev, stream):
-        O = _out(O, "O", _FLOAT, V.shape, dev, o_dtype)
-        S_out = _out(S_out, "S_out", (torch.float32,), state, dev, torch.float32)
+        O = _out(O, "O", _FLOAT, V.shape, dev, o_dtype, V)
+        S_out = _out(S_out, "S_out", (torch.float32,), state, dev, torch.float32, S)
         st = _lib.gdn_lin_decode(ctypes.byref(sh), _at(Q), _at(K), _at(V), _TORCH_DTYPE[K.dtype], _at(g), _at(S),
                                  _at(S_out), _at(O), _TORCH_DTYPE[O.dtype], _current(dev))
     _check(st, "gdn_lin_decode")
@@ -716,8 +711,8 @@ def gdn_residual_norm_fwd(X, Y, w_post=None, s=None, alpha: float = 1.0, w_pre=N
     Returns (R, N)."""
     rows, D, dev = _res_args(X, Y, w_post, s, w_pre, "X")
     with _scope(dev, stream):
-        R = _out(R, "R", (X.dtype,), X.shape, dev, X.dtype)
-        N = _out(N, "N", (Y.dtype,), Y.shape, dev, Y.dtype) if want_norm else None
+        R = _out(R, "R", (X.dtype,), X.shape, dev, X.dtype, X)
+        N = _out(N, "N", (Y.dtype,), Y.shape, dev, Y.dtype, Y) if want_norm else None
         st = _lib.gdn_residual_norm_fwd(_at(X), _TORCH_DTYPE[X.dtype], _at(Y), _TORCH_DTYPE[Y.dtype], _at(w_post),
                                         _at(s), float(alpha), _at(w_pre), _at(R), _at(N), rows, D, float(eps),
                                         _current(dev))

@@ -425,6 +425,7 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
       lds_handover();
       int slot = 0;
       for (int it = 0; it < n; ++it) {
+        if constexpr (OUT && PARTS == 1) __builtin_amdgcn_iglp_opt(1);  // interleaves MFMA and VALU: 3 to 8 % less
         const LinGates& GT = gates[it & 1];
         const __bf16* bs = rows_b[slot].v;
         const __bf16* cs = rows_c[slot].v;
