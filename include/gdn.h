@@ -270,8 +270,9 @@ gdn_status gdn_decode(const void* Q, const void* K, const void* V, int32_t qkv_d
  *   [B][H][T][d_v], g [B][H][T] (or [H]).
  * offsets != NULL: B packed sequences in T tokens, sequence s at tokens offsets[s] ..
  *   offsets[s+1] - 1 (DEVICE int32 [B+1], 0 <= offsets[s] <= offsets[s+1] <= T; empty
- *   sequences are valid); Q, K [H_qk][T][d_k], V, O [H][T][d_v], g [H][T] (or [H]).  Rows of
- *   no sequence are neither read into a result nor written.  Offsets that break the rule
+ *   sequences are valid); Q, K [H_qk][T][d_k], V, O [H][T][d_v], g [H][T] (or [H]).  Rows
+ *   before offsets[0] and from offsets[B] on belong to no sequence: they are not read into a
+ *   result, O is not written there, and gradients there are zero.  Offsets that break the rule
  *   are clamped: no access leaves the tensors, the results are unspecified.
  * States are [B][H][d_k][d_v] fp32 either way.  T is any length up to 2^31 - 65; T == 0 and
  * empty sequences return the given states unchanged (or zeros).  g <= 0 is expected, -inf

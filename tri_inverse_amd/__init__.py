@@ -601,10 +601,8 @@ def gdn_lin_chunk_bwd(Q, K, V, g, dO, scale: float | None = None, S0=None, dS=No
     if grad_dtype not in _FLOAT:
         raise TypeError("grad_dtype is %s, expected one of %s" % (grad_dtype, _FLOAT))
     with _scope(dev, stream):
-        # rows of no packed sequence get no gradient
-        new = torch.empty if offsets is None else torch.zeros
-        dQ, dK, dV = (new(t.shape, device=dev, dtype=grad_dtype) for t in (Q, K, V))
-        dg = new(g.shape, device=dev, dtype=torch.float32) if want_dg else None
+        dQ, dK, dV = (torch.empty(t.shape, device=dev, dtype=grad_dtype) for t in (Q, K, V))
+        dg = torch.empty_like(g) if want_dg else None
         dS0 = None if S0 is None else torch.empty(state, device=dev, dtype=torch.float32)
         ws, ws_bytes = _scratch(workspace, _lib.gdn_lin_chunk_bwd_workspace_bytes(ctypes.byref(sh)), dev)
         st = _lib.gdn_lin_chunk_bwd(ctypes.byref(sh), _at(Q), _at(K), _at(V), GDN_BF16, _at(g), _at(S0), _at(dO),

@@ -77,7 +77,6 @@ struct ScanArgs {
   Cut cut;
   int g_per_head;
   int skip;            // without OUT: a sequence's end segment is not wanted
-  int64_t st_row, st_col;  // strides of the states in this scan's (row, column) order
   float s_intra, s_inter, s_state;
 };
 
@@ -397,14 +396,22 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
         from = A.init + ((int64_t)sp.seq * A.H + head) * head_state;
       if ((REV ? sp.first : sp.last) && A.fin) to = A.fin + ((int64_t)sp.seq * A.H + head) * head_state;
     }
+    // states lie [d_k][d_v]: rows of X by columns, or (dQ, dK) columns of X by rows, where a
+    // lane's four rows are 16 contiguous bytes
     f32x4 X[HC][NA];
 #pragma unroll
     for (int h = 0; h < HC; ++h)
 #pragma unroll
-      for (int t = 0; t < NA; ++t)
+      for (int t = 0; t < NA; ++t) {
+        X[h][t] = zero4();
+        if (!from) continue;
+        if constexpr (DOTS) {
+          X[h][t] = *reinterpret_cast<const f32x4*>(from + (col + 16 * h) * DK + state_dim(t, g, 0));
+        } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          X[h][t][r] = from ? from[state_dim(t, g, r) * A.st_row + (col + 16 * h) * A.st_col] : 0.f;
+          for (int r = 0; r < 4; ++r) X[h][t][r] = from[(int64_t)state_dim(t, g, r) * A.dc + col + 16 * h];
+        }
+      }
     if (n > 0) {
       // rows of a as operands: lane (g, c) reads row 16I + c, 16 bytes at 32p + 8g
       int a_at[NP];
@@ -534,14 +541,13 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
         lds_handover();
       }
     }
-    if (to) {
+    if (!DOTS && to) {
 #pragma unroll
       for (int h = 0; h < HC; ++h)
 #pragma unroll
         for (int t = 0; t < NA; ++t)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            to[state_dim(t, g, r) * A.st_row + (col + 16 * h) * A.st_col] = X[h][t][r];
+          for (int r = 0; r < 4; ++r) to[(int64_t)state_dim(t, g, r) * A.dc + col + 16 * h] = X[h][t][r];
     }
     return;
   }
@@ -731,20 +737,25 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
   }
 }
 
-// The segments' own states joined in order: slot[k] becomes the state after segment k (before
-// it, REV), from the states given per sequence.  One thread per four state values.
-template <bool REV>
-__global__ __launch_bounds__(256) void lin_join_kernel(float* slot, const float* slot_decay, const float* init, Cut cut,
-                                                       int H, int size, int skip) {
+// The segments' own states joined in order, from the states given per sequence: slot[k] becomes
+// the state after segment k, or before it (back).  One thread per four state values.
+struct JoinArgs {
+  float* slot;
+  const float* decay;
+  const float* init;
+  int skip, back;
+};
+__global__ __launch_bounds__(256) void lin_join_kernel(JoinArgs a0, JoinArgs a1, Cut cut, int H, int size) {
+  const JoinArgs a = blockIdx.y ? a1 : a0;
   const int per = (size / 4 + 255) / 256;  // workgroups of one state
   const int head = (int)(blockIdx.x / per) % H, seq = (int)(blockIdx.x / per) / H;
   int ns;
   const int s0 = first_segment(cut, seq, ns);
   if (s0 + ns > cut.n_seg) return;  // offsets out of order: more segments than there can be
-  const int n = ns - skip;
+  const int n = ns - a.skip;
   const int e = 4 * (int)((blockIdx.x % per) * 256 + threadIdx.x);
   if (e >= size) return;
-  f32x4 x = init ? *reinterpret_cast<const f32x4*>(init + ((int64_t)seq * H + head) * size + e) : zero4();
+  f32x4 x = a.init ? *reinterpret_cast<const f32x4*>(a.init + ((int64_t)seq * H + head) * size + e) : zero4();
   // eight segments' values asked for together: the loads do not wait for the sums
   constexpr int N = 8;
   for (int i0 = 0; i0 < n; i0 += N) {
@@ -754,10 +765,10 @@ __global__ __launch_bounds__(256) void lin_join_kernel(float* slot, const float*
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const int i = min(i0 + k, n - 1);
-      const int64_t sh = (int64_t)(REV ? s0 + ns - 1 - i : s0 + i) * H + head;
-      at[k] = reinterpret_cast<f32x4*>(slot + sh * size + e);
+      const int64_t sh = (int64_t)(a.back ? s0 + ns - 1 - i : s0 + i) * H + head;
+      at[k] = reinterpret_cast<f32x4*>(a.slot + sh * size + e);
       v[k] = *at[k];
-      d[k] = slot_decay[sh];
+      d[k] = a.decay[sh];
     }
 #pragma unroll
     for (int k = 0; k < N; ++k)
@@ -853,11 +864,37 @@ __global__ __launch_bounds__(64) void lin_dgate_head_kernel(const double* dg_seg
   if (lane_id() == 0) dg[blockIdx.x] = (float)x;
 }
 
+// rows before the first and behind the last packed sequence: their gradients are zero
+struct Outside {
+  char* p[4];
+  int heads[4];
+  int row_bytes[4];  // a multiple of 4
+};
+__global__ __launch_bounds__(256) void lin_outside_kernel(Outside o, const int32_t* offsets, int n_seq, int64_t T) {
+  int lo, hi, unused;
+  seq_bounds(offsets, 0, T, lo, unused);
+  seq_bounds(offsets, n_seq - 1, T, unused, hi);
+  if (hi < lo) hi = lo;
+  const int64_t rows = lo + (T - hi);
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+  for (int k = 0; k < 4; ++k) {
+    const int words = o.row_bytes[k] / 4;
+    if (!o.p[k]) continue;
+    for (int64_t i = at; i < rows * o.heads[k] * words; i += step) {
+      const int64_t r = i / words % rows, head = i / words / rows;
+      const int64_t row = r < lo ? r : hi + (r - lo);
+      reinterpret_cast<uint32_t*>(o.p[k])[(head * T + row) * words + i % words] = 0u;
+    }
+  }
+}
+
 // gradients of shared heads: the group's fp32 parts summed in order and rounded once; rows
 // before the first and behind the last packed sequence are left as they are
-__global__ __launch_bounds__(256) void lin_group_sum_kernel(const float* part, void* out, int out_bf16, int64_t n,
-                                                            int64_t head_size, int d, int group,
-                                                            const int32_t* offsets, int n_seq) {
+__global__ __launch_bounds__(256) void lin_group_sum_kernel(const float* part_q, const float* part_k, void* out_q,
+                                                            void* out_k, int out_bf16, int64_t n, int64_t head_size,
+                                                            int d, int group, const int32_t* offsets, int n_seq) {
+  const float* part = blockIdx.y ? part_k : part_q;
+  void* out = blockIdx.y ? out_k : out_q;
   const int64_t e = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
   if (e >= n) return;
   const int64_t hd = e / head_size, in = e % head_size;
@@ -1010,14 +1047,11 @@ ScanArgs base_args(const LinLaunch& p, const LinPlan& q) {
   return a;
 }
 
-void join(bool rev, float* slot, const float* decay, const float* init, const LinLaunch& p, const LinPlan& q,
-          int skip, hipStream_t s) {
+// joins n (1 or 2) sets of segment states
+void join(const JoinArgs* a, int n, const LinLaunch& p, const LinPlan& q, hipStream_t s) {
   const int size = p.d_k * p.d_v;
-  const dim3 grid((unsigned)((size / 4 + 255) / 256 * p.H * p.n_seq)), block(256);
-  if (rev)
-    hipLaunchKernelGGL((lin_join_kernel<true>), grid, block, 0, s, slot, decay, init, q.cut, p.H, size, skip);
-  else
-    hipLaunchKernelGGL((lin_join_kernel<false>), grid, block, 0, s, slot, decay, init, q.cut, p.H, size, skip);
+  const dim3 grid((unsigned)((size / 4 + 255) / 256 * p.H * p.n_seq), (unsigned)n), block(256);
+  hipLaunchKernelGGL(lin_join_kernel, grid, block, 0, s, a[0], a[n - 1], q.cut, p.H, size);
 }
 
 const __bf16* bf(const void* p) { return reinterpret_cast<const __bf16*>(p); }
@@ -1042,8 +1076,6 @@ int launch_lin_fwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   a.c = bf(p.V);
   a.group_a = a.group_b = p.H / p.H_qk;
   a.dc = p.d_v;
-  a.st_row = p.d_v;
-  a.st_col = 1;
   a.init = p.S0;
   a.fin = p.S_out;
   a.out = p.O;
@@ -1055,7 +1087,8 @@ int launch_lin_fwd(const LinLaunch& p, void* workspace, hipStream_t s) {
     a.skip = 1;
     const int rc = scan<false, false, 1, false, float>(p.d_k, q.width, a, s);
     if (rc) return rc;
-    join(false, a.slot, a.slot_decay, p.S0, p, q, 1, s);
+    const JoinArgs j{a.slot, a.slot_decay, p.S0, 1, 0};
+    join(&j, 1, p, q, s);
   }
   // a bf16 output is formed with its fp32 factors as one bf16 part: each term is rounded once
   // more, together as much as the output's own rounding; an fp32 output with three
@@ -1071,7 +1104,15 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   const int wk = grad_width(p.d_k);
   float* slot_s = reinterpret_cast<float*>(ws + q.slot_s);
   float* slot_d = reinterpret_cast<float*>(ws + q.slot_d);
-  int rc = 0;
+  if (p.offsets && p.T > 0) {
+    const int size = p.grad_bf16 ? 2 : 4;
+    const Outside o{{(char*)p.dQ, (char*)p.dK, (char*)p.dV, p.g_per_head ? nullptr : (char*)p.dg},
+                    {p.H_qk, p.H_qk, p.H, p.H},
+                    {p.d_k * size, p.d_k * size, p.d_v * size, 4}};
+    hipLaunchKernelGGL(lin_outside_kernel, dim3(128), dim3(256), 0, s, o, p.offsets, p.n_seq, p.T);
+  }
+  int rc = 0, n_joins = 0;
+  JoinArgs joins[2];
   // states after the segments
   if (q.ahead || end) {
     ScanArgs f = base_args(p, q);
@@ -1079,15 +1120,13 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
     f.c = bf(p.V);
     f.group_a = f.group_b = group;
     f.dc = p.d_v;
-    f.st_row = p.d_v;
-    f.st_col = 1;
-    f.s_state = 1.f;
+        f.s_state = 1.f;
     f.slot = slot_s;
     f.slot_decay = reinterpret_cast<float*>(ws + q.decay_s);
     f.skip = end ? 0 : 1;
     rc = scan<false, false, 1, false, float>(p.d_k, q.width, f, s);
     if (rc) return rc;
-    join(false, f.slot, f.slot_decay, p.S0, p, q, f.skip, s);
+    joins[n_joins++] = {f.slot, f.slot_decay, p.S0, f.skip, 0};
   }
   // gradients of the states before the segments; dV, and the gradient of the states given
   ScanArgs r = base_args(p, q);
@@ -1096,8 +1135,6 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   r.c = bf(p.dO);
   r.group_a = r.group_b = group;
   r.dc = p.d_v;
-  r.st_row = p.d_v;
-  r.st_col = 1;
   r.s_state = p.scale;
   r.slot = slot_d;
   r.slot_decay = reinterpret_cast<float*>(ws + q.decay_d);
@@ -1105,8 +1142,9 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   if (q.ahead) {
     rc = scan<true, false, 1, false, float>(p.d_k, q.width, r, s);
     if (rc) return rc;
-    join(true, r.slot, r.slot_decay, p.dS, p, q, r.skip, s);
+    joins[n_joins++] = {r.slot, r.slot_decay, p.dS, 1, 1};
   }
+  if (n_joins) join(joins, n_joins, p, q, s);
   r.init = p.dS;
   r.fin = p.dS0;
   r.out = p.dV;
@@ -1118,8 +1156,6 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   // dK and dQ: the transposed states, contraction over d_v; three parts, as dg is a difference
   // of their products
   ScanArgs k = base_args(p, q);
-  k.st_row = 1;
-  k.st_col = p.d_v;
   k.dc = p.d_k;
   k.a = bf(p.V);
   k.b = bf(p.dO);
@@ -1150,11 +1186,10 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   if (rc) return rc;
   if (group > 1 && p.T > 0) {
     const int64_t n = (int64_t)(p.offsets ? 1 : p.n_seq) * p.H_qk * p.T * p.d_k;
-    const dim3 grid((unsigned)ceil_div(n / 4, 256)), block(256);
-    hipLaunchKernelGGL(lin_group_sum_kernel, grid, block, 0, s, reinterpret_cast<const float*>(ws + q.part_k), p.dK,
-                       p.grad_bf16, n, p.T * p.d_k, p.d_k, group, p.offsets, p.n_seq);
-    hipLaunchKernelGGL(lin_group_sum_kernel, grid, block, 0, s, reinterpret_cast<const float*>(ws + q.part_q), p.dQ,
-                       p.grad_bf16, n, p.T * p.d_k, p.d_k, group, p.offsets, p.n_seq);
+    const dim3 grid((unsigned)ceil_div(n / 4, 256), 2), block(256);
+    hipLaunchKernelGGL(lin_group_sum_kernel, grid, block, 0, s, reinterpret_cast<const float*>(ws + q.part_q),
+                       reinterpret_cast<const float*>(ws + q.part_k), p.dQ, p.dK, p.grad_bf16, n, p.T * p.d_k, p.d_k,
+                       group, p.offsets, p.n_seq);
   }
   if (!p.dg) return 0;
   double* dg_seg = p.g_per_head ? reinterpret_cast<double*>(ws + q.dg_seg) : nullptr;
