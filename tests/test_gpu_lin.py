@@ -445,3 +445,57 @@ def test_workspace_queries():
     assert fwd(1, 3, 100, 96, 64) == 0 and bwd(1, 3, 100, 64, 32) == 0  # refused arguments
     assert bwd(0, 4, 100, 64, 64) == 0 and bwd(2, 4, 100, 64, 64) > 0
     assert bwd(2, 4, 100, 64, 64, H_qk=2) > bwd(2, 4, 100, 64, 64)
+
+
+@gpu
+def test_rows_beyond_32_bits():
+    """16 heads of 1.1 million tokens: 2.25e9 values a tensor.  Every head forgets at one token
+    near the end, so the rest equals a call on that rest alone."""
+    H, T, t0, d = 16, 1_100_000, 1_099_000, 128
+    say("lin forward beyond 2^31 values")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn((1, H, T, d), generator=gen, device="cuda", dtype=torch.bfloat16) * 0.1 for _ in range(3))
+    g = torch.full((1, H, T), -0.05, device="cuda")
+    g[:, :, t0] = -float("inf")
+    O, S = tri.gdn_lin_chunk_fwd(q, k, v, g)
+    cut = lambda x: x[:, :, t0:].contiguous()  # noqa: E731
+    O2, S2 = tri.gdn_lin_chunk_fwd(cut(q), cut(k), cut(v), cut(g))
+    torch.cuda.synchronize()
+    # the chunks' borders differ: fp32 sums in another order, and the one part's roundings
+    assert relF(S.cpu(), S2.cpu()) <= 2.0 ** -17
+    assert relF(O[:, :, t0:].cpu().double(), O2.cpu().double()) <= 2.0 ** -7
+
+
+@gpu
+def test_two_calls_at_once():
+    """Calls on two streams, each with its own workspace, give the bits of one after the other."""
+    say("lin on two streams")
+    xs = [{k: cuda(t) for k, t in ref.lin_inputs(71 + i, 1, 4, 2, 5000, 64, 64).items()} for i in range(2)]
+    call = lambda x, s=None: (tri.gdn_lin_chunk_fwd(x["Q"], x["K"], x["V"], x["g"], S0=x["S0"], stream=s) +  # noqa: E731
+                              tri.gdn_lin_chunk_bwd(x["Q"], x["K"], x["V"], x["g"], x["dO"], dS=x["dS"], stream=s)[:4])
+    one = [call(x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(3):
+        both = [call(x, s) for x, s in zip(xs, streams)]
+        for s in streams:
+            s.synchronize()
+        for a, b in zip(one, both):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@gpu
+def test_backward_leaves_nothing_unwritten():
+    """Every gradient is written in full, rows of no sequence as zeros: a call into memory that
+    held NaN (the allocator hands freed blocks out again) shows none."""
+    say("lin backward outputs whole")
+    lens, first, behind = [70, 0, 64, 1], 3, 6
+    T = first + sum(lens) + behind
+    x = {k: cuda(t) for k, t in ref.lin_inputs(81, 1, 4, 2, T, 64, 64, n_state=len(lens)).items()}
+    off = cuda(offsets_of(lens, first))
+    for _ in range(3):
+        out = tri.gdn_lin_chunk_bwd(x["Q"], x["K"], x["V"], x["g"], x["dO"], S0=x["S0"], offsets=off)
+        assert all(torch.isfinite(t).all() for t in out)
+        for t in out:
+            t.fill_(float("nan"))
+        del out, t

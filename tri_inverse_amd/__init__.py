@@ -538,8 +538,8 @@ def _lin_shape(Q, K, V, g, scale, offsets, dtypes):
     if offsets is not None:
         if B != 1:
             raise ValueError("packed sequences lie in one row: B must be 1, got %d" % B)
-        if offsets.dim() != 1 or offsets.numel() < 1:
-            raise ValueError("offsets must be [sequences + 1]")
+        if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
+            raise ValueError("offsets must be [sequences + 1], of one sequence at least")
         n = offsets.numel() - 1
         _arg(offsets, "offsets", (torch.int32,), (n + 1,), dev)
     sh = gdn_lin_shape(T, _at(offsets), n, H, Hk, dk, dv, per_head, dk ** -0.5 if scale is None else float(scale))

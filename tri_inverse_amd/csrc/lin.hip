@@ -20,24 +20,35 @@
 // differences r_s would lose digits, so the sum runs within a segment of at most 1024 tokens
 // and starts from <D, S> at the segment's end, formed from the two states there.
 //
-// Precision: a, b and c are bf16 as given, so a . b is exact up to the fp32 sums of the
-// MFMA.  The fp32 factor of every other product enters as a sum of bf16 parts: w (a . b) and
-// X (outputs) as two, col c (the state) as three, which keeps all 24 bits of the state that
-// is carried from chunk to chunk and returned in fp32.  G is summed in fp64 and handed over
-// as two floats: the exponent of w is a difference of two sums that can both be large.
+// Precision: a, b and c are bf16 as given, so a . b is exact up to the fp32 sums of the MFMA.
+// The fp32 factor of every other product enters as a sum of bf16 parts.  col c (the state) is
+// three parts, which hold all 24 bits: the state is carried from chunk to chunk in fp32 and
+// returned so.  w (a . b) and X in the outputs: fp32 outputs, and dQ and dK, whose products with
+// q and k make dg as small differences, take three parts (two left 1e-5 in dg on the training
+// workload, three 1.4e-6); O and dV in bf16 take one, whose rounding is as large as that of the
+// output itself (0.0023 against 0.0017 in the norm with two; 8 to 30 % of the time).  G is
+// summed in fp64 and handed over as two floats: the exponent of w is a difference of two sums
+// that can both be large.
 //
-// Work split: one workgroup per (segment, head, 32 columns of c), eight waves.
-//   waves 0..3  state waves (column half h, contraction half kh): each keeps its DK/2 x 16
-//               part of X in registers, adds a X to the chunk's output (partial over kh,
-//               through LDS) and updates X.
-//   waves 4..7  output waves, one 16-row tile each, one chunk behind: w (a . b), its product
-//               with c, the sum with the state waves' part, the store.
-// Rows of b and c and the decay factors pass through a ring of three LDS slots; a comes
-// straight from memory in operand order (16 contiguous bytes per lane).  One barrier per
-// chunk.  A segment is a run of chunks of one sequence: where sequences and heads alone fill
-// the machine a segment is a whole sequence; else each segment's own state is formed first
-// (the same kernel without outputs), the segments are joined in order, and every segment
-// then starts from its state.
+// Work split: one workgroup per (segment, head, W columns of c), W = 32, 64 or 128.
+//   column waves  32 columns each at W = 128, else 16: they keep their columns of X in
+//                 registers, form a X, then split col c and update X, and after the barrier in
+//                 the middle of a chunk add w (a . b) c and store.
+//   weight waves  two: w (a . b) for row tiles 0 and 3, 1 and 2, handed over through LDS.
+//   one wave forms the next chunk's decay factors, one loads its rows of a, b and c straight
+//   into LDS.
+// What a workgroup does per chunk whatever its columns (w (a . b), the rows of a and b) is
+// shared by W columns, so wide workgroups take fewer instructions: B4 H16 T8192 d128 took 185 us
+// as 256 workgroups of 32 columns over whole sequences, 171 as 256 of 128 columns over quarters,
+// their states formed first.  A segment is a run of chunks of one sequence: where sequences and
+// heads alone fill the GPU a segment is a whole sequence; else each segment's own state is
+// formed first (the same kernel without outputs), the segments are joined in order, and every
+// segment then starts from its state.
+//
+// What bounds it: with every CU at work, memory and the column waves' issue together.  256 heads
+// of 2048 tokens (whole sequences, 537 MB) take 119 us, 4.5 TB/s.  A chunk of a column wave is
+// 140 MFMA (2240 cycles) and about 460 vector instructions (1840), of which little overlaps, 330
+// KB of LDS traffic in all; without its loads the prefill workload still took 171 of 185 us.
 #include "gdn_kernels.hpp"
 #include "gdn_device.hpp"
 
@@ -289,11 +300,8 @@ __device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t r, int off, float 
 __device__ __forceinline__ void load16_lds(__amdgpu_buffer_rsrc_t r, __bf16* p, int off) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)p, 16, off, 0, 0, 0);
 }
-// until at most N of this wave's vector memory operations are in flight
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
+// until all of this wave's vector memory operations are done
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // two adjacent 16-column tiles of a row as bf16, 16 contiguous bytes per lane: group g then
 // holds columns 16(g % 2) + 8(g / 2) .. + 7
@@ -334,11 +342,10 @@ constexpr int scan_per_simd(int W, bool out) { return (scan_waves(W, out) * (out
 
 template <int DK, int W, bool REV, bool OUT, int PARTS, bool DOTS, class TO>
 __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) void lin_scan_kernel(ScanArgs A) {
-  // slots of the rows: where one part of everything leaves the room, two chunks are under way
-  // beside the one in use
-  constexpr int RING = 2;
-  __shared__ LinRows<DK> rows_a[OUT ? RING : 1], rows_b[RING];
-  __shared__ LinRows<W> rows_c[RING], rows_w[DOTS ? RING : 1];
+  // two slots of everything: one in use, one being filled (a third for the rows measured level:
+  // 191 against 185 us on the prefill workload)
+  __shared__ LinRows<DK> rows_a[OUT ? 2 : 1], rows_b[2];
+  __shared__ LinRows<W> rows_c[2], rows_w[DOTS ? 2 : 1];
   __shared__ LinGates gates[2];
   __shared__ bf16x8 weights[OUT ? PARTS : 1][LNT][2][WAVE];  // w (a . b) as operands: [part][row tile][32-wide step]
   __shared__ float dot_part[DOTS ? W / (16 * scan_tiles(W)) : 1][LC];
@@ -430,16 +437,15 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
       constexpr bool PAIR = HC == 2 && sizeof(TO) == 2;  // 16 bytes a lane from two tiles
       const int ooff = (c * A.dc + slice * W + col0 + (PAIR ? 16 * (g & 1) + 8 * (g >> 1) : 4 * g)) * (int)sizeof(TO);
       lds_handover();
-      int slot = 0;
       for (int it = 0; it < n; ++it) {
         if constexpr (OUT && PARTS == 1) __builtin_amdgcn_iglp_opt(1);  // interleaves MFMA and VALU: 3 to 8 % less
         const LinGates& GT = gates[it & 1];
-        const __bf16* bs = rows_b[slot].v;
-        const __bf16* cs = rows_c[slot].v;
+        const __bf16* bs = rows_b[it & 1].v;
+        const __bf16* cs = rows_c[it & 1].v;
         // a X: lane (g, c) holds row 16I + c, columns 4g + r of each tile
         f32x4 o[HC][LNT];
         if constexpr (OUT) {
-          const __bf16* as = rows_a[slot].v;
+          const __bf16* as = rows_a[it & 1].v;
 #pragma unroll
           for (int h = 0; h < HC; ++h)
 #pragma unroll
@@ -514,7 +520,7 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
               float s = 0.f, s0, s1;
 #pragma unroll
               for (int h = 0; h < HC; ++h) {
-                const f32x4 w = unpack4(*reinterpret_cast<const bf16x4*>(rows_w[slot].v + w_at[h] + 16 * I * W));
+                const f32x4 w = unpack4(*reinterpret_cast<const bf16x4*>(rows_w[it & 1].v + w_at[h] + 16 * I * W));
 #pragma unroll
                 for (int q = 0; q < 4; ++q) s = fmaf(w[q], o[h][I][q], s);
               }
@@ -537,7 +543,6 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
             }
           }
         }
-        slot = slot == RING - 1 ? 0 : slot + 1;
         lds_handover();
       }
     }
@@ -610,7 +615,7 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
     return;
   }
   if (wave == W_ROWS) {
-    // ---- rows of a, b, c straight into LDS, RING - 1 chunks ahead ------------------------
+    // ---- rows of a, b, c straight into LDS, one chunk ahead -------------------------------
     if (n <= 0) return;
     constexpr int NB = LC * DK * 2 / 1024, NC = LC * W * 2 / 1024;  // 1 KB an instruction
     const int64_t arow = row_of(A.group_a), brow = row_of(A.group_b);
@@ -637,22 +642,13 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
         for (int i = 0; i < NC; ++i) load16_lds(rw, rows_w[s].v + 512 * i, coff[i]);
       }
     };
-    // all loads but those of the last RING - 2 chunks asked for have arrived
-    constexpr int LATER = (RING - 2) * (NB + NC + (OUT ? NB : 0) + (DOTS ? NC : 0));
-    static_assert(LATER < 64, "the counter of loads in flight");
-    for (int j = 0; j < RING - 1; ++j) load(j, j);
-    wait_loads<LATER>();
+    load(0, 0);
+    wait_loads();
     lds_handover();
-    int slot = RING - 1;
     for (int it = 0; it < n; ++it) {
-      const bool more = it + RING - 1 < n;
-      if (more) load(it + RING - 1, slot);
-      slot = slot == RING - 1 ? 0 : slot + 1;
+      if (it + 1 < n) load(it + 1, (it + 1) & 1);
       if (OUT) lds_handover();
-      if (more)
-        wait_loads<LATER>();
-      else
-        wait_loads<0>();
+      wait_loads();
       lds_handover();
     }
     return;
@@ -668,11 +664,10 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
 #pragma unroll
       for (int p = 0; p < NP; ++p) row_at[p] = LinRows<DK>::at(c, 32 * p + 8 * g);
       lds_handover();
-      int slot = 0;
       for (int it = 0; it < n; ++it) {
         const LinGates& GT = gates[it & 1];
-        const __bf16* as = rows_a[slot].v;
-        const __bf16* bs = rows_b[slot].v;
+        const __bf16* as = rows_a[it & 1].v;
+        const __bf16* bs = rows_b[it & 1].v;
         // P_ij = w_ij (a_i . b_j): lane (g, c) holds row i = 16I + c, columns 16J + 4g + r
         f32x4 P[2][LNT];
         bf16x8 af[2][NP];
@@ -724,7 +719,6 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
             for (int k = 0; k < PARTS; ++k) weights[k][I][p][l] = s[k];
           }
         }
-        slot = slot == RING - 1 ? 0 : slot + 1;
         lds_handover();
         lds_handover();
       }
@@ -923,17 +917,20 @@ struct LinPlan {
 };
 
 bool fits(int d, int width) { return d % width == 0; }
+// of a scan for the segments' states: without outputs there is no w (a . b) to share, and more,
+// smaller workgroups spread better (prefill 179 -> 170 us, 13 packed sequences 160 -> 149)
+int state_width(int width) { return width < 64 ? width : 64; }
 // of d_k in the backward pass (64 or 128)
 int grad_width(int d) { return d == 128 ? 128 : 64; }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Microseconds of one launch, after whole launches at d = 128: a workgroup of 128 / 64 / 32
-// columns takes 3.0 / 2.3 / 2.05 a chunk with outputs (one workgroup a CU) and 1.7 / 1.3 / 1.1
-// without (two), starts and ends in 8, and memory gives 4.5 MB a microsecond.
+// columns takes 3.0 / 2.3 / 2.05 a chunk with outputs (one workgroup a CU) and 1.7 / 1.5 at 64 /
+// 32 columns without (two a CU), starts and ends in 8, and memory gives 4.5 MB a microsecond.
 double scan_cost(const LinLaunch& p, int width, int64_t groups, int64_t chunks, bool out, double bytes) {
-  const double chunk = (out ? (width == 128 ? 3.0 : width == 64 ? 2.3 : 2.05)
-                            : (width == 128 ? 1.7 : width == 64 ? 1.3 : 1.1)) * (p.d_k == 128 ? 1.0 : 0.7);
+  const double chunk = (out ? (width == 128 ? 3.0 : width == 64 ? 2.3 : 2.05) : width == 64 ? 1.7 : 1.5) *
+                       (p.d_k == 128 ? 1.0 : 0.7);
   const double work = (double)ceil_div(groups, out ? 256 : 512) * ((double)chunks * chunk + 8.0);
   const double memory = bytes / 4.5e6 + 6.0;
   return work > memory ? work : memory;
@@ -954,7 +951,8 @@ LinPlan make_plan(const LinLaunch& p, bool bwd) {
     // Whole sequences, or segments that give every CU one to four workgroups: their own states
     // cost another reading of K and V, and the launches and the joining some more.  B4 H16
     // T8192 d128: four segments a sequence 181 us, eight 203, whole sequences in four slices
-    // of 32 columns 262; 128 heads of 4096: two slices 151, two segments about 200.
+    // of 32 columns 262; 128 heads of 4096: two slices 151, two segments about 200 (as measured
+    // when the rule was set).
     const double rows = (double)(p.offsets ? 1 : p.n_seq) * (double)p.T;
     const double bytes = rows * 2.0 * ((double)p.H_qk * p.d_k + (double)p.H * p.d_v);  // K and V
     const double state = 4.0 * p.H * p.d_k * p.d_v;
@@ -969,8 +967,8 @@ LinPlan make_plan(const LinLaunch& p, bool bwd) {
         const int64_t per = ceil_div(longest, len), n = p.offsets ? ceil_div(all, len) : p.n_seq * per;
         double cost = scan_cost(p, w, n * items, len, true, 2.0 * bytes);
         if (per > 1)
-          cost += scan_cost(p, w, (n - seqs) * items, len, false, bytes * (double)(per - 1) / (double)per) + 8.0 +
-                  3.0 * (double)n * state / 4e6;
+          cost += scan_cost(p, state_width(w), (n - seqs) * p.H * (p.d_v / state_width(w)), len, false,
+                            bytes * (double)(per - 1) / (double)per) + 8.0 + 3.0 * (double)n * state / 4e6;
         if (cost < best) {
           best = cost;
           q.width = w;
@@ -1025,7 +1023,8 @@ int scan(int dk, int width, const ScanArgs& a, hipStream_t s) {
   };
   using std::integral_constant;
   auto by_width = [&](auto d) {
-    if (width == 128) return go(d, integral_constant<int, 128>{});
+    if constexpr (OUT)
+      if (width == 128) return go(d, integral_constant<int, 128>{});
     if (width == 64) return go(d, integral_constant<int, 64>{});
     // the backward pass has d_k and d_v of 64 and 128 only
     if constexpr (!REV && !DOTS) return go(d, integral_constant<int, 32>{});
@@ -1085,7 +1084,7 @@ int launch_lin_fwd(const LinLaunch& p, void* workspace, hipStream_t s) {
     a.slot = reinterpret_cast<float*>(ws + q.slot_s);
     a.slot_decay = reinterpret_cast<float*>(ws + q.decay_s);
     a.skip = 1;
-    const int rc = scan<false, false, 1, false, float>(p.d_k, q.width, a, s);
+    const int rc = scan<false, false, 1, false, float>(p.d_k, state_width(q.width), a, s);
     if (rc) return rc;
     const JoinArgs j{a.slot, a.slot_decay, p.S0, 1, 0};
     join(&j, 1, p, q, s);
@@ -1124,7 +1123,7 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
     f.slot = slot_s;
     f.slot_decay = reinterpret_cast<float*>(ws + q.decay_s);
     f.skip = end ? 0 : 1;
-    rc = scan<false, false, 1, false, float>(p.d_k, q.width, f, s);
+    rc = scan<false, false, 1, false, float>(p.d_k, state_width(q.width), f, s);
     if (rc) return rc;
     joins[n_joins++] = {f.slot, f.slot_decay, p.S0, f.skip, 0};
   }
@@ -1140,7 +1139,7 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   r.slot_decay = reinterpret_cast<float*>(ws + q.decay_d);
   r.skip = 1;
   if (q.ahead) {
-    rc = scan<true, false, 1, false, float>(p.d_k, q.width, r, s);
+    rc = scan<true, false, 1, false, float>(p.d_k, state_width(q.width), r, s);
     if (rc) return rc;
     joins[n_joins++] = {r.slot, r.slot_decay, p.dS, 1, 1};
   }
