@@ -17,8 +17,8 @@
 //
 // Gradient of the log-decays: with r_t = q_t . dq_t - k_t . dk_t, dg_t = sum_{s>=t} r_s over
 // the rest of the sequence + <dS_out, S_out>.  Summed over a whole long sequence the
-// differences r_s would lose digits, so the sum runs within a segment of at most 1024 tokens
-// and starts from <D, S> at the segment's end, formed from the two states there.
+// differences r_s would lose digits, so the sum runs within a segment of at most 1024 tokens,
+// between <D, S> at the segment's two ends, formed from the states there.
 //
 // Precision: a, b and c are bf16 as given, so a . b is exact up to the fp32 sums of the MFMA.
 // The fp32 factor of every other product enters as a sum of bf16 parts.  col c (the state) is
@@ -242,6 +242,12 @@ __device__ __forceinline__ double wave_scan_f64(double v) {
 __device__ __forceinline__ double clamp_log2(double x) { return x < -512.0 ? -512.0 : x; }
 
 __device__ __forceinline__ float exp2_f32(float x) { return __builtin_amdgcn_exp2f(x); }
+// 2^x with the whole part set apart before the fraction becomes a float: rounding an exponent
+// of -10 to a float alone costs 3e-7 of the result
+__device__ __forceinline__ float exp2_f64(double x) {
+  const double n = rint(x);
+  return ldexpf(exp2_f32((float)(x - n)), (int)n);
+}
 
 __device__ __forceinline__ f32x4 lo4(const bf16x8& v) { return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]}; }
 __device__ __forceinline__ f32x4 hi4(const bf16x8& v) { return f32x4{(float)v[4], (float)v[5], (float)v[6], (float)v[7]}; }
@@ -442,14 +448,19 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
         const LinGates& GT = gates[it & 1];
         const __bf16* bs = rows_b[it & 1].v;
         const __bf16* cs = rows_c[it & 1].v;
-        // a X: lane (g, c) holds row 16I + c, columns 4g + r of each tile
-        f32x4 o[HC][LNT];
+        // a X: lane (g, c) holds row 16I + c, columns 4g + r of each tile.  With several parts the
+        // smaller ones have sums of their own, so that the sums of the first part round only as
+        // often as they have terms (dg on the training workload: 1.2e-6 with one sum).
+        f32x4 o[HC][LNT], low[HC][PARTS > 1 ? LNT : 1];
         if constexpr (OUT) {
           const __bf16* as = rows_a[it & 1].v;
 #pragma unroll
           for (int h = 0; h < HC; ++h)
 #pragma unroll
-            for (int I = 0; I < LNT; ++I) o[h][I] = zero4();
+            for (int I = 0; I < LNT; ++I) {
+              o[h][I] = zero4();
+              if constexpr (PARTS > 1) low[h][I] = zero4();
+            }
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
             bf16x8 s[HC][PARTS];
@@ -459,9 +470,11 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
             for (int I = 0; I < LNT; ++I) {
               const bf16x8 af = *reinterpret_cast<const bf16x8*>(as + a_at[p] + 16 * I * DK);
 #pragma unroll
-              for (int h = 0; h < HC; ++h)
+              for (int h = 0; h < HC; ++h) {
 #pragma unroll
-                for (int k = PARTS - 1; k >= 0; --k) o[h][I] = mma_bf16(s[h][k], af, o[h][I]);
+                for (int k = PARTS - 1; k > 0; --k) low[h][I] = mma_bf16(s[h][k], af, low[h][I]);
+                o[h][I] = mma_bf16(s[h][0], af, o[h][I]);
+              }
             }
           }
         }
@@ -498,7 +511,10 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
           for (int I = 0; I < LNT; ++I) {
             const float rw = GT.row[16 * I + c];
 #pragma unroll
-            for (int h = 0; h < HC; ++h) o[h][I] = o[h][I] * rw;
+            for (int h = 0; h < HC; ++h) {
+              o[h][I] = o[h][I] * rw;
+              if constexpr (PARTS > 1) low[h][I] = low[h][I] * rw;
+            }
           }
           lds_handover();  // the weights are there
 #pragma unroll
@@ -510,9 +526,18 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
               for (int k = PARTS - 1; k >= 0; --k) {
                 const bf16x8 wf = weights[k][I][p][l];
 #pragma unroll
-                for (int h = 0; h < HC; ++h) o[h][I] = mma_bf16(cf[h][p], wf, o[h][I]);
+                for (int h = 0; h < HC; ++h) {
+                  f32x4& sum = k > 0 ? low[h][PARTS > 1 ? I : 0] : o[h][I];
+                  sum = mma_bf16(cf[h][p], wf, sum);
+                }
               }
             }
+          if constexpr (PARTS > 1) {
+#pragma unroll
+            for (int h = 0; h < HC; ++h)
+#pragma unroll
+              for (int I = 0; I < LNT; ++I) o[h][I] = o[h][I] + low[h][I];
+          }
           const auto r = chunk_rows(A.out, orow, it, (int)sizeof(TO) * A.dc);  // rows past the end are not stored
 #pragma unroll
           for (int I = 0; I < LNT; ++I) {
@@ -568,9 +593,9 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
     auto store = [&](float gl, LinGates& GT) {
       const double G = wave_scan_f64(clamp_log2((double)gl * LOG2E)), GC = readlane_d(G, WAVE - 1);
       const float hi = (float)G;
-      const float eG = exp2_f32(hi), eR = exp2_f32((float)(GC - G));
+      const float eG = exp2_f64(G), eR = exp2_f64(GC - G);
       GT.col[l] = (REV ? eG : eR) * A.s_state;
-      if (l == 0) GT.end = exp2_f32((float)GC);
+      if (l == 0) GT.end = exp2_f64(GC);
       if constexpr (OUT) {
         GT.hi[l] = hi;
         GT.lo[l] = (float)(G - (double)hi);
@@ -580,9 +605,9 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
 #pragma unroll
         for (int B = 0; B < LNT - 1; ++B) {
           const double Gb = readlane_d(G, 16 * B + 15);
-          const float e = exp2_f32((float)(REV ? G - Gb : Gb - G));
+          const float e = exp2_f64(REV ? G - Gb : Gb - G);
           if (REV ? l > 16 * B + 15 : l <= 16 * B + 15) GT.from[B][l] = e;
-          if ((l >> 4) == (REV ? B : B + 1)) GT.to[l] = exp2_f32((float)(REV ? Gb - G : G - Gb)) * A.s_intra;
+          if ((l >> 4) == (REV ? B : B + 1)) GT.to[l] = exp2_f64(REV ? Gb - G : G - Gb) * A.s_intra;
         }
       }
       decay += GC;
@@ -611,7 +636,7 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
       }
       if constexpr (DOTS) sum_dots(n - 1);
     }
-    if (!OUT && slice == 0 && l == 0) A.slot_decay[(int64_t)seg * A.H + head] = exp2_f32((float)decay);
+    if (!OUT && slice == 0 && l == 0) A.slot_decay[(int64_t)seg * A.H + head] = exp2_f64(decay);
     return;
   }
   if (wave == W_ROWS) {
@@ -773,28 +798,40 @@ __global__ __launch_bounds__(256) void lin_join_kernel(JoinArgs a0, JoinArgs a1,
   }
 }
 
-// dg of one (segment, head): from the segment's end backwards, dg_t = <D, S> at the end +
-// sum_{s>=t} (q_s . dq_s - k_s . dk_s), the sums in fp64.  Per-head decays: the segment's sum.
+// dg of one (segment, head).  From the segment's end backwards dg_t = <D, S> there + sum_{s>=t}
+// (q_s . dq_s - k_s . dk_s), and at the segment's first token dg is <D, S> before it.  The
+// rounding errors of the sum grow like a random walk; what it misses the second product by is
+// taken back in proportion to the tokens summed, which leaves a bridge between two exact ends (a
+// third of the mean square error).  All sums in fp64.  Per-head decays: the segment's sum.
 __global__ __launch_bounds__(256) void lin_dgate_kernel(const float* dot_q, const float* dot_k, int n_dots,
-                                                        const float* slot_s, const float* slot_d, const float* dS,
-                                                        float* dg, double* dg_seg, Cut cut, int64_t heads_T, int H,
-                                                        int size) {
-  __shared__ double red[4];
+                                                        const float* slot_s, const float* slot_d, const float* S0,
+                                                        const float* dS0, const float* dS, float* dg, double* dg_seg,
+                                                        Cut cut, int64_t heads_T, int H, int size) {
+  __shared__ double red[4][2];
   const int head = (int)blockIdx.x % H;
   const int l = lane_id(), wave = threadIdx.x / WAVE;
   Span sp;
   const int64_t seg = blockIdx.x / H;
   if (!find_segment(cut, (int)seg, sp)) return;
-  auto block_sum = [&](double x) {
+  auto wave_sum = [&](double x) {
 #pragma unroll
     for (int d = 1; d < WAVE; d <<= 1) x += __shfl_xor(x, d);
+    return x;
+  };
+  auto block_sum = [&](double x, double y, double& sx, double& sy) {
+    x = wave_sum(x);
+    y = wave_sum(y);
     __syncthreads();
-    if (l == 0) red[wave] = x;
+    if (l == 0) {
+      red[wave][0] = x;
+      red[wave][1] = y;
+    }
     __syncthreads();
-    return (red[0] + red[1]) + (red[2] + red[3]);
+    sx = (red[0][0] + red[1][0]) + (red[2][0] + red[3][0]);
+    sy = (red[0][1] + red[1][1]) + (red[2][1] + red[3][1]);
   };
   // thread i holds tokens t1 - 1 - i - 256 k: all are asked for before anything is summed
-  constexpr int RUNS = (int)BWD_SEG_CHUNKS * LC / 256;
+  constexpr int RUNS = BWD_SEG_CHUNKS * LC / 256;
   const int64_t row0 = ((cut.offsets ? 0 : (int64_t)sp.seq * H) + head) * cut.T + sp.tok0;
   const int t0 = sp.c0 * LC, t1 = min(sp.len, (sp.c0 + sp.nc) * LC);
   float rq[RUNS][2], rk[RUNS][2];
@@ -807,42 +844,60 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(const float* dot_q, cons
       rk[k][s] = s < n_dots && t >= t0 ? dot_k[s * heads_T + row0 + t] : 0.f;
     }
   }
-  // the states at the segment's end; none given there: their product is zero
-  double run = 0.0;
-  const float* D = sp.last ? (dS ? dS + ((int64_t)sp.seq * H + head) * size : nullptr)
-                           : slot_d + ((seg + 1) * H + head) * size;
-  if (D) {
-    const float* S = slot_s + (seg * H + head) * size;
-    double x = 0.0;
-#pragma unroll 4
-    for (int e = 4 * (int)threadIdx.x; e < size; e += 1024) {
-      const f32x4 a = *reinterpret_cast<const f32x4*>(D + e), b = *reinterpret_cast<const f32x4*>(S + e);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) x = fma((double)a[r], (double)b[r], x);
+  // the states at the segment's two ends (none given: zeros, and so is their product)
+  auto of = [&](const float* p, int64_t i) { return p ? p + (i * H + head) * size : nullptr; };
+  const float* De = sp.last ? of(dS, sp.seq) : of(slot_d, seg + 1);
+  const float* Se = De ? of(slot_s, seg) : nullptr;
+  const float* Sb = sp.first ? of(S0, sp.seq) : of(slot_s, seg - 1);
+  const float* Db = sp.first ? of(dS0, sp.seq) : of(slot_d, seg);
+  double end = 0.0, begin = 0.0;
+#pragma unroll 2
+  for (int e = 4 * (int)threadIdx.x; e < size; e += 1024) {
+    f32x4 a = zero4(), b = zero4(), c = zero4(), d = zero4();
+    if (De) {
+      a = *reinterpret_cast<const f32x4*>(De + e);
+      b = *reinterpret_cast<const f32x4*>(Se + e);
     }
-    run = block_sum(x);
+    if (Sb && Db) {
+      c = *reinterpret_cast<const f32x4*>(Db + e);
+      d = *reinterpret_cast<const f32x4*>(Sb + e);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      end = fma((double)a[r], (double)b[r], end);
+      begin = fma((double)c[r], (double)d[r], begin);
+    }
   }
-  double sum = 0.0;
+  block_sum(end, begin, end, begin);
+  // sums from the segment's end, this thread's tokens
+  double run = end, at[RUNS];
 #pragma unroll
   for (int k = 0; k < RUNS; ++k) {
-    if (t1 - 256 * k <= t0) break;
-    const int t = t1 - 1 - (int)threadIdx.x - 256 * k;
     const double r = wave_scan_f64(((double)rq[k][0] - (double)rk[k][0]) + ((double)rq[k][1] - (double)rk[k][1]));
     __syncthreads();
-    if (l == WAVE - 1) red[wave] = r;
+    if (l == WAVE - 1) red[wave][0] = r;
     __syncthreads();
-    double before = run;
+    at[k] = run + r;
     for (int w = 0; w < 4; ++w) {
-      if (w < wave) before += red[w];
-      run += red[w];
+      if (w < wave) at[k] += red[w][0];
+      run += red[w][0];
     }
+  }
+  // a state given whose gradient is not formed: nothing to compare the sum with
+  const double miss = Sb && !Db ? 0.0 : begin - run;
+  const double share = t1 > t0 ? miss / (double)(t1 - t0) : 0.0;
+  double sum = 0.0, unused;
+#pragma unroll
+  for (int k = 0; k < RUNS; ++k) {
+    const int t = t1 - 1 - (int)threadIdx.x - 256 * k;
     if (t >= t0) {
-      if (dg) dg[row0 + t] = (float)(before + r);
-      sum += before + r;
+      const double x = at[k] + share * (double)(t1 - t);
+      if (dg) dg[row0 + t] = (float)x;
+      sum += x;
     }
   }
   if (dg_seg) {
-    sum = block_sum(sum);
+    block_sum(sum, 0.0, sum, unused);
     if (threadIdx.x == 0) dg_seg[seg * H + head] = sum;
   }
 }
@@ -1194,8 +1249,8 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   double* dg_seg = p.g_per_head ? reinterpret_cast<double*>(ws + q.dg_seg) : nullptr;
   hipLaunchKernelGGL(lin_dgate_kernel, dim3((unsigned)(p.H * q.cut.n_seg)), dim3(256), 0, s,
                      reinterpret_cast<const float*>(ws + q.dot_q), reinterpret_cast<const float*>(ws + q.dot_k),
-                     p.d_k / wk, slot_s, slot_d, p.dS, p.g_per_head ? nullptr : p.dg, dg_seg, q.cut, k.heads_T, p.H,
-                     p.d_k * p.d_v);
+                     p.d_k / wk, slot_s, slot_d, p.S0, p.dS0, p.dS, p.g_per_head ? nullptr : p.dg, dg_seg, q.cut, k.heads_T,
+                     p.H, p.d_k * p.d_v);
   if (p.g_per_head)
     hipLaunchKernelGGL(lin_dgate_head_kernel, dim3((unsigned)p.H), dim3(64), 0, s, dg_seg, p.dg, q.cut, p.H);
   return 0;
