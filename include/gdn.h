@@ -297,7 +297,8 @@ size_t gdn_lin_chunk_bwd_workspace_bytes(const gdn_lin_shape* shape);
  * GDN_F32; S0 NULL = zeros; S_out NULL = not wanted.  d_k in {64, 128}, d_v a multiple of
  * 32, at most 256 (GDN_ERR_UNSUPPORTED otherwise).  workspace: 16-byte aligned scratch of at
  * least the query's bytes, not to be shared by two calls in flight (GDN_ERR_WORKSPACE if it
- * is needed and NULL or smaller). */
+ * is needed and NULL or smaller).  A token's row of O depends on no later token, whatever that
+ * holds: rows that pad a sequence at its end may be infinities or NaN. */
 gdn_status gdn_lin_chunk_fwd(const gdn_lin_shape* shape, const void* Q, const void* K, const void* V,
                              int32_t qkv_dtype, const float* g, const float* S0, void* O,
                              int32_t o_dtype, float* S_out, void* workspace, size_t workspace_bytes,
@@ -307,7 +308,9 @@ gdn_status gdn_lin_chunk_fwd(const gdn_lin_shape* shape, const void* Q, const vo
  * NULL = zeros).  dQ, dK, dV as Q, K, V in grad_dtype (GDN_BF16 or GDN_F32; shared heads get
  * the sum over their group), dg fp32 as g (per head: the sum over all its tokens; NULL = not
  * wanted), dS0 [B][H][d_k][d_v] fp32 (NULL = not wanted).  d_k and d_v in {64, 128}.  The
- * call reads no output of the forward pass.  The same call gives the same bits. */
+ * call reads no output of the forward pass.  The same call gives the same bits.  An infinity or
+ * a NaN in a row may reach all gradients of its sequence and head: rows that pad a sequence must
+ * be finite here. */
 gdn_status gdn_lin_chunk_bwd(const gdn_lin_shape* shape, const void* Q, const void* K, const void* V,
                              int32_t qkv_dtype, const float* g, const float* S0, const void* dO,
                              const float* dS, void* dQ, void* dK, void* dV, int32_t grad_dtype,
@@ -332,7 +335,7 @@ typedef enum gdn_gate_act { GDN_GATE_SILU = 0, GDN_GATE_SIGMOID = 1 } gdn_gate_a
  * over the d values of a row.  O [B][H][T][d] as the entry points above and gdn_chunk_fwd /
  * gdn_decode write it, Z [B][T] rows of H * d values, z_stride values apart (a part of a
  * wider projection; a multiple of 8, >= H * d), Y [B][T][H][d]; dtype GDN_BF16 or GDN_F32 for
- * all three; w fp32 [d], NULL = ones.  d a multiple of 32, at most 256. */
+ * all three; w fp32 [d], NULL = ones.  d a multiple of 32, at most 256; fewer than 2^34 values. */
 gdn_status gdn_gate_norm_fwd(const void* O, const void* Z, int64_t z_stride, const float* w, void* Y,
                              int32_t dtype, int32_t B, int32_t H, int64_t T, int32_t d, int32_t act,
                              float eps, void* stream);

@@ -499,3 +499,72 @@ def test_backward_leaves_nothing_unwritten():
         for t in out:
             t.fill_(float("nan"))
         del out, t
+
+
+@gpu
+@pytest.mark.parametrize("T,n,dk,dv,odt", [
+    (64, 1, 128, 128, torch.bfloat16), (100, 37, 64, 64, torch.float32), (130, 66, 128, 256, torch.bfloat16),
+    (200, 160, 64, 32, torch.bfloat16), (4500, 4301, 128, 128, torch.float32), (300, 255, 128, 128, torch.float32)])
+def test_what_pads_a_sequence_reaches_no_earlier_row(T, n, dk, dv, odt):
+    """The rows behind the first n hold NaN, infinities and the largest values: the first n rows
+    of O are those of the n tokens alone (fp32 sums in another order, one rounding of the type).
+    Infinities in single columns of V leave the other columns of later rows finite."""
+    say(f"lin forward, {T - n} bad rows behind {n}")
+    x = ref.lin_inputs(T + n, 2, 2, 1, T, dk, dv)
+    bad = {k: x[k].clone() for k in ("Q", "K", "V", "g")}
+    for i, k in enumerate(("Q", "K", "V", "g")):
+        bad[k][:, :, n:] = float("nan")
+        bad[k][:, :, n + 1::3] = (-1) ** i * float("inf")
+        bad[k][:, :, n + 2::3] = torch.finfo(bad[k].dtype).max
+    O, _ = run_forward(bad, 0.2, x["S0"], o_dtype=odt)
+    some = dict(x, V=x["V"].clone())
+    some["V"][:, :, n, 5::7] = float("inf")
+    P, _ = run_forward(some, 0.2, x["S0"], o_dtype=odt)
+    torch.cuda.synchronize()
+    want, mag = ref.lin_forward(x, 0.2, x["S0"]), ref.lin_forward(x, 0.2, x["S0"], magnitude=True)
+    tol = TOL_O if odt == torch.float32 else TOL_ONE
+    close(O[:, :, :n], want[0][:, :, :n], mag[0][:, :, :n], tol, "O before the padding")
+    close(P[:, :, :n], want[0][:, :, :n], mag[0][:, :, :n], tol, "O before infinities in V")
+    fine = [c for c in range(dv) if c % 7 != 5]
+    close(P[..., fine], want[0][..., fine], mag[0][..., fine], tol, "the other columns")
+    assert not torch.isfinite(P[:, :, n, 5::7]).any()
+
+
+@gpu
+def test_backward_of_no_sequence():
+    """No sequence at all: the heads' decays get zeros, and so do packed rows (from C, where offsets
+    of one entry are valid)."""
+    say("lin backward without sequences")
+    x = ref.lin_inputs(3, 0, 4, 2, 70, 64, 64, "head")
+    dQ, dK, dV, dg, _ = tri.gdn_lin_chunk_bwd(*(cuda(x[n]) for n in ("Q", "K", "V", "g", "dO")))
+    assert dQ.numel() == 0 and dV.numel() == 0 and dg.shape == (4,)
+    y = ref.lin_inputs(3, 1, 4, 2, 70, 64, 64, "head")
+    t = {n: cuda(y[n]) for n in ("Q", "K", "V", "g", "dO")}
+    out = [torch.full_like(t[n], 7.0) for n in ("Q", "K", "V", "g")]
+    off = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sh = tri.gdn_lin_shape(70, off.data_ptr(), 0, 4, 2, 64, 64, 1, 1.0)
+    at = lambda n: t[n].data_ptr()  # noqa: E731
+    st = tri._lib.gdn_lin_chunk_bwd(ctypes.byref(sh), at("Q"), at("K"), at("V"), tri.GDN_BF16, at("g"), None, at("dO"), None,
+                                    out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), tri.GDN_BF16,
+                                    out[3].data_ptr(), None, None, 0, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0 and torch.count_nonzero(dg) == 0
+    assert all(torch.count_nonzero(o) == 0 for o in out)
+
+
+@gpu
+def test_the_given_state_is_not_the_returned_one():
+    x = ref.lin_inputs(3, 1, 2, 2, 70, 64, 64)
+    S = cuda(x["S0"])
+    with pytest.raises(ValueError, match="S_out must not be S0"):
+        tri.gdn_lin_chunk_fwd(*(cuda(x[n]) for n in ("Q", "K", "V", "g")), S0=S, S_out=S)
+
+
+def test_c_refusals_of_launches_too_large():
+    """Sizes whose launches would have more than 2^32 threads are refused before anything runs."""
+    for call in (c_fwd, c_bwd):
+        assert call(shape(B=2 ** 23, H=2, H_qk=2, T=64)) == 5
+        assert call(shape(B=2 ** 30, H=1, H_qk=1, T=2 ** 30)) == 5
+    assert tri.gdn_lin_chunk_fwd_workspace_bytes(2 ** 30, 1, 2 ** 30, 64, 64) == 0
+    assert tri.gdn_lin_chunk_bwd_workspace_bytes(2 ** 30, 1, 2 ** 30, 64, 64) == 0
+    assert tri._lib.gdn_gate_norm_fwd(FAKE, FAKE, 4 * 128, None, FAKE, 1, 2, 4, 2 ** 24, 128, 0, 1e-6, None) == 5

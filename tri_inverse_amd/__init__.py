@@ -572,7 +572,7 @@ def gdn_lin_chunk_fwd(Q, K, V, g, scale: float | None = None, S0=None, offsets=N
 
     Q, K [B,H_qk,T,d_k], V [B,H,T,d_v] bf16 (H_qk divides H); g fp32, [B,H,T] log-decays or
     [H] for one decay per head.  offsets: int32 [n+1] for n packed sequences in B = 1 rows of
-    T tokens.  S0 [B or n,H,d_k,d_v] fp32 or None (zeros).  Any T.  workspace: a uint8 tensor
+    T tokens.  S0 [B or n,H,d_k,d_v] fp32 or None (zeros; not the same tensor as S_out).  Any T.  workspace: a uint8 tensor
     of gdn_lin_chunk_fwd_workspace_bytes(...) bytes, or None to have one allocated here.
     Returns (O [B,H,T,d_v], S_out [B or n,H,d_k,d_v] fp32)."""
     sh, state, dev = _lin_shape(Q, K, V, g, scale, offsets, _BF16)
@@ -581,6 +581,8 @@ def gdn_lin_chunk_fwd(Q, K, V, g, scale: float | None = None, S0=None, offsets=N
     with _scope(dev, stream):
         O = _out(O, "O", _FLOAT, V.shape, dev, o_dtype, V)
         S_out = _out(S_out, "S_out", (torch.float32,), state, dev, torch.float32, S0)
+        if S0 is not None and S_out.data_ptr() == S0.data_ptr() and S0.numel():
+            raise ValueError("S_out must not be S0: a sequence's parts read the one while others write the other")
         ws, ws_bytes = _scratch(workspace, _lib.gdn_lin_chunk_fwd_workspace_bytes(ctypes.byref(sh)), dev)
         st = _lib.gdn_lin_chunk_fwd(ctypes.byref(sh), _at(Q), _at(K), _at(V), GDN_BF16, _at(g), _at(S0), _at(O),
                                     _TORCH_DTYPE[O.dtype], _at(S_out), _at(ws), ws_bytes, _current(dev))

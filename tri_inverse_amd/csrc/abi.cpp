@@ -375,12 +375,12 @@ static bool all_aligned16(std::initializer_list<const void*> ps) {
 }
 
 size_t gdn_lin_chunk_fwd_workspace_bytes(const gdn_lin_shape* s) {
-  if (check_lin(s, false) != GDN_OK || s->B == 0 || s->H == 0) return 0;
+  if (check_lin(s, false) != GDN_OK || s->B == 0 || s->H == 0 || !gdn::lin_grid_ok(lin_launch(s), false)) return 0;
   return gdn::lin_workspace(lin_launch(s), false);
 }
 
 size_t gdn_lin_chunk_bwd_workspace_bytes(const gdn_lin_shape* s) {
-  if (check_lin(s, true) != GDN_OK || s->B == 0 || s->H == 0) return 0;
+  if (check_lin(s, true) != GDN_OK || s->B == 0 || s->H == 0 || !gdn::lin_grid_ok(lin_launch(s), true)) return 0;
   return gdn::lin_workspace(lin_launch(s), true);
 }
 
@@ -417,12 +417,15 @@ gdn_status gdn_lin_chunk_bwd(const gdn_lin_shape* s, const void* Q, const void* 
   if (st != GDN_OK) return st;
   if (qkv_dtype != GDN_BF16) return qkv_dtype == GDN_F32 ? GDN_ERR_UNSUPPORTED : GDN_ERR_BAD_DTYPE;
   if (grad_dtype != GDN_F32 && grad_dtype != GDN_BF16) return GDN_ERR_BAD_DTYPE;
-  if (s->B == 0 || s->H == 0) return GDN_OK;
-  if (s->T > 0 && (!Q || !K || !V || !g || !dO || !dQ || !dK || !dV)) return GDN_ERR_NULL_POINTER;
+  if (s->H == 0) return GDN_OK;
+  // without a sequence all rows' gradients are zero, and so are those of the heads' decays
+  const bool rows = s->T > 0 && (s->B > 0 || s->offsets);
+  if (rows && (!Q || !K || !V || !g || !dO || !dQ || !dK || !dV)) return GDN_ERR_NULL_POINTER;
+  if (s->B == 0 && !rows && !(dg && s->g_per_head)) return GDN_OK;
   if (!all_aligned16({Q, K, V, g, S0, dO, dS, dQ, dK, dV, dg, dS0, s->offsets})) return GDN_ERR_BAD_ALIGNMENT;
   gdn::LinLaunch p = lin_launch(s);
   if (!gdn::lin_grid_ok(p, true)) return GDN_ERR_UNSUPPORTED;
-  st = check_workspace(gdn::lin_workspace(p, true), workspace, workspace_bytes);
+  st = check_workspace(s->B > 0 ? gdn::lin_workspace(p, true) : 0, workspace, workspace_bytes);
   if (st != GDN_OK) return st;
   p.Q = Q;
   p.K = K;
@@ -484,8 +487,8 @@ static gdn_status check_gate(int32_t dtype, int32_t B, int32_t H, int64_t T, int
   if (z_stride < (int64_t)H * d) return GDN_ERR_BAD_SHAPE;
   if (z_stride % 8 != 0) return GDN_ERR_BAD_ALIGNMENT;
   if (d % 32 != 0 || d > 256) return GDN_ERR_UNSUPPORTED;
-  // row indices are 32 bits
-  if (H > 0 && B > 0 && T > INT32_MAX / ((int64_t)B * H)) return GDN_ERR_UNSUPPORTED;
+  // row indices and the threads of a launch (at most d / 4 a row) are 32 bits
+  if (H > 0 && B > 0 && T > (((int64_t)1 << 34) - 1) / d / ((int64_t)B * H)) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
 

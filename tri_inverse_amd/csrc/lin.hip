@@ -517,21 +517,47 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
             }
           }
           lds_handover();  // the weights are there
+          // Rows of V behind row i reach it with weight 0, which leaves a finite row out but not
+          // an infinity or a NaN (the rows that pad a batch may hold anything).  Any such value is
+          // in every row of its column of the new state; the sums then run row by row.
+          bool plain = true;
+          if constexpr (!REV && !DOTS) {
+            float x = X[0][0][0];
+            if constexpr (HC > 1) x += X[1][0][0];
+            plain = __builtin_amdgcn_ballot_w64(!(fabsf(x) < __builtin_inff())) == 0;
+          }
+          if (plain) {
 #pragma unroll
-          for (int I = 0; I < LNT; ++I)
+            for (int I = 0; I < LNT; ++I)
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              if (REV ? 2 * p + 1 < I : 2 * p > I) continue;
+              for (int p = 0; p < 2; ++p) {
+                if (REV ? 2 * p + 1 < I : 2 * p > I) continue;
 #pragma unroll
-              for (int k = PARTS - 1; k >= 0; --k) {
-                const bf16x8 wf = weights[k][I][p][l];
+                for (int k = PARTS - 1; k >= 0; --k) {
+                  const bf16x8 wf = weights[k][I][p][l];
 #pragma unroll
-                for (int h = 0; h < HC; ++h) {
-                  f32x4& sum = k > 0 ? low[h][PARTS > 1 ? I : 0] : o[h][I];
-                  sum = mma_bf16(cf[h][p], wf, sum);
+                  for (int h = 0; h < HC; ++h) {
+                    f32x4& sum = k > 0 ? low[h][PARTS > 1 ? I : 0] : o[h][I];
+                    sum = mma_bf16(cf[h][p], wf, sum);
+                  }
                 }
               }
-            }
+          } else {
+            for (int j = 0; j < LC; ++j)
+#pragma unroll
+              for (int I = 0; I < LNT; ++I) {
+                if (j > 16 * I + 15) continue;
+                float wj = 0.f;
+#pragma unroll
+                for (int k = PARTS - 1; k >= 0; --k)
+                  wj += (float)weights[k][I][j / 32][16 * (j % 16 / 4) + c][4 * (j % 32 / 16) + j % 4];
+#pragma unroll
+                for (int h = 0; h < HC; ++h) {
+                  const f32x4 v = unpack4(*reinterpret_cast<const bf16x4*>(cs + LinRows<W>::at(j, col0 + 16 * h + 4 * g)));
+                  if (j <= 16 * I + c) o[h][I] = o[h][I] + wj * v;
+                }
+              }
+          }
           if constexpr (PARTS > 1) {
 #pragma unroll
             for (int h = 0; h < HC; ++h)
@@ -904,8 +930,8 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(const float* dot_q, cons
 
 // per-head decays: the segments' sums in order
 __global__ __launch_bounds__(64) void lin_dgate_head_kernel(const double* dg_seg, float* dg, Cut cut, int H) {
-  int ns;
-  const int n = min(cut.n_seg, first_segment(cut, cut.n_seq - 1, ns) + ns);
+  int ns = 0;
+  const int n = cut.n_seq > 0 ? min(cut.n_seg, first_segment(cut, cut.n_seq - 1, ns) + ns) : 0;
   double x = 0.0;
   for (int s = lane_id(); s < n; s += WAVE) x += dg_seg[(int64_t)s * H + blockIdx.x];
 #pragma unroll
@@ -920,9 +946,11 @@ struct Outside {
   int row_bytes[4];  // a multiple of 4
 };
 __global__ __launch_bounds__(256) void lin_outside_kernel(Outside o, const int32_t* offsets, int n_seq, int64_t T) {
-  int lo, hi, unused;
-  seq_bounds(offsets, 0, T, lo, unused);
-  seq_bounds(offsets, n_seq - 1, T, unused, hi);
+  int lo = (int)T, hi = (int)T, unused;
+  if (n_seq > 0) {
+    seq_bounds(offsets, 0, T, lo, unused);
+    seq_bounds(offsets, n_seq - 1, T, unused, hi);
+  }
   if (hi < lo) hi = lo;
   const int64_t rows = lo + (T - hi);
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
@@ -966,6 +994,7 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 // how a call is cut and where its workspace holds what
 struct LinPlan {
   Cut cut;
+  int64_t n_seg;
   int width;   // columns of c per workgroup, of d_v
   bool ahead;  // the segments' states are formed ahead
   size_t slot_s, slot_d, decay_s, decay_d, dot_q, dot_k, dg_seg, part_q, part_k, bytes;
@@ -1037,7 +1066,8 @@ LinPlan make_plan(const LinLaunch& p, bool bwd) {
   q.cut.chunks = (int)chunks;
   q.cut.segments = (int)ceil_div(longest, chunks);
   // packed: sum over sequences of max(1, ceil(len / (64 chunks))) <= T / (64 chunks) + sequences
-  q.cut.n_seg = (int)(p.offsets ? nch / chunks + p.n_seq : (int64_t)q.cut.segments * p.n_seq);
+  q.n_seg = p.offsets ? nch / chunks + p.n_seq : (int64_t)q.cut.segments * p.n_seq;
+  q.cut.n_seg = (int)q.n_seg;  // lin_grid_ok: it is one
   q.ahead = q.cut.segments > 1;
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -1045,7 +1075,7 @@ LinPlan make_plan(const LinLaunch& p, bool bwd) {
     at += up256(n);
     return x;
   };
-  const size_t one = (size_t)p.d_k * p.d_v * 4, sh = (size_t)q.cut.n_seg * p.H;
+  const size_t one = (size_t)p.d_k * p.d_v * 4, sh = (size_t)q.n_seg * p.H;
   const size_t tokens = (size_t)(p.offsets ? 1 : p.n_seq) * p.H * p.T;
   if (q.ahead || bwd) {
     q.slot_s = take(sh * one);
@@ -1116,9 +1146,13 @@ size_t lin_workspace(const LinLaunch& p, bool bwd) { return make_plan(p, bwd).by
 
 bool lin_grid_ok(const LinLaunch& p, bool bwd) {
   const LinPlan q = make_plan(p, bwd);
-  const int64_t cols = p.d_k > p.d_v ? p.d_k : p.d_v;
-  // with the last round of families filled up
-  return ((int64_t)q.cut.n_seg + 8) * p.H * (cols / 32) < ((int64_t)1 << 31);
+  // threads of a launch are below 2^32; all factors are, and the doubles round by far less than
+  // their products are away from overflow
+  const double most = 4294967295.0, cols = p.d_k > p.d_v ? p.d_k : p.d_v, H = p.H, n_seq = p.n_seq;
+  const double scan = ((double)q.n_seg + 8.0) * H * cols * 12.0;  // 6 waves for 32 columns, the last round of families full
+  const double join = n_seq * H * p.d_k * p.d_v / 4.0;
+  const double sum = (p.offsets ? 1.0 : n_seq) * H * (double)p.T * p.d_k / 4.0;
+  return scan < most && (!q.ahead || join < most) && (!bwd || p.H == p.H_qk || sum < most);
 }
 
 int launch_lin_fwd(const LinLaunch& p, void* workspace, hipStream_t s) {
@@ -1165,6 +1199,11 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
                     {p.d_k * size, p.d_k * size, p.d_v * size, 4}};
     hipLaunchKernelGGL(lin_outside_kernel, dim3(128), dim3(256), 0, s, o, p.offsets, p.n_seq, p.T);
   }
+  if (p.n_seq == 0) {  // no sequence: nothing but zeros
+    if (p.dg && p.g_per_head)
+      hipLaunchKernelGGL(lin_dgate_head_kernel, dim3((unsigned)p.H), dim3(64), 0, s, nullptr, p.dg, q.cut, p.H);
+    return 0;
+  }
   int rc = 0, n_joins = 0;
   JoinArgs joins[2];
   // states after the segments
@@ -1174,7 +1213,7 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
     f.c = bf(p.V);
     f.group_a = f.group_b = group;
     f.dc = p.d_v;
-        f.s_state = 1.f;
+    f.s_state = 1.f;
     f.slot = slot_s;
     f.slot_decay = reinterpret_cast<float*>(ws + q.decay_s);
     f.skip = end ? 0 : 1;
