@@ -82,8 +82,7 @@ struct ScanArgs {
   float* slot_decay;   // [segment][head] decay over the segment, written without OUT
   void* out;
   const __bf16* dotw;  // rows whose product with the output rows goes to dots,
-  float* dots;         // [slice][head row]
-  int64_t heads_T;     // rows of all heads, B * H * T
+  double* dots;        // [head row] (one slice)
   int H, group_a, group_b, group_c, dc;
   Cut cut;
   int g_per_head;
@@ -237,6 +236,16 @@ __device__ __forceinline__ double wave_scan_f64(double v) {
   return v + ((row >= 1 ? t0 : 0.0) + (row >= 2 ? t1 : 0.0) + (row >= 3 ? t2 : 0.0));
 }
 
+// sum over lanes l ^ W (16 or 32)
+template <int W>
+__device__ __forceinline__ double swap_sum_d(double x) {
+  const u32x2 w = __builtin_bit_cast(u32x2, x);
+  uint32_t lo[2], hi[2];
+  self_swap<W>(w[0], lo[0], lo[1]);
+  self_swap<W>(w[1], hi[0], hi[1]);
+  return __builtin_bit_cast(double, u32x2{lo[0], hi[0]}) + __builtin_bit_cast(double, u32x2{lo[1], hi[1]});
+}
+
 // log-decays below 2^-512 are e^g = 0 in every product: clamped, so that -inf (a state that is
 // forgotten) keeps the differences of G finite.  A NaN stays one.
 __device__ __forceinline__ double clamp_log2(double x) { return x < -512.0 ? -512.0 : x; }
@@ -299,8 +308,8 @@ __device__ __forceinline__ void store16b(__amdgpu_buffer_rsrc_t r, int off, cons
 __device__ __forceinline__ void store8b(__amdgpu_buffer_rsrc_t r, int off, const bf16x4& x) {
   __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, x), r, off, 0, 0);
 }
-__device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t r, int off, float x) {
-  __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, x), r, off, 0, 0);
+__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, int off, double x) {
+  __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, x), r, off, 0, 0);
 }
 // 16 bytes a lane straight to LDS, at p + 16 bytes x lane (p uniform)
 __device__ __forceinline__ void load16_lds(__amdgpu_buffer_rsrc_t r, __bf16* p, int off) {
@@ -354,7 +363,7 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
   __shared__ LinRows<W> rows_c[2], rows_w[DOTS ? 2 : 1];
   __shared__ LinGates gates[2];
   __shared__ bf16x8 weights[OUT ? PARTS : 1][LNT][2][WAVE];  // w (a . b) as operands: [part][row tile][32-wide step]
-  __shared__ float dot_part[DOTS ? W / (16 * scan_tiles(W)) : 1][LC];
+  __shared__ double dot_part[DOTS ? W / (16 * scan_tiles(W)) : 1][LC];
   constexpr int HC = scan_tiles(W), COLS = W / (16 * HC), NP = DK / 32;
   constexpr int W_GATES = COLS + (OUT ? 2 : 0), W_ROWS = W_GATES + 1;
 
@@ -568,17 +577,19 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
 #pragma unroll
           for (int I = 0; I < LNT; ++I) {
             if constexpr (DOTS) {
-              float s = 0.f, s0, s1;
+              // four terms in fp32, the sums of these in fp64 (dg on the training workload: 1.07e-6
+              // with fp32 throughout)
+              double s = 0.0;
 #pragma unroll
               for (int h = 0; h < HC; ++h) {
                 const f32x4 w = unpack4(*reinterpret_cast<const bf16x4*>(rows_w[it & 1].v + w_at[h] + 16 * I * W));
+                float four = w[0] * o[h][I][0];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) s = fmaf(w[q], o[h][I][q], s);
+                for (int q = 1; q < 4; ++q) four = fmaf(w[q], o[h][I][q], four);
+                s += (double)four;
               }
-              self_swap_f<16>(s, s0, s1);
-              s = s0 + s1;
-              self_swap_f<32>(s, s0, s1);
-              if (g == 0) dot_part[wave][16 * I + c] = s0 + s1;
+              s = swap_sum_d<32>(swap_sum_d<16>(s));
+              if (g == 0) dot_part[wave][16 * I + c] = s;
             }
             const int at = ooff + 16 * I * A.dc * (int)sizeof(TO);
             if constexpr (PAIR) {
@@ -640,10 +651,10 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
     };
     // products of a chunk's output rows with those of dotw: the column waves' parts in order
     auto sum_dots = [&](int j) {
-      float s = 0.f;
+      double s = 0.0;
 #pragma unroll
       for (int w = 0; w < COLS; ++w) s += dot_part[w][l];
-      store4(chunk_rows(A.dots + slice * A.heads_T, orow, j, 4), 4 * l, s);
+      store8(chunk_rows(A.dots, orow, j, 8), 8 * l, s);
     };
     if (n > 0) {
       store(load(0), gates[0]);
@@ -829,10 +840,10 @@ __global__ __launch_bounds__(256) void lin_join_kernel(JoinArgs a0, JoinArgs a1,
 // rounding errors of the sum grow like a random walk; what it misses the second product by is
 // taken back in proportion to the tokens summed, which leaves a bridge between two exact ends (a
 // third of the mean square error).  All sums in fp64.  Per-head decays: the segment's sum.
-__global__ __launch_bounds__(256) void lin_dgate_kernel(const float* dot_q, const float* dot_k, int n_dots,
-                                                        const float* slot_s, const float* slot_d, const float* S0,
-                                                        const float* dS0, const float* dS, float* dg, double* dg_seg,
-                                                        Cut cut, int64_t heads_T, int H, int size) {
+__global__ __launch_bounds__(256) void lin_dgate_kernel(const double* dot_q, const double* dot_k, const float* slot_s,
+                                                        const float* slot_d, const float* S0, const float* dS0,
+                                                        const float* dS, float* dg, double* dg_seg, Cut cut, int H,
+                                                        int size) {
   __shared__ double red[4][2];
   const int head = (int)blockIdx.x % H;
   const int l = lane_id(), wave = threadIdx.x / WAVE;
@@ -860,15 +871,12 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(const float* dot_q, cons
   constexpr int RUNS = BWD_SEG_CHUNKS * LC / 256;
   const int64_t row0 = ((cut.offsets ? 0 : (int64_t)sp.seq * H) + head) * cut.T + sp.tok0;
   const int t0 = sp.c0 * LC, t1 = min(sp.len, (sp.c0 + sp.nc) * LC);
-  float rq[RUNS][2], rk[RUNS][2];
+  double rq[RUNS], rk[RUNS];
 #pragma unroll
   for (int k = 0; k < RUNS; ++k) {
     const int t = t1 - 1 - (int)threadIdx.x - 256 * k;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      rq[k][s] = s < n_dots && t >= t0 ? dot_q[s * heads_T + row0 + t] : 0.f;
-      rk[k][s] = s < n_dots && t >= t0 ? dot_k[s * heads_T + row0 + t] : 0.f;
-    }
+    rq[k] = t >= t0 ? dot_q[row0 + t] : 0.0;
+    rk[k] = t >= t0 ? dot_k[row0 + t] : 0.0;
   }
   // the states at the segment's two ends (none given: zeros, and so is their product)
   auto of = [&](const float* p, int64_t i) { return p ? p + (i * H + head) * size : nullptr; };
@@ -899,7 +907,7 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(const float* dot_q, cons
   double run = end, at[RUNS];
 #pragma unroll
   for (int k = 0; k < RUNS; ++k) {
-    const double r = wave_scan_f64(((double)rq[k][0] - (double)rk[k][0]) + ((double)rq[k][1] - (double)rk[k][1]));
+    const double r = wave_scan_f64(rq[k] - rk[k]);
     __syncthreads();
     if (l == WAVE - 1) red[wave][0] = r;
     __syncthreads();
@@ -1004,9 +1012,6 @@ bool fits(int d, int width) { return d % width == 0; }
 // of a scan for the segments' states: without outputs there is no w (a . b) to share, and more,
 // smaller workgroups spread better (prefill 179 -> 170 us, 13 packed sequences 160 -> 149)
 int state_width(int width) { return width < 64 ? width : 64; }
-// of d_k in the backward pass (64 or 128)
-int grad_width(int d) { return d == 128 ? 128 : 64; }
-
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Microseconds of one launch, after whole launches at d = 128: a workgroup of 128 / 64 / 32
@@ -1024,7 +1029,7 @@ LinPlan make_plan(const LinLaunch& p, bool bwd) {
   LinPlan q{};
   const int64_t nch = ceil_div(p.T, LC), longest = nch > 0 ? nch : 1;
   const int64_t all = p.offsets ? nch + p.n_seq : longest * p.n_seq;  // chunks, at most
-  q.width = bwd ? grad_width(p.d_v) : fits(p.d_v, 128) ? 128 : fits(p.d_v, 64) ? 64 : 32;
+  q.width = bwd ? p.d_v : fits(p.d_v, 128) ? 128 : fits(p.d_v, 64) ? 64 : 32;
   int64_t chunks = longest;
   if (bwd) {
     // segments bound the sums of dg; shorter ones where the workgroups would be too few
@@ -1084,8 +1089,8 @@ LinPlan make_plan(const LinLaunch& p, bool bwd) {
   if (bwd) {
     q.slot_d = take(sh * one);
     q.decay_d = take(sh * 4);
-    q.dot_q = take(tokens * (p.d_k / grad_width(p.d_k)) * 4);
-    q.dot_k = take(tokens * (p.d_k / grad_width(p.d_k)) * 4);
+    q.dot_q = take(tokens * 8);
+    q.dot_k = take(tokens * 8);
     if (p.g_per_head) q.dg_seg = take(sh * 8);
     if (p.H != p.H_qk) {
       q.part_q = take(tokens * p.d_k * 4);
@@ -1124,7 +1129,6 @@ ScanArgs base_args(const LinLaunch& p, const LinPlan& q) {
   ScanArgs a{};
   a.g = p.g;
   a.cut = q.cut;
-  a.heads_T = (int64_t)(p.offsets ? 1 : p.n_seq) * p.H * p.T;
   a.H = p.H;
   a.group_a = a.group_b = a.group_c = 1;
   a.g_per_head = p.g_per_head;
@@ -1189,7 +1193,6 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   char* ws = reinterpret_cast<char*>(workspace);
   const int group = p.H / p.H_qk;
   const bool end = p.dS != nullptr && p.dg != nullptr;  // <dS, S> at the sequences' ends is wanted
-  const int wk = grad_width(p.d_k);
   float* slot_s = reinterpret_cast<float*>(ws + q.slot_s);
   float* slot_d = reinterpret_cast<float*>(ws + q.slot_d);
   if (p.offsets && p.T > 0) {
@@ -1257,12 +1260,12 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   k.init = p.dS;
   k.slot = slot_d;
   k.dotw = bf(p.K);
-  k.dots = reinterpret_cast<float*>(ws + q.dot_k);
+  k.dots = reinterpret_cast<double*>(ws + q.dot_k);
   k.out = group > 1 ? (void*)(ws + q.part_k) : p.dK;
   const bool part_bf16 = group == 1 && p.grad_bf16;
   k.s_intra = k.s_state = p.scale;
   k.s_inter = 1.f;
-  rc = part_bf16 ? scan<true, true, 3, true, __bf16>(p.d_v, wk, k, s) : scan<true, true, 3, true, float>(p.d_v, wk, k, s);
+  rc = part_bf16 ? scan<true, true, 3, true, __bf16>(p.d_v, p.d_k, k, s) : scan<true, true, 3, true, float>(p.d_v, p.d_k, k, s);
   if (rc) return rc;
   k.a = bf(p.dO);
   k.b = bf(p.V);
@@ -1270,12 +1273,12 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   k.init = p.S0;
   k.slot = slot_s;
   k.dotw = bf(p.Q);
-  k.dots = reinterpret_cast<float*>(ws + q.dot_q);
+  k.dots = reinterpret_cast<double*>(ws + q.dot_q);
   k.out = group > 1 ? (void*)(ws + q.part_q) : p.dQ;
   k.s_intra = k.s_inter = p.scale;
   k.s_state = 1.f;
-  rc = part_bf16 ? scan<false, true, 3, true, __bf16>(p.d_v, wk, k, s)
-                 : scan<false, true, 3, true, float>(p.d_v, wk, k, s);
+  rc = part_bf16 ? scan<false, true, 3, true, __bf16>(p.d_v, p.d_k, k, s)
+                 : scan<false, true, 3, true, float>(p.d_v, p.d_k, k, s);
   if (rc) return rc;
   if (group > 1 && p.T > 0) {
     const int64_t n = (int64_t)(p.offsets ? 1 : p.n_seq) * p.H_qk * p.T * p.d_k;
@@ -1287,9 +1290,8 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   if (!p.dg) return 0;
   double* dg_seg = p.g_per_head ? reinterpret_cast<double*>(ws + q.dg_seg) : nullptr;
   hipLaunchKernelGGL(lin_dgate_kernel, dim3((unsigned)(p.H * q.cut.n_seg)), dim3(256), 0, s,
-                     reinterpret_cast<const float*>(ws + q.dot_q), reinterpret_cast<const float*>(ws + q.dot_k),
-                     p.d_k / wk, slot_s, slot_d, p.S0, p.dS0, p.dS, p.g_per_head ? nullptr : p.dg, dg_seg, q.cut, k.heads_T,
-                     p.H, p.d_k * p.d_v);
+                     reinterpret_cast<const double*>(ws + q.dot_q), reinterpret_cast<const double*>(ws + q.dot_k), slot_s,
+                     slot_d, p.S0, p.dS0, p.dS, p.g_per_head ? nullptr : p.dg, dg_seg, q.cut, p.H, p.d_k * p.d_v);
   if (p.g_per_head)
     hipLaunchKernelGGL(lin_dgate_head_kernel, dim3((unsigned)p.H), dim3(64), 0, s, dg_seg, p.dg, q.cut, p.H);
   return 0;
