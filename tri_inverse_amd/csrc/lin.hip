@@ -1014,15 +1014,46 @@ bool fits(int d, int width) { return d % width == 0; }
 int state_width(int width) { return width < 64 ? width : 64; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Microseconds of one launch, after whole launches at d = 128: a workgroup of 128 / 64 / 32
-// columns takes 3.0 / 2.3 / 2.05 a chunk with outputs (one workgroup a CU) and 1.7 / 1.5 at 64 /
-// 32 columns without (two a CU), starts and ends in 8, and memory gives 4.5 MB a microsecond.
-double scan_cost(const LinLaunch& p, int width, int64_t groups, int64_t chunks, bool out, double bytes) {
+// Microseconds of one scan, after whole launches at d = 128: a workgroup of 128 / 64 / 32 columns
+// takes 3.0 / 2.3 / 2.05 a chunk with outputs (one workgroup a CU) and 1.7 / 1.5 at 64 / 32
+// columns without (two a CU), starts and ends in 8, and memory gives 4.5 MB a microsecond.
+// Segments of equal length run in whole rounds; packed sequences leave segments of all lengths,
+// and whichever CU is free takes the next.  groups workgroups of at most len chunks, all chunks.
+double scan_cost(const LinLaunch& p, int width, double groups, double len, double all, bool out, double bytes) {
   const double chunk = (out ? (width == 128 ? 3.0 : width == 64 ? 2.3 : 2.05) : width == 64 ? 1.7 : 1.5) *
                        (p.d_k == 128 ? 1.0 : 0.7);
-  const double work = (double)ceil_div(groups, out ? 256 : 512) * ((double)chunks * chunk + 8.0);
+  const double rounds = groups / (out ? 256 : 512);
+  const double work = rounds <= 1.0 || !p.offsets
+                          ? ceil(rounds) * (len * chunk + 8.0)
+                          : (all / groups * rounds + 0.5 * len) * chunk + 8.0 * rounds;
   const double memory = bytes / 4.5e6 + 6.0;
   return work > memory ? work : memory;
+}
+
+// Microseconds of a whole pass over segments of len chunks by workgroups of width columns
+double plan_cost(const LinLaunch& p, bool bwd, int width, int64_t len) {
+  const int64_t longest = ceil_div(p.T, LC), per = ceil_div(longest, len);
+  // packed: sequences end half a chunk and half a segment before the next on average; one of
+  // them may hold nearly all tokens
+  const double seqs = p.offsets ? 1.0 : p.n_seq, ends = p.offsets ? 0.5 * p.n_seq : 0.0;
+  const double all = (double)longest * seqs + ends;
+  double n = p.offsets ? all / (double)len + ends : (double)(per * p.n_seq);
+  if (n < p.n_seq) n = p.n_seq;
+  const double slices = p.d_v / width, H = p.H;
+  const double bytes = seqs * (double)p.T * 2.0 * ((double)p.H_qk * p.d_k + H * p.d_v);  // K and V
+  // dQ and dK in three parts take 5.2 a chunk, dV 3.1
+  double cost = bwd ? 3.0 * scan_cost(p, width, n * H, 1.5 * (double)len, 1.5 * all * H, true, 3.0 * bytes)
+                    : scan_cost(p, width, n * H * slices, (double)len, all * H * slices, true, 2.0 * bytes);
+  if (per > 1) {
+    const int w = state_width(width);
+    const double inner = (n - seqs) * H * (p.d_v / w), most = all * H * (p.d_v / w);
+    const double state = 4.0 * p.H * p.d_k * p.d_v, share = (double)(per - 1) / (double)per;
+    // the segments' states, and joining them: read and written (backwards both kinds, and read
+    // once more for dg)
+    cost += (bwd ? 2.0 : 1.0) * scan_cost(p, w, inner, (double)len, most * share, false, bytes * share) + 8.0 +
+            (bwd ? 8.0 : 2.0) * n * state / 6e6;
+  }
+  return cost;
 }
 
 LinPlan make_plan(const LinLaunch& p, bool bwd) {
@@ -1030,40 +1061,38 @@ LinPlan make_plan(const LinLaunch& p, bool bwd) {
   const int64_t nch = ceil_div(p.T, LC), longest = nch > 0 ? nch : 1;
   const int64_t all = p.offsets ? nch + p.n_seq : longest * p.n_seq;  // chunks, at most
   q.width = bwd ? p.d_v : fits(p.d_v, 128) ? 128 : fits(p.d_v, 64) ? 64 : 32;
+  // Whole sequences, or segments for more workgroups: their own states cost another reading of K
+  // and V, and the launches and the joining some more.  B4 H16 T8192 d128: four segments a
+  // sequence 181 us, eight 203, whole sequences in four slices of 32 columns 262; 128 heads of
+  // 4096: two slices 151, two segments about 200 (as measured when the rule was set).  Backwards
+  // (12 heads, 7 packed sequences, 5003 tokens) segments of 4 chunks 123 us, 5 108, 6 113, 8 127.
+  // There a segment also bounds the sums of dg.
   int64_t chunks = longest;
+  double best = 1e300;
+  const int widest = q.width;
+  auto consider = [&](int width, int64_t len) {
+    const double cost = plan_cost(p, bwd, width, len);
+    if (cost < best) {
+      best = cost;
+      q.width = width;
+      chunks = len;
+    }
+  };
   if (bwd) {
-    // segments bound the sums of dg; shorter ones where the workgroups would be too few
-    if (chunks > BWD_SEG_CHUNKS) chunks = BWD_SEG_CHUNKS;
-    const int64_t items = (int64_t)p.H * (p.d_v / q.width);
-    while (chunks > 4 && ceil_div(all, chunks) * items < 256) chunks = (chunks + 1) / 2;
+    for (int64_t len = BWD_SEG_CHUNKS < longest ? BWD_SEG_CHUNKS : longest; len >= (longest < 2 ? 1 : 2); --len)
+      consider(widest, len);
   } else if (longest > 4) {
-    // Whole sequences, or segments that give every CU one to four workgroups: their own states
-    // cost another reading of K and V, and the launches and the joining some more.  B4 H16
-    // T8192 d128: four segments a sequence 181 us, eight 203, whole sequences in four slices
-    // of 32 columns 262; 128 heads of 4096: two slices 151, two segments about 200 (as measured
-    // when the rule was set).
-    const double rows = (double)(p.offsets ? 1 : p.n_seq) * (double)p.T;
-    const double bytes = rows * 2.0 * ((double)p.H_qk * p.d_k + (double)p.H * p.d_v);  // K and V
-    const double state = 4.0 * p.H * p.d_k * p.d_v;
-    const int64_t seqs = p.offsets ? 1 : p.n_seq;  // packed: one may hold nearly all tokens
-    double best = 1e300;
-    const int widest = q.width;
-    for (int w = widest; w >= 32; w /= 2)
-      for (int rounds = 0; rounds <= 4; ++rounds) {
-        const int64_t items = (int64_t)p.H * (p.d_v / w);
-        int64_t len = rounds ? ceil_div(all * items, 256 * rounds) : longest;
-        len = len < 4 ? 4 : len > longest ? longest : len;
-        const int64_t per = ceil_div(longest, len), n = p.offsets ? ceil_div(all, len) : p.n_seq * per;
-        double cost = scan_cost(p, w, n * items, len, true, 2.0 * bytes);
-        if (per > 1)
-          cost += scan_cost(p, state_width(w), (n - seqs) * p.H * (p.d_v / state_width(w)), len, false,
-                            bytes * (double)(per - 1) / (double)per) + 8.0 + 3.0 * (double)n * state / 4e6;
-        if (cost < best) {
-          best = cost;
-          q.width = w;
-          chunks = len;
+    for (int w = widest; w >= 32; w /= 2) {
+      consider(w, longest);
+      if (p.offsets) {
+        for (int64_t len = 4; len < longest; len += 1 + len / 4) consider(w, len);
+      } else {
+        for (int rounds = 1; rounds <= 4; ++rounds) {
+          const int64_t len = ceil_div(all * p.H * (p.d_v / w), 256 * rounds);
+          if (len < longest) consider(w, len < 2 ? 2 : len);
         }
       }
+    }
   }
   q.cut.offsets = p.offsets;
   q.cut.T = p.T;
