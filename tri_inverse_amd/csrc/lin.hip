@@ -18,14 +18,15 @@
 // Gradient of the log-decays: with r_t = q_t . dq_t - k_t . dk_t, dg_t = sum_{s>=t} r_s over
 // the rest of the sequence + <dS_out, S_out>.  Summed over a whole long sequence the
 // differences r_s would lose digits, so the sum runs within a segment of at most 1024 tokens,
-// between <D, S> at the segment's two ends, formed from the states there.
+// between <D, S> at the segment's two ends, formed from the states there.  The products q . dq and
+// k . dk are summed in fp64 from four terms on.
 //
 // Precision: a, b and c are bf16 as given, so a . b is exact up to the fp32 sums of the MFMA.
 // The fp32 factor of every other product enters as a sum of bf16 parts.  col c (the state) is
 // three parts, which hold all 24 bits: the state is carried from chunk to chunk in fp32 and
 // returned so.  w (a . b) and X in the outputs: fp32 outputs, and dQ and dK, whose products with
 // q and k make dg as small differences, take three parts (two left 1e-5 in dg on the training
-// workload, three 1.4e-6); O and dV in bf16 take one, whose rounding is as large as that of the
+// workload, three 4e-7); O and dV in bf16 take one, whose rounding is as large as that of the
 // output itself (0.0023 against 0.0017 in the norm with two; 8 to 30 % of the time).  G is
 // summed in fp64 and handed over as two floats: the exponent of w is a difference of two sums
 // that can both be large.
@@ -45,10 +46,19 @@
 // formed first (the same kernel without outputs), the segments are joined in order, and every
 // segment then starts from its state.
 //
-// What bounds it: with every CU at work, memory and the column waves' issue together.  256 heads
-// of 2048 tokens (whole sequences, 537 MB) take 119 us, 4.5 TB/s.  A chunk of a column wave is
-// 140 MFMA (2240 cycles) and about 460 vector instructions (1840), of which little overlaps, 330
-// KB of LDS traffic in all; without its loads the prefill workload still took 171 of 185 us.
+// What bounds it: the issue of the column waves, then memory.  A chunk of a column wave is 140
+// MFMA (2240 cycles) and about 460 vector instructions (1840) on one SIMD, of which little
+// overlaps, and 330 KB of LDS traffic in all; without its loads the prefill workload took 171 of
+// 185 us.  256 heads of 2048 tokens, whole sequences (537 MB), take 119 us, 4.5 TB/s.
+// Measured, whole calls (profiles of the single kernels: MFMA busy 34 %, VALU 38 %):
+//   forward   B4 H16 T8192 d128                166-171 us (3.2 TB/s of inputs and outputs; 60 us
+//                                              of it the segments' states, read a second time)
+//             B1 H8 T32768 d128                91 us
+//             13 packed, 11171 tokens, H16 128 x 256   145-151 us (uneven segments)
+//   backward  B4 H16 T4096 d128                291 us (dQ and dK 85-95 each, dV 55, states 70,
+//                                              joining 10, dg 13)
+//             7 packed, 5003 tokens, H12 64 x 128      108 us (one round of 5 chunks in each of
+//                                              five scans, ten launches)
 #include "gdn_kernels.hpp"
 #include "gdn_device.hpp"
 
@@ -59,6 +69,7 @@ namespace {
 constexpr int LC = 64;     // tokens of a chunk
 constexpr int LNT = 4;     // 16-row tiles of a chunk
 constexpr int BWD_SEG_CHUNKS = 16;  // at most 1024 tokens are summed into dg from one pair of states
+constexpr int JOIN_GROUPS = 2048;    // 256 CUs with eight workgroups each
 constexpr double LOG2E = 1.4426950408889634;
 
 // How sequences are cut into segments, runs of chunks that one workgroup (for some columns) walks
@@ -453,7 +464,7 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
       const int ooff = (c * A.dc + slice * W + col0 + (PAIR ? 16 * (g & 1) + 8 * (g >> 1) : 4 * g)) * (int)sizeof(TO);
       lds_handover();
       for (int it = 0; it < n; ++it) {
-        if constexpr (OUT && PARTS == 1) __builtin_amdgcn_iglp_opt(1);  // interleaves MFMA and VALU: 3 to 8 % less
+        if constexpr (OUT && PARTS == 1) __builtin_amdgcn_iglp_opt(1);  // interleaves MFMA and VALU: 3 to 8 % less time (three parts: none)
         const LinGates& GT = gates[it & 1];
         const __bf16* bs = rows_b[it & 1].v;
         const __bf16* cs = rows_c[it & 1].v;
@@ -794,44 +805,44 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
 }
 
 // The segments' own states joined in order, from the states given per sequence: slot[k] becomes
-// the state after segment k, or before it (back).  One thread per four state values.
+// the state after segment k, or before it (back).  Threads take four values of a state at a time;
 struct JoinArgs {
   float* slot;
   const float* decay;
   const float* init;
   int skip, back;
 };
-__global__ __launch_bounds__(256) void lin_join_kernel(JoinArgs a0, JoinArgs a1, Cut cut, int H, int size) {
+// per workgroups share a state.
+__global__ __launch_bounds__(256) void lin_join_kernel(JoinArgs a0, JoinArgs a1, Cut cut, int H, int size, int per) {
   const JoinArgs a = blockIdx.y ? a1 : a0;
-  const int per = (size / 4 + 255) / 256;  // workgroups of one state
   const int head = (int)(blockIdx.x / per) % H, seq = (int)(blockIdx.x / per) / H;
   int ns;
   const int s0 = first_segment(cut, seq, ns);
   if (s0 + ns > cut.n_seg) return;  // offsets out of order: more segments than there can be
   const int n = ns - a.skip;
-  const int e = 4 * (int)((blockIdx.x % per) * 256 + threadIdx.x);
-  if (e >= size) return;
-  f32x4 x = a.init ? *reinterpret_cast<const f32x4*>(a.init + ((int64_t)seq * H + head) * size + e) : zero4();
   // eight segments' values asked for together: the loads do not wait for the sums
   constexpr int N = 8;
-  for (int i0 = 0; i0 < n; i0 += N) {
-    f32x4* at[N];
-    f32x4 v[N];
-    float d[N];
+  for (int e = 4 * (int)((blockIdx.x % per) * 256 + threadIdx.x); n > 0 && e < size; e += 1024 * per) {
+    f32x4 x = a.init ? *reinterpret_cast<const f32x4*>(a.init + ((int64_t)seq * H + head) * size + e) : zero4();
+    for (int i0 = 0; i0 < n; i0 += N) {
+      f32x4* at[N];
+      f32x4 v[N];
+      float d[N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int i = min(i0 + k, n - 1);
-      const int64_t sh = (int64_t)(a.back ? s0 + ns - 1 - i : s0 + i) * H + head;
-      at[k] = reinterpret_cast<f32x4*>(a.slot + sh * size + e);
-      v[k] = *at[k];
-      d[k] = a.decay[sh];
-    }
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (i0 + k < n) {
-        x = x * d[k] + v[k];
-        *at[k] = x;
+      for (int k = 0; k < N; ++k) {
+        const int i = min(i0 + k, n - 1);
+        const int64_t sh = (int64_t)(a.back ? s0 + ns - 1 - i : s0 + i) * H + head;
+        at[k] = reinterpret_cast<f32x4*>(a.slot + sh * size + e);
+        v[k] = *at[k];
+        d[k] = a.decay[sh];
       }
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (i0 + k < n) {
+          x = x * d[k] + v[k];
+          *at[k] = x;
+        }
+    }
   }
 }
 
@@ -839,7 +850,8 @@ __global__ __launch_bounds__(256) void lin_join_kernel(JoinArgs a0, JoinArgs a1,
 // (q_s . dq_s - k_s . dk_s), and at the segment's first token dg is <D, S> before it.  The
 // rounding errors of the sum grow like a random walk; what it misses the second product by is
 // taken back in proportion to the tokens summed, which leaves a bridge between two exact ends (a
-// third of the mean square error).  All sums in fp64.  Per-head decays: the segment's sum.
+// third of the mean square error).  Bound by memory: four states a segment (B4 H16 T4096 d128: 67
+// MB in 13 us).  All sums in fp64.  Per-head decays: the segment's sum.
 __global__ __launch_bounds__(256) void lin_dgate_kernel(const double* dot_q, const double* dot_k, const float* slot_s,
                                                         const float* slot_d, const float* S0, const float* dS0,
                                                         const float* dS, float* dg, double* dg_seg, Cut cut, int H,
@@ -1166,9 +1178,14 @@ ScanArgs base_args(const LinLaunch& p, const LinPlan& q) {
 
 // joins n (1 or 2) sets of segment states
 void join(const JoinArgs* a, int n, const LinLaunch& p, const LinPlan& q, hipStream_t s) {
-  const int size = p.d_k * p.d_v;
-  const dim3 grid((unsigned)((size / 4 + 255) / 256 * p.H * p.n_seq), (unsigned)n), block(256);
-  hipLaunchKernelGGL(lin_join_kernel, grid, block, 0, s, a[0], a[n - 1], q.cut, p.H, size);
+  const int size = p.d_k * p.d_v, heads = p.H * p.n_seq;
+  // a state's values over as many workgroups as keep the GPU in one round of them: each has to
+  // find its segments first (13 packed sequences, 16 heads, 128 x 256: the call takes 145.3 us,
+  // 146.6 with 32 workgroups each, 149.4 with half as many as here)
+  int per = JOIN_GROUPS / heads;
+  per = per < 1 ? 1 : per > (size + 1023) / 1024 ? (size + 1023) / 1024 : per;
+  const dim3 grid((unsigned)(per * heads), (unsigned)n), block(256);
+  hipLaunchKernelGGL(lin_join_kernel, grid, block, 0, s, a[0], a[n - 1], q.cut, p.H, size, per);
 }
 
 const __bf16* bf(const void* p) { return reinterpret_cast<const __bf16*>(p); }
@@ -1183,9 +1200,8 @@ bool lin_grid_ok(const LinLaunch& p, bool bwd) {
   // their products are away from overflow
   const double most = 4294967295.0, cols = p.d_k > p.d_v ? p.d_k : p.d_v, H = p.H, n_seq = p.n_seq;
   const double scan = ((double)q.n_seg + 8.0) * H * cols * 12.0;  // 6 waves for 32 columns, the last round of families full
-  const double join = n_seq * H * p.d_k * p.d_v / 4.0;
   const double sum = (p.offsets ? 1.0 : n_seq) * H * (double)p.T * p.d_k / 4.0;
-  return scan < most && (!q.ahead || join < most) && (!bwd || p.H == p.H_qk || sum < most);
+  return scan < most && (!bwd || p.H == p.H_qk || sum < most);
 }
 
 int launch_lin_fwd(const LinLaunch& p, void* workspace, hipStream_t s) {

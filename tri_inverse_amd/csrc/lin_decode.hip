@@ -7,7 +7,12 @@
 //
 // One wave per (b, h, 32 columns of d_v).  Lane l = 8 rg + cg holds columns 4 cg .. + 3 of
 // rows RPL rg .. + RPL - 1 (RPL = d_k / 8); every access to S moves 8 rows of 128 bytes.
-// The output's sum over d_k runs over a lane's rows, then over the 8 row groups.
+// The output's sum over d_k runs over a lane's rows, then over the 8 row groups.  A wave for
+// each 32 columns and not for a head: one token is all latency, and 8 KB of state a wave keeps
+// enough loads in flight.
+//
+// Measured: 64 sequences, 32 heads, d = 128, one token: 47.5 us for 270 MB, 5.7 TB/s (a copy of
+// 1 GiB reaches 5.2); one sequence 4.3 us, launch and the latency of one round of loads.
 #include "gdn_device.hpp"
 #include "gdn_kernels.hpp"
 
