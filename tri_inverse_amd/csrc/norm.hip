@@ -18,7 +18,7 @@
 // Measured (a copy of 1 GiB reaches 5.2 TB/s): gated norm B4 H16 T8192 d128 bf16, 403 MB, 74 us,
 // 5.4 TB/s (its vector instructions, the exponentials mostly, take as long); backward B3 H16
 // T4099, 252 MB, 57 us of which the column sum 4.7; residual norm backward, 16384 rows of 4096,
-// fp32 and bf16, 1208 MB, 229 us, 5.3 TB/s; forward, 64 rows of 2048, 3.4 us, latency.
+// fp32 and bf16, 1208 MB, 226 us, 5.4 TB/s; forward, 64 rows of 2048, 3.4 us, latency.
 #include "gdn_device.hpp"
 #include "gdn_kernels.hpp"
 
@@ -472,6 +472,8 @@ int by_lanes(int d, F&& f) {
 
 // Waves and vectors of a row by its length: 8 values a lane where 16 waves hold the row, so that
 // the row's tensors and, backwards, two column sums fit the registers; 16 values above 8192.
+// Backwards one such row fills a CU's registers, so nothing hides its latency: 4096 rows of
+// 16384 run at 2.7 TB/s, 8192 rows of 8192 at 5.1 (forwards 4.9 and 5.4).
 template <class F>
 int by_row(int D, F&& f) {
   using std::integral_constant;
