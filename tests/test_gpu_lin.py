@@ -568,3 +568,23 @@ def test_c_refusals_of_launches_too_large():
     assert tri.gdn_lin_chunk_fwd_workspace_bytes(2 ** 30, 1, 2 ** 30, 64, 64) == 0
     assert tri.gdn_lin_chunk_bwd_workspace_bytes(2 ** 30, 1, 2 ** 30, 64, 64) == 0
     assert tri._lib.gdn_gate_norm_fwd(FAKE, FAKE, 4 * 128, None, FAKE, 1, 2, 4, 2 ** 24, 128, 0, 1e-6, None) == 5
+
+
+@gpu
+def test_no_tokens_without_tensors():
+    """T = 0 from C with every tensor of rows NULL, a decay per head among them: the states pass."""
+    say("lin C calls, T=0, no tensors")
+    S0 = torch.randn((2, 3, 64, 64), device="cuda")
+    S, D = torch.full_like(S0, 7.0), torch.full_like(S0, 7.0)
+    for per_head in (0, 1):
+        sh = tri.gdn_lin_shape(0, None, 2, 3, 3, 64, 64, per_head, 1.0)
+        stream = torch.cuda.current_stream().cuda_stream
+        assert tri._lib.gdn_lin_chunk_fwd(ctypes.byref(sh), None, None, None, tri.GDN_BF16, None, S0.data_ptr(), None,
+                                          tri.GDN_BF16, S.data_ptr(), None, 0, stream) == 0
+        need = tri._lib.gdn_lin_chunk_bwd_workspace_bytes(ctypes.byref(sh))
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+        assert tri._lib.gdn_lin_chunk_bwd(ctypes.byref(sh), None, None, None, tri.GDN_BF16, None, S0.data_ptr(), None,
+                                          S0.data_ptr(), None, None, None, tri.GDN_BF16, None, D.data_ptr(),
+                                          ws.data_ptr(), need, stream) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(S, S0) and torch.equal(D, S0)

@@ -632,7 +632,7 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
   if (wave == W_GATES) {
     // ---- decay factors, one chunk ahead (lane = token) ----------------------------------
     double decay = 0.0;  // sum of G_C over the segment
-    const float g_head = A.g_per_head ? A.g[head] : 0.f;
+    const float g_head = n > 0 && A.g_per_head ? A.g[head] : 0.f;  // without tokens g may be NULL
     auto load = [&](int j) {
       const int t0 = token_of(j);
       if (A.g_per_head) return t0 + l < sp.len ? g_head : 0.f;
