@@ -46,13 +46,14 @@
 // formed first (the same kernel without outputs), the segments are joined in order, and every
 // segment then starts from its state.
 //
-// What bounds it: the issue of the column waves, then memory.  A chunk of a column wave is 140
-// MFMA (2240 cycles) and about 460 vector instructions (1840) on one SIMD, of which little
-// overlaps, and 330 KB of LDS traffic in all; without its loads the prefill workload took 171 of
-// 185 us.  256 heads of 2048 tokens, whole sequences (537 MB), take 119 us, 4.5 TB/s.
-// Measured, whole calls (profiles of the single kernels: MFMA busy 34 %, VALU 38 %):
-//   forward   B4 H16 T8192 d128                166-171 us (3.2 TB/s of inputs and outputs; 60 us
-//                                              of it the segments' states, read a second time)
+// What bounds it: memory for one part (O, dV: 5.3 to 5.6 TB/s of what they move, where a copy
+// reaches 5.2), the issue of the column waves for three parts (dQ, dK: 4.1 TB/s) and for the
+// states alone (3.6 to 3.9).  A chunk of a column wave with one part is 140 MFMA (2240 cycles) and
+// about 460 vector instructions (1840) on one SIMD, of which little overlaps, and 330 KB of LDS
+// traffic in all.  256 heads of 2048 tokens, whole sequences (537 MB), take 119 us.
+// Measured, whole calls:
+//   forward   B4 H16 T8192 d128                166-171 us (800 MB moved: 100 the outputs, 56 the
+//                                              segments' states, which read K and V again)
 //             B1 H8 T32768 d128                91 us
 //             13 packed, 11171 tokens, H16 128 x 256   145-151 us (uneven segments)
 //   backward  B4 H16 T4096 d128                291 us (dQ and dK 85-95 each, dV 55, states 70,
