@@ -26,10 +26,11 @@
 // three parts, which hold all 24 bits: the state is carried from chunk to chunk in fp32 and
 // returned so.  w (a . b) and X in the outputs: fp32 outputs, and dQ and dK, whose products with
 // q and k make dg as small differences, take three parts (two left 1e-5 in dg on the training
-// workload, three 4e-7); O and dV in bf16 take one, whose rounding is as large as that of the
-// output itself (0.0023 against 0.0017 in the norm with two; 8 to 30 % of the time).  G is
-// summed in fp64 and handed over as two floats: the exponent of w is a difference of two sums
-// that can both be large.
+// workload, three 4e-7); O and dV in bf16 take one of X, whose rounding is as large as
+// that of the output itself, and two of w (a . b), whose roundings whole rows share (a call of 10
+// tokens: 0.0025 in the norm with one, 0.0017 is the output's own).  Two of X would take 12 to
+// 17 % of the time, the second of w (a . b) 2 %.  G is summed in fp64 and handed over as two
+// floats: the exponent of w is a difference of two sums that can both be large.
 //
 // Work split: one workgroup per (segment, head, W columns of c), W = 32, 64 or 128.
 //   column waves  32 columns each at W = 128, else 16: they keep their columns of X in
@@ -48,15 +49,15 @@
 //
 // What bounds it: memory for one part (O, dV: 5.3 to 5.6 TB/s of what they move, where a copy
 // reaches 5.2), the issue of the column waves for three parts (dQ, dK: 4.1 TB/s) and for the
-// states alone (3.6 to 3.9).  A chunk of a column wave with one part is 140 MFMA (2240 cycles) and
-// about 460 vector instructions (1840) on one SIMD, of which little overlaps, and 330 KB of LDS
+// states alone (3.6 to 3.9).  A chunk of a column wave with one part of X is 152 MFMA (2430 cycles)
+// and about 460 vector instructions (1840) on one SIMD, of which little overlaps, and 330 KB of LDS
 // traffic in all.  256 heads of 2048 tokens, whole sequences (537 MB), take 119 us.
 // Measured, whole calls:
-//   forward   B4 H16 T8192 d128                166-171 us (800 MB moved: 100 the outputs, 56 the
+//   forward   B4 H16 T8192 d128                168-178 us (800 MB moved: 100 the outputs, 56 the
 //                                              segments' states, which read K and V again)
-//             B1 H8 T32768 d128                91 us
-//             13 packed, 11171 tokens, H16 128 x 256   145-151 us (uneven segments)
-//   backward  B4 H16 T4096 d128                291 us (dQ and dK 85-95 each, dV 55, states 70,
+//             B1 H8 T32768 d128                92-98 us
+//             13 packed, 11171 tokens, H16 128 x 256   147-151 us (uneven segments)
+//   backward  B4 H16 T4096 d128                291-320 us (dQ and dK 85-95 each, dV 55, states 70,
 //                                              joining 10, dg 13)
 //             7 packed, 5003 tokens, H12 64 x 128      108 us (one round of 5 chunks in each of
 //                                              five scans, ten launches)
@@ -372,12 +373,13 @@ constexpr int scan_per_simd(int W, bool out) { return (scan_waves(W, out) * (out
 
 template <int DK, int W, bool REV, bool OUT, int PARTS, bool DOTS, class TO>
 __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) void lin_scan_kernel(ScanArgs A) {
+  constexpr int WPARTS = PARTS == 1 ? 2 : PARTS;  // of w (a . b)
   // two slots of everything: one in use, one being filled (a third for the rows measured level:
   // 191 against 185 us on the prefill workload)
   __shared__ LinRows<DK> rows_a[OUT ? 2 : 1], rows_b[2];
   __shared__ LinRows<W> rows_c[2], rows_w[DOTS ? 2 : 1];
   __shared__ LinGates gates[2];
-  __shared__ bf16x8 weights[OUT ? PARTS : 1][LNT][2][WAVE];  // w (a . b) as operands: [part][row tile][32-wide step]
+  __shared__ bf16x8 weights[OUT ? WPARTS : 1][LNT][2][WAVE];  // w (a . b) as operands: [part][row tile][32-wide step]
   __shared__ double dot_part[DOTS ? W / (16 * scan_tiles(W)) : 1][LC];
   constexpr int HC = scan_tiles(W), COLS = W / (16 * HC), NP = DK / 32;
   constexpr int W_GATES = COLS + (OUT ? 2 : 0), W_ROWS = W_GATES + 1;
@@ -557,11 +559,11 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
               for (int p = 0; p < 2; ++p) {
                 if (REV ? 2 * p + 1 < I : 2 * p > I) continue;
 #pragma unroll
-                for (int k = PARTS - 1; k >= 0; --k) {
+                for (int k = WPARTS - 1; k >= 0; --k) {
                   const bf16x8 wf = weights[k][I][p][l];
 #pragma unroll
                   for (int h = 0; h < HC; ++h) {
-                    f32x4& sum = k > 0 ? low[h][PARTS > 1 ? I : 0] : o[h][I];
+                    f32x4& sum = PARTS > 1 && k > 0 ? low[h][PARTS > 1 ? I : 0] : o[h][I];
                     sum = mma_bf16(cf[h][p], wf, sum);
                   }
                 }
@@ -573,7 +575,7 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
                 if (j > 16 * I + 15) continue;
                 float wj = 0.f;
 #pragma unroll
-                for (int k = PARTS - 1; k >= 0; --k)
+                for (int k = WPARTS - 1; k >= 0; --k)
                   wj += (float)weights[k][I][j / 32][16 * (j % 16 / 4) + c][4 * (j % 32 / 16) + j % 4];
 #pragma unroll
                 for (int h = 0; h < HC; ++h) {
@@ -790,10 +792,10 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             if (REV ? 2 * p + 1 < I : 2 * p > I) continue;
-            bf16x8 s[PARTS];
-            split<PARTS>(P[i][2 * p], P[i][2 * p + 1], s);
+            bf16x8 s[WPARTS];
+            split<WPARTS>(P[i][2 * p], P[i][2 * p + 1], s);
 #pragma unroll
-            for (int k = 0; k < PARTS; ++k) weights[k][I][p][l] = s[k];
+            for (int k = 0; k < WPARTS; ++k) weights[k][I][p][l] = s[k];
           }
         }
         lds_handover();
@@ -1231,8 +1233,8 @@ int launch_lin_fwd(const LinLaunch& p, void* workspace, hipStream_t s) {
     const JoinArgs j{a.slot, a.slot_decay, p.S0, 1, 0};
     join(&j, 1, p, q, s);
   }
-  // a bf16 output is formed with its fp32 factors as one bf16 part: each term is rounded once
-  // more, together as much as the output's own rounding; an fp32 output with three
+  // a bf16 output is formed with X as one bf16 part: each of its terms is rounded once more,
+  // together as much as the output's own rounding; an fp32 output with three
   return p.o_bf16 ? scan<false, true, 1, false, __bf16>(p.d_k, q.width, a, s)
                   : scan<false, true, 3, false, float>(p.d_k, q.width, a, s);
 }
