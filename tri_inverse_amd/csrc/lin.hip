@@ -22,15 +22,15 @@
 // k . dk are summed in fp64 from four terms on.
 //
 // Precision: a, b and c are bf16 as given, so a . b is exact up to the fp32 sums of the MFMA.
-// The fp32 factor of every other product enters as a sum of bf16 parts.  col c (the state) is
-// three parts, which hold all 24 bits: the state is carried from chunk to chunk in fp32 and
-// returned so.  w (a . b) and X in the outputs: fp32 outputs, and dQ and dK, whose products with
-// q and k make dg as small differences, take three parts (two left 1e-5 in dg on the training
-// workload, three 4e-7); O and dV in bf16 take one of X, whose rounding is as large as
-// that of the output itself, and two of w (a . b), whose roundings whole rows share (a call of 10
-// tokens: 0.0025 in the norm with one, 0.0017 is the output's own).  Two of X would take 12 to
-// 17 % of the time, the second of w (a . b) 2 %.  G is summed in fp64 and handed over as two
-// floats: the exponent of w is a difference of two sums that can both be large.
+// The fp32 factor of every other product (col c of the state, X and w (a . b) of the outputs)
+// enters as a sum of three bf16 parts, which hold all 24 bits.  The state is carried from chunk
+// to chunk in fp32 and returned so, and an output in bf16 is the one in fp32 rounded once: its
+// type changes no product.  For bf16 outputs one part of X and two of w (a . b) would take 169
+// instead of 217 us on the prefill workload, two of both 203; but where decays are slow one part
+// leaves O at 0.0023 in the norm (0.0017 is its own rounding), and two leave 1e-5 in dg, the
+// small difference of products with q and k, where three leave 4e-7.  G is summed in fp64 and
+// handed over as two floats: the exponent of w is a difference of two sums that can both be
+// large.
 //
 // Work split: one workgroup per (segment, head, W columns of c), W = 32, 64 or 128.
 //   column waves  32 columns each at W = 128, else 16: they keep their columns of X in
@@ -40,26 +40,24 @@
 //   one wave forms the next chunk's decay factors, one loads its rows of a, b and c straight
 //   into LDS.
 // What a workgroup does per chunk whatever its columns (w (a . b), the rows of a and b) is
-// shared by W columns, so wide workgroups take fewer instructions: B4 H16 T8192 d128 took 185 us
-// as 256 workgroups of 32 columns over whole sequences, 171 as 256 of 128 columns over quarters,
+// shared by W columns, so wide workgroups take fewer instructions: B4 H16 T8192 d128 takes 305 us
+// as 256 workgroups of 32 columns over whole sequences, 217 as 256 of 128 columns over quarters,
 // their states formed first.  A segment is a run of chunks of one sequence: where sequences and
 // heads alone fill the GPU a segment is a whole sequence; else each segment's own state is
 // formed first (the same kernel without outputs), the segments are joined in order, and every
 // segment then starts from its state.
 //
-// What bounds it: memory for one part (O, dV: 5.3 to 5.6 TB/s of what they move, where a copy
-// reaches 5.2), the issue of the column waves for three parts (dQ, dK: 4.1 TB/s) and for the
-// states alone (3.6 to 3.9).  A chunk of a column wave with one part of X is 152 MFMA (2430 cycles)
-// and about 460 vector instructions (1840) on one SIMD, of which little overlaps, and 330 KB of LDS
-// traffic in all.  256 heads of 2048 tokens, whole sequences (537 MB), take 119 us.
+// What bounds it: the issue of the column waves, and where they wait for the weights in the middle
+// of a chunk.  A chunk of a column wave of 32 columns at d_k = 128 is 228 MFMA (3650 cycles) on one
+// SIMD, which its vector instructions overlap little, and takes 4.2 us (10000 cycles).  256 heads of
+// 2048 tokens, whole sequences (537 MB), take 158 us, 3.4 TB/s; the states alone reach 3.6 to 3.9.
 // Measured, whole calls:
-//   forward   B4 H16 T8192 d128                168-178 us (800 MB moved: 100 the outputs, 56 the
-//                                              segments' states, which read K and V again)
-//             B1 H8 T32768 d128                92-98 us
-//             13 packed, 11171 tokens, H16 128 x 256   147-151 us (uneven segments)
-//   backward  B4 H16 T4096 d128                291-320 us (dQ and dK 85-95 each, dV 55, states 70,
-//                                              joining 10, dg 13)
-//             7 packed, 5003 tokens, H12 64 x 128      108 us (one round of 5 chunks in each of
+//   forward   B4 H16 T8192 d128                212-220 us (800 MB moved; the segments' states, which
+//                                              read K and V again, 56)
+//             B1 H8 T32768 d128                111-122 us
+//             13 packed, 11171 tokens, H16 128 x 256   189-194 us (uneven segments)
+//   backward  B4 H16 T4096 d128                320-334 us
+//             7 packed, 5003 tokens, H12 64 x 128      113 us (one round of 5 chunks in each of
 //                                              five scans, ten launches)
 #include "gdn_kernels.hpp"
 #include "gdn_device.hpp"
@@ -70,6 +68,7 @@ namespace {
 
 constexpr int LC = 64;     // tokens of a chunk
 constexpr int LNT = 4;     // 16-row tiles of a chunk
+constexpr int PARTS = 3;   // bf16 parts of an fp32 factor: 24 bits
 constexpr int BWD_SEG_CHUNKS = 16;  // at most 1024 tokens are summed into dg from one pair of states
 constexpr int JOIN_GROUPS = 2048;    // 256 CUs with eight workgroups each
 constexpr double LOG2E = 1.4426950408889634;
@@ -371,15 +370,13 @@ constexpr int scan_waves(int W, bool out) { return W / (16 * scan_tiles(W)) + (o
 // waves a SIMD has to hold: those of one workgroup, of two without outputs
 constexpr int scan_per_simd(int W, bool out) { return (scan_waves(W, out) * (out ? 1 : 2) + 3) / 4; }
 
-template <int DK, int W, bool REV, bool OUT, int PARTS, bool DOTS, class TO>
+template <int DK, int W, bool REV, bool OUT, bool DOTS, class TO>
 __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) void lin_scan_kernel(ScanArgs A) {
-  constexpr int WPARTS = PARTS == 1 ? 2 : PARTS;  // of w (a . b)
-  // two slots of everything: one in use, one being filled (a third for the rows measured level:
-  // 191 against 185 us on the prefill workload)
+  // two slots of everything: one in use, one being filled
   __shared__ LinRows<DK> rows_a[OUT ? 2 : 1], rows_b[2];
   __shared__ LinRows<W> rows_c[2], rows_w[DOTS ? 2 : 1];
   __shared__ LinGates gates[2];
-  __shared__ bf16x8 weights[OUT ? WPARTS : 1][LNT][2][WAVE];  // w (a . b) as operands: [part][row tile][32-wide step]
+  __shared__ bf16x8 weights[OUT ? PARTS : 1][LNT][2][WAVE];  // w (a . b) as operands: [part][row tile][32-wide step]
   __shared__ double dot_part[DOTS ? W / (16 * scan_tiles(W)) : 1][LC];
   constexpr int HC = scan_tiles(W), COLS = W / (16 * HC), NP = DK / 32;
   constexpr int W_GATES = COLS + (OUT ? 2 : 0), W_ROWS = W_GATES + 1;
@@ -470,23 +467,19 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
       const int ooff = (c * A.dc + slice * W + col0 + (PAIR ? 16 * (g & 1) + 8 * (g >> 1) : 4 * g)) * (int)sizeof(TO);
       lds_handover();
       for (int it = 0; it < n; ++it) {
-        if constexpr (OUT && PARTS == 1) __builtin_amdgcn_iglp_opt(1);  // interleaves MFMA and VALU: 3 to 8 % less time (three parts: none)
         const LinGates& GT = gates[it & 1];
         const __bf16* bs = rows_b[it & 1].v;
         const __bf16* cs = rows_c[it & 1].v;
-        // a X: lane (g, c) holds row 16I + c, columns 4g + r of each tile.  With several parts the
-        // smaller ones have sums of their own, so that the sums of the first part round only as
-        // often as they have terms (dg on the training workload: 1.2e-6 with one sum).
-        f32x4 o[HC][LNT], low[HC][PARTS > 1 ? LNT : 1];
+        // a X: lane (g, c) holds row 16I + c, columns 4g + r of each tile.  The smaller parts have
+        // sums of their own, so that the sums of the first part round only as often as they have
+        // terms (dg on the training workload: 1.2e-6 with one sum).
+        f32x4 o[HC][LNT], low[HC][LNT];
         if constexpr (OUT) {
           const __bf16* as = rows_a[it & 1].v;
 #pragma unroll
           for (int h = 0; h < HC; ++h)
 #pragma unroll
-            for (int I = 0; I < LNT; ++I) {
-              o[h][I] = zero4();
-              if constexpr (PARTS > 1) low[h][I] = zero4();
-            }
+            for (int I = 0; I < LNT; ++I) o[h][I] = low[h][I] = zero4();
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
             bf16x8 s[HC][PARTS];
@@ -539,7 +532,7 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
 #pragma unroll
             for (int h = 0; h < HC; ++h) {
               o[h][I] = o[h][I] * rw;
-              if constexpr (PARTS > 1) low[h][I] = low[h][I] * rw;
+              low[h][I] = low[h][I] * rw;
             }
           }
           lds_handover();  // the weights are there
@@ -559,11 +552,11 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
               for (int p = 0; p < 2; ++p) {
                 if (REV ? 2 * p + 1 < I : 2 * p > I) continue;
 #pragma unroll
-                for (int k = WPARTS - 1; k >= 0; --k) {
+                for (int k = PARTS - 1; k >= 0; --k) {
                   const bf16x8 wf = weights[k][I][p][l];
 #pragma unroll
                   for (int h = 0; h < HC; ++h) {
-                    f32x4& sum = PARTS > 1 && k > 0 ? low[h][PARTS > 1 ? I : 0] : o[h][I];
+                    f32x4& sum = k > 0 ? low[h][I] : o[h][I];
                     sum = mma_bf16(cf[h][p], wf, sum);
                   }
                 }
@@ -575,7 +568,7 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
                 if (j > 16 * I + 15) continue;
                 float wj = 0.f;
 #pragma unroll
-                for (int k = WPARTS - 1; k >= 0; --k)
+                for (int k = PARTS - 1; k >= 0; --k)
                   wj += (float)weights[k][I][j / 32][16 * (j % 16 / 4) + c][4 * (j % 32 / 16) + j % 4];
 #pragma unroll
                 for (int h = 0; h < HC; ++h) {
@@ -584,12 +577,10 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
                 }
               }
           }
-          if constexpr (PARTS > 1) {
 #pragma unroll
-            for (int h = 0; h < HC; ++h)
+          for (int h = 0; h < HC; ++h)
 #pragma unroll
-              for (int I = 0; I < LNT; ++I) o[h][I] = o[h][I] + low[h][I];
-          }
+            for (int I = 0; I < LNT; ++I) o[h][I] = o[h][I] + low[h][I];
           const auto r = chunk_rows(A.out, orow, it, (int)sizeof(TO) * A.dc);  // rows past the end are not stored
 #pragma unroll
           for (int I = 0; I < LNT; ++I) {
@@ -792,10 +783,10 @@ __global__ __launch_bounds__(scan_waves(W, OUT) * WAVE, scan_per_simd(W, OUT)) v
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             if (REV ? 2 * p + 1 < I : 2 * p > I) continue;
-            bf16x8 s[WPARTS];
-            split<WPARTS>(P[i][2 * p], P[i][2 * p + 1], s);
+            bf16x8 s[PARTS];
+            split<PARTS>(P[i][2 * p], P[i][2 * p + 1], s);
 #pragma unroll
-            for (int k = 0; k < WPARTS; ++k) weights[k][I][p][l] = s[k];
+            for (int k = 0; k < PARTS; ++k) weights[k][I][p][l] = s[k];
           }
         }
         lds_handover();
@@ -1033,12 +1024,14 @@ int state_width(int width) { return width < 64 ? width : 64; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Microseconds of one scan, after whole launches at d = 128: a workgroup of 128 / 64 / 32 columns
-// takes 3.0 / 2.3 / 2.05 a chunk with outputs (one workgroup a CU) and 1.7 / 1.5 at 64 / 32
-// columns without (two a CU), starts and ends in 8, and memory gives 4.5 MB a microsecond.
+// takes 4.2 / 2.6 / 2.35 a chunk with outputs (one workgroup a CU) and 1.7 / 1.5 at 64 / 32
+// columns without (two a CU; a third fits, but then memory sets the rate: 256, 512, 768 and 1024
+// workgroups of 64 columns take 1.4, 2.2, 3.2 and 4.1 a chunk), starts and ends in 8, and memory
+// gives 4.5 MB a microsecond.
 // Segments of equal length run in whole rounds; packed sequences leave segments of all lengths,
 // and whichever CU is free takes the next.  groups workgroups of at most len chunks, all chunks.
 double scan_cost(const LinLaunch& p, int width, double groups, double len, double all, bool out, double bytes) {
-  const double chunk = (out ? (width == 128 ? 3.0 : width == 64 ? 2.3 : 2.05) : width == 64 ? 1.7 : 1.5) *
+  const double chunk = (out ? (width == 128 ? 4.2 : width == 64 ? 2.6 : 2.35) : width == 64 ? 1.7 : 1.5) *
                        (p.d_k == 128 ? 1.0 : 0.7);
   const double rounds = groups / (out ? 256 : 512);
   const double work = rounds <= 1.0 || !p.offsets
@@ -1059,8 +1052,8 @@ double plan_cost(const LinLaunch& p, bool bwd, int width, int64_t len) {
   if (n < p.n_seq) n = p.n_seq;
   const double slices = p.d_v / width, H = p.H;
   const double bytes = seqs * (double)p.T * 2.0 * ((double)p.H_qk * p.d_k + H * p.d_v);  // K and V
-  // dQ and dK in three parts take 5.2 a chunk, dV 3.1
-  double cost = bwd ? 3.0 * scan_cost(p, width, n * H, 1.5 * (double)len, 1.5 * all * H, true, 3.0 * bytes)
+  // dQ and dK, with their products for dg, take 5.2 a chunk, dV 4.2: 1.15 on average
+  double cost = bwd ? 3.0 * scan_cost(p, width, n * H, 1.15 * (double)len, 1.15 * all * H, true, 3.0 * bytes)
                     : scan_cost(p, width, n * H * slices, (double)len, all * H * slices, true, 2.0 * bytes);
   if (per > 1) {
     const int w = state_width(width);
@@ -1081,10 +1074,10 @@ LinPlan make_plan(const LinLaunch& p, bool bwd) {
   q.width = bwd ? p.d_v : fits(p.d_v, 128) ? 128 : fits(p.d_v, 64) ? 64 : 32;
   // Whole sequences, or segments for more workgroups: their own states cost another reading of K
   // and V, and the launches and the joining some more.  B4 H16 T8192 d128: four segments a
-  // sequence 181 us, eight 203, whole sequences in four slices of 32 columns 262; 128 heads of
-  // 4096: two slices 151, two segments about 200 (as measured when the rule was set).  Backwards
-  // (12 heads, 7 packed sequences, 5003 tokens) segments of 4 chunks 123 us, 5 108, 6 113, 8 127.
-  // There a segment also bounds the sums of dg.
+  // sequence 217 us, eight 238, whole sequences in two slices of 64 columns 314, in four of 32 305;
+  // 128 heads of 4096: two slices 184, two segments 210.  Backwards (12 heads, 7 packed sequences,
+  // 5003 tokens) segments of 4 chunks 130 us, 5 113, 6 120, 8 136.  There a segment also bounds
+  // the sums of dg.
   int64_t chunks = longest;
   double best = 1e300;
   const int widest = q.width;
@@ -1148,13 +1141,13 @@ LinPlan make_plan(const LinLaunch& p, bool bwd) {
   return q;
 }
 
-template <bool REV, bool OUT, int PARTS, bool DOTS, class TO>
+template <bool REV, bool OUT, bool DOTS, class TO>
 int scan(int dk, int width, const ScanArgs& a, hipStream_t s) {
   const int64_t family = (int64_t)(a.dc / width) * (a.group_a > a.group_c ? a.group_a : a.group_c);
   const int64_t total = (int64_t)a.cut.n_seg * a.H * (a.dc / width);
   const dim3 grid((unsigned)(8 * family * ceil_div(total, 8 * family)));
   auto go = [&](auto d, auto w) {
-    hipLaunchKernelGGL((lin_scan_kernel<d.value, w.value, REV, OUT, PARTS, DOTS, TO>), grid,
+    hipLaunchKernelGGL((lin_scan_kernel<d.value, w.value, REV, OUT, DOTS, TO>), grid,
                        dim3(scan_waves(w.value, OUT) * WAVE), 0, s, a);
     return 0;
   };
@@ -1228,15 +1221,13 @@ int launch_lin_fwd(const LinLaunch& p, void* workspace, hipStream_t s) {
     a.slot = reinterpret_cast<float*>(ws + q.slot_s);
     a.slot_decay = reinterpret_cast<float*>(ws + q.decay_s);
     a.skip = 1;
-    const int rc = scan<false, false, 1, false, float>(p.d_k, state_width(q.width), a, s);
+    const int rc = scan<false, false, false, float>(p.d_k, state_width(q.width), a, s);
     if (rc) return rc;
     const JoinArgs j{a.slot, a.slot_decay, p.S0, 1, 0};
     join(&j, 1, p, q, s);
   }
-  // a bf16 output is formed with X as one bf16 part: each of its terms is rounded once more,
-  // together as much as the output's own rounding; an fp32 output with three
-  return p.o_bf16 ? scan<false, true, 1, false, __bf16>(p.d_k, q.width, a, s)
-                  : scan<false, true, 3, false, float>(p.d_k, q.width, a, s);
+  return p.o_bf16 ? scan<false, true, false, __bf16>(p.d_k, q.width, a, s)
+                  : scan<false, true, false, float>(p.d_k, q.width, a, s);
 }
 
 int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
@@ -1271,7 +1262,7 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
     f.slot = slot_s;
     f.slot_decay = reinterpret_cast<float*>(ws + q.decay_s);
     f.skip = end ? 0 : 1;
-    rc = scan<false, false, 1, false, float>(p.d_k, state_width(q.width), f, s);
+    rc = scan<false, false, false, float>(p.d_k, state_width(q.width), f, s);
     if (rc) return rc;
     joins[n_joins++] = {f.slot, f.slot_decay, p.S0, f.skip, 0};
   }
@@ -1287,7 +1278,7 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   r.slot_decay = reinterpret_cast<float*>(ws + q.decay_d);
   r.skip = 1;
   if (q.ahead) {
-    rc = scan<true, false, 1, false, float>(p.d_k, state_width(q.width), r, s);
+    rc = scan<true, false, false, float>(p.d_k, state_width(q.width), r, s);
     if (rc) return rc;
     joins[n_joins++] = {r.slot, r.slot_decay, p.dS, 1, 1};
   }
@@ -1297,11 +1288,10 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   r.out = p.dV;
   r.s_intra = p.scale;
   r.s_inter = 1.f;
-  rc = p.grad_bf16 ? scan<true, true, 1, false, __bf16>(p.d_k, q.width, r, s)
-                   : scan<true, true, 3, false, float>(p.d_k, q.width, r, s);
+  rc = p.grad_bf16 ? scan<true, true, false, __bf16>(p.d_k, q.width, r, s)
+                   : scan<true, true, false, float>(p.d_k, q.width, r, s);
   if (rc) return rc;
-  // dK and dQ: the transposed states, contraction over d_v; three parts, as dg is a difference
-  // of their products
+  // dK and dQ: the transposed states, contraction over d_v
   ScanArgs k = base_args(p, q);
   k.dc = p.d_k;
   k.a = bf(p.V);
@@ -1316,7 +1306,7 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   const bool part_bf16 = group == 1 && p.grad_bf16;
   k.s_intra = k.s_state = p.scale;
   k.s_inter = 1.f;
-  rc = part_bf16 ? scan<true, true, 3, true, __bf16>(p.d_v, p.d_k, k, s) : scan<true, true, 3, true, float>(p.d_v, p.d_k, k, s);
+  rc = part_bf16 ? scan<true, true, true, __bf16>(p.d_v, p.d_k, k, s) : scan<true, true, true, float>(p.d_v, p.d_k, k, s);
   if (rc) return rc;
   k.a = bf(p.dO);
   k.b = bf(p.V);
@@ -1328,8 +1318,8 @@ int launch_lin_bwd(const LinLaunch& p, void* workspace, hipStream_t s) {
   k.out = group > 1 ? (void*)(ws + q.part_q) : p.dQ;
   k.s_intra = k.s_inter = p.scale;
   k.s_state = 1.f;
-  rc = part_bf16 ? scan<false, true, 3, true, __bf16>(p.d_v, p.d_k, k, s)
-                 : scan<false, true, 3, true, float>(p.d_v, p.d_k, k, s);
+  rc = part_bf16 ? scan<false, true, true, __bf16>(p.d_v, p.d_k, k, s)
+                 : scan<false, true, true, float>(p.d_v, p.d_k, k, s);
   if (rc) return rc;
   if (group > 1 && p.T > 0) {
     const int64_t n = (int64_t)(p.offsets ? 1 : p.n_seq) * p.H_qk * p.T * p.d_k;
