@@ -149,7 +149,9 @@ __global__ __launch_bounds__(256) void gate_norm_bwd_kernel(GateNormLaunch a, ui
     float ss = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-    const float rstd = 1.f / sqrtf(group_sum<LPR>(ss) / (float)a.d + a.eps);
+    // past the last row the norm of zeros would be infinite where eps is 0, and dw not a number
+    const float norm = group_sum<LPR>(ss) / (float)a.d + a.eps;
+    const float rstd = r < rows ? 1.f / sqrtf(norm) : 0.f;
     float dot = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -379,7 +381,8 @@ __global__ __launch_bounds__(WPR * WAVE < 256 ? 256 : WPR * WAVE) void res_norm_
       }
     }
     if (a.dN) {
-      const float rstd = 1.f / sqrtf(row_sum(ssx) * inv + a.eps);
+      const float norm = row_sum(ssx) * inv + a.eps;
+      const float rstd = row_on ? 1.f / sqrtf(norm) : 0.f;  // a row past the last adds nothing, eps 0 or not
       const float m = row_sum(dot) * inv * rstd;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -392,7 +395,11 @@ __global__ __launch_bounds__(WPR * WAVE < 256 ? 256 : WPR * WAVE) void res_norm_
         }
       }
     }
-    const float ry = a.w_post ? 1.f / sqrtf(row_sum(ssy) * inv + a.eps) : 1.f;
+    float ry = 1.f;
+    if (a.w_post) {
+      const float norm = row_sum(ssy) * inv + a.eps;
+      ry = row_on ? 1.f / sqrtf(norm) : 0.f;
+    }
     dot = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
