@@ -1,5 +1,5 @@
 """The norms' gradients where they can go wrong: eps = 0 with numbers of rows that leave part of a
-workgroup without a row.
+workgroup without a row; gates far from 0.
 
 Tolerances: fp32 arithmetic on the values as given, a row's sums right to 2^-20 and exponentials
 and divisions to 2^-21, so an element is right to 2^-18 of M, the same expression over absolute
@@ -97,3 +97,21 @@ def test_gate_norm_without_eps(B, H, T, d, dtype):
 def test_residual_norm_without_eps(rows, D, xt, yt):
     say(f"residual norm eps=0 rows={rows} D={D} {xt} {yt}")
     check_residual(*residual_inputs(rows, rows, D, xt, yt), eps=0.0)
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+def test_gate_derivative_far_from_zero(act):
+    """dZ relative to itself: the derivative is e^-|z| in size for far gates of the sigmoid, for z > 0
+    as for z < 0.  The exponential's argument in units of log 2 is rounded in the product (half a
+    step, 2^-24 of it) and through log2 e (at most 2^-25): less than 2^-23 |z| of the derivative."""
+    say(f"gate derivative {act}")
+    z = torch.cat([torch.linspace(-30.0, 30.0, 241), torch.tensor([0.0, -1e-3, 1e-3, 10.0, 15.0, 17.0, 20.0])])
+    T = z.numel()
+    Z = z.view(1, T, 1, 1).expand(1, T, 1, 32).contiguous()
+    O, dY = torch.ones((1, 1, T, 32)), torch.ones((1, T, 1, 32))
+    _, dZ, _ = tri.gdn_gate_norm_bwd(cuda(dY), cuda(O), cuda(Z), eps=0.0, act=act)
+    torch.cuda.synchronize()
+    zd = Z.double()
+    sg, rest = torch.sigmoid(zd), torch.sigmoid(-zd)
+    want, mag = (sg * (1 + zd * rest), sg * (1 + zd.abs() * rest)) if act == "silu" else (sg * rest, sg * rest)
+    close(dZ, want, mag, TOL + 2.0 ** -23 * zd.abs(), "dZ")
