@@ -1,5 +1,6 @@
 """The norms' gradients where they can go wrong: eps = 0 with numbers of rows that leave part of a
-workgroup without a row; gates far from 0.
+workgroup without a row; gates far from 0; more rows than all workgroups take at a time; the delta
+rule's outputs in front of them.
 
 Tolerances: fp32 arithmetic on the values as given, a row's sums right to 2^-20 and exponentials
 and divisions to 2^-21, so an element is right to 2^-18 of M, the same expression over absolute
@@ -115,3 +116,52 @@ def test_gate_derivative_far_from_zero(act):
     sg, rest = torch.sigmoid(zd), torch.sigmoid(-zd)
     want, mag = (sg * (1 + zd * rest), sg * (1 + zd.abs() * rest)) if act == "silu" else (sg * rest, sg * rest)
     close(dZ, want, mag, TOL + 2.0 ** -23 * zd.abs(), "dZ")
+
+
+def test_gate_norm_rows_beyond_one_round():
+    """More rows than all workgroups take at a time: each walks on, its column sums carried over."""
+    say("gate norm, 22004 rows of 128")
+    check_gate(*gate_inputs(3, 1, 4, 5501, 128, BF), eps=1e-5)
+
+
+@pytest.mark.parametrize("rows,D", [(2100, 264), (1100, 520), (600, 2056), (1030, 4096)])
+def test_residual_norm_rows_beyond_one_round(rows, D):
+    say(f"residual norm backward, {rows} rows of {D}")
+    check_residual(*residual_inputs(rows, rows, D, F32, BF), eps=1e-5)
+
+
+@pytest.mark.parametrize("rows,D", [(8200, 264), (4100, 520), (2100, 2056)])
+def test_residual_norm_forward_rows_beyond_one_round(rows, D):
+    say(f"residual norm, {rows} rows of {D}")
+    X, Y, _, _, wq, s, wp = residual_inputs(rows, rows, D, F32, BF)
+    R, N = tri.gdn_residual_norm_fwd(cuda(X), cuda(Y), w_post=cuda(wq), s=cuda(s), alpha=0.6, w_pre=cuda(wp), eps=1e-5)
+    torch.cuda.synchronize()
+    r, n = ref.residual_norm(X, Y, wq, s, 0.6, wp, 1e-5)
+    y = Y.double()
+    z = y * (y.square().mean(-1, keepdim=True) + 1e-5).rsqrt() * wq.double()
+    mr = X.double().abs() + (0.6 * s.double() * z).abs()
+    close(R, r, mr, TOL, "R")
+    # N: the sum's own error, and the row's error through its norm
+    rs = (r.square().mean(-1, keepdim=True) + 1e-5).rsqrt()
+    close(N, n, mr * rs * wp.double().abs() + n.abs() * (mr.square().mean(-1, keepdim=True).sqrt() * rs), 2 * TOL, "N")
+
+
+def test_gate_norm_behind_the_delta_rule():
+    """The gated norm reads the gated delta rule's outputs as gdn_chunk_fwd and gdn_decode write them."""
+    import synth
+
+    say("gate norm behind gdn_chunk_fwd and gdn_decode")
+    B, H, T, d = 2, 3, 192, 128
+    x = {k: cuda(v) for k, v in synth.prefill(5, B, H, T, d, d).items() if isinstance(v, torch.Tensor)}
+    g = torch.Generator().manual_seed(5)
+    Z, w = torch.randn((B, T, H, d), generator=g).to(BF), 1 + 0.1 * torch.randn(d, generator=g)
+    O, S = tri.gdn_chunk_fwd(x["Q"], x["K"], x["V"], x["beta"], x["g"], C=64, scale=d ** -0.5, N=3)
+    Y = tri.gdn_gate_norm_fwd(O, cuda(Z), cuda(w))
+    token = [x[k][:, :, :1].contiguous() for k in ("Q", "K", "V", "beta", "g")]
+    o, _ = tri.gdn_decode(*token, S=S, scale=d ** -0.5)
+    y = tri.gdn_gate_norm_fwd(o, cuda(Z[:, :1]), cuda(w))
+    torch.cuda.synchronize()
+    for out, got, z in ((O, Y, Z), (o, y, Z[:, :1])):
+        assert out.dtype == BF and float(out.float().abs().max()) > 0
+        want = ref.gate_norm(out.cpu(), z, w, 1e-6, "silu")
+        close(got, want, want.abs(), TOL, "Y")
