@@ -2,14 +2,12 @@
 single tokens) against the fp64 token recurrence on the same inputs.
 
 Tolerances are elementwise, relative to M, the same sums over absolute values:
-  * products with an fp32 factor split into two or more bf16 parts lose at most 2^-16 of a term
-    (two roundings of half a step, 2^-8 each); an output is a sum of two such products, the
-    exponentials add 2^-22 and the fp32 sums of a chunk at most about 2^-17: 2^-14 M.  That holds
-    for fp32 outputs, and for dQ and dK in either type;
-  * O and dV stored in bf16 are formed with that factor as one bf16 part: half a step, 2^-8, of
-    each term, 2^-8 M + 2^-14 M.  Over a whole tensor the terms' roundings are independent of
-    each other and of the output's own, each at most 2^-8 / sqrt(3) in the root mean square: less
-    than 2^-8 together in the norm;
+  * products with an fp32 factor split into two or more bf16 parts (three are used) lose at most
+    2^-16 of a term (two roundings of half a step, 2^-8 each); an output is a sum of two such
+    products, the exponentials add 2^-22 and the fp32 sums of a chunk at most about 2^-17: 2^-14 M;
+  * O and dV stored in bf16 are these sums rounded once (test_gpu_lin_rounding.py compares them
+    so).  Here they have 2^-8 M more, half a step of each term, and in the norm 2^-8, where that
+    rounding is at most 2^-8 / sqrt(3) in the root mean square;
   * states: three parts (2^-24), exponentials, fp32 sums of 64 terms a chunk carried over at
     most 40 chunks: 2^-17 M;
   * outputs stored in bf16 add half a step, 2^-8 of the value;

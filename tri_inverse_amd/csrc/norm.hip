@@ -17,7 +17,7 @@
 //
 // Measured (a copy of 1 GiB reaches 5.2 TB/s): gated norm B4 H16 T8192 d128 bf16, 403 MB, 74 us,
 // 5.4 TB/s (its vector instructions, the exponentials mostly, take as long); backward B3 H16
-// T4099, 252 MB, 57 us of which the column sum 4.7; residual norm backward, 16384 rows of 4096,
+// T4099, 252 MB, 57 us, 4.4 TB/s, of which the column sum 4.7; residual norm backward, 16384 rows of 4096,
 // fp32 and bf16, 1208 MB, 226 us, 5.4 TB/s; forward, 64 rows of 2048, 3.4 us, latency.
 #include "gdn_device.hpp"
 #include "gdn_kernels.hpp"
@@ -230,7 +230,8 @@ namespace {
 
 template <int WPR>
 struct RowSum {
-  // sums over the row of two values at once; every wave of the workgroup calls it together
+  // sum over the row; every wave of the workgroup calls it together.  Two buffers of WPR values
+  // (the memory behind red, taken flat) in turn
   float (*red)[2];
   int phase = 0;
   __device__ __forceinline__ float operator()(float x) {
@@ -330,8 +331,9 @@ __global__ __launch_bounds__(WPR * WAVE < 256 ? 256 : WPR * WAVE) void res_norm_
   const int tid = threadIdx.x % TPR;
   const float inv = 1.f / (float)a.D;
   float wp[V][8], wb[V][8], g_pre[V][8], g_y[V][8];
-  // the weights of vector v: w_pre, and s w_post.  With two vectors they would not fit beside the
-  // row (130 registers to scratch memory), and come anew from the caches where they are used.
+  // the weights of vector v: w_pre, and s w_post.  With two vectors they do not fit beside the row
+  // and come anew from the caches where they are used: 36 to 53 registers still go to scratch
+  // memory (108 to 120 bytes a lane), with the weights kept it would be 130.
   auto weights = [&](int v) {
     const int col = 8 * (tid + TPR * v);
     fill8(wp[v], 1.f);
@@ -481,8 +483,9 @@ int by_lanes(int d, F&& f) {
 
 // Waves and vectors of a row by its length: 8 values a lane where 16 waves hold the row, so that
 // the row's tensors and, backwards, two column sums fit the registers; 16 values above 8192.
-// Backwards one such row fills a CU's registers, so nothing hides its latency: 4096 rows of
-// 16384 run at 2.7 TB/s, 8192 rows of 8192 at 5.1 (forwards 4.9 and 5.4).
+// Backwards one such row takes more registers than a CU has for it, so some go to scratch memory
+// and nothing hides its latency: 4096 rows of 16384 run at 2.7 TB/s, 8192 rows of 8192 at 5.1
+// (forwards 4.9 and 5.4).
 template <class F>
 int by_row(int D, F&& f) {
   using std::integral_constant;
