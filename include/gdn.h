@@ -294,9 +294,9 @@ size_t gdn_lin_chunk_fwd_workspace_bytes(const gdn_lin_shape* shape);
 size_t gdn_lin_chunk_bwd_workspace_bytes(const gdn_lin_shape* shape);
 
 /* O and S_out of whole sequences, chunk by chunk.  qkv_dtype GDN_BF16; o_dtype GDN_BF16 or
- * GDN_F32; S0 NULL = zeros; S_out NULL = not wanted.  d_k in {64, 128}, d_v a multiple of
- * 32, at most 256 (GDN_ERR_UNSUPPORTED otherwise).  workspace: 16-byte aligned scratch of at
- * least the query's bytes, not to be shared by two calls in flight (GDN_ERR_WORKSPACE if it
+ * GDN_F32 (in bf16 it is the fp32 output rounded once); S0 NULL = zeros; S_out NULL = not
+ * wanted.  d_k in {64, 128}, d_v a multiple of 32, at most 256 (GDN_ERR_UNSUPPORTED
+ * otherwise).  workspace: 16-byte aligned scratch of at least the query's bytes, not to be shared by two calls in flight (GDN_ERR_WORKSPACE if it
  * is needed and NULL or smaller).  A token's row of O depends on no later token, whatever that
  * holds: rows that pad a sequence at its end may be infinities or NaN. */
 gdn_status gdn_lin_chunk_fwd(const gdn_lin_shape* shape, const void* Q, const void* K, const void* V,
@@ -305,9 +305,9 @@ gdn_status gdn_lin_chunk_fwd(const gdn_lin_shape* shape, const void* Q, const vo
                              void* stream);
 
 /* Its backward pass: gradients of a loss from dO (GDN_BF16, as O) and dS (gradient of S_out;
- * NULL = zeros).  dQ, dK, dV as Q, K, V in grad_dtype (GDN_BF16 or GDN_F32; shared heads get
- * the sum over their group), dg fp32 as g (per head: the sum over all its tokens; NULL = not
- * wanted), dS0 [B][H][d_k][d_v] fp32 (NULL = not wanted).  d_k and d_v in {64, 128}.  The
+ * NULL = zeros).  dQ, dK, dV as Q, K, V in grad_dtype (GDN_BF16 or GDN_F32, in bf16 the fp32
+ * gradients rounded once; shared heads get the sum over their group), dg fp32 as g (per head:
+ * the sum over all its tokens; NULL = not wanted), dS0 [B][H][d_k][d_v] fp32 (NULL = not wanted).  d_k and d_v in {64, 128}.  The
  * call reads no output of the forward pass.  The same call gives the same bits.  An infinity or
  * a NaN in a row may reach all gradients of its sequence and head: rows that pad a sequence must
  * be finite here. */
