@@ -372,6 +372,108 @@ gdn_status gdn_residual_norm_bwd(const void* dN, const void* dR, const void* R, 
                                  float* dw_post, float* ds, int64_t rows, int32_t D, float eps,
                                  void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- queries and keys in front of the token mixer --------------------------------------- */
+
+/* norm n(x) of a head's row: 1; sqrt(mean(x^2) + eps); sqrt(sum(x^2) + eps) (unit rows, as the
+ * delta rule takes its keys) */
+typedef enum gdn_qk_norm { GDN_QK_NONE = 0, GDN_QK_RMS = 1, GDN_QK_L2 = 2 } gdn_qk_norm;
+/* pair i of the r rotated values, the first r of a row: (i, i + r/2), or (2i, 2i + 1) */
+typedef enum gdn_qk_pairs { GDN_PAIRS_HALVES = 0, GDN_PAIRS_NEIGHBOURS = 1 } gdn_qk_pairs;
+#define GDN_QK_MAX_PAIRS 128
+#define GDN_QK_MAX_AXES 4
+
+/* The rows of H_q query heads and H_k key heads (either may be 0), normed and rotated in one pass,
+ * from the projection's rows to the layout that gdn_chunk_fwd, gdn_decode, gdn_lin_chunk_fwd and
+ * gdn_lin_decode read:
+ *   Q_out[b][h][t] = R(p) (Q[b][t][h] / n(Q[b][t][h]) * wq),   K_out likewise
+ * R(p) turns pair i (x, y) into (x cos - y sin, x sin + y cos) of the angle p[axis[i]] freqs[i],
+ * formed in fp64 and taken to a turn before its rounding, so far positions lose nothing.
+ *   Q [B][T] rows of H_q * d values, q_stride values apart, K of H_k * d, k_stride apart (parts of a
+ *     wider projection; multiples of 8); Q_out [B][H_q][T][d], K_out [B][H_k][T][d]; one dtype,
+ *     GDN_BF16 or GDN_F32.  wq, wk fp32 [d], NULL = ones.
+ *   rot = r, a multiple of 8, at most d; 0 = no rotation, freqs is then not read.  freqs fp64
+ *     [r / 2], radians for one position.  positions int32 [axes][B][T], NULL = the token's index
+ *     t on every axis.  axis[i] < axes is the axis of pair i.
+ *   d a multiple of 32, at most 256; fewer than 2^34 values. */
+typedef struct gdn_qk_shape {
+  int64_t T;
+  int64_t q_stride, k_stride;
+  int32_t B, H_q, H_k, d;
+  int32_t dtype;
+  int32_t norm;
+  float eps;
+  int32_t rot, pairs;
+  int32_t axes; /* 1 .. GDN_QK_MAX_AXES */
+  uint8_t axis[GDN_QK_MAX_PAIRS];
+} gdn_qk_shape;
+
+gdn_status gdn_qk_norm_fwd(const gdn_qk_shape* shape, const void* Q, const void* K, const float* wq,
+                           const float* wk, const double* freqs, const int32_t* positions, void* Q_out,
+                           void* K_out, void* stream);
+
+/* Its backward pass from dQ_out, dK_out (as Q_out, K_out): dQ [B][T][H_q][d], dK [B][T][H_k][d] in
+ * dtype, dwq, dwk fp32 [d] (NULL = not wanted).  workspace as for gdn_lin_chunk_bwd, needed for dwq
+ * and dwk.  The same call gives the same bits. */
+size_t gdn_qk_norm_bwd_workspace_bytes(const gdn_qk_shape* shape);
+gdn_status gdn_qk_norm_bwd(const gdn_qk_shape* shape, const void* dQ_out, const void* dK_out, const void* Q,
+                           const void* K, const float* wq, const float* wk, const double* freqs,
+                           const int32_t* positions, void* dQ, void* dK, float* dwq, float* dwk,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- gated linear recurrence of every channel ------------------------------------------- */
+
+/* the log-decay from A, s = 1 / (1 + exp(-x)): -w s(A) with w fp32 [D], >= 0; log s(A); A itself, <= 0 */
+typedef enum gdn_rec_decay { GDN_DECAY_POWER = 0, GDN_DECAY_SIGMOID = 1, GDN_DECAY_LOG = 2 } gdn_rec_decay;
+/* the input's factor b, a = exp(log-decay): sqrt(1 - a^2), 1 - a, or 1 */
+typedef enum gdn_rec_norm { GDN_REC_NORM_SQRT = 0, GDN_REC_NORM_LINEAR = 1, GDN_REC_NORM_NONE = 2 } gdn_rec_norm;
+#define GDN_REC_TILE 64
+
+/* Per sequence and channel, tokens in order, state h fp32:
+ *   h_t = a_t h_{t-1} + b_t s(I_t) X_t        (I NULL: b_t X_t)
+ * offsets == NULL: B sequences of T tokens each; X, A, I [B][T] rows of D values, x_stride,
+ *   a_stride, i_stride values apart (parts of wider projections; multiples of 8), H [B][T][D].
+ * offsets != NULL: B packed sequences in T tokens, as in gdn_lin_shape, rows of the T tokens; rows of
+ *   no sequence are not read into a result, H is not written there, and gradients there are zero.
+ * X, A, I, H and their gradients in dtype (GDN_BF16 or GDN_F32); states [B][D] fp32.  D a multiple of
+ * 8.  Empty sequences and T == 0 return the given states unchanged (or zeros).  A log-decay of
+ * -inf forgets the state; where a = 1 the gradient of b = sqrt(1 - a^2) = 0 counts as 0. */
+typedef struct gdn_rec_shape {
+  int64_t T;
+  const int32_t* offsets;
+  int64_t x_stride, a_stride, i_stride;
+  int32_t B, D;
+  int32_t decay, norm;
+  int32_t dtype;
+} gdn_rec_shape;
+
+/* Device workspace in bytes of gdn_rec_fwd and gdn_rec_bwd (0 for arguments they reject; offsets only
+ * selects the layout and is not read). */
+size_t gdn_rec_fwd_workspace_bytes(const gdn_rec_shape* shape);
+size_t gdn_rec_bwd_workspace_bytes(const gdn_rec_shape* shape);
+
+/* H and h_out (NULL = not wanted) of whole sequences from h0 (NULL = zeros).  states: NULL, or fp32
+ * [B][ceil(T / GDN_REC_TILE)][D] (packed: [ceil(T / GDN_REC_TILE)][D]), h before every GDN_REC_TILE-th token
+ * (0 where that token does not continue a sequence), for the backward pass.  workspace as for
+ * gdn_lin_chunk_fwd.  A row of H depends on no later token.  The same call gives the same bits. */
+gdn_status gdn_rec_fwd(const gdn_rec_shape* shape, const void* X, const void* A, const void* I, const float* w,
+                       const float* h0, void* H, float* h_out, float* states, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* Its backward pass: gradients of a loss from dH (as H) and dh (gradient of h_out, NULL = zeros): dX,
+ * dA, dI (with I only) [B][T][D] in dtype, dw fp32 [D] and dh0 fp32 [B][D] (NULL = not wanted; dw with
+ * GDN_DECAY_POWER only).  states as gdn_rec_fwd wrote them for the same inputs; NULL: they are formed
+ * anew.  The same call gives the same bits. */
+gdn_status gdn_rec_bwd(const gdn_rec_shape* shape, const void* X, const void* A, const void* I, const float* w,
+                       const float* h0, const float* states, const void* dH, const float* dh, void* dX,
+                       void* dA, void* dI, float* dw, float* dh0, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/* The recurrence one token at a time (decode), T = the tokens of the call (offsets must be NULL:
+ * GDN_ERR_UNSUPPORTED otherwise).  The state is read and written once per call and h_out MAY equal
+ * h_in. */
+gdn_status gdn_rec_step(const gdn_rec_shape* shape, const void* X, const void* A, const void* I, const float* w,
+                        const float* h_in, float* h_out, void* H, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,6 +28,12 @@ _lib = ctypes.CDLL(LIB_PATH)
 GDN_F32, GDN_BF16, GDN_FP8_E4M3, GDN_INT8, GDN_INT16 = 0, 1, 2, 3, 4
 GDN_INV_NEUMANN, GDN_INV_EXACT, GDN_INV_NEUMANN_PRODUCTS = 0, 1, 2
 GDN_GATE_SILU, GDN_GATE_SIGMOID = 0, 1
+GDN_QK_NONE, GDN_QK_RMS, GDN_QK_L2 = 0, 1, 2
+GDN_PAIRS_HALVES, GDN_PAIRS_NEIGHBOURS = 0, 1
+GDN_QK_MAX_PAIRS, GDN_QK_MAX_AXES = 128, 4
+GDN_DECAY_POWER, GDN_DECAY_SIGMOID, GDN_DECAY_LOG = 0, 1, 2
+GDN_REC_NORM_SQRT, GDN_REC_NORM_LINEAR, GDN_REC_NORM_NONE = 0, 1, 2
+GDN_REC_TILE = 64
 GDN_OK = 0
 GDN_ERR_UNSUPPORTED, GDN_ERR_WORKSPACE, GDN_ERR_HIP = 5, 6, 7
 FP8_STATS_FIELDS = ("nonfinite", "sat_dynamic", "sat_static", "underflow")
@@ -53,6 +59,21 @@ class gdn_lin_shape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("offsets", ctypes.c_void_p), ("B", ctypes.c_int32),
                 ("H", ctypes.c_int32), ("H_qk", ctypes.c_int32), ("d_k", ctypes.c_int32),
                 ("d_v", ctypes.c_int32), ("g_per_head", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class gdn_qk_shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("B", ctypes.c_int32), ("H_q", ctypes.c_int32), ("H_k", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("norm", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("rot", ctypes.c_int32), ("pairs", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("axis", ctypes.c_uint8 * GDN_QK_MAX_PAIRS)]
+
+
+class gdn_rec_shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("offsets", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("a_stride", ctypes.c_int64), ("i_stride", ctypes.c_int64), ("B", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("decay", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
 
 
 _vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
@@ -111,6 +132,22 @@ _lib.gdn_residual_norm_bwd_workspace_bytes.argtypes = [_i64, _i32]
 _lib.gdn_residual_norm_bwd.restype = _i32
 _lib.gdn_residual_norm_bwd.argtypes = [_vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _vp, _vp,
                                        _i64, _i32, _f32, _vp, _sz, _vp]
+_lib.gdn_qk_norm_fwd.restype = _i32
+_lib.gdn_qk_norm_fwd.argtypes = [_P(gdn_qk_shape)] + [_vp] * 9
+_lib.gdn_qk_norm_bwd_workspace_bytes.restype = _sz
+_lib.gdn_qk_norm_bwd_workspace_bytes.argtypes = [_P(gdn_qk_shape)]
+_lib.gdn_qk_norm_bwd.restype = _i32
+_lib.gdn_qk_norm_bwd.argtypes = [_P(gdn_qk_shape)] + [_vp] * 13 + [_sz, _vp]
+_lib.gdn_rec_fwd_workspace_bytes.restype = _sz
+_lib.gdn_rec_fwd_workspace_bytes.argtypes = [_P(gdn_rec_shape)]
+_lib.gdn_rec_bwd_workspace_bytes.restype = _sz
+_lib.gdn_rec_bwd_workspace_bytes.argtypes = [_P(gdn_rec_shape)]
+_lib.gdn_rec_fwd.restype = _i32
+_lib.gdn_rec_fwd.argtypes = [_P(gdn_rec_shape)] + [_vp] * 9 + [_sz, _vp]
+_lib.gdn_rec_bwd.restype = _i32
+_lib.gdn_rec_bwd.argtypes = [_P(gdn_rec_shape)] + [_vp] * 14 + [_sz, _vp]
+_lib.gdn_rec_step.restype = _i32
+_lib.gdn_rec_step.argtypes = [_P(gdn_rec_shape)] + [_vp] * 8
 
 EXPORTED = ("gdn_abi_version", "gdn_status_string", "gdn_build_A", "gdn_tri_inverse_neumann",
             "gdn_tri_inverse_exact", "gdn_tri_inverse_residual", "gdn_tri_inverse_fs", "gdn_wy",
@@ -118,7 +155,8 @@ EXPORTED = ("gdn_abi_version", "gdn_status_string", "gdn_build_A", "gdn_tri_inve
             "gdn_lin_chunk_fwd_workspace_bytes", "gdn_lin_chunk_bwd_workspace_bytes", "gdn_lin_chunk_fwd",
             "gdn_lin_chunk_bwd", "gdn_lin_decode", "gdn_gate_norm_fwd", "gdn_gate_norm_bwd_workspace_bytes",
             "gdn_gate_norm_bwd", "gdn_residual_norm_fwd", "gdn_residual_norm_bwd_workspace_bytes",
-            "gdn_residual_norm_bwd")
+            "gdn_residual_norm_bwd", "gdn_qk_norm_fwd", "gdn_qk_norm_bwd_workspace_bytes", "gdn_qk_norm_bwd",
+            "gdn_rec_fwd_workspace_bytes", "gdn_rec_bwd_workspace_bytes", "gdn_rec_fwd", "gdn_rec_bwd", "gdn_rec_step")
 GDN_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -742,3 +780,253 @@ def gdn_residual_norm_bwd(dN, dR, R, Y, w_post=None, s=None, alpha: float = 1.0,
                                         _at(ws), ws_bytes, _current(dev))
     _check(st, "gdn_residual_norm_bwd")
     return dX, dY, dw_pre, dw_post, ds
+
+
+# ---- queries and keys in front of the mixer, and the recurrence of every channel ------------------
+
+_QK_NORM = {"none": GDN_QK_NONE, "rms": GDN_QK_RMS, "l2": GDN_QK_L2}
+_PAIRS = {"halves": GDN_PAIRS_HALVES, "neighbours": GDN_PAIRS_NEIGHBOURS}
+_DECAY = {"power": GDN_DECAY_POWER, "sigmoid": GDN_DECAY_SIGMOID, "log": GDN_DECAY_LOG}
+_REC_NORM = {"sqrt": GDN_REC_NORM_SQRT, "linear": GDN_REC_NORM_LINEAR, "none": GDN_REC_NORM_NONE}
+
+
+def _choice(value, name, table):
+    if value not in table:
+        raise ValueError("%s must be one of %s" % (name, tuple(table)))
+    return table[value]
+
+
+def _token_rows(t, name, dtypes, shape, dev):
+    """A tensor [B, T, ...] whose tokens may lie at any one stride (a part of a wider projection), the
+    values of a token together; returns that stride."""
+    width = 1
+    for n in shape[2:]:
+        width *= n
+    if type(t) is torch.Tensor and t.shape == shape and t.dtype in dtypes and t.get_device() == dev.index and t.is_contiguous():
+        return width
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA (HIP) tensor" % name)
+    if t.dtype not in dtypes:
+        raise TypeError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtypes))
+    if t.device != dev:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if not t.numel():
+        return width
+    B, T = shape[:2]
+    step = t.stride(1) if T > 1 else t.stride(0) if B > 1 else width
+    inner = width
+    for i in range(2, t.dim()):
+        inner //= shape[i]
+        if shape[i] > 1 and t.stride(i) != inner:
+            raise ValueError("the values of a token of %s must be contiguous" % name)
+    if (B > 1 and T > 1 and t.stride(0) != T * step) or step < width:
+        raise ValueError("the tokens of %s must be at one stride" % name)
+    return step
+
+
+def _qk_args(Q, K, wq, wk, freqs, positions, norm, eps, pairs, axis):
+    """The gdn_qk_shape of a call after the inputs' checks; returns (shape, device, dtype)."""
+    one = Q if Q is not None else K
+    if not isinstance(one, torch.Tensor) or one.dim() != 4:
+        raise ValueError("Q and K must be [B, T, heads, d], one of them at least given")
+    B, T, _, d = one.shape
+    dev = one.device
+    sh = gdn_qk_shape()
+    if not one.is_cuda:
+        raise TypeError("Q and K must be CUDA (HIP) tensors")
+    if Q is not None:
+        sh.H_q, sh.q_stride = Q.shape[2], _token_rows(Q, "Q", _FLOAT, Q.shape, dev)
+    if K is not None:
+        if K.dim() != 4:
+            raise ValueError("K must be [B, T, heads, d]")
+        sh.H_k, sh.k_stride = K.shape[2], _token_rows(K, "K", (one.dtype,), (B, T, K.shape[2], d), dev)
+    for w, name, t in ((wq, "wq", Q), (wk, "wk", K)):
+        if w is not None:
+            if t is None:
+                raise ValueError("%s is given without its heads" % name)
+            _arg(w, name, (torch.float32,), (d,), dev)
+    axes = 1
+    if freqs is None:
+        if positions is not None or axis is not None:
+            raise ValueError("positions and axis need freqs")
+    else:
+        if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1 or 2 * freqs.numel() > d:
+            raise ValueError("freqs must be [rotated values / 2], at most d / 2 of them")
+        n = freqs.numel()
+        _arg(freqs, "freqs", (torch.float64,), (n,), dev)
+        if axis is not None:
+            if len(axis) != n:
+                raise ValueError("axis must give an axis for each of the %d pairs" % n)
+            if positions is None or positions.dim() != 3:
+                raise ValueError("axis needs positions [axes, B, T]")
+            axes = positions.shape[0]
+            if not 1 <= axes <= GDN_QK_MAX_AXES or min(axis, default=0) < 0 or max(axis, default=0) >= axes:
+                raise ValueError("axis must name one of the positions' 1 to %d axes, got %d of them" % (GDN_QK_MAX_AXES, axes))
+            ctypes.memmove(sh.axis, bytes(axis), n)
+        if positions is not None:
+            _arg(positions, "positions", (torch.int32,), (B, T) if axis is None else (axes, B, T), dev)
+        sh.rot = 2 * n
+    sh.T, sh.B, sh.d, sh.dtype, sh.axes = T, B, d, _TORCH_DTYPE[one.dtype], axes
+    sh.norm, sh.pairs, sh.eps = _choice(norm, "norm", _QK_NORM), _choice(pairs, "pairs", _PAIRS), eps
+    return sh, dev, one.dtype
+
+
+def gdn_qk_norm_fwd(Q, K=None, wq=None, wk=None, freqs=None, positions=None, norm: str = "rms", eps: float = 1e-6,
+                    pairs: str = "halves", axis=None, Q_out=None, K_out=None, stream=None):
+    """Queries and keys in front of the mixer, normed for each head and rotated in one pass:
+    Q [B,T,H_q,d], K [B,T,H_k,d] (parts of a projection's rows, bf16 or fp32; either may be None) ->
+    Q_out [B,H_q,T,d], K_out [B,H_k,T,d], as gdn_chunk_fwd, gdn_lin_chunk_fwd and the decode entry points read them.
+
+    norm "rms" (x / sqrt(mean(x^2) + eps)), "l2" (x / sqrt(sum(x^2) + eps)) or "none", times wq, wk [d]
+    fp32 (None: ones).  freqs: fp64 [r/2], the radians by which pair i of the first r values turns for
+    one position (None: no rotation); pairs "halves" (i, i + r/2) or "neighbours" (2i, 2i + 1).
+    positions: int32 [B,T] (None: the token's index), or [axes,B,T] with axis, a sequence that names
+    the axis of each pair.  Returns (Q_out, K_out)."""
+    sh, dev, dtype = _qk_args(Q, K, wq, wk, freqs, positions, norm, eps, pairs, axis)
+    B, T, d = sh.B, sh.T, sh.d
+    with _scope(dev, stream):
+        Q_out = None if Q is None else _out(Q_out, "Q_out", (dtype,), (B, sh.H_q, T, d), dev, dtype)
+        K_out = None if K is None else _out(K_out, "K_out", (dtype,), (B, sh.H_k, T, d), dev, dtype)
+        st = _lib.gdn_qk_norm_fwd(ctypes.byref(sh), _at(Q), _at(K), _at(wq), _at(wk), _at(freqs), _at(positions),
+                                  _at(Q_out), _at(K_out), _current(dev))
+    _check(st, "gdn_qk_norm_fwd")
+    return Q_out, K_out
+
+
+def gdn_qk_norm_bwd(dQ_out, dK_out, Q, K=None, wq=None, wk=None, freqs=None, positions=None, norm: str = "rms",
+                    eps: float = 1e-6, pairs: str = "halves", axis=None, workspace=None, stream=None):
+    """Backward pass of gdn_qk_norm_fwd from dQ_out [B,H_q,T,d] and dK_out [B,H_k,T,d].  Returns (dQ
+    [B,T,H_q,d], dK [B,T,H_k,d], dwq, dwk [d] fp32), each None without its tensor."""
+    sh, dev, dtype = _qk_args(Q, K, wq, wk, freqs, positions, norm, eps, pairs, axis)
+    B, T, d = sh.B, sh.T, sh.d
+    for t, name, x, H in ((dQ_out, "dQ_out", Q, sh.H_q), (dK_out, "dK_out", K, sh.H_k)):
+        if x is not None:
+            _arg(t, name, (dtype,), (B, H, T, d), dev)
+        elif t is not None:
+            raise ValueError("%s is given without its heads" % name)
+    with _scope(dev, stream):
+        dQ, dK = (None if t is None else torch.empty((B, T, H, d), device=dev, dtype=dtype)
+                  for t, H in ((Q, sh.H_q), (K, sh.H_k)))
+        dwq, dwk = (None if w is None else torch.empty((d,), device=dev, dtype=torch.float32) for w in (wq, wk))
+        ws, ws_bytes = (None, 0) if dwq is dwk is None else _scratch(
+            workspace, _lib.gdn_qk_norm_bwd_workspace_bytes(ctypes.byref(sh)), dev)
+        st = _lib.gdn_qk_norm_bwd(ctypes.byref(sh), _at(dQ_out), _at(dK_out), _at(Q), _at(K), _at(wq), _at(wk),
+                                  _at(freqs), _at(positions), _at(dQ), _at(dK), _at(dwq), _at(dwk), _at(ws), ws_bytes,
+                                  _current(dev))
+    _check(st, "gdn_qk_norm_bwd")
+    return dQ, dK, dwq, dwk
+
+
+def _rec_shape(X, A, I, w, offsets, decay, norm):
+    """The gdn_rec_shape of a call after the inputs' checks; returns (shape, the states' shape, device)."""
+    if not isinstance(X, torch.Tensor) or X.dim() != 3:
+        raise ValueError("X must be [B, T, D]")
+    if not X.is_cuda:
+        raise TypeError("X must be a CUDA (HIP) tensor")
+    B, T, D = X.shape
+    dev, dtype = X.device, (X.dtype,)
+    xs = _token_rows(X, "X", _FLOAT, X.shape, dev)
+    as_ = _token_rows(A, "A", dtype, X.shape, dev)
+    is_ = D if I is None else _token_rows(I, "I", dtype, X.shape, dev)
+    kind = _choice(decay, "decay", _DECAY)
+    if kind == GDN_DECAY_POWER:
+        _arg(w, "w", (torch.float32,), (D,), dev)
+    elif w is not None:
+        raise ValueError('w belongs to decay "power"')
+    n = B
+    if offsets is not None:
+        if B != 1:
+            raise ValueError("packed sequences lie in one row: B must be 1, got %d" % B)
+        if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
+            raise ValueError("offsets must be [sequences + 1], of one sequence at least")
+        n = offsets.numel() - 1
+        _arg(offsets, "offsets", (torch.int32,), (n + 1,), dev)
+    sh = gdn_rec_shape(T, _at(offsets), xs, as_, is_, n, D, kind, _choice(norm, "norm", _REC_NORM),
+                       _TORCH_DTYPE[X.dtype])
+    return sh, (n, D), dev
+
+
+def _plain_rec(B, T, D, decay, packed):
+    # of the offsets only their presence counts
+    return gdn_rec_shape(int(T), 16 if packed else None, int(D), int(D), int(D), int(B), int(D),
+                         _choice(decay, "decay", _DECAY), GDN_REC_NORM_SQRT, GDN_F32)
+
+
+def gdn_rec_fwd_workspace_bytes(B: int, T: int, D: int, decay: str = "power", packed: bool = False) -> int:
+    """Device workspace (bytes) gdn_rec_fwd needs for B sequences (0: none)."""
+    return int(_lib.gdn_rec_fwd_workspace_bytes(ctypes.byref(_plain_rec(B, T, D, decay, packed))))
+
+
+def gdn_rec_bwd_workspace_bytes(B: int, T: int, D: int, decay: str = "power", packed: bool = False) -> int:
+    """Device workspace (bytes) gdn_rec_bwd needs for B sequences."""
+    return int(_lib.gdn_rec_bwd_workspace_bytes(ctypes.byref(_plain_rec(B, T, D, decay, packed))))
+
+
+def gdn_rec_fwd(X, A, I=None, w=None, h0=None, offsets=None, decay: str = "power", norm: str = "sqrt",
+                want_states: bool = False, H=None, h_out=None, workspace=None, stream=None):
+    """Gated linear recurrence of every channel, whole sequences: h_t = a_t h_{t-1} + b_t sigmoid(I_t) X_t.
+
+    X, A, I [B,T,D] (bf16 or fp32, one dtype, their tokens at any stride; I None: no input gate).  decay:
+    log a = -w sigmoid(A) ("power", w [D] fp32, >= 0), log sigmoid(A) ("sigmoid") or A ("log");
+    norm: b = sqrt(1 - a^2) ("sqrt"), 1 - a ("linear") or 1 ("none").  offsets: int32 [n+1] for n packed
+    sequences in B = 1 rows of T tokens.  h0 [B or n,D] fp32 or None (zeros; not the same tensor as
+    h_out).  Any T.  workspace: a uint8 tensor of gdn_rec_fwd_workspace_bytes(...) bytes, or None.
+    Returns (H [B,T,D], h_out [B or n,D] fp32, states for gdn_rec_bwd with want_states, else None)."""
+    sh, state, dev = _rec_shape(X, A, I, w, offsets, decay, norm)
+    if h0 is not None:
+        _arg(h0, "h0", (torch.float32,), state, dev)
+    with _scope(dev, stream):
+        H = _out(H, "H", (X.dtype,), X.shape, dev, X.dtype)
+        h_out = _out(h_out, "h_out", (torch.float32,), state, dev, torch.float32, h0)
+        if h0 is not None and h_out.data_ptr() == h0.data_ptr() and h0.numel():
+            raise ValueError("h_out must not be h0: a sequence's parts read the one while others write the other")
+        states = None
+        if want_states:
+            states = torch.empty((X.shape[0], -(-sh.T // GDN_REC_TILE), sh.D), device=dev, dtype=torch.float32)
+        ws, ws_bytes = _scratch(workspace, _lib.gdn_rec_fwd_workspace_bytes(ctypes.byref(sh)), dev)
+        st = _lib.gdn_rec_fwd(ctypes.byref(sh), _at(X), _at(A), _at(I), _at(w), _at(h0), _at(H), _at(h_out),
+                              _at(states), _at(ws), ws_bytes, _current(dev))
+    _check(st, "gdn_rec_fwd")
+    return H, h_out, states
+
+
+def gdn_rec_bwd(X, A, dH, I=None, w=None, h0=None, dh=None, offsets=None, decay: str = "power", norm: str = "sqrt",
+                states=None, workspace=None, stream=None):
+    """Backward pass of gdn_rec_fwd from dH (as X, contiguous) and dh (gradient of h_out, or None), with the
+    states that gdn_rec_fwd returned for the same inputs (None: they are formed anew).  Returns (dX,
+    dA, dI, dw, dh0), dI None without I, dw (fp32 [D]) without w, dh0 (fp32) without h0."""
+    sh, state, dev = _rec_shape(X, A, I, w, offsets, decay, norm)
+    _arg(dH, "dH", (X.dtype,), X.shape, dev)
+    for t, name in ((h0, "h0"), (dh, "dh")):
+        if t is not None:
+            _arg(t, name, (torch.float32,), state, dev)
+    if states is not None:
+        _arg(states, "states", (torch.float32,), (X.shape[0], -(-sh.T // GDN_REC_TILE), sh.D), dev)
+    with _scope(dev, stream):
+        dX, dA = (torch.empty(X.shape, device=dev, dtype=X.dtype) for _ in range(2))
+        dI = None if I is None else torch.empty(X.shape, device=dev, dtype=X.dtype)
+        dw = None if w is None else torch.empty_like(w)
+        dh0 = None if h0 is None else torch.empty_like(h0)
+        ws, ws_bytes = _scratch(workspace, _lib.gdn_rec_bwd_workspace_bytes(ctypes.byref(sh)), dev)
+        st = _lib.gdn_rec_bwd(ctypes.byref(sh), _at(X), _at(A), _at(I), _at(w), _at(h0), _at(states), _at(dH),
+                              _at(dh), _at(dX), _at(dA), _at(dI), _at(dw), _at(dh0), _at(ws), ws_bytes, _current(dev))
+    _check(st, "gdn_rec_bwd")
+    return dX, dA, dI, dw, dh0
+
+
+def gdn_rec_step(X, A, I=None, w=None, h=None, decay: str = "power", norm: str = "sqrt", h_out=None, H=None,
+                 stream=None):
+    """The recurrence of gdn_rec_fwd token by token with the state in registers: X, A, I [B,n,D], h [B,D]
+    fp32 or None (zeros).  Pass h_out=h to update the state in place.  Returns (H [B,n,D], h_out)."""
+    sh, state, dev = _rec_shape(X, A, I, w, None, decay, norm)
+    if h is not None:
+        _arg(h, "h", (torch.float32,), state, dev)
+    with _scope(dev, stream):
+        H = _out(H, "H", (X.dtype,), X.shape, dev, X.dtype)
+        h_out = _out(h_out, "h_out", (torch.float32,), state, dev, torch.float32, h)
+        st = _lib.gdn_rec_step(ctypes.byref(sh), _at(X), _at(A), _at(I), _at(w), _at(h), _at(h_out), _at(H),
+                               _current(dev))
+    _check(st, "gdn_rec_step")
+    return H, h_out

@@ -623,6 +623,218 @@ gdn_status gdn_residual_norm_bwd(const void* dN, const void* dR, const void* R, 
   return launch_result(gdn::launch_res_norm_bwd(p, workspace, as_stream(stream)));
 }
 
+// ---- queries and keys in front of the token mixer ---------------------------------------
+
+static gdn_status check_qk(const gdn_qk_shape* s) {
+  if (!s) return GDN_ERR_NULL_POINTER;
+  if (s->B < 0 || s->H_q < 0 || s->H_k < 0 || s->T < 0 || s->d <= 0 || !(s->eps >= 0.f)) return GDN_ERR_BAD_SHAPE;
+  if (!float_dtype(s->dtype)) return GDN_ERR_BAD_DTYPE;
+  if (s->norm < GDN_QK_NONE || s->norm > GDN_QK_L2) return GDN_ERR_BAD_SHAPE;
+  if (s->pairs != GDN_PAIRS_HALVES && s->pairs != GDN_PAIRS_NEIGHBOURS) return GDN_ERR_BAD_SHAPE;
+  if (s->d % 32 != 0 || s->d > 256) return GDN_ERR_UNSUPPORTED;
+  if (s->rot < 0 || s->rot > s->d || s->rot % 8 != 0) return GDN_ERR_BAD_SHAPE;
+  if (s->axes < 1 || s->axes > GDN_QK_MAX_AXES) return GDN_ERR_BAD_SHAPE;
+  for (int i = 0; i < s->rot / 2; ++i)
+    if (s->axis[i] >= s->axes) return GDN_ERR_BAD_SHAPE;
+  if (s->q_stride < (int64_t)s->H_q * s->d || s->k_stride < (int64_t)s->H_k * s->d) return GDN_ERR_BAD_SHAPE;
+  if (s->q_stride % 8 != 0 || s->k_stride % 8 != 0) return GDN_ERR_BAD_ALIGNMENT;
+  // tokens and the threads of a launch (at most d / 5 a token) are 32 bits
+  const int64_t heads = (int64_t)s->H_q + s->H_k;
+  if (s->B > 0 && s->T > (((int64_t)1 << 34) - 1) / s->d / (heads > 0 ? heads : 1) / s->B) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+static gdn::QkLaunch qk_launch(const gdn_qk_shape* s) {
+  gdn::QkLaunch p{};
+  p.q_stride = s->q_stride;
+  p.k_stride = s->k_stride;
+  p.T = s->T;
+  p.B = s->B;
+  p.Hq = s->H_q;
+  p.Hk = s->H_k;
+  p.d = s->d;
+  p.norm = s->norm;
+  p.rot = s->rot;
+  p.halves = s->pairs == GDN_PAIRS_HALVES;
+  p.bf16 = s->dtype == GDN_BF16;
+  p.eps = s->eps;
+  for (int i = 0; i < s->rot / 2; ++i) p.axis[i] = s->axis[i];
+  return p;
+}
+
+static bool qk_empty(const gdn_qk_shape* s) { return s->B == 0 || s->T == 0 || (s->H_q == 0 && s->H_k == 0); }
+
+gdn_status gdn_qk_norm_fwd(const gdn_qk_shape* s, const void* Q, const void* K, const float* wq, const float* wk,
+                           const double* freqs, const int32_t* positions, void* Q_out, void* K_out, void* stream) {
+  const gdn_status st = check_qk(s);
+  if (st != GDN_OK) return st;
+  if (qk_empty(s)) return GDN_OK;
+  if ((s->H_q > 0 && (!Q || !Q_out)) || (s->H_k > 0 && (!K || !K_out)) || (s->rot > 0 && !freqs))
+    return GDN_ERR_NULL_POINTER;
+  if (!all_aligned16({Q, K, wq, wk, freqs, positions, Q_out, K_out})) return GDN_ERR_BAD_ALIGNMENT;
+  gdn::QkLaunch p = qk_launch(s);
+  p.Q_in = Q;
+  p.K_in = K;
+  p.wq = wq;
+  p.wk = wk;
+  p.freqs = freqs;
+  p.positions = positions;
+  p.Q = Q_out;
+  p.K = K_out;
+  return launch_result(gdn::launch_qk(p, as_stream(stream)));
+}
+
+size_t gdn_qk_norm_bwd_workspace_bytes(const gdn_qk_shape* s) {
+  if (check_qk(s) != GDN_OK || qk_empty(s)) return 0;
+  return gdn::qk_bwd_workspace(qk_launch(s));
+}
+
+gdn_status gdn_qk_norm_bwd(const gdn_qk_shape* s, const void* dQ_out, const void* dK_out, const void* Q, const void* K,
+                           const float* wq, const float* wk, const double* freqs, const int32_t* positions, void* dQ,
+                           void* dK, float* dwq, float* dwk, void* workspace, size_t workspace_bytes, void* stream) {
+  gdn_status st = check_qk(s);
+  if (st != GDN_OK) return st;
+  const bool sums = dwq || dwk, empty = qk_empty(s);
+  if (empty && !sums) return GDN_OK;
+  if (!empty && ((s->H_q > 0 && (!dQ_out || !Q || !dQ)) || (s->H_k > 0 && (!dK_out || !K || !dK)) ||
+                 (s->rot > 0 && !freqs)))
+    return GDN_ERR_NULL_POINTER;
+  if (!all_aligned16({dQ_out, dK_out, Q, K, wq, wk, freqs, positions, dQ, dK, dwq, dwk})) return GDN_ERR_BAD_ALIGNMENT;
+  gdn::QkLaunch p = qk_launch(s);
+  st = check_workspace(sums && !empty ? gdn::qk_bwd_workspace(p) : 0, workspace, workspace_bytes);
+  if (st != GDN_OK) return st;
+  p.Q_in = Q;
+  p.K_in = K;
+  p.wq = wq;
+  p.wk = wk;
+  p.freqs = freqs;
+  p.positions = positions;
+  p.dQ = dQ_out;
+  p.dK = dK_out;
+  p.Q = dQ;
+  p.K = dK;
+  p.dwq = dwq;
+  p.dwk = dwk;
+  return launch_result(gdn::launch_qk_bwd(p, workspace, as_stream(stream)));
+}
+
+// ---- gated linear recurrence of every channel ------------------------------------------
+
+static gdn_status check_rec(const gdn_rec_shape* s) {
+  if (!s) return GDN_ERR_NULL_POINTER;
+  if (s->B < 0 || s->T < 0 || s->D <= 0) return GDN_ERR_BAD_SHAPE;
+  if (s->decay < GDN_DECAY_POWER || s->decay > GDN_DECAY_LOG) return GDN_ERR_BAD_SHAPE;
+  if (s->norm < GDN_REC_NORM_SQRT || s->norm > GDN_REC_NORM_NONE) return GDN_ERR_BAD_SHAPE;
+  if (!float_dtype(s->dtype)) return GDN_ERR_BAD_DTYPE;
+  if (s->D % 8 != 0) return GDN_ERR_UNSUPPORTED;
+  if (s->x_stride < s->D || s->a_stride < s->D || s->i_stride < s->D) return GDN_ERR_BAD_SHAPE;
+  if (s->x_stride % 8 != 0 || s->a_stride % 8 != 0 || s->i_stride % 8 != 0) return GDN_ERR_BAD_ALIGNMENT;
+  if (s->T > INT32_MAX - GDN_REC_TILE) return GDN_ERR_UNSUPPORTED;  // token indices in a row are 32 bits
+  return GDN_OK;
+}
+
+static gdn::RecLaunch rec_launch(const gdn_rec_shape* s) {
+  gdn::RecLaunch p{};
+  p.offsets = s->offsets;
+  p.x_stride = s->x_stride;
+  p.a_stride = s->a_stride;
+  p.i_stride = s->i_stride;
+  p.T = s->T;
+  p.tiles = (s->T + GDN_REC_TILE - 1) / GDN_REC_TILE;
+  p.n_seq = s->B;
+  p.D = s->D;
+  p.decay = s->decay;
+  p.norm = s->norm;
+  p.bf16 = s->dtype == GDN_BF16;
+  return p;
+}
+
+// without offsets a call of no sequences has no rows; with them its rows belong to none
+static bool rec_rows(const gdn_rec_shape* s) { return s->T > 0 && (s->B > 0 || s->offsets); }
+
+size_t gdn_rec_fwd_workspace_bytes(const gdn_rec_shape* s) {
+  if (check_rec(s) != GDN_OK || !rec_rows(s) || !gdn::rec_grid_ok(rec_launch(s))) return 0;
+  return gdn::rec_workspace(rec_launch(s), false);
+}
+
+size_t gdn_rec_bwd_workspace_bytes(const gdn_rec_shape* s) {
+  if (check_rec(s) != GDN_OK || !rec_rows(s) || !gdn::rec_grid_ok(rec_launch(s))) return 0;
+  return gdn::rec_workspace(rec_launch(s), true);
+}
+
+gdn_status gdn_rec_fwd(const gdn_rec_shape* s, const void* X, const void* A, const void* I, const float* w,
+                       const float* h0, void* H, float* h_out, float* states, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  gdn_status st = check_rec(s);
+  if (st != GDN_OK) return st;
+  if (s->B == 0) return GDN_OK;  // no sequence, no row of H
+  if (rec_rows(s) && (!X || !A || !H || (s->decay == GDN_DECAY_POWER && !w))) return GDN_ERR_NULL_POINTER;
+  if (!all_aligned16({X, A, I, w, h0, H, h_out, states, s->offsets})) return GDN_ERR_BAD_ALIGNMENT;
+  gdn::RecLaunch p = rec_launch(s);
+  if (!gdn::rec_grid_ok(p)) return GDN_ERR_UNSUPPORTED;
+  st = check_workspace(gdn::rec_workspace(p, false), workspace, workspace_bytes);
+  if (st != GDN_OK) return st;
+  p.X = X;
+  p.A = A;
+  p.I = I;
+  p.w = w;
+  p.h0 = h0;
+  p.H = H;
+  p.h_out = h_out;
+  p.states = states;
+  return launch_result(gdn::launch_rec_fwd(p, workspace, as_stream(stream)));
+}
+
+gdn_status gdn_rec_bwd(const gdn_rec_shape* s, const void* X, const void* A, const void* I, const float* w,
+                       const float* h0, const float* states, const void* dH, const float* dh, void* dX, void* dA,
+                       void* dI, float* dw, float* dh0, void* workspace, size_t workspace_bytes, void* stream) {
+  gdn_status st = check_rec(s);
+  if (st != GDN_OK) return st;
+  if (dw && s->decay != GDN_DECAY_POWER) return GDN_ERR_UNSUPPORTED;
+  const bool rows = rec_rows(s);
+  if (rows && (!X || !A || !dH || !dX || !dA || (I && !dI) || (s->decay == GDN_DECAY_POWER && !w)))
+    return GDN_ERR_NULL_POINTER;
+  if (!all_aligned16({X, A, I, w, h0, states, dH, dh, dX, dA, dI, dw, dh0, s->offsets})) return GDN_ERR_BAD_ALIGNMENT;
+  gdn::RecLaunch p = rec_launch(s);
+  if (!gdn::rec_grid_ok(p)) return GDN_ERR_UNSUPPORTED;
+  st = check_workspace(rows ? gdn::rec_workspace(p, true) : 0, workspace, workspace_bytes);
+  if (st != GDN_OK) return st;
+  p.X = X;
+  p.A = A;
+  p.I = I;
+  p.w = w;
+  p.h0 = h0;
+  p.states = const_cast<float*>(states);  // written only where they are not given
+  p.dH = dH;
+  p.dh = dh;
+  p.dX = dX;
+  p.dA = dA;
+  p.dI = dI;
+  p.dw = dw;
+  p.dh0 = dh0;
+  return launch_result(gdn::launch_rec_bwd(p, workspace, as_stream(stream)));
+}
+
+gdn_status gdn_rec_step(const gdn_rec_shape* s, const void* X, const void* A, const void* I, const float* w,
+                        const float* h_in, float* h_out, void* H, void* stream) {
+  const gdn_status st = check_rec(s);
+  if (st != GDN_OK) return st;
+  if (s->offsets) return GDN_ERR_UNSUPPORTED;
+  if (s->B == 0) return GDN_OK;
+  if (!h_out || (s->T > 0 && (!X || !A || !H || (s->decay == GDN_DECAY_POWER && !w)))) return GDN_ERR_NULL_POINTER;
+  if (!all_aligned16({X, A, I, w, h_in, h_out, H})) return GDN_ERR_BAD_ALIGNMENT;
+  gdn::RecLaunch p = rec_launch(s);
+  if (!gdn::rec_step_grid_ok(p)) return GDN_ERR_UNSUPPORTED;
+  p.X = X;
+  p.A = A;
+  p.I = I;
+  p.w = w;
+  p.h0 = h_in;
+  p.h_out = h_out;
+  p.H = H;
+  return launch_result(gdn::launch_rec_step(p, as_stream(stream)));
+}
+
 }  // extern "C"
 
 namespace gdn {

@@ -213,4 +213,73 @@ struct ResNormLaunch {
 size_t res_norm_bwd_workspace(const ResNormLaunch& p);
 int launch_res_norm(const ResNormLaunch& p, hipStream_t s);
 int launch_res_norm_bwd(const ResNormLaunch& p, void* workspace, hipStream_t s);
+// out0, out1 [D] = the sums over k < n of part[k][0][i] and part[k][1][i] (n_in 1 or 2), in order, in fp64
+// (norm.hip; NULL = not wanted)
+void launch_column_sum(const float* part, int64_t n, int D, int n_in, float* out0, float* out1, hipStream_t s);
+
+// gated linear recurrence of every channel (offsets: packed sequences, n_seq of them in T tokens;
+// NULL: n_seq sequences of T tokens each); D a multiple of 8
+constexpr int REC_TILE = GDN_REC_TILE;  // tokens between two states
+struct RecLaunch {
+  const void* X;
+  const void* A;
+  const void* I;       // NULL = no input gate
+  const float* w;      // decay GDN_DECAY_POWER
+  const float* h0;     // NULL = zeros
+  const int32_t* offsets;
+  int64_t x_stride, a_stride, i_stride;
+  int64_t T, tiles;    // of a row: T tokens in tiles of REC_TILE
+  int n_seq, D;
+  int decay, norm, bf16;
+  // forward and step
+  void* H;
+  float* h_out;        // NULL = not wanted
+  float* states;       // h before each tile; forward: NULL = not wanted, backward: NULL = not given
+  // backward
+  const void* dH;
+  const float* dh;     // NULL = zeros
+  void* dX;
+  void* dA;
+  void* dI;
+  float* dw;           // NULL = not wanted
+  float* dh0;          // NULL = not wanted
+  // in the workspace
+  float* tile_P;
+  float* tile_h;
+  int* tile_flags;
+  float* tile_e;
+  float* part;
+};
+size_t rec_workspace(const RecLaunch& p, bool bwd);
+bool rec_grid_ok(const RecLaunch& p);  // the launches' grids stay within their limits
+bool rec_step_grid_ok(const RecLaunch& p);
+int launch_rec_fwd(const RecLaunch& p, void* workspace, hipStream_t s);
+int launch_rec_bwd(const RecLaunch& p, void* workspace, hipStream_t s);
+int launch_rec_step(const RecLaunch& p, hipStream_t s);
+
+// norm and rotation of query and key heads: Q_in, K_in [B][T] rows of heads at their strides, Q, K
+// [B][H][T][d]; d a multiple of 32 up to 256, rot a multiple of 8 up to d
+struct QkLaunch {
+  const void* Q_in;
+  const void* K_in;
+  int64_t q_stride, k_stride;
+  const float* wq;  // NULL = ones
+  const float* wk;
+  const double* freqs;
+  const int32_t* positions;  // NULL = the token's index
+  void* Q;  // backward: dQ_in, dK_in [B][T][H][d]
+  void* K;
+  const void* dQ;  // [B][H][T][d]
+  const void* dK;
+  float* dwq;  // NULL = not wanted
+  float* dwk;
+  int64_t T;
+  int B, Hq, Hk, d;
+  int norm, rot, halves, bf16;
+  float eps;
+  uint8_t axis[GDN_QK_MAX_PAIRS];
+};
+size_t qk_bwd_workspace(const QkLaunch& p);
+int launch_qk(const QkLaunch& p, hipStream_t s);
+int launch_qk_bwd(const QkLaunch& p, void* workspace, hipStream_t s);
 }  // namespace gdn

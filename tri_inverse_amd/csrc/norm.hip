@@ -515,6 +515,10 @@ void column_sum(const float* part, int64_t n, int D, int n_in, const ColumnSum& 
 
 }  // namespace
 
+void launch_column_sum(const float* part, int64_t n, int D, int n_in, float* out0, float* out1, hipStream_t s) {
+  column_sum(part, n, D, n_in, {out0, out1, nullptr, nullptr, nullptr}, s);
+}
+
 size_t gate_norm_bwd_workspace(const GateNormLaunch& p) { return (size_t)gate_bwd_groups(p) * p.d * 4; }
 
 int launch_gate_norm(const GateNormLaunch& p, hipStream_t s) {
