@@ -740,7 +740,7 @@ static gdn::RecLaunch rec_launch(const gdn_rec_shape* s) {
   p.a_stride = s->a_stride;
   p.i_stride = s->i_stride;
   p.T = s->T;
-  p.tiles = (s->T + GDN_REC_TILE - 1) / GDN_REC_TILE;
+  p.n_states = (s->T + GDN_REC_TILE - 1) / GDN_REC_TILE;
   p.n_seq = s->B;
   p.D = s->D;
   p.decay = s->decay;

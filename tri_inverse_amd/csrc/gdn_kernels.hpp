@@ -219,7 +219,7 @@ void launch_column_sum(const float* part, int64_t n, int D, int n_in, float* out
 
 // gated linear recurrence of every channel (offsets: packed sequences, n_seq of them in T tokens;
 // NULL: n_seq sequences of T tokens each); D a multiple of 8
-constexpr int REC_TILE = GDN_REC_TILE;  // tokens between two states
+constexpr int REC_FWD_TILE = 64, REC_BWD_TILE = 64;  // tokens of a workgroup
 struct RecLaunch {
   const void* X;
   const void* A;
@@ -228,13 +228,13 @@ struct RecLaunch {
   const float* h0;     // NULL = zeros
   const int32_t* offsets;
   int64_t x_stride, a_stride, i_stride;
-  int64_t T, tiles;    // of a row: T tokens in tiles of REC_TILE
+  int64_t T, n_states; // of a row: T tokens, the states at every GDN_REC_TILE-th of them
   int n_seq, D;
   int decay, norm, bf16;
   // forward and step
   void* H;
   float* h_out;        // NULL = not wanted
-  float* states;       // h before each tile; forward: NULL = not wanted, backward: NULL = not given
+  float* states;       // [rows][n_states][D]; forward: NULL = not wanted, backward: NULL = not given
   // backward
   const void* dH;
   const float* dh;     // NULL = zeros
@@ -243,11 +243,12 @@ struct RecLaunch {
   void* dI;
   float* dw;           // NULL = not wanted
   float* dh0;          // NULL = not wanted
-  // in the workspace
-  float* tile_P;
-  float* tile_h;
-  int* tile_flags;
-  float* tile_e;
+  // set by the launchers: a row's tiles and, in the workspace, what links them
+  int64_t tiles;
+  uint64_t* chain_tiles;
+  uint64_t* chain_eights;
+  uint32_t* chain_states;
+  uint32_t* tickets;
   float* part;
 };
 size_t rec_workspace(const RecLaunch& p, bool bwd);

@@ -10,11 +10,23 @@
 //   dA = -w s'(A) dg | (1 - s(A)) dg | dg,  dw = -sum s(A) dg,  dh_0 = e_1
 //
 // h is affine in its start: over a run of tokens h = P h_start + h_run, P the product of the run's
-// decays.  A workgroup takes a tile of 64 tokens and 128 channels, two to a lane, so that a row
-// of a wave is 256 contiguous bytes (bf16), each wave a run of 8 tokens in registers.  The ends of the runs
-// join in LDS; the ends of the tiles in a second launch; a third forms the outputs from every
-// tile's start.  Decays, states and sums are fp32; 1 - a is formed without cancelling (expm1),
-// each output is rounded once.
+// decays.  A workgroup takes a tile of 8 runs and 128 channels, two to a lane, so that a row of a
+// wave is 256 contiguous bytes (bf16), each wave a run of tokens in registers.  The ends of the runs
+// join in LDS.  The tiles of a row and 128 channels form a chain, and the data is read once: a
+// workgroup publishes its tile's end (P, h), waits for those before it, and forms its outputs from the
+// registers it still holds.  Ends join by eights: a tile reads the ends of the tiles before it in its
+// eight, of the eights before its own in their eight, and the state before those 64 tiles, so a chain
+// has one step in a row for 64 tiles, whatever the order of the workgroups' progress the sums'
+// order is one, and the same call gives the same bits.
+//
+// Waiting: a word of a chain carries its value and, by not being NOT_YET, that it is there, in one
+// 64-bit (32-bit) store, so no fence is needed.  A workgroup takes its tile from its chain's counter,
+// in the order of the workgroups' starts: whatever it waits for has been taken by a workgroup that is
+// already running, which itself waits only for earlier ones, so every wait ends.  A wait is bounded
+// all the same: past the bound it takes NaN for the state.
+//
+// Decays, states and sums are fp32; 1 - a is formed without cancelling (expm1), each output is
+// rounded once.
 #include "gdn_device.hpp"
 #include "gdn_kernels.hpp"
 
@@ -22,11 +34,10 @@ namespace gdn {
 
 namespace {
 
-constexpr int RUN = 8;      // tokens of a wave
-constexpr int RUNS = 8;     // waves of a workgroup
-constexpr int TILE = REC_TILE;
+constexpr int RUNS = 8;       // waves of a workgroup, a run of tokens each
 constexpr int CH = 2 * WAVE;  // channels of a workgroup
-static_assert(RUN * RUNS == TILE, "");
+constexpr int FWD_RUN = REC_FWD_TILE / RUNS, BWD_RUN = REC_BWD_TILE / RUNS;
+static_assert(GDN_REC_TILE % FWD_RUN == 0 && REC_BWD_TILE % GDN_REC_TILE == 0, "states at the starts of runs and tiles");
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
@@ -114,31 +125,35 @@ struct Gate {
 
 // ---- sequences in a run of tokens ---------------------------------------------------------
 
-// bit j of the masks: token t0 + j belongs to a sequence, is its first, its last one.  seq: in lane j
-// the sequence of token t0 + j.  Offsets are clamped to the tokens, sequences to the given ones, so
-// offsets that break their rule lead to no access outside.
+// bit j of the masks: token t0 + j belongs to a sequence, is its first, its last one.  In lane j: the
+// sequence of token t0 + j, its first token and the one behind its last.  Offsets are clamped to the
+// tokens, sequences to the given ones, so offsets that break their rule lead to no access outside.
+template <int RUN>
 struct Run {
   uint32_t in, first, last;
-  int seq;
+  int seq, from, to;
   // all tokens in one sequence that neither starts nor ends here
-  __device__ __forceinline__ bool plain() const { return in == (1u << RUN) - 1 && (first | last) == 0; }
+  __device__ __forceinline__ bool plain() const { return in == (uint32_t)((1ull << RUN) - 1) && (first | last) == 0; }
   __device__ __forceinline__ int seq_of(int j) const { return __builtin_amdgcn_readlane(seq, j); }
 };
 
-__device__ __forceinline__ int64_t offset_at(const RecLaunch& a, int i) {
-  const int64_t o = a.offsets[i];
-  return o < 0 ? 0 : o > a.T ? a.T : o;
+__device__ __forceinline__ int offset_at(const RecLaunch& a, int i) {
+  const int o = a.offsets[i];
+  return o < 0 ? 0 : o > (int)a.T ? (int)a.T : o;
 }
 
-__device__ __forceinline__ Run find_run(const RecLaunch& a, int64_t t0, int b) {
-  Run r;
+template <int RUN>
+__device__ __forceinline__ Run<RUN> find_run(const RecLaunch& a, int64_t t0, int b) {
+  Run<RUN> r;
   if (!a.offsets) {
     const int64_t left = a.T - t0;
     const int n = left < 0 ? 0 : left > RUN ? RUN : (int)left;
-    r.in = (1u << n) - 1;
+    r.in = (uint32_t)((1ull << n) - 1);
     r.first = t0 == 0 && n > 0 ? 1u : 0u;
     r.last = left >= 1 && left <= RUN ? 1u << (n - 1) : 0u;
     r.seq = b;
+    r.from = 0;
+    r.to = (int)a.T;
     return r;
   }
   const int64_t t = t0 + lane_id();
@@ -152,36 +167,48 @@ __device__ __forceinline__ Run find_run(const RecLaunch& a, int64_t t0, int b) {
   }
   const bool some = lo >= 0;
   r.seq = some ? lo : 0;
-  const int64_t s = some ? offset_at(a, lo) : 0, e = some ? offset_at(a, lo + 1) : 0;
-  const bool in = some && t < e && t < a.T && lane_id() < RUN;
+  r.from = some ? offset_at(a, lo) : 0;
+  r.to = some ? offset_at(a, lo + 1) : 0;
+  const bool in = some && t < r.to && t < a.T && lane_id() < RUN;
   r.in = (uint32_t)__builtin_amdgcn_ballot_w64(in);
-  r.first = (uint32_t)__builtin_amdgcn_ballot_w64(in && t == s);
-  r.last = (uint32_t)__builtin_amdgcn_ballot_w64(in && t + 1 == e);
+  r.first = (uint32_t)__builtin_amdgcn_ballot_w64(in && t == r.from);
+  r.last = (uint32_t)__builtin_amdgcn_ballot_w64(in && t + 1 == r.to);
   return r;
 }
 
-// what joining needs to know of a tile
-enum { TILE_STARTS = 1, TILE_CONTINUES = 2, TILE_ENDS = 4, TILE_GOES_ON = 8 };
+// ---- a workgroup's place, its rows -----------------------------------------------------------
 
+// the workgroup's chain (a row b and 128 channels) and its tile in the chain's order: forwards the
+// tiles in order, backwards from the last one on
 struct Where {
-  int wave, cb, b;
-  int64_t tile, t0;  // the tile in its row; the run's first token
-  int c;             // the lane's first channel; D or more: none
-  __device__ __forceinline__ Where(const RecLaunch& a) {
-    wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-    const uint32_t blocks = (uint32_t)((a.D + CH - 1) / CH);
-    const uint32_t i = blockIdx.x / blocks;
-    cb = (int)(blockIdx.x - i * blocks);
-    b = (int)(i / (uint32_t)a.tiles);
-    tile = i - (uint32_t)b * (uint32_t)a.tiles;
-    t0 = tile * TILE + (int64_t)wave * RUN;
-    c = cb * CH + 2 * lane_id();
-  }
+  int wave, b, c;     // c: the lane's first channel; D or more: none
+  int chain, order;
+  int64_t tile, t0;   // the tile in its row; the run's first token
 };
+
+template <int RUN, bool BWD>
+__device__ __forceinline__ Where find_place(const RecLaunch& a) {
+  __shared__ uint32_t ticket;
+  Where at;
+  at.wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+  const uint32_t blocks = (uint32_t)((a.D + CH - 1) / CH), chains = gridDim.x / (uint32_t)a.tiles;
+  at.chain = (int)(blockIdx.x % chains);
+  at.order = 0;
+  if (a.tiles > 1) {
+    if (threadIdx.x == 0) ticket = __hip_atomic_fetch_add(a.tickets + at.chain, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    at.order = __builtin_amdgcn_readfirstlane((int)(ticket + 1u));  // the counter starts at NOT_YET
+  }
+  at.b = at.chain / (int)blocks;
+  at.c = (at.chain - at.b * (int)blocks) * CH + 2 * lane_id();
+  at.tile = BWD ? a.tiles - 1 - at.order : at.order;
+  at.t0 = at.tile * (RUN * RUNS) + at.wave * RUN;
+  return at;
+}
 
 // the run's rows of a tensor, two channels a lane: rows past the last token and lanes past the last
 // channel load what lies inside instead
-template <class E>
+template <class E, int RUN>
 __device__ __forceinline__ void load_run(const RecLaunch& a, const Where& at, const void* p, int64_t stride,
                                          typename Pair<E>::raw (&v)[RUN]) {
   const E* base = reinterpret_cast<const E*>(p) + (int64_t)at.b * a.T * stride;
@@ -200,18 +227,19 @@ __device__ __forceinline__ void store_row(const RecLaunch& a, const Where& at, v
         Pair<E>::close(v);
 }
 
-__device__ __forceinline__ f32x2 state_in(const RecLaunch& a, const float* S, int seq, int c) {
+__device__ __forceinline__ f32x2 state_in(const RecLaunch& a, const float* S, int64_t row, int c) {
   f32x2 h{0.f, 0.f};
-  if (S && c < a.D) h = *reinterpret_cast<const f32x2*>(S + (int64_t)seq * a.D + c);
+  if (S && c < a.D) h = *reinterpret_cast<const f32x2*>(S + row * a.D + c);
   return h;
 }
-__device__ __forceinline__ void state_out(const RecLaunch& a, float* S, int seq, int c, f32x2 h) {
-  if (S && c < a.D) *reinterpret_cast<f32x2*>(S + (int64_t)seq * a.D + c) = h;
+__device__ __forceinline__ void state_out(const RecLaunch& a, float* S, int64_t row, int c, f32x2 h) {
+  if (S && c < a.D) *reinterpret_cast<f32x2*>(S + row * a.D + c) = h;
 }
 
 __device__ __forceinline__ f32x2 fma2(f32x2 x, f32x2 y, f32x2 z) {
   return f32x2{fmaf(x[0], y[0], z[0]), fmaf(x[1], y[1], z[1])};
 }
+__device__ __forceinline__ f32x2 mul2(f32x2 x, f32x2 y) { return f32x2{x[0] * y[0], x[1] * y[1]}; }
 
 __device__ __forceinline__ f32x2 channel_w(const RecLaunch& a, int c) {
   f32x2 w{0.f, 0.f};
@@ -219,13 +247,165 @@ __device__ __forceinline__ f32x2 channel_w(const RecLaunch& a, int c) {
   return w;
 }
 
+// sequences without tokens return their states as they were given; dealt out over the tiles
+__device__ __forceinline__ void empty_sequences(const RecLaunch& a, const Where& at, const float* from, float* to) {
+  if (!a.offsets || !to || at.wave != 0) return;
+  for (int64_t s = at.tile; s < a.n_seq; s += a.tiles)
+    if (offset_at(a, (int)s) >= offset_at(a, (int)s + 1)) state_out(a, to, s, at.c, state_in(a, from, s, at.c));
+}
+
+// ---- chains -------------------------------------------------------------------------------
+
+constexpr uint32_t NOT_YET = ~0u;  // what the workspace is filled with; the bits of one NaN, never published
+constexpr int EIGHT = 8;
+constexpr int WAIT_ROUNDS = 1 << 22;  // some seconds
+
+// (P, h) of two channels, and h alone
+__device__ __forceinline__ uint32_t there(float h) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, h);
+  return u == NOT_YET ? 0x7fc00000u : u;
+}
+__device__ __forceinline__ void publish(uint64_t* p, f32x2 P, f32x2 h) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float Pk = P[k], hk = h[k];
+    __hip_atomic_store(p + k, (uint64_t)there(hk) << 32 | __builtin_bit_cast(uint32_t, Pk), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+  }
+}
+__device__ __forceinline__ void publish(uint32_t* p, f32x2 h) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) __hip_atomic_store(p + k, there(h[k]), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// every lane of the wave calls it; lanes that are off wait for nothing
+__device__ __forceinline__ void await(const uint64_t* p, bool on, f32x2& P, f32x2& h) {
+  uint64_t v[2] = {0, 0};
+  for (int i = 0;; ++i) {
+    if (on)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) v[k] = __hip_atomic_load(p + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const bool ready = (uint32_t)(v[0] >> 32) != NOT_YET && (uint32_t)(v[1] >> 32) != NOT_YET;
+    if (wave_all(ready) || i == WAIT_ROUNDS) break;
+    __builtin_amdgcn_s_sleep(1);
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t lo = (uint32_t)v[k], hi = (uint32_t)(v[k] >> 32);
+    P[k] = __builtin_bit_cast(float, lo);
+    h[k] = __builtin_bit_cast(float, hi);  // past the bound NOT_YET, a NaN
+  }
+}
+__device__ __forceinline__ f32x2 await(const uint32_t* p, bool on) {
+  uint32_t v[2] = {0, 0};
+  for (int i = 0;; ++i) {
+    if (on)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) v[k] = __hip_atomic_load(p + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (wave_all(v[0] != NOT_YET && v[1] != NOT_YET) || i == WAIT_ROUNDS) break;
+    __builtin_amdgcn_s_sleep(1);
+  }
+  const uint32_t lo = v[0], hi = v[1];
+  return f32x2{__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi)};
+}
+
+// ends of runs, of tiles and of eights, two channels a lane
+template <int N>
+struct Ends {
+  f32x2 P[N][WAVE], h[N][WAVE];
+  __device__ __forceinline__ void put(int i, f32x2 p, f32x2 x) {
+    P[i][lane_id()] = p;
+    h[i][lane_id()] = x;
+  }
+  // h behind entry i that starts from x; fresh: a sequence starts in it, so nothing comes from before
+  __device__ __forceinline__ f32x2 behind(int i, f32x2 x, bool fresh) const {
+    const f32x2 y = h[i][lane_id()];
+    return fresh ? y : fma2(P[i][lane_id()], x, y);
+  }
+};
+
+// the runs of a tile in the chain's order, and what comes from before the tile
+struct Link {
+  Ends<RUNS> run;
+  int fresh[RUNS];  // a sequence starts (backwards: ends) in the run
+  int from;         // the first tile in the chain's order that the tile's start comes from; its own: none
+  Ends<EIGHT - 1> tiles, eights;
+  f32x2 before[WAVE];
+
+  // the state before run n of the tile that starts from x
+  __device__ __forceinline__ f32x2 before_run(int n, f32x2 x) const {
+    for (int k = 0; k < n; ++k) x = run.behind(k, x, fresh[k] != 0);
+    return x;
+  }
+};
+
+// The tile's start; all waves call it, after the barrier behind the runs' ends.  order: the wave's run in the
+// chain's order.
+__device__ __forceinline__ f32x2 tile_start(const RecLaunch& a, const Where& at, int wave, Link& l) {
+  f32x2 x{0.f, 0.f};
+  if (a.tiles == 1) return x;
+  const int q = at.order, eight = q / EIGHT, block = eight / EIGHT, from = l.from, tiles = (int)a.tiles;
+  const bool on = at.c < a.D;
+  // words of this row, tile by tile [D]
+  const int64_t row = (int64_t)at.b * tiles;
+  uint64_t* ends = a.chain_tiles + row * a.D + at.c;
+  const int eights = tiles / EIGHT, blocks = eights / EIGHT;
+  uint64_t* eight_ends = a.chain_eights + (int64_t)at.b * eights * a.D + at.c;
+  uint32_t* states = a.chain_states + (int64_t)at.b * blocks * a.D + at.c;
+  f32x2 P{1.f, 1.f}, h{0.f, 0.f};
+  bool fresh = false;
+  if (wave == 0) {
+    for (int k = 0; k < RUNS; ++k) {
+      h = l.run.behind(k, h, l.fresh[k] != 0);
+      P = mul2(P, l.run.P[k][lane_id()]);
+      fresh = fresh || l.fresh[k] != 0;
+    }
+    if (on && q + 1 < tiles) publish(ends + (int64_t)q * a.D, P, h);
+  }
+  const int tile0 = eight * EIGHT, tile1 = from > tile0 ? from : tile0;
+  if (from < q) {
+    const int k = tile0 + wave;
+    if (wave < EIGHT - 1 && k >= tile1 && k < q) {
+      f32x2 Pk, hk;
+      await(ends + (int64_t)k * a.D, on, Pk, hk);
+      l.tiles.put(wave, Pk, hk);
+    }
+    __syncthreads();
+  }
+  if (wave == 0 && q % EIGHT == EIGHT - 1 && q + 1 < tiles) {
+    // the eight's end; its P is read only where the eight has no start
+    f32x2 y{0.f, 0.f}, Py{1.f, 1.f};
+    for (int k = tile1; k < q; ++k) {
+      y = l.tiles.behind(k - tile0, y, k == from);
+      Py = mul2(Py, l.tiles.P[k - tile0][lane_id()]);
+    }
+    y = fresh || from == q ? h : fma2(P, y, h);
+    if (on) publish(eight_ends + (int64_t)eight * a.D, mul2(Py, P), y);
+  }
+  const int eight0 = block * EIGHT, eight1 = from / EIGHT > eight0 ? from / EIGHT : eight0;
+  if (from < tile0) {
+    const int k = eight0 + wave;
+    if (wave < EIGHT - 1 && k >= eight1 && k < eight) {
+      f32x2 Pk, hk;
+      await(eight_ends + (int64_t)k * a.D, on, Pk, hk);
+      l.eights.put(wave, Pk, hk);
+    }
+    if (wave == EIGHT - 1 && from < eight0 * EIGHT) l.before[lane_id()] = await(states + (int64_t)(block - 1) * a.D, on);
+    __syncthreads();
+    if (from < eight0 * EIGHT) x = l.before[lane_id()];
+    for (int k2 = eight1; k2 < eight; ++k2) x = l.eights.behind(k2 - eight0, x, k2 == from / EIGHT);
+  }
+  for (int k = tile1; k < q; ++k) x = l.tiles.behind(k - tile0, x, k == from);
+  // the state behind 64 tiles
+  if (wave == 0 && q % (EIGHT * EIGHT) == EIGHT * EIGHT - 1 && q + 1 < tiles && on)
+    publish(states + (int64_t)block * a.D, fresh || from == q ? h : fma2(P, x, h));
+  return x;
+}
+
 // a and u of every token of the run
-template <class E, int DECAY, int NORM>
-__device__ __forceinline__ void open_run(const RecLaunch& a, const Where& at, f32x2 (&dec)[RUN], f32x2 (&u)[RUN]) {
-  typename Pair<E>::raw A[RUN], X[RUN], I[RUN];
-  load_run<E>(a, at, a.A, a.a_stride, A);
-  load_run<E>(a, at, a.X, a.x_stride, X);
-  if (a.I) load_run<E>(a, at, a.I, a.i_stride, I);
+template <class E, int DECAY, int NORM, int RUN>
+__device__ __forceinline__ void open_run(const RecLaunch& a, const Where& at, const typename Pair<E>::raw (&A)[RUN],
+                                         const typename Pair<E>::raw (&X)[RUN], const typename Pair<E>::raw (&I)[RUN],
+                                         f32x2 (&dec)[RUN], f32x2 (&u)[RUN]) {
   const f32x2 w = channel_w(a, at.c);
 #pragma unroll
   for (int j = 0; j < RUN; ++j) {
@@ -244,248 +424,114 @@ __device__ __forceinline__ void open_run(const RecLaunch& a, const Where& at, f3
   }
 }
 
-// the end of a run that starts from h: P and h on entry (1, start), reset where a sequence starts
-template <bool PLAIN, class Fn>
-__device__ __forceinline__ void walk(const RecLaunch& a, const Where& at, const Run& r, const f32x2 (&dec)[RUN],
+// the run's end (P, h) from P = 1 and h; each(j, h) before every token
+template <bool PLAIN, int RUN, class Fn>
+__device__ __forceinline__ void walk(const RecLaunch& a, const Where& at, const Run<RUN>& r, const f32x2 (&dec)[RUN],
                                      const f32x2 (&u)[RUN], f32x2& P, f32x2& h, Fn&& each) {
 #pragma unroll
   for (int j = 0; j < RUN; ++j) {
     if (!PLAIN) {
       if (!(r.in >> j & 1)) continue;
-      if (r.first >> j & 1) {
-        h = state_in(a, a.h0, r.seq_of(j), at.c);
-        P = f32x2{0.f, 0.f};
-      }
+      if (r.first >> j & 1) h = state_in(a, a.h0, r.seq_of(j), at.c);
     }
     each(j, h);
     h = fma2(dec[j], h, u[j]);
-    P = f32x2{P[0] * dec[j][0], P[1] * dec[j][1]};
+    P = mul2(P, dec[j]);
   }
-}
-
-// runs and tiles join by (P, h): a run in which a sequence starts takes nothing from before
-__device__ __forceinline__ f32x2 join(f32x2 P, f32x2 h, f32x2 start, bool starts) {
-  return starts ? h : fma2(P, start, h);
-}
-
-struct RunEnds {
-  f32x2 P[RUNS][WAVE], h[RUNS][WAVE];
-  int starts[RUNS];
-};
-
-// the state before run n of the tile that starts from h
-__device__ __forceinline__ f32x2 before_run(const RunEnds& e, int n, f32x2 h) {
-  for (int k = 0; k < n; ++k) h = join(e.P[k][lane_id()], e.h[k][lane_id()], h, e.starts[k] != 0);
-  return h;
-}
-
-// sequences without tokens return their states as they were given; dealt out over the tiles
-__device__ __forceinline__ void empty_sequences(const RecLaunch& a, const Where& at, const float* from, float* to) {
-  if (!a.offsets || !to || at.wave != 0) return;
-  for (int64_t s = at.tile; s < a.n_seq; s += a.tiles)
-    if (offset_at(a, (int)s) >= offset_at(a, (int)s + 1)) state_out(a, to, (int)s, at.c, state_in(a, from, (int)s, at.c));
 }
 
 }  // namespace
 
-// the ends (P, h) of every tile, and its flags
+// H, the last states and the states at the tiles' starts (each where wanted)
 template <class E, int DECAY, int NORM>
-__global__ __launch_bounds__(RUNS* WAVE) void rec_ends_kernel(RecLaunch a) {
-  __shared__ RunEnds ends;
-  __shared__ uint32_t masks[RUNS][3];
-  const Where at(a);
-  f32x2 dec[RUN], u[RUN];
-  const Run r = find_run(a, at.t0, at.b);
-  open_run<E, DECAY, NORM>(a, at, dec, u);
-  f32x2 P{1.f, 1.f}, h{0.f, 0.f};
-  auto nothing = [](int, f32x2) {};
-  if (r.plain())
-    walk<true>(a, at, r, dec, u, P, h, nothing);
-  else
-    walk<false>(a, at, r, dec, u, P, h, nothing);
-  ends.P[at.wave][lane_id()] = P;
-  ends.h[at.wave][lane_id()] = h;
-  ends.starts[at.wave] = r.first != 0;
-  if (lane_id() == 0) {
-    masks[at.wave][0] = r.in;
-    masks[at.wave][1] = r.first;
-    masks[at.wave][2] = r.last;
-  }
-  __syncthreads();
-  if (at.wave != 0) return;
-  P = f32x2{1.f, 1.f};
-  h = f32x2{0.f, 0.f};
-  uint32_t first = 0, last = 0;
-  for (int k = 0; k < RUNS; ++k) {
-    h = join(ends.P[k][lane_id()], ends.h[k][lane_id()], h, ends.starts[k] != 0);
-    const f32x2 Pk = ends.P[k][lane_id()];
-    P = f32x2{P[0] * Pk[0], P[1] * Pk[1]};
-    first |= masks[k][1];
-    last |= masks[k][2];
-  }
-  const int64_t i = (int64_t)at.b * a.tiles + at.tile;
-  if (at.c < a.D) {
-    *reinterpret_cast<f32x2*>(a.tile_P + i * a.D + at.c) = P;
-    *reinterpret_cast<f32x2*>(a.tile_h + i * a.D + at.c) = h;
-  }
-  if (at.cb == 0 && lane_id() == 0)
-    a.tile_flags[i] = (first ? TILE_STARTS : 0) | (last ? TILE_ENDS : 0) |
-                      ((masks[0][0] & 1) && !(masks[0][1] & 1) ? TILE_CONTINUES : 0) |
-                      ((masks[RUNS - 1][0] >> (RUN - 1)) && !(masks[RUNS - 1][2] >> (RUN - 1)) ? TILE_GOES_ON : 0);
-}
-
-// the ends (P, e) of every tile backwards
-template <class E, int DECAY, int NORM>
-__global__ __launch_bounds__(RUNS* WAVE) void rec_ends_bwd_kernel(RecLaunch a) {
-  __shared__ RunEnds ends;
-  const Where at(a);
-  const Run r = find_run(a, at.t0, at.b);
-  typename Pair<E>::raw A[RUN], G[RUN];
-  load_run<E>(a, at, a.A, a.a_stride, A);
-  load_run<E>(a, at, a.dH, a.D, G);
-  const f32x2 w = channel_w(a, at.c);
-  f32x2 P{1.f, 1.f}, e{0.f, 0.f};
-#pragma unroll
-  for (int j = RUN - 1; j >= 0; --j) {
-    if (!(r.in >> j & 1)) continue;
-    if (r.last >> j & 1) {
-      e = state_in(a, a.dh, r.seq_of(j), at.c);
-      P = f32x2{0.f, 0.f};
-    }
-    const f32x2 Av = Pair<E>::open(A[j]), d = Pair<E>::open(G[j]);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const Gate<DECAY, GDN_REC_NORM_NONE> g(Av[k], w[k]);
-      e[k] = g.a * (d[k] + e[k]);
-      P[k] *= g.a;
-    }
-  }
-  ends.P[at.wave][lane_id()] = P;
-  ends.h[at.wave][lane_id()] = e;
-  ends.starts[at.wave] = r.last != 0;
-  __syncthreads();
-  if (at.wave != 0) return;
-  P = f32x2{1.f, 1.f};
-  e = f32x2{0.f, 0.f};
-  for (int k = RUNS - 1; k >= 0; --k) {
-    const f32x2 Pk = ends.P[k][lane_id()];
-    e = join(Pk, ends.h[k][lane_id()], e, ends.starts[k] != 0);
-    P = f32x2{P[0] * Pk[0], P[1] * Pk[1]};
-  }
-  const int64_t i = (int64_t)at.b * a.tiles + at.tile;
-  if (at.c < a.D) {
-    *reinterpret_cast<f32x2*>(a.tile_P + i * a.D + at.c) = P;
-    *reinterpret_cast<f32x2*>(a.tile_h + i * a.D + at.c) = e;
-  }
-}
-
-// every tile's start from the tiles' ends, in order (backwards: from the last tile on); a wave for each
-// 128 channels of a row
-__global__ __launch_bounds__(WAVE) void rec_join_kernel(RecLaunch a, int backwards, float* starts) {
-  const int blocks = (a.D + CH - 1) / CH, b = blockIdx.x / blocks, c = (blockIdx.x - b * blocks) * CH + 2 * lane_id();
-  const bool on = c < a.D;
-  const int stops = backwards ? TILE_ENDS : TILE_STARTS, takes = backwards ? TILE_GOES_ON : TILE_CONTINUES;
-  f32x2 h{0.f, 0.f};
-  for (int64_t k = 0; k < a.tiles; ++k) {
-    const int64_t i = (int64_t)b * a.tiles + (backwards ? a.tiles - 1 - k : k), o = i * a.D + c;
-    const int flags = a.tile_flags[i];
-    if (!(flags & takes)) h = f32x2{0.f, 0.f};
-    if (on) {
-      *reinterpret_cast<f32x2*>(starts + o) = h;
-      h = join(*reinterpret_cast<const f32x2*>(a.tile_P + o), *reinterpret_cast<const f32x2*>(a.tile_h + o), h,
-               (flags & stops) != 0);
-    }
-  }
-}
-
-// H from every tile's start, and the last states
-template <class E, int DECAY, int NORM>
-__global__ __launch_bounds__(RUNS* WAVE) void rec_out_kernel(RecLaunch a) {
-  __shared__ RunEnds ends;
-  const Where at(a);
-  f32x2 dec[RUN], u[RUN];
-  const Run r = find_run(a, at.t0, at.b);
-  open_run<E, DECAY, NORM>(a, at, dec, u);
-  f32x2 P{1.f, 1.f}, h{0.f, 0.f};
-  auto nothing = [](int, f32x2) {};
-  if (r.plain())
-    walk<true>(a, at, r, dec, u, P, h, nothing);
-  else
-    walk<false>(a, at, r, dec, u, P, h, nothing);
-  ends.P[at.wave][lane_id()] = P;
-  ends.h[at.wave][lane_id()] = h;
-  ends.starts[at.wave] = r.first != 0;
-  __syncthreads();
-  const int64_t i = (int64_t)at.b * a.tiles + at.tile;
-  h = before_run(ends, at.wave, a.tiles > 1 ? state_in(a, a.states, (int)i, at.c) : f32x2{0.f, 0.f});
-#pragma unroll
-  for (int j = 0; j < RUN; ++j) {
-    if (!(r.in >> j & 1)) continue;
-    if (r.first >> j & 1) h = state_in(a, a.h0, r.seq_of(j), at.c);
-    h = fma2(dec[j], h, u[j]);
-    store_row<E>(a, at, a.H, j, h);
-    if (r.last >> j & 1) state_out(a, a.h_out, r.seq_of(j), at.c, h);
-  }
-  if (a.tiles == 1 && at.wave == 0) state_out(a, a.states, (int)i, at.c, f32x2{0.f, 0.f});
-  empty_sequences(a, at, a.h0, a.h_out);
-}
-
-// all gradients from every tile's start, forwards and backwards
-template <class E, int DECAY, int NORM>
-__global__ __launch_bounds__(RUNS* WAVE) void rec_bwd_kernel(RecLaunch a) {
-  __shared__ RunEnds fwd, bwd;
-  const Where at(a);
-  const Run r = find_run(a, at.t0, at.b);
-  typename Pair<E>::raw A[RUN], X[RUN], I[RUN], G[RUN];
+__global__ __launch_bounds__(RUNS* WAVE) void rec_fwd_kernel(RecLaunch a) {
+  constexpr int RUN = FWD_RUN;
+  __shared__ Link l;
+  const Where at = find_place<RUN, false>(a);
+  typename Pair<E>::raw A[RUN], X[RUN], I[RUN];
   load_run<E>(a, at, a.A, a.a_stride, A);
   load_run<E>(a, at, a.X, a.x_stride, X);
   if (a.I) load_run<E>(a, at, a.I, a.i_stride, I);
+  const Run<RUN> r = find_run<RUN>(a, at.t0, at.b);
+  f32x2 dec[RUN], u[RUN];
+  open_run<E, DECAY, NORM>(a, at, A, X, I, dec, u);
+  f32x2 P{1.f, 1.f}, h{0.f, 0.f};
+  auto nothing = [](int, f32x2) {};
+  if (r.plain())
+    walk<true>(a, at, r, dec, u, P, h, nothing);
+  else
+    walk<false>(a, at, r, dec, u, P, h, nothing);
+  l.run.put(at.wave, P, h);
+  const bool goes_on = (r.in & 1) && !(r.first & 1);  // the run's first token continues a sequence
+  if (lane_id() == 0) {
+    l.fresh[at.wave] = r.first != 0;
+    if (at.wave == 0) l.from = goes_on ? r.from / (RUN * RUNS) : at.order;
+  }
+  __syncthreads();
+  h = l.before_run(at.wave, tile_start(a, at, at.wave, l));
+  if (at.t0 % GDN_REC_TILE == 0 && at.t0 < a.T)
+    state_out(a, a.states, (int64_t)at.b * a.n_states + at.t0 / GDN_REC_TILE, at.c, goes_on ? h : f32x2{0.f, 0.f});
+  if (a.H || a.h_out) {
+#pragma unroll
+    for (int j = 0; j < RUN; ++j) {
+      if (!(r.in >> j & 1)) continue;
+      if (r.first >> j & 1) h = state_in(a, a.h0, r.seq_of(j), at.c);
+      h = fma2(dec[j], h, u[j]);
+      if (a.H) store_row<E>(a, at, a.H, j, h);
+      if (r.last >> j & 1) state_out(a, a.h_out, r.seq_of(j), at.c, h);
+    }
+    empty_sequences(a, at, a.h0, a.h_out);
+  }
+}
+
+// all gradients, from the states at the tiles' starts; the chain runs backwards
+template <class E, int DECAY, int NORM>
+__global__ __launch_bounds__(RUNS* WAVE) void rec_bwd_kernel(RecLaunch a) {
+  constexpr int RUN = BWD_RUN;
+  __shared__ Link l;
+  __shared__ Ends<RUNS> fwd;
+  __shared__ int starts[RUNS];
+  const Where at = find_place<RUN, true>(a);
+  typename Pair<E>::raw A[RUN], X[RUN], I[RUN], G[RUN];
+  load_run<E>(a, at, a.A, a.a_stride, A);
   load_run<E>(a, at, a.dH, a.D, G);
+  load_run<E>(a, at, a.X, a.x_stride, X);
+  if (a.I) load_run<E>(a, at, a.I, a.i_stride, I);
+  f32x2 h = a.tiles > 1 ? state_in(a, a.states, (int64_t)at.b * a.n_states + at.tile * (REC_BWD_TILE / GDN_REC_TILE), at.c)
+                        : f32x2{0.f, 0.f};
+  const Run<RUN> r = find_run<RUN>(a, at.t0, at.b);
   const f32x2 w = channel_w(a, at.c);
   f32x2 dec[RUN], u[RUN];
+  open_run<E, DECAY, NORM>(a, at, A, X, I, dec, u);
+  const int order = RUNS - 1 - at.wave;
+  {
+    f32x2 P{1.f, 1.f}, x{0.f, 0.f}, e{0.f, 0.f};
+    walk<false>(a, at, r, dec, u, P, x, [](int, f32x2) {});
+    fwd.put(at.wave, P, x);
 #pragma unroll
-  for (int j = 0; j < RUN; ++j) {
-    const f32x2 Av = Pair<E>::open(A[j]), x = Pair<E>::open(X[j]);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const Gate<DECAY, NORM> g(Av[k], w[k]);
-      dec[j][k] = g.a;
-      u[j][k] = g.b * x[k];
+    for (int j = RUN - 1; j >= 0; --j) {
+      if (!(r.in >> j & 1)) continue;
+      if (r.last >> j & 1) e = state_in(a, a.dh, r.seq_of(j), at.c);
+      const f32x2 d = Pair<E>::open(G[j]);
+      e = f32x2{dec[j][0] * (d[0] + e[0]), dec[j][1] * (d[1] + e[1])};
     }
-    if (a.I) {
-      const f32x2 i = Pair<E>::open(I[j]);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) u[j][k] *= sigmoid1(i[k]);
-    }
+    l.run.put(order, P, e);
   }
-  f32x2 P{1.f, 1.f}, h{0.f, 0.f}, e{0.f, 0.f};
-  walk<false>(a, at, r, dec, u, P, h, [](int, f32x2) {});
-  fwd.P[at.wave][lane_id()] = P;
-  fwd.h[at.wave][lane_id()] = h;
-  fwd.starts[at.wave] = r.first != 0;
-  P = f32x2{1.f, 1.f};
-#pragma unroll
-  for (int j = RUN - 1; j >= 0; --j) {
-    if (!(r.in >> j & 1)) continue;
-    if (r.last >> j & 1) e = state_in(a, a.dh, r.seq_of(j), at.c);
-    const f32x2 d = Pair<E>::open(G[j]);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      e[k] = dec[j][k] * (d[k] + e[k]);
-      P[k] *= dec[j][k];
-    }
+  if (lane_id() == 0) {
+    starts[at.wave] = r.first != 0;
+    l.fresh[order] = r.last != 0;
   }
-  bwd.P[at.wave][lane_id()] = P;
-  bwd.h[at.wave][lane_id()] = e;
-  bwd.starts[at.wave] = r.last != 0;
+  if (order == 0) {
+    // the tile's last token goes on into the next tile
+    const bool goes_on = (r.in >> (RUN - 1) & 1) && !(r.last >> (RUN - 1) & 1);
+    const int to = __builtin_amdgcn_readlane(r.to, RUN - 1);
+    if (lane_id() == 0) l.from = goes_on ? (int)a.tiles - 1 - (to - 1) / (RUN * RUNS) : at.order;
+  }
   __syncthreads();
-  const int64_t i = (int64_t)at.b * a.tiles + at.tile;
-  h = before_run(fwd, at.wave, a.tiles > 1 ? state_in(a, a.states, (int)i, at.c) : f32x2{0.f, 0.f});
-  e = a.tiles > 1 ? state_in(a, a.tile_e, (int)i, at.c) : f32x2{0.f, 0.f};
-  for (int k = RUNS - 1; k > at.wave; --k)
-    e = join(bwd.P[k][lane_id()], bwd.h[k][lane_id()], e, bwd.starts[k] != 0);
-  f32x2 before[RUN];
+  for (int k = 0; k < at.wave; ++k) h = fwd.behind(k, h, starts[k] != 0);
+  f32x2 before[RUN], P{1.f, 1.f};
   walk<false>(a, at, r, dec, u, P, h, [&](int j, f32x2 x) { before[j] = x; });
+  f32x2 e = l.before_run(order, tile_start(a, at, order, l));
   f32x2 dw{0.f, 0.f};
 #pragma unroll
   for (int j = RUN - 1; j >= 0; --j) {
@@ -524,7 +570,7 @@ __global__ __launch_bounds__(RUNS* WAVE) void rec_bwd_kernel(RecLaunch a) {
   if (at.wave != 0 || at.c >= a.D) return;
   dw = f32x2{0.f, 0.f};
   for (int k = 0; k < RUNS; ++k) dw += fwd.P[k][lane_id()];
-  *reinterpret_cast<f32x2*>(a.part + i * a.D + at.c) = dw;
+  *reinterpret_cast<f32x2*>(a.part + ((int64_t)at.b * a.tiles + at.tile) * a.D + at.c) = dw;
 }
 
 // token by token, the state in registers for the whole call: a wave for each 128 channels of a
@@ -560,6 +606,12 @@ __global__ __launch_bounds__(256) void rec_copy_kernel(const float* from, float*
     to[i] = from ? from[i] : 0.f;
 }
 
+// NOT_YET in every word of the chains
+__global__ __launch_bounds__(256) void rec_clear_kernel(u32x4* p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+    p[i] = u32x4{NOT_YET, NOT_YET, NOT_YET, NOT_YET};
+}
+
 // ---- host side ----------------------------------------------------------------------------
 
 namespace {
@@ -587,38 +639,47 @@ int64_t channel_blocks(const RecLaunch& p) { return (p.D + CH - 1) / CH; }
 int64_t rows_of(const RecLaunch& p) { return p.offsets ? 1 : p.n_seq; }
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
-// the workspace in order: the tiles' ends, their flags, their starts (backwards both ways), dw's parts
+// the workspace in order: a chain's words (the ends of the tiles and of their eights, the states behind 64
+// tiles, the counters), backwards those of a pass for the states and the states themselves, dw's parts
 struct Parts {
-  size_t P, h, flags, states, e, part, bytes;
+  size_t tiles, eights, states, tickets, chain;  // offsets in a chain's words, and their size
+  size_t fwd_chain, starts, part, bytes;         // backwards
   Parts(const RecLaunch& p, bool bwd) {
-    const size_t n = (size_t)(rows_of(p) * p.tiles), v = up16(n * p.D * 4);
-    size_t at = 0;
-    auto take = [&](size_t s) {
-      const size_t here = at;
-      at += s;
-      return here;
-    };
-    const bool many = p.tiles > 1;
-    P = take(many ? v : 0);
-    h = take(many ? v : 0);
-    flags = take(many ? up16(n * 4) : 0);
-    states = take(many ? v : 0);
-    e = take(many && bwd ? v : 0);
-    part = take(bwd && p.decay == GDN_DECAY_POWER ? v : 0);
-    bytes = at;
+    chain_of(p, bwd ? REC_BWD_TILE : REC_FWD_TILE);
+    bytes = chain;
+    if (!bwd) return;
+    const Parts f(p, false);
+    fwd_chain = bytes;
+    starts = fwd_chain + f.chain;
+    const int64_t rows = rows_of(p);
+    part = starts + (tiles_of(p, REC_BWD_TILE) > 1 ? up16((size_t)(rows * p.n_states * p.D) * 4) : 0);
+    bytes = part + (p.decay == GDN_DECAY_POWER ? up16((size_t)(rows * tiles_of(p, REC_BWD_TILE) * p.D) * 4) : 0);
+  }
+  static int64_t tiles_of(const RecLaunch& p, int tile) { return (p.T + tile - 1) / tile; }
+  void chain_of(const RecLaunch& p, int tile) {
+    const int64_t n = tiles_of(p, tile), v = rows_of(p) * p.D;
+    tiles = 0;
+    eights = tiles + up16((size_t)(n * v) * 8);
+    states = eights + up16((size_t)(n / EIGHT * v) * 8);
+    tickets = states + up16((size_t)(n / EIGHT / EIGHT * v) * 4);
+    chain = n > 1 ? tickets + up16((size_t)(rows_of(p) * channel_blocks(p)) * 4) : 0;
   }
 };
 
-RecLaunch placed(const RecLaunch& p, void* workspace, bool bwd) {
+// the call with its chain's words at ws, filled
+RecLaunch chained(const RecLaunch& p, bool bwd, char* ws, hipStream_t s) {
   RecLaunch q = p;
   const Parts at(p, bwd);
-  char* ws = reinterpret_cast<char*>(workspace);
-  q.tile_P = reinterpret_cast<float*>(ws + at.P);
-  q.tile_h = reinterpret_cast<float*>(ws + at.h);
-  q.tile_flags = reinterpret_cast<int*>(ws + at.flags);
-  if (!q.states && p.tiles > 1) q.states = reinterpret_cast<float*>(ws + at.states);
-  q.tile_e = reinterpret_cast<float*>(ws + at.e);
-  q.part = reinterpret_cast<float*>(ws + at.part);
+  q.tiles = Parts::tiles_of(p, bwd ? REC_BWD_TILE : REC_FWD_TILE);
+  if (q.tiles > 1) {
+    q.chain_tiles = reinterpret_cast<uint64_t*>(ws + at.tiles);
+    q.chain_eights = reinterpret_cast<uint64_t*>(ws + at.eights);
+    q.chain_states = reinterpret_cast<uint32_t*>(ws + at.states);
+    q.tickets = reinterpret_cast<uint32_t*>(ws + at.tickets);
+    const int64_t n = (int64_t)(at.chain / 16), g = (n + 255) / 256;
+    hipLaunchKernelGGL(rec_clear_kernel, dim3((unsigned)(g < 2048 ? g : 2048)), dim3(256), 0, s,
+                       reinterpret_cast<u32x4*>(ws), n);
+  }
   return q;
 }
 
@@ -628,13 +689,7 @@ void copy_states(const float* from, float* to, int64_t n, hipStream_t s) {
   hipLaunchKernelGGL(rec_copy_kernel, dim3((unsigned)(g < 1024 ? g : 1024)), dim3(256), 0, s, from, to, n);
 }
 
-template <class E, int DECAY, int NORM>
-void find_states(const RecLaunch& q, dim3 grid, hipStream_t s) {
-  const dim3 block(RUNS * WAVE);
-  hipLaunchKernelGGL((rec_ends_kernel<E, DECAY, NORM>), grid, block, 0, s, q);
-  hipLaunchKernelGGL(rec_join_kernel, dim3((unsigned)(channel_blocks(q) * rows_of(q))), dim3(WAVE), 0, s, q, 0,
-                     q.states);
-}
+dim3 grid_of(const RecLaunch& q) { return dim3((unsigned)(q.tiles * rows_of(q) * channel_blocks(q))); }
 
 }  // namespace
 
@@ -642,7 +697,9 @@ size_t rec_workspace(const RecLaunch& p, bool bwd) { return p.T == 0 ? 0 : Parts
 
 bool rec_grid_ok(const RecLaunch& p) {
   // a launch has fewer than 2^32 threads
-  return p.tiles <= (((int64_t)1 << 32) - 1) / (RUNS * WAVE) / channel_blocks(p) / (rows_of(p) > 0 ? rows_of(p) : 1);
+  constexpr int least = REC_FWD_TILE < REC_BWD_TILE ? REC_FWD_TILE : REC_BWD_TILE;
+  const int64_t tiles = (p.T + least - 1) / least, rows = rows_of(p) > 0 ? rows_of(p) : 1;
+  return tiles <= (((int64_t)1 << 32) - 1) / (RUNS * WAVE) / channel_blocks(p) / rows;
 }
 bool rec_step_grid_ok(const RecLaunch& p) { return p.n_seq <= (((int64_t)1 << 32) - 256) / WAVE / channel_blocks(p); }
 
@@ -651,12 +708,10 @@ int launch_rec_fwd(const RecLaunch& p, void* workspace, hipStream_t s) {
     copy_states(p.h0, p.h_out, (int64_t)p.n_seq * p.D, s);
     return 0;
   }
-  const RecLaunch q = placed(p, workspace, false);
-  const dim3 grid((unsigned)(q.tiles * rows_of(q) * channel_blocks(q))), block(RUNS * WAVE);
+  const RecLaunch q = chained(p, false, reinterpret_cast<char*>(workspace), s);
   return by_kind(p, [&](auto e, auto decay, auto norm) {
     typedef std::remove_pointer_t<decltype(e)> E;
-    if (q.tiles > 1) find_states<E, decay.value, norm.value>(q, grid, s);
-    hipLaunchKernelGGL((rec_out_kernel<E, decay.value, norm.value>), grid, block, 0, s, q);
+    hipLaunchKernelGGL((rec_fwd_kernel<E, decay.value, norm.value>), grid_of(q), dim3(RUNS * WAVE), 0, s, q);
     return 0;
   });
 }
@@ -667,17 +722,23 @@ int launch_rec_bwd(const RecLaunch& p, void* workspace, hipStream_t s) {
     copy_states(nullptr, p.dw, p.D, s);
     return 0;
   }
-  const RecLaunch q = placed(p, workspace, true);
-  const dim3 grid((unsigned)(q.tiles * rows_of(q) * channel_blocks(q))), block(RUNS * WAVE);
+  char* ws = reinterpret_cast<char*>(workspace);
+  const Parts at(p, true);
+  RecLaunch q = chained(p, true, ws, s);
+  q.part = reinterpret_cast<float*>(ws + at.part);
+  const bool form = q.tiles > 1 && !p.states;
+  RecLaunch f{};
+  if (form) {
+    q.states = reinterpret_cast<float*>(ws + at.starts);
+    f = chained(p, false, ws + at.fwd_chain, s);
+    f.H = nullptr;
+    f.h_out = nullptr;
+    f.states = q.states;
+  }
   return by_kind(p, [&](auto e, auto decay, auto norm) {
     typedef std::remove_pointer_t<decltype(e)> E;
-    if (q.tiles > 1) {
-      find_states<E, decay.value, norm.value>(q, grid, s);
-      hipLaunchKernelGGL((rec_ends_bwd_kernel<E, decay.value, norm.value>), grid, block, 0, s, q);
-      hipLaunchKernelGGL(rec_join_kernel, dim3((unsigned)(channel_blocks(q) * rows_of(q))), dim3(WAVE), 0, s, q,
-                         1, q.tile_e);
-    }
-    hipLaunchKernelGGL((rec_bwd_kernel<E, decay.value, norm.value>), grid, block, 0, s, q);
+    if (form) hipLaunchKernelGGL((rec_fwd_kernel<E, decay.value, norm.value>), grid_of(f), dim3(RUNS * WAVE), 0, s, f);
+    hipLaunchKernelGGL((rec_bwd_kernel<E, decay.value, norm.value>), grid_of(q), dim3(RUNS * WAVE), 0, s, q);
     if (q.dw) launch_column_sum(q.part, q.tiles * rows_of(q), q.D, 1, q.dw, nullptr, s);
     return 0;
   });
