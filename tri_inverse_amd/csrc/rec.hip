@@ -67,57 +67,76 @@ struct Pair<float> {
 
 __device__ __forceinline__ float rcp(float x) { return __builtin_amdgcn_rcpf(x); }
 
-// sigmoid and what it leaves of 1, neither by a difference that cancels
-__device__ __forceinline__ void sigmoid2(float z, float& s, float& rest) {
-  const float e = __expf(-z);
+// exponentials are of 2, which the hardware forms: log-decays are held in units of log 2
+constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f;
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + exp2_of(-LOG2E * z)); }
+// sigmoid and what it leaves of 1, which a difference would cancel; 2^-126 and not 0 for far z < 0
+__device__ __forceinline__ void sigmoid_rest(float z, float& s, float& rest) {
+  const float e = exp2_of(fminf(-LOG2E * z, 126.f));
   s = rcp(1.f + e);
-  rest = z < 0.f ? 1.f - s : e * s;
-}
-__device__ __forceinline__ float sigmoid1(float z) { return rcp(1.f + __expf(-z)); }
-
-// e^g - 1, a = e^g known: near 0 the series, whose first term left out is below 2^-24 of it
-__device__ __forceinline__ float expm1_of(float g, float a) {
-  float p = 1.f / 720.f;
-  p = fmaf(p, g, 1.f / 120.f);
-  p = fmaf(p, g, 1.f / 24.f);
-  p = fmaf(p, g, 1.f / 6.f);
-  p = fmaf(p, g, 0.5f);
-  p = fmaf(p, g, 1.f);
-  return fabsf(g) < 0.25f ? p * g : a - 1.f;
+  rest = e * s;
 }
 
-// the decay of a token, the factor b of its input; backwards also b'(g) and what turns dg into dA
-// (to_A) and dw (r)
-template <int DECAY, int NORM>
+// 1 - 2^(n gl), n = 1 or 2, p = 2^(n gl) known: below 1/4 in n g the series (its first term left out is below
+// 2^-24 of it), above it the difference, right to 2^-21
+template <int N>
+__device__ __forceinline__ float rest_of(float gl, float p) {
+  constexpr float x = N * LN2, x2 = x * x, x3 = x2 * x;
+  float r = -x3 * x3 / 720.f;
+  r = fmaf(r, gl, -x3 * x2 / 120.f);
+  r = fmaf(r, gl, -x2 * x2 / 24.f);
+  r = fmaf(r, gl, -x3 / 6.f);
+  r = fmaf(r, gl, -x2 / 2.f);
+  r = fmaf(r, gl, -x);
+  return fabsf(gl) < 0.25f * LOG2E / N ? r * gl : p;
+}
+
+// the decay of a token and the factor b of its input; backwards also b'(g), and what turns dg into dA
+// (to_A) and into dw (r).  wl = -w log2 e.
+template <int DECAY, int NORM, bool BWD>
 struct Gate {
   float a, b, db, to_A, r;
-  __device__ __forceinline__ Gate(float A, float w) {
-    float m = 0.f;  // a - 1
+  __device__ __forceinline__ Gate(float A, float wl) {
     db = 0.f;
     r = 0.f;
+    to_A = 1.f;
+    float q = 1.f;  // 1 - a, or 1 - a^2
     if constexpr (DECAY == GDN_DECAY_SIGMOID) {
-      sigmoid2(A, a, to_A);
-      m = -to_A;
+      const float e = exp2_of(-LOG2E * A);
+      a = rcp(1.f + e);
+      const float rest = A < 0.f ? 1.f - a : e * a;  // e may be infinite
+      to_A = rest;
+      q = NORM == GDN_REC_NORM_SQRT ? rest * (1.f + a) : rest;
     } else {
-      float g = A;
-      to_A = 1.f;
+      float gl;
       if constexpr (DECAY == GDN_DECAY_POWER) {
-        float rest;
-        sigmoid2(A, r, rest);
-        g = -w * r;
-        to_A = g * rest;
+        if constexpr (BWD) {
+          float rest;
+          sigmoid_rest(A, r, rest);
+          gl = wl * r;
+          to_A = LN2 * gl * rest;
+        } else {
+          gl = wl * sigmoid(A);
+        }
+      } else {
+        gl = LOG2E * A;
       }
-      a = __expf(g);
-      if constexpr (NORM != GDN_REC_NORM_NONE) m = expm1_of(g, a);
+      a = exp2_of(gl);
+      if constexpr (NORM == GDN_REC_NORM_SQRT) q = rest_of<2>(gl, fmaf(-a, a, 1.f));
+      if constexpr (NORM == GDN_REC_NORM_LINEAR) q = rest_of<1>(gl, 1.f - a);
     }
     if constexpr (NORM == GDN_REC_NORM_SQRT) {
-      const float q = -m * (2.f + m);  // 1 - a^2
-      // a = 1: b = 0, whose own gradient counts as 0
-      const float rs = q == 0.f ? 0.f : __builtin_amdgcn_rsqf(q);
-      b = q * rs;
-      db = -a * a * rs;
+      if constexpr (BWD) {
+        // a = 1: b = 0, whose gradient counts as 0; so do fp32's subnormal numbers
+        const float rs = fabsf(q) < 1.17549435e-38f ? 0.f : __builtin_amdgcn_rsqf(q);
+        b = q * rs;
+        db = -a * a * rs;
+      } else {
+        b = __builtin_amdgcn_sqrtf(q);
+      }
     } else {
-      b = NORM == GDN_REC_NORM_LINEAR ? -m : 1.f;
+      b = NORM == GDN_REC_NORM_NONE ? 1.f : q;
       if constexpr (NORM == GDN_REC_NORM_LINEAR) db = -a;
     }
   }
@@ -183,7 +202,7 @@ __device__ __forceinline__ Run<RUN> find_run(const RecLaunch& a, int64_t t0, int
 struct Where {
   int wave, b, c;     // c: the lane's first channel; D or more: none
   int chain, order;
-  int64_t tile, t0;   // the tile in its row; the run's first token
+  int tile, t0;       // the tile in its row; the run's first token
 };
 
 template <int RUN, bool BWD>
@@ -201,7 +220,7 @@ __device__ __forceinline__ Where find_place(const RecLaunch& a) {
   }
   at.b = at.chain / (int)blocks;
   at.c = (at.chain - at.b * (int)blocks) * CH + 2 * lane_id();
-  at.tile = BWD ? a.tiles - 1 - at.order : at.order;
+  at.tile = BWD ? (int)a.tiles - 1 - at.order : at.order;
   at.t0 = at.tile * (RUN * RUNS) + at.wave * RUN;
   return at;
 }
@@ -211,20 +230,23 @@ __device__ __forceinline__ Where find_place(const RecLaunch& a) {
 template <class E, int RUN>
 __device__ __forceinline__ void load_run(const RecLaunch& a, const Where& at, const void* p, int64_t stride,
                                          typename Pair<E>::raw (&v)[RUN]) {
-  const E* base = reinterpret_cast<const E*>(p) + (int64_t)at.b * a.T * stride;
-  const int c = at.c < a.D ? at.c : 0;
+  // uniform rows and a lane's offset of 32 bits
+  const int64_t step = stride * (int64_t)sizeof(E);
+  const int T = (int)a.T, t0 = at.t0 < T ? at.t0 : T - 1;
+  const char* row = reinterpret_cast<const char*>(p) + ((int64_t)at.b * a.T + t0) * step;
+  const uint32_t c = (at.c < a.D ? (uint32_t)at.c : 0u) * (uint32_t)sizeof(E);
 #pragma unroll
   for (int j = 0; j < RUN; ++j) {
-    const int64_t t = at.t0 + j < a.T ? at.t0 + j : a.T - 1;
-    v[j] = *reinterpret_cast<const typename Pair<E>::raw*>(base + t * stride + c);
+    v[j] = *reinterpret_cast<const typename Pair<E>::raw*>(row + c);
+    if (at.t0 + j + 1 < T) row += step;
   }
 }
 
 template <class E>
 __device__ __forceinline__ void store_row(const RecLaunch& a, const Where& at, void* p, int j, f32x2 v) {
+  char* row = reinterpret_cast<char*>(reinterpret_cast<E*>(p) + ((int64_t)at.b * a.T + at.t0 + j) * a.D);
   if (at.c < a.D)
-    *reinterpret_cast<typename Pair<E>::raw*>(reinterpret_cast<E*>(p) + ((int64_t)at.b * a.T + at.t0 + j) * a.D + at.c) =
-        Pair<E>::close(v);
+    *reinterpret_cast<typename Pair<E>::raw*>(row + (uint32_t)at.c * (uint32_t)sizeof(E)) = Pair<E>::close(v);
 }
 
 __device__ __forceinline__ f32x2 state_in(const RecLaunch& a, const float* S, int64_t row, int c) {
@@ -241,10 +263,11 @@ __device__ __forceinline__ f32x2 fma2(f32x2 x, f32x2 y, f32x2 z) {
 }
 __device__ __forceinline__ f32x2 mul2(f32x2 x, f32x2 y) { return f32x2{x[0] * y[0], x[1] * y[1]}; }
 
+// -w log2 e
 __device__ __forceinline__ f32x2 channel_w(const RecLaunch& a, int c) {
   f32x2 w{0.f, 0.f};
   if (a.w && c < a.D) w = *reinterpret_cast<const f32x2*>(a.w + c);
-  return w;
+  return f32x2{-LOG2E * w[0], -LOG2E * w[1]};
 }
 
 // sequences without tokens return their states as they were given; dealt out over the tiles
@@ -402,7 +425,7 @@ __device__ __forceinline__ f32x2 tile_start(const RecLaunch& a, const Where& at,
 }
 
 // a and u of every token of the run
-template <class E, int DECAY, int NORM, int RUN>
+template <class E, int DECAY, int NORM, bool BWD, int RUN>
 __device__ __forceinline__ void open_run(const RecLaunch& a, const Where& at, const typename Pair<E>::raw (&A)[RUN],
                                          const typename Pair<E>::raw (&X)[RUN], const typename Pair<E>::raw (&I)[RUN],
                                          f32x2 (&dec)[RUN], f32x2 (&u)[RUN]) {
@@ -412,14 +435,21 @@ __device__ __forceinline__ void open_run(const RecLaunch& a, const Where& at, co
     const f32x2 Av = Pair<E>::open(A[j]), x = Pair<E>::open(X[j]);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const Gate<DECAY, NORM> g(Av[k], w[k]);
+      const Gate<DECAY, NORM, BWD> g(Av[k], w[k]);
       dec[j][k] = g.a;
       u[j][k] = g.b * x[k];
     }
     if (a.I) {
       const f32x2 i = Pair<E>::open(I[j]);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) u[j][k] *= sigmoid1(i[k]);
+      for (int k = 0; k < 2; ++k) {
+        float s, rest;
+        if constexpr (BWD)
+          sigmoid_rest(i[k], s, rest);
+        else
+          s = sigmoid(i[k]);
+        u[j][k] *= s;
+      }
     }
   }
 }
@@ -454,7 +484,7 @@ __global__ __launch_bounds__(RUNS* WAVE) void rec_fwd_kernel(RecLaunch a) {
   if (a.I) load_run<E>(a, at, a.I, a.i_stride, I);
   const Run<RUN> r = find_run<RUN>(a, at.t0, at.b);
   f32x2 dec[RUN], u[RUN];
-  open_run<E, DECAY, NORM>(a, at, A, X, I, dec, u);
+  open_run<E, DECAY, NORM, false>(a, at, A, X, I, dec, u);
   f32x2 P{1.f, 1.f}, h{0.f, 0.f};
   auto nothing = [](int, f32x2) {};
   if (r.plain())
@@ -502,7 +532,7 @@ __global__ __launch_bounds__(RUNS* WAVE) void rec_bwd_kernel(RecLaunch a) {
   const Run<RUN> r = find_run<RUN>(a, at.t0, at.b);
   const f32x2 w = channel_w(a, at.c);
   f32x2 dec[RUN], u[RUN];
-  open_run<E, DECAY, NORM>(a, at, A, X, I, dec, u);
+  open_run<E, DECAY, NORM, true>(a, at, A, X, I, dec, u);
   const int order = RUNS - 1 - at.wave;
   {
     f32x2 P{1.f, 1.f}, x{0.f, 0.f}, e{0.f, 0.f};
@@ -542,11 +572,11 @@ __global__ __launch_bounds__(RUNS* WAVE) void rec_bwd_kernel(RecLaunch a) {
       const f32x2 iv = a.I ? Pair<E>::open(I[j]) : f32x2{0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const Gate<DECAY, NORM> g(Av[k], w[k]);
+        const Gate<DECAY, NORM, true> g(Av[k], w[k]);
         const float D = d[k] + e[k];
         e[k] = g.a * D;
         float s = 1.f, rest = 0.f;
-        if (a.I) sigmoid2(iv[k], s, rest);
+        if (a.I) sigmoid_rest(iv[k], s, rest);
         const float dz = D * g.b, z = s * x[k];
         dX[k] = dz * s;
         dI[k] = dz * z * rest;
@@ -592,8 +622,8 @@ __global__ __launch_bounds__(256) void rec_step_kernel(RecLaunch a) {
     if (a.I) iv = Pair<E>::open(*reinterpret_cast<const raw*>(reinterpret_cast<const E*>(a.I) + row * a.i_stride + c));
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const Gate<DECAY, NORM> g(Av[k], w[k]);
-      h[k] = fmaf(g.a, h[k], g.b * (a.I ? sigmoid1(iv[k]) : 1.f) * x[k]);
+      const Gate<DECAY, NORM, false> g(Av[k], w[k]);
+      h[k] = fmaf(g.a, h[k], g.b * (a.I ? sigmoid(iv[k]) : 1.f) * x[k]);
     }
     *reinterpret_cast<raw*>(reinterpret_cast<E*>(a.H) + row * a.D + c) = Pair<E>::close(h);
   }
