@@ -219,7 +219,6 @@ void launch_column_sum(const float* part, int64_t n, int D, int n_in, float* out
 
 // gated linear recurrence of every channel (offsets: packed sequences, n_seq of them in T tokens;
 // NULL: n_seq sequences of T tokens each); D a multiple of 8
-constexpr int REC_FWD_TILE = 64, REC_BWD_TILE = 64;  // tokens of a workgroup
 struct RecLaunch {
   const void* X;
   const void* A;
@@ -247,7 +246,7 @@ struct RecLaunch {
   int64_t tiles;
   uint64_t* chain_tiles;
   uint64_t* chain_eights;
-  uint32_t* chain_states;
+  uint64_t* chain_states;
   uint32_t* tickets;
   float* part;
 };

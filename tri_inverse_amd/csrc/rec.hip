@@ -36,10 +36,16 @@ namespace {
 
 constexpr int RUNS = 8;       // waves of a workgroup, a run of tokens each
 constexpr int CH = 2 * WAVE;  // channels of a workgroup
-constexpr int FWD_RUN = REC_FWD_TILE / RUNS, BWD_RUN = REC_BWD_TILE / RUNS;
-static_assert(GDN_REC_TILE % FWD_RUN == 0 && REC_BWD_TILE % GDN_REC_TILE == 0, "states at the starts of runs and tiles");
+constexpr int FWD_TILE = 128, BWD_TILE = 64;  // tokens of a tile: as many as leave room for two workgroups a CU
+static_assert(GDN_REC_TILE % (FWD_TILE / RUNS) == 0 && BWD_TILE % GDN_REC_TILE == 0, "states at the starts of runs and tiles");
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// a value of which the compiler knows nothing from here on
+template <class V>
+__device__ __forceinline__ void hide(V& v) {
+  asm volatile("" : "+v"(v));
+}
 
 // two neighbouring channels as they lie in memory, and as fp32
 template <class E>
@@ -92,52 +98,43 @@ __device__ __forceinline__ float rest_of(float gl, float p) {
   return fabsf(gl) < 0.25f * LOG2E / N ? r * gl : p;
 }
 
-// the decay of a token and the factor b of its input; backwards also b'(g), and what turns dg into dA
-// (to_A) and into dw (r).  wl = -w log2 e.
-template <int DECAY, int NORM, bool BWD>
+// the decay of a token and the factor b of its input.  wl = -w log2 e.
+template <int DECAY, int NORM>
 struct Gate {
-  float a, b, db, to_A, r;
+  float a, b;
   __device__ __forceinline__ Gate(float A, float wl) {
-    db = 0.f;
-    r = 0.f;
-    to_A = 1.f;
     float q = 1.f;  // 1 - a, or 1 - a^2
     if constexpr (DECAY == GDN_DECAY_SIGMOID) {
       const float e = exp2_of(-LOG2E * A);
       a = rcp(1.f + e);
       const float rest = A < 0.f ? 1.f - a : e * a;  // e may be infinite
-      to_A = rest;
       q = NORM == GDN_REC_NORM_SQRT ? rest * (1.f + a) : rest;
     } else {
-      float gl;
-      if constexpr (DECAY == GDN_DECAY_POWER) {
-        if constexpr (BWD) {
-          float rest;
-          sigmoid_rest(A, r, rest);
-          gl = wl * r;
-          to_A = LN2 * gl * rest;
-        } else {
-          gl = wl * sigmoid(A);
-        }
-      } else {
-        gl = LOG2E * A;
-      }
+      const float gl = DECAY == GDN_DECAY_POWER ? wl * sigmoid(A) : LOG2E * A;
       a = exp2_of(gl);
       if constexpr (NORM == GDN_REC_NORM_SQRT) q = rest_of<2>(gl, fmaf(-a, a, 1.f));
       if constexpr (NORM == GDN_REC_NORM_LINEAR) q = rest_of<1>(gl, 1.f - a);
     }
-    if constexpr (NORM == GDN_REC_NORM_SQRT) {
-      if constexpr (BWD) {
-        // a = 1: b = 0, whose gradient counts as 0; so do fp32's subnormal numbers
-        const float rs = fabsf(q) < 1.17549435e-38f ? 0.f : __builtin_amdgcn_rsqf(q);
-        b = q * rs;
-        db = -a * a * rs;
-      } else {
-        b = __builtin_amdgcn_sqrtf(q);
-      }
-    } else {
-      b = NORM == GDN_REC_NORM_NONE ? 1.f : q;
-      if constexpr (NORM == GDN_REC_NORM_LINEAR) db = -a;
+    b = NORM == GDN_REC_NORM_SQRT ? __builtin_amdgcn_sqrtf(q) : NORM == GDN_REC_NORM_LINEAR ? q : 1.f;
+  }
+};
+// b'(g) of a and b
+template <int NORM>
+__device__ __forceinline__ float slope(float a, float b) {
+  if constexpr (NORM == GDN_REC_NORM_NONE) return 0.f;
+  if constexpr (NORM == GDN_REC_NORM_LINEAR) return -a;
+  return b == 0.f ? 0.f : -a * a * rcp(b);  // where a = 1 the gradient of b = 0 counts as 0
+}
+// what turns dg into dA (first) and into dw (r)
+template <int DECAY>
+struct GateGrad {
+  float to_A = 1.f, r = 0.f;
+  __device__ __forceinline__ GateGrad(float A, float wl) {
+    float rest;
+    if constexpr (DECAY == GDN_DECAY_SIGMOID) sigmoid_rest(A, r, to_A);
+    if constexpr (DECAY == GDN_DECAY_POWER) {
+      sigmoid_rest(A, r, rest);
+      to_A = LN2 * (wl * r) * rest;
     }
   }
 };
@@ -197,12 +194,12 @@ __device__ __forceinline__ Run<RUN> find_run(const RecLaunch& a, int64_t t0, int
 
 // ---- a workgroup's place, its rows -----------------------------------------------------------
 
-// the workgroup's chain (a row b and 128 channels) and its tile in the chain's order: forwards the
-// tiles in order, backwards from the last one on
+// the workgroup's chain (a row b and 128 channels) and its tile, in the chain's order: forwards the tiles in
+// order, backwards from the last one on
 struct Where {
-  int wave, b, c;     // c: the lane's first channel; D or more: none
-  int chain, order;
-  int tile, t0;       // the tile in its row; the run's first token
+  int wave, b, c;  // c: the lane's first channel; D or more: none
+  int order;
+  int tile, t0;    // the tile in its row; the run's first token
 };
 
 template <int RUN, bool BWD>
@@ -211,35 +208,18 @@ __device__ __forceinline__ Where find_place(const RecLaunch& a) {
   Where at;
   at.wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
   const uint32_t blocks = (uint32_t)((a.D + CH - 1) / CH), chains = gridDim.x / (uint32_t)a.tiles;
-  at.chain = (int)(blockIdx.x % chains);
+  const uint32_t chain = blockIdx.x % chains;
   at.order = 0;
   if (a.tiles > 1) {
-    if (threadIdx.x == 0) ticket = __hip_atomic_fetch_add(a.tickets + at.chain, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (threadIdx.x == 0) ticket = __hip_atomic_fetch_add(a.tickets + chain, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
     at.order = __builtin_amdgcn_readfirstlane((int)(ticket + 1u));  // the counter starts at NOT_YET
   }
-  at.b = at.chain / (int)blocks;
-  at.c = (at.chain - at.b * (int)blocks) * CH + 2 * lane_id();
+  at.b = (int)(chain / blocks);
+  at.c = (int)(chain - (uint32_t)at.b * blocks) * CH + 2 * lane_id();
   at.tile = BWD ? (int)a.tiles - 1 - at.order : at.order;
-  at.t0 = at.tile * (RUN * RUNS) + at.wave * RUN;
+  at.t0 = at.tile * RUN * RUNS + at.wave * RUN;
   return at;
-}
-
-// the run's rows of a tensor, two channels a lane: rows past the last token and lanes past the last
-// channel load what lies inside instead
-template <class E, int RUN>
-__device__ __forceinline__ void load_run(const RecLaunch& a, const Where& at, const void* p, int64_t stride,
-                                         typename Pair<E>::raw (&v)[RUN]) {
-  // uniform rows and a lane's offset of 32 bits
-  const int64_t step = stride * (int64_t)sizeof(E);
-  const int T = (int)a.T, t0 = at.t0 < T ? at.t0 : T - 1;
-  const char* row = reinterpret_cast<const char*>(p) + ((int64_t)at.b * a.T + t0) * step;
-  const uint32_t c = (at.c < a.D ? (uint32_t)at.c : 0u) * (uint32_t)sizeof(E);
-#pragma unroll
-  for (int j = 0; j < RUN; ++j) {
-    v[j] = *reinterpret_cast<const typename Pair<E>::raw*>(row + c);
-    if (at.t0 + j + 1 < T) row += step;
-  }
 }
 
 template <class E>
@@ -283,7 +263,7 @@ constexpr uint32_t NOT_YET = ~0u;  // what the workspace is filled with; the bit
 constexpr int EIGHT = 8;
 constexpr int WAIT_ROUNDS = 1 << 22;  // some seconds
 
-// (P, h) of two channels, and h alone
+// (P, h) of two channels
 __device__ __forceinline__ uint32_t there(float h) {
   const uint32_t u = __builtin_bit_cast(uint32_t, h);
   return u == NOT_YET ? 0x7fc00000u : u;
@@ -296,40 +276,31 @@ __device__ __forceinline__ void publish(uint64_t* p, f32x2 P, f32x2 h) {
                        __HIP_MEMORY_SCOPE_AGENT);
   }
 }
-__device__ __forceinline__ void publish(uint32_t* p, f32x2 h) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k) __hip_atomic_store(p + k, there(h[k]), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-// every lane of the wave calls it; lanes that are off wait for nothing
-__device__ __forceinline__ void await(const uint64_t* p, bool on, f32x2& P, f32x2& h) {
+// a lane's words of one entry, looked at until they are there.  Every lane of the wave calls look and wait;
+// lanes that are off (p NULL) wait for nothing.
+struct Words {
+  const uint64_t* p;
   uint64_t v[2] = {0, 0};
-  for (int i = 0;; ++i) {
-    if (on)
+  __device__ __forceinline__ explicit Words(const uint64_t* at) : p(at) { look(); }
+  __device__ __forceinline__ void look() {
+    if (p)
 #pragma unroll
       for (int k = 0; k < 2; ++k) v[k] = __hip_atomic_load(p + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const bool ready = (uint32_t)(v[0] >> 32) != NOT_YET && (uint32_t)(v[1] >> 32) != NOT_YET;
-    if (wave_all(ready) || i == WAIT_ROUNDS) break;
-    __builtin_amdgcn_s_sleep(1);
   }
+  __device__ __forceinline__ void wait(f32x2& P, f32x2& h) {
+    for (int i = 0; i < WAIT_ROUNDS; ++i) {
+      if (wave_all((uint32_t)(v[0] >> 32) != NOT_YET && (uint32_t)(v[1] >> 32) != NOT_YET)) break;
+      __builtin_amdgcn_s_sleep(1);
+      look();
+    }
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const uint32_t lo = (uint32_t)v[k], hi = (uint32_t)(v[k] >> 32);
-    P[k] = __builtin_bit_cast(float, lo);
-    h[k] = __builtin_bit_cast(float, hi);  // past the bound NOT_YET, a NaN
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t lo = (uint32_t)v[k], hi = (uint32_t)(v[k] >> 32);
+      P[k] = __builtin_bit_cast(float, lo);
+      h[k] = __builtin_bit_cast(float, hi);  // past the bound NOT_YET, a NaN
+    }
   }
-}
-__device__ __forceinline__ f32x2 await(const uint32_t* p, bool on) {
-  uint32_t v[2] = {0, 0};
-  for (int i = 0;; ++i) {
-    if (on)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) v[k] = __hip_atomic_load(p + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (wave_all(v[0] != NOT_YET && v[1] != NOT_YET) || i == WAIT_ROUNDS) break;
-    __builtin_amdgcn_s_sleep(1);
-  }
-  const uint32_t lo = v[0], hi = v[1];
-  return f32x2{__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi)};
-}
+};
 
 // ends of runs, of tiles and of eights, two channels a lane
 template <int N>
@@ -361,19 +332,18 @@ struct Link {
   }
 };
 
-// The tile's start; all waves call it, after the barrier behind the runs' ends.  order: the wave's run in the
+// The tile's start; all waves call it, after the barrier behind the runs' ends.  wave: the wave's run in the
 // chain's order.
 __device__ __forceinline__ f32x2 tile_start(const RecLaunch& a, const Where& at, int wave, Link& l) {
   f32x2 x{0.f, 0.f};
   if (a.tiles == 1) return x;
   const int q = at.order, eight = q / EIGHT, block = eight / EIGHT, from = l.from, tiles = (int)a.tiles;
   const bool on = at.c < a.D;
-  // words of this row, tile by tile [D]
-  const int64_t row = (int64_t)at.b * tiles;
-  uint64_t* ends = a.chain_tiles + row * a.D + at.c;
+  // words of this row, entry by entry [D]
+  uint64_t* ends = a.chain_tiles + (int64_t)at.b * tiles * a.D + at.c;
   const int eights = tiles / EIGHT, blocks = eights / EIGHT;
   uint64_t* eight_ends = a.chain_eights + (int64_t)at.b * eights * a.D + at.c;
-  uint32_t* states = a.chain_states + (int64_t)at.b * blocks * a.D + at.c;
+  uint64_t* states = a.chain_states + (int64_t)at.b * blocks * a.D + at.c;
   f32x2 P{1.f, 1.f}, h{0.f, 0.f};
   bool fresh = false;
   if (wave == 0) {
@@ -385,86 +355,118 @@ __device__ __forceinline__ f32x2 tile_start(const RecLaunch& a, const Where& at,
     if (on && q + 1 < tiles) publish(ends + (int64_t)q * a.D, P, h);
   }
   const int tile0 = eight * EIGHT, tile1 = from > tile0 ? from : tile0;
-  if (from < q) {
-    const int k = tile0 + wave;
-    if (wave < EIGHT - 1 && k >= tile1 && k < q) {
-      f32x2 Pk, hk;
-      await(ends + (int64_t)k * a.D, on, Pk, hk);
-      l.tiles.put(wave, Pk, hk);
-    }
-    __syncthreads();
-  }
-  if (wave == 0 && q % EIGHT == EIGHT - 1 && q + 1 < tiles) {
-    // the eight's end; its P is read only where the eight has no start
-    f32x2 y{0.f, 0.f}, Py{1.f, 1.f};
-    for (int k = tile1; k < q; ++k) {
-      y = l.tiles.behind(k - tile0, y, k == from);
-      Py = mul2(Py, l.tiles.P[k - tile0][lane_id()]);
-    }
-    y = fresh || from == q ? h : fma2(P, y, h);
-    if (on) publish(eight_ends + (int64_t)eight * a.D, mul2(Py, P), y);
-  }
   const int eight0 = block * EIGHT, eight1 = from / EIGHT > eight0 ? from / EIGHT : eight0;
-  if (from < tile0) {
-    const int k = eight0 + wave;
-    if (wave < EIGHT - 1 && k >= eight1 && k < eight) {
-      f32x2 Pk, hk;
-      await(eight_ends + (int64_t)k * a.D, on, Pk, hk);
-      l.eights.put(wave, Pk, hk);
+  const bool closes = q % EIGHT == EIGHT - 1 && q + 1 < tiles;  // the tile ends its eight, for others to use
+  if (from < q) {
+    // all words are asked for at once.  The wave behind the eights' takes the state.
+    const int kt = tile0 + wave, ke = eight0 + wave;
+    const bool one = wave < EIGHT - 1 && kt >= tile1 && kt < q;
+    const bool two = from < tile0 && wave < EIGHT - 1 && ke >= eight1 && ke < eight;
+    const bool three = wave == EIGHT - 1 && from < eight0 * EIGHT;
+    Words near(one && on ? ends + (int64_t)kt * a.D : nullptr);
+    Words far(on && two ? eight_ends + (int64_t)ke * a.D : on && three ? states + (int64_t)(block - 1) * a.D : nullptr);
+    f32x2 Pk, hk;
+    near.wait(Pk, hk);
+    if (one) l.tiles.put(wave, Pk, hk);
+    // the eight's end does not wait for what comes before the eight
+    if (closes) {
+      __syncthreads();
+      if (wave == 0) {
+        f32x2 y{0.f, 0.f}, Py{1.f, 1.f};  // Py is read only where no sequence starts in the eight
+        for (int k = tile1; k < q; ++k) {
+          y = l.tiles.behind(k - tile0, y, k == from);
+          Py = mul2(Py, l.tiles.P[k - tile0][lane_id()]);
+        }
+        if (on) publish(eight_ends + (int64_t)eight * a.D, mul2(Py, P), fresh ? h : fma2(P, y, h));
+      }
     }
-    if (wave == EIGHT - 1 && from < eight0 * EIGHT) l.before[lane_id()] = await(states + (int64_t)(block - 1) * a.D, on);
+    far.wait(Pk, hk);
+    if (two) l.eights.put(wave, Pk, hk);
+    if (three) l.before[lane_id()] = hk;
     __syncthreads();
     if (from < eight0 * EIGHT) x = l.before[lane_id()];
-    for (int k2 = eight1; k2 < eight; ++k2) x = l.eights.behind(k2 - eight0, x, k2 == from / EIGHT);
+    if (from < tile0)
+      for (int k = eight1; k < eight; ++k) x = l.eights.behind(k - eight0, x, k == from / EIGHT);
+    for (int k = tile1; k < q; ++k) x = l.tiles.behind(k - tile0, x, k == from);
+  } else if (closes && wave == 0 && on) {
+    publish(eight_ends + (int64_t)eight * a.D, P, h);  // nothing comes from before: h alone is read
   }
-  for (int k = tile1; k < q; ++k) x = l.tiles.behind(k - tile0, x, k == from);
   // the state behind 64 tiles
   if (wave == 0 && q % (EIGHT * EIGHT) == EIGHT * EIGHT - 1 && q + 1 < tiles && on)
-    publish(states + (int64_t)block * a.D, fresh || from == q ? h : fma2(P, x, h));
+    publish(states + (int64_t)block * a.D, P, fresh || from == q ? h : fma2(P, x, h));
   return x;
 }
 
-// a and u of every token of the run
-template <class E, int DECAY, int NORM, bool BWD, int RUN>
-__device__ __forceinline__ void open_run(const RecLaunch& a, const Where& at, const typename Pair<E>::raw (&A)[RUN],
-                                         const typename Pair<E>::raw (&X)[RUN], const typename Pair<E>::raw (&I)[RUN],
-                                         f32x2 (&dec)[RUN], f32x2 (&u)[RUN]) {
-  const f32x2 w = channel_w(a, at.c);
+// the rows of a run, two channels a lane: A, X, I and backwards dH
+template <class E, int RUN, bool GATE, bool BWD>
+struct Raw {
+  typename Pair<E>::raw A[RUN], X[RUN], I[GATE ? RUN : 1], G[BWD ? RUN : 1];
+};
+// they are loaded token by token (backwards from the last one): rows past the last token and lanes past
+// the last channel load what lies inside instead.  Rows are uniform, a lane's offset in them 32 bits.
+template <class E, int RUN, bool GATE, bool BWD>
+struct Loader {
+  const char *A, *X, *I, *G;
+  uint32_t c;
+  int t;
+  __device__ __forceinline__ Loader(const RecLaunch& a, const Where& at) {
+    t = BWD ? at.t0 + RUN - 1 : at.t0;
+    const int64_t row = (int64_t)at.b * a.T + (t < (int)a.T ? t : (int)a.T - 1);
+    const int64_t size = sizeof(E);
+    A = reinterpret_cast<const char*>(a.A) + row * a.a_stride * size;
+    X = reinterpret_cast<const char*>(a.X) + row * a.x_stride * size;
+    I = reinterpret_cast<const char*>(a.I) + row * a.i_stride * size;
+    G = reinterpret_cast<const char*>(a.dH) + row * a.D * size;
+    c = (at.c < a.D ? (uint32_t)at.c : 0u) * (uint32_t)sizeof(E);
+  }
+  __device__ __forceinline__ void next(const RecLaunch& a, Raw<E, RUN, GATE, BWD>& r, int j) {
+    typedef typename Pair<E>::raw raw;
+    r.A[j] = *reinterpret_cast<const raw*>(A + c);
+    if constexpr (BWD) r.G[j] = *reinterpret_cast<const raw*>(G + c);
+    r.X[j] = *reinterpret_cast<const raw*>(X + c);
+    if constexpr (GATE) r.I[j] = *reinterpret_cast<const raw*>(I + c);
+    const bool move = BWD ? t < (int)a.T && t > 0 : t + 1 < (int)a.T;
+    t += BWD ? -1 : 1;
+    const int64_t size = BWD ? -(int64_t)sizeof(E) : (int64_t)sizeof(E);
+    A += move ? a.a_stride * size : 0;
+    X += move ? a.x_stride * size : 0;
+    if constexpr (GATE) I += move ? a.i_stride * size : 0;
+    if constexpr (BWD) G += move ? a.D * size : 0;
+  }
+};
+
+// a, b and u = b s(I) X of every token of the run
+template <class E, int DECAY, int NORM, bool GATE, bool BWD, int RUN>
+__device__ __forceinline__ void open_run(const Raw<E, RUN, GATE, BWD>& raw, f32x2 w, f32x2 (&dec)[RUN],
+                                         f32x2 (&b)[RUN], f32x2 (&u)[RUN]) {
 #pragma unroll
   for (int j = 0; j < RUN; ++j) {
-    const f32x2 Av = Pair<E>::open(A[j]), x = Pair<E>::open(X[j]);
+    const f32x2 Av = Pair<E>::open(raw.A[j]), x = Pair<E>::open(raw.X[j]);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const Gate<DECAY, NORM, BWD> g(Av[k], w[k]);
+      const Gate<DECAY, NORM> g(Av[k], w[k]);
       dec[j][k] = g.a;
+      b[j][k] = g.b;
       u[j][k] = g.b * x[k];
     }
-    if (a.I) {
-      const f32x2 i = Pair<E>::open(I[j]);
+    if constexpr (GATE) {
+      const f32x2 i = Pair<E>::open(raw.I[j]);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float s, rest;
-        if constexpr (BWD)
-          sigmoid_rest(i[k], s, rest);
-        else
-          s = sigmoid(i[k]);
-        u[j][k] *= s;
-      }
+      for (int k = 0; k < 2; ++k) u[j][k] *= sigmoid(i[k]);
     }
   }
 }
 
-// the run's end (P, h) from P = 1 and h; each(j, h) before every token
-template <bool PLAIN, int RUN, class Fn>
+// the run's end (P, h) from P = 1 and h
+template <bool PLAIN, int RUN>
 __device__ __forceinline__ void walk(const RecLaunch& a, const Where& at, const Run<RUN>& r, const f32x2 (&dec)[RUN],
-                                     const f32x2 (&u)[RUN], f32x2& P, f32x2& h, Fn&& each) {
+                                     const f32x2 (&u)[RUN], f32x2& P, f32x2& h) {
 #pragma unroll
   for (int j = 0; j < RUN; ++j) {
     if (!PLAIN) {
       if (!(r.in >> j & 1)) continue;
       if (r.first >> j & 1) h = state_in(a, a.h0, r.seq_of(j), at.c);
     }
-    each(j, h);
     h = fma2(dec[j], h, u[j]);
     P = mul2(P, dec[j]);
   }
@@ -473,24 +475,23 @@ __device__ __forceinline__ void walk(const RecLaunch& a, const Where& at, const 
 }  // namespace
 
 // H, the last states and the states at the tiles' starts (each where wanted)
-template <class E, int DECAY, int NORM>
-__global__ __launch_bounds__(RUNS* WAVE) void rec_fwd_kernel(RecLaunch a) {
-  constexpr int RUN = FWD_RUN;
+template <class E, int DECAY, int NORM, bool GATE>
+__global__ __launch_bounds__(RUNS* WAVE) __attribute__((amdgpu_waves_per_eu(4, 4))) void rec_fwd_kernel(RecLaunch a) {
+  constexpr int RUN = FWD_TILE / RUNS;
   __shared__ Link l;
   const Where at = find_place<RUN, false>(a);
-  typename Pair<E>::raw A[RUN], X[RUN], I[RUN];
-  load_run<E>(a, at, a.A, a.a_stride, A);
-  load_run<E>(a, at, a.X, a.x_stride, X);
-  if (a.I) load_run<E>(a, at, a.I, a.i_stride, I);
+  Raw<E, RUN, GATE, false> raw;
+  Loader<E, RUN, GATE, false> rows(a, at);
+#pragma unroll
+  for (int j = 0; j < RUN; ++j) rows.next(a, raw, j);
   const Run<RUN> r = find_run<RUN>(a, at.t0, at.b);
-  f32x2 dec[RUN], u[RUN];
-  open_run<E, DECAY, NORM, false>(a, at, A, X, I, dec, u);
+  f32x2 dec[RUN], b[RUN], u[RUN];
+  open_run<E, DECAY, NORM>(raw, channel_w(a, at.c), dec, b, u);
   f32x2 P{1.f, 1.f}, h{0.f, 0.f};
-  auto nothing = [](int, f32x2) {};
   if (r.plain())
-    walk<true>(a, at, r, dec, u, P, h, nothing);
+    walk<true>(a, at, r, dec, u, P, h);
   else
-    walk<false>(a, at, r, dec, u, P, h, nothing);
+    walk<false>(a, at, r, dec, u, P, h);
   l.run.put(at.wave, P, h);
   const bool goes_on = (r.in & 1) && !(r.first & 1);  // the run's first token continues a sequence
   if (lane_id() == 0) {
@@ -501,57 +502,55 @@ __global__ __launch_bounds__(RUNS* WAVE) void rec_fwd_kernel(RecLaunch a) {
   h = l.before_run(at.wave, tile_start(a, at, at.wave, l));
   if (at.t0 % GDN_REC_TILE == 0 && at.t0 < a.T)
     state_out(a, a.states, (int64_t)at.b * a.n_states + at.t0 / GDN_REC_TILE, at.c, goes_on ? h : f32x2{0.f, 0.f});
-  if (a.H || a.h_out) {
+  if (!a.H) return;  // the states alone
 #pragma unroll
-    for (int j = 0; j < RUN; ++j) {
-      if (!(r.in >> j & 1)) continue;
-      if (r.first >> j & 1) h = state_in(a, a.h0, r.seq_of(j), at.c);
-      h = fma2(dec[j], h, u[j]);
-      if (a.H) store_row<E>(a, at, a.H, j, h);
-      if (r.last >> j & 1) state_out(a, a.h_out, r.seq_of(j), at.c, h);
-    }
-    empty_sequences(a, at, a.h0, a.h_out);
+  for (int j = 0; j < RUN; ++j) {
+    if (!(r.in >> j & 1)) continue;
+    if (r.first >> j & 1) h = state_in(a, a.h0, r.seq_of(j), at.c);
+    h = fma2(dec[j], h, u[j]);
+    store_row<E>(a, at, a.H, j, h);
+    if (r.last >> j & 1) state_out(a, a.h_out, r.seq_of(j), at.c, h);
   }
+  empty_sequences(a, at, a.h0, a.h_out);
 }
 
 // all gradients, from the states at the tiles' starts; the chain runs backwards
-template <class E, int DECAY, int NORM>
-__global__ __launch_bounds__(RUNS* WAVE) void rec_bwd_kernel(RecLaunch a) {
-  constexpr int RUN = BWD_RUN;
+template <class E, int DECAY, int NORM, bool GATE>
+__global__ __launch_bounds__(RUNS* WAVE) __attribute__((amdgpu_waves_per_eu(4, 4))) void rec_bwd_kernel(RecLaunch a) {
+  constexpr int RUN = BWD_TILE / RUNS;
   __shared__ Link l;
-  __shared__ Ends<RUNS> fwd;
+  __shared__ Ends<RUNS> fwd;  // the runs' ends forwards
   __shared__ int starts[RUNS];
   const Where at = find_place<RUN, true>(a);
-  typename Pair<E>::raw A[RUN], X[RUN], I[RUN], G[RUN];
-  load_run<E>(a, at, a.A, a.a_stride, A);
-  load_run<E>(a, at, a.dH, a.D, G);
-  load_run<E>(a, at, a.X, a.x_stride, X);
-  if (a.I) load_run<E>(a, at, a.I, a.i_stride, I);
-  f32x2 h = a.tiles > 1 ? state_in(a, a.states, (int64_t)at.b * a.n_states + at.tile * (REC_BWD_TILE / GDN_REC_TILE), at.c)
-                        : f32x2{0.f, 0.f};
+  const int run = RUNS - 1 - at.wave;  // in the chain's order
+  Raw<E, RUN, GATE, true> raw;
+  Loader<E, RUN, GATE, true> rows(a, at);
+#pragma unroll
+  for (int j = RUN - 1; j >= 0; --j) rows.next(a, raw, j);
+  f32x2 h{0.f, 0.f};
+  if (a.tiles > 1) h = state_in(a, a.states, (int64_t)at.b * a.n_states + at.tile * (BWD_TILE / GDN_REC_TILE), at.c);
   const Run<RUN> r = find_run<RUN>(a, at.t0, at.b);
   const f32x2 w = channel_w(a, at.c);
-  f32x2 dec[RUN], u[RUN];
-  open_run<E, DECAY, NORM, true>(a, at, A, X, I, dec, u);
-  const int order = RUNS - 1 - at.wave;
+  f32x2 dec[RUN], b[RUN], u[RUN];
+  open_run<E, DECAY, NORM>(raw, w, dec, b, u);
   {
     f32x2 P{1.f, 1.f}, x{0.f, 0.f}, e{0.f, 0.f};
-    walk<false>(a, at, r, dec, u, P, x, [](int, f32x2) {});
+    walk<false>(a, at, r, dec, u, P, x);
     fwd.put(at.wave, P, x);
 #pragma unroll
     for (int j = RUN - 1; j >= 0; --j) {
       if (!(r.in >> j & 1)) continue;
       if (r.last >> j & 1) e = state_in(a, a.dh, r.seq_of(j), at.c);
-      const f32x2 d = Pair<E>::open(G[j]);
+      const f32x2 d = Pair<E>::open(raw.G[j]);
       e = f32x2{dec[j][0] * (d[0] + e[0]), dec[j][1] * (d[1] + e[1])};
     }
-    l.run.put(order, P, e);
+    l.run.put(run, P, e);
   }
   if (lane_id() == 0) {
     starts[at.wave] = r.first != 0;
-    l.fresh[order] = r.last != 0;
+    l.fresh[run] = r.last != 0;
   }
-  if (order == 0) {
+  if (run == 0) {
     // the tile's last token goes on into the next tile
     const bool goes_on = (r.in >> (RUN - 1) & 1) && !(r.last >> (RUN - 1) & 1);
     const int to = __builtin_amdgcn_readlane(r.to, RUN - 1);
@@ -559,28 +558,43 @@ __global__ __launch_bounds__(RUNS* WAVE) void rec_bwd_kernel(RecLaunch a) {
   }
   __syncthreads();
   for (int k = 0; k < at.wave; ++k) h = fwd.behind(k, h, starts[k] != 0);
-  f32x2 before[RUN], P{1.f, 1.f};
-  walk<false>(a, at, r, dec, u, P, h, [&](int j, f32x2 x) { before[j] = x; });
-  f32x2 e = l.before_run(order, tile_start(a, at, order, l));
+  // u gives way to the states before the tokens
+#pragma unroll
+  for (int j = 0; j < RUN; ++j) {
+    if (!(r.in >> j & 1)) continue;
+    if (r.first >> j & 1) h = state_in(a, a.h0, r.seq_of(j), at.c);
+    const f32x2 before = h;
+    h = fma2(dec[j], h, u[j]);
+    u[j] = before;
+  }
+  // the rows are opened anew below: kept open from above they would take twice the registers
+#pragma unroll
+  for (int j = 0; j < RUN; ++j) {
+    hide(raw.A[j]);
+    hide(raw.X[j]);
+    hide(raw.G[j]);
+    if constexpr (GATE) hide(raw.I[j]);
+  }
+  f32x2 e = l.before_run(run, tile_start(a, at, run, l));
   f32x2 dw{0.f, 0.f};
 #pragma unroll
   for (int j = RUN - 1; j >= 0; --j) {
     f32x2 dX{0.f, 0.f}, dA{0.f, 0.f}, dI{0.f, 0.f};
     if (r.in >> j & 1) {
       if (r.last >> j & 1) e = state_in(a, a.dh, r.seq_of(j), at.c);
-      const f32x2 d = Pair<E>::open(G[j]), Av = Pair<E>::open(A[j]), x = Pair<E>::open(X[j]);
-      const f32x2 iv = a.I ? Pair<E>::open(I[j]) : f32x2{0.f, 0.f};
+      const f32x2 d = Pair<E>::open(raw.G[j]), Av = Pair<E>::open(raw.A[j]), x = Pair<E>::open(raw.X[j]);
+      const f32x2 iv = Pair<E>::open(raw.I[GATE ? j : 0]);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const Gate<DECAY, NORM, true> g(Av[k], w[k]);
+        const GateGrad<DECAY> g(Av[k], w[k]);
         const float D = d[k] + e[k];
-        e[k] = g.a * D;
+        e[k] = dec[j][k] * D;
         float s = 1.f, rest = 0.f;
-        if (a.I) sigmoid_rest(iv[k], s, rest);
-        const float dz = D * g.b, z = s * x[k];
+        if constexpr (GATE) sigmoid_rest(iv[k], s, rest);
+        const float dz = D * b[j][k], z = s * x[k];
         dX[k] = dz * s;
         dI[k] = dz * z * rest;
-        const float dg = fmaf(e[k], before[j][k], D * z * g.db);
+        const float dg = fmaf(e[k], u[j][k], D * z * slope<NORM>(dec[j][k], b[j][k]));
         dA[k] = dg * g.to_A;
         dw[k] = fmaf(-g.r, dg, dw[k]);
       }
@@ -589,7 +603,7 @@ __global__ __launch_bounds__(RUNS* WAVE) void rec_bwd_kernel(RecLaunch a) {
     if (at.t0 + j < a.T) {  // rows of no sequence: zeros
       store_row<E>(a, at, a.dX, j, dX);
       store_row<E>(a, at, a.dA, j, dA);
-      if (a.I) store_row<E>(a, at, a.dI, j, dI);
+      if constexpr (GATE) store_row<E>(a, at, a.dI, j, dI);
     }
   }
   empty_sequences(a, at, a.dh, a.dh0);
@@ -605,7 +619,7 @@ __global__ __launch_bounds__(RUNS* WAVE) void rec_bwd_kernel(RecLaunch a) {
 
 // token by token, the state in registers for the whole call: a wave for each 128 channels of a
 // sequence.  h_out may be h0: a lane reads and writes its own channels alone.
-template <class E, int DECAY, int NORM>
+template <class E, int DECAY, int NORM, bool GATE>
 __global__ __launch_bounds__(256) void rec_step_kernel(RecLaunch a) {
   const uint32_t blocks = (uint32_t)((a.D + CH - 1) / CH);
   const uint32_t i = blockIdx.x * 4 + threadIdx.x / WAVE, b = i / blocks;
@@ -619,11 +633,11 @@ __global__ __launch_bounds__(256) void rec_step_kernel(RecLaunch a) {
     const f32x2 Av = Pair<E>::open(*reinterpret_cast<const raw*>(reinterpret_cast<const E*>(a.A) + row * a.a_stride + c));
     const f32x2 x = Pair<E>::open(*reinterpret_cast<const raw*>(reinterpret_cast<const E*>(a.X) + row * a.x_stride + c));
     f32x2 iv{0.f, 0.f};
-    if (a.I) iv = Pair<E>::open(*reinterpret_cast<const raw*>(reinterpret_cast<const E*>(a.I) + row * a.i_stride + c));
+    if constexpr (GATE) iv = Pair<E>::open(*reinterpret_cast<const raw*>(reinterpret_cast<const E*>(a.I) + row * a.i_stride + c));
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const Gate<DECAY, NORM, false> g(Av[k], w[k]);
-      h[k] = fmaf(g.a, h[k], g.b * (a.I ? sigmoid(iv[k]) : 1.f) * x[k]);
+      const Gate<DECAY, NORM> g(Av[k], w[k]);
+      h[k] = fmaf(g.a, h[k], g.b * (GATE ? sigmoid(iv[k]) : 1.f) * x[k]);
     }
     *reinterpret_cast<raw*>(reinterpret_cast<E*>(a.H) + row * a.D + c) = Pair<E>::close(h);
   }
@@ -648,11 +662,14 @@ namespace {
 
 template <class F>
 int by_kind(const RecLaunch& p, F&& f) {
+  auto gate = [&](auto e, auto decay, auto norm) {
+    return p.I ? f(e, decay, norm, std::true_type{}) : f(e, decay, norm, std::false_type{});
+  };
   auto norm = [&](auto e, auto decay) {
     switch (p.norm) {
-      case GDN_REC_NORM_SQRT: return f(e, decay, std::integral_constant<int, GDN_REC_NORM_SQRT>{});
-      case GDN_REC_NORM_LINEAR: return f(e, decay, std::integral_constant<int, GDN_REC_NORM_LINEAR>{});
-      default: return f(e, decay, std::integral_constant<int, GDN_REC_NORM_NONE>{});
+      case GDN_REC_NORM_SQRT: return gate(e, decay, std::integral_constant<int, GDN_REC_NORM_SQRT>{});
+      case GDN_REC_NORM_LINEAR: return gate(e, decay, std::integral_constant<int, GDN_REC_NORM_LINEAR>{});
+      default: return gate(e, decay, std::integral_constant<int, GDN_REC_NORM_NONE>{});
     }
   };
   auto decay = [&](auto e) {
@@ -672,27 +689,24 @@ size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 // the workspace in order: a chain's words (the ends of the tiles and of their eights, the states behind 64
 // tiles, the counters), backwards those of a pass for the states and the states themselves, dw's parts
 struct Parts {
+  int64_t n;
   size_t tiles, eights, states, tickets, chain;  // offsets in a chain's words, and their size
   size_t fwd_chain, starts, part, bytes;         // backwards
   Parts(const RecLaunch& p, bool bwd) {
-    chain_of(p, bwd ? REC_BWD_TILE : REC_FWD_TILE);
-    bytes = chain;
-    if (!bwd) return;
-    const Parts f(p, false);
-    fwd_chain = bytes;
-    starts = fwd_chain + f.chain;
-    const int64_t rows = rows_of(p);
-    part = starts + (tiles_of(p, REC_BWD_TILE) > 1 ? up16((size_t)(rows * p.n_states * p.D) * 4) : 0);
-    bytes = part + (p.decay == GDN_DECAY_POWER ? up16((size_t)(rows * tiles_of(p, REC_BWD_TILE) * p.D) * 4) : 0);
-  }
-  static int64_t tiles_of(const RecLaunch& p, int tile) { return (p.T + tile - 1) / tile; }
-  void chain_of(const RecLaunch& p, int tile) {
-    const int64_t n = tiles_of(p, tile), v = rows_of(p) * p.D;
+    const int tile = bwd ? BWD_TILE : FWD_TILE;
+    const int64_t rows = rows_of(p), v = rows * p.D;
+    n = (p.T + tile - 1) / tile;
     tiles = 0;
     eights = tiles + up16((size_t)(n * v) * 8);
     states = eights + up16((size_t)(n / EIGHT * v) * 8);
-    tickets = states + up16((size_t)(n / EIGHT / EIGHT * v) * 4);
-    chain = n > 1 ? tickets + up16((size_t)(rows_of(p) * channel_blocks(p)) * 4) : 0;
+    tickets = states + up16((size_t)(n / EIGHT / EIGHT * v) * 8);
+    chain = n > 1 ? tickets + up16((size_t)(rows * channel_blocks(p)) * 4) : 0;
+    bytes = chain;
+    if (!bwd) return;
+    fwd_chain = bytes;
+    starts = fwd_chain + Parts(p, false).chain;
+    part = starts + (n > 1 ? up16((size_t)(rows * p.n_states * p.D) * 4) : 0);
+    bytes = part + (p.decay == GDN_DECAY_POWER ? up16((size_t)(n * v) * 4) : 0);
   }
 };
 
@@ -700,11 +714,11 @@ struct Parts {
 RecLaunch chained(const RecLaunch& p, bool bwd, char* ws, hipStream_t s) {
   RecLaunch q = p;
   const Parts at(p, bwd);
-  q.tiles = Parts::tiles_of(p, bwd ? REC_BWD_TILE : REC_FWD_TILE);
+  q.tiles = at.n;
   if (q.tiles > 1) {
     q.chain_tiles = reinterpret_cast<uint64_t*>(ws + at.tiles);
     q.chain_eights = reinterpret_cast<uint64_t*>(ws + at.eights);
-    q.chain_states = reinterpret_cast<uint32_t*>(ws + at.states);
+    q.chain_states = reinterpret_cast<uint64_t*>(ws + at.states);
     q.tickets = reinterpret_cast<uint32_t*>(ws + at.tickets);
     const int64_t n = (int64_t)(at.chain / 16), g = (n + 255) / 256;
     hipLaunchKernelGGL(rec_clear_kernel, dim3((unsigned)(g < 2048 ? g : 2048)), dim3(256), 0, s,
@@ -723,11 +737,11 @@ dim3 grid_of(const RecLaunch& q) { return dim3((unsigned)(q.tiles * rows_of(q) *
 
 }  // namespace
 
-size_t rec_workspace(const RecLaunch& p, bool bwd) { return p.T == 0 ? 0 : Parts(p, bwd).bytes; }
+size_t rec_workspace(const RecLaunch& p, bool bwd) { return p.T == 0 || rows_of(p) == 0 ? 0 : Parts(p, bwd).bytes; }
 
 bool rec_grid_ok(const RecLaunch& p) {
   // a launch has fewer than 2^32 threads
-  constexpr int least = REC_FWD_TILE < REC_BWD_TILE ? REC_FWD_TILE : REC_BWD_TILE;
+  constexpr int least = FWD_TILE < BWD_TILE ? FWD_TILE : BWD_TILE;
   const int64_t tiles = (p.T + least - 1) / least, rows = rows_of(p) > 0 ? rows_of(p) : 1;
   return tiles <= (((int64_t)1 << 32) - 1) / (RUNS * WAVE) / channel_blocks(p) / rows;
 }
@@ -739,9 +753,9 @@ int launch_rec_fwd(const RecLaunch& p, void* workspace, hipStream_t s) {
     return 0;
   }
   const RecLaunch q = chained(p, false, reinterpret_cast<char*>(workspace), s);
-  return by_kind(p, [&](auto e, auto decay, auto norm) {
+  return by_kind(p, [&](auto e, auto decay, auto norm, auto gate) {
     typedef std::remove_pointer_t<decltype(e)> E;
-    hipLaunchKernelGGL((rec_fwd_kernel<E, decay.value, norm.value>), grid_of(q), dim3(RUNS * WAVE), 0, s, q);
+    hipLaunchKernelGGL((rec_fwd_kernel<E, decay.value, norm.value, gate.value>), grid_of(q), dim3(RUNS * WAVE), 0, s, q);
     return 0;
   });
 }
@@ -765,10 +779,10 @@ int launch_rec_bwd(const RecLaunch& p, void* workspace, hipStream_t s) {
     f.h_out = nullptr;
     f.states = q.states;
   }
-  return by_kind(p, [&](auto e, auto decay, auto norm) {
+  return by_kind(p, [&](auto e, auto decay, auto norm, auto gate) {
     typedef std::remove_pointer_t<decltype(e)> E;
-    if (form) hipLaunchKernelGGL((rec_fwd_kernel<E, decay.value, norm.value>), grid_of(f), dim3(RUNS * WAVE), 0, s, f);
-    hipLaunchKernelGGL((rec_bwd_kernel<E, decay.value, norm.value>), grid_of(q), dim3(RUNS * WAVE), 0, s, q);
+    if (form) hipLaunchKernelGGL((rec_fwd_kernel<E, decay.value, norm.value, gate.value>), grid_of(f), dim3(RUNS * WAVE), 0, s, f);
+    hipLaunchKernelGGL((rec_bwd_kernel<E, decay.value, norm.value, gate.value>), grid_of(q), dim3(RUNS * WAVE), 0, s, q);
     if (q.dw) launch_column_sum(q.part, q.tiles * rows_of(q), q.D, 1, q.dw, nullptr, s);
     return 0;
   });
@@ -777,8 +791,8 @@ int launch_rec_bwd(const RecLaunch& p, void* workspace, hipStream_t s) {
 int launch_rec_step(const RecLaunch& p, hipStream_t s) {
   const int64_t waves = (int64_t)p.n_seq * channel_blocks(p);
   const dim3 grid((unsigned)((waves + 3) / 4)), block(256);
-  return by_kind(p, [&](auto e, auto decay, auto norm) {
-    hipLaunchKernelGGL((rec_step_kernel<std::remove_pointer_t<decltype(e)>, decay.value, norm.value>), grid, block, 0, s, p);
+  return by_kind(p, [&](auto e, auto decay, auto norm, auto gate) {
+    hipLaunchKernelGGL((rec_step_kernel<std::remove_pointer_t<decltype(e)>, decay.value, norm.value, gate.value>), grid, block, 0, s, p);
     return 0;
   });
 }
