@@ -431,7 +431,7 @@ typedef enum gdn_rec_norm { GDN_REC_NORM_SQRT = 0, GDN_REC_NORM_LINEAR = 1, GDN_
 /* Per sequence and channel, tokens in order, state h fp32:
  *   h_t = a_t h_{t-1} + b_t s(I_t) X_t        (I NULL: b_t X_t)
  * offsets == NULL: B sequences of T tokens each; X, A, I [B][T] rows of D values, x_stride,
- *   a_stride, i_stride values apart (parts of wider projections; multiples of 8), H [B][T][D].
+ *   a_stride, i_stride values apart (parts of wider projections; multiples of 8, at most 2^24), H [B][T][D].
  * offsets != NULL: B packed sequences in T tokens, as in gdn_lin_shape, rows of the T tokens; rows of
  *   no sequence are not read into a result, H is not written there, and gradients there are zero.
  * X, A, I, H and their gradients in dtype (GDN_BF16 or GDN_F32); states [B][D] fp32.  D a multiple of

@@ -729,7 +729,9 @@ static gdn_status check_rec(const gdn_rec_shape* s) {
   if (s->D % 8 != 0) return GDN_ERR_UNSUPPORTED;
   if (s->x_stride < s->D || s->a_stride < s->D || s->i_stride < s->D) return GDN_ERR_BAD_SHAPE;
   if (s->x_stride % 8 != 0 || s->a_stride % 8 != 0 || s->i_stride % 8 != 0) return GDN_ERR_BAD_ALIGNMENT;
-  if (s->T > INT32_MAX - GDN_REC_TILE) return GDN_ERR_UNSUPPORTED;  // token indices in a row are 32 bits
+  if (s->T > INT32_MAX - 128) return GDN_ERR_UNSUPPORTED;  // token indices in a row are 32 bits, up to a tile's end
+  for (const int64_t stride : {s->x_stride, s->a_stride, s->i_stride})
+    if (stride > gdn::REC_MAX_STRIDE) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
 

@@ -219,6 +219,7 @@ void launch_column_sum(const float* part, int64_t n, int D, int n_in, float* out
 
 // gated linear recurrence of every channel (offsets: packed sequences, n_seq of them in T tokens;
 // NULL: n_seq sequences of T tokens each); D a multiple of 8
+constexpr int64_t REC_MAX_STRIDE = (int64_t)1 << 24;  // values between tokens
 struct RecLaunch {
   const void* X;
   const void* A;

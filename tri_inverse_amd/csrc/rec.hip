@@ -53,6 +53,12 @@ struct Pair;
 template <>
 struct Pair<__bf16> {
   typedef uint32_t raw;
+  static __device__ __forceinline__ raw load(__amdgpu_buffer_rsrc_t p, uint32_t lane, uint32_t row) {
+    return __builtin_amdgcn_raw_buffer_load_b32(p, lane, row, 0);
+  }
+  static __device__ __forceinline__ void store(raw v, __amdgpu_buffer_rsrc_t p, uint32_t lane, uint32_t row) {
+    __builtin_amdgcn_raw_buffer_store_b32(v, p, lane, row, 0);
+  }
   static __device__ __forceinline__ f32x2 open(raw v) {
     return f32x2{__builtin_bit_cast(float, v << 16), __builtin_bit_cast(float, v & 0xffff0000u)};
   }
@@ -67,6 +73,12 @@ struct Pair<__bf16> {
 template <>
 struct Pair<float> {
   typedef f32x2 raw;
+  static __device__ __forceinline__ raw load(__amdgpu_buffer_rsrc_t p, uint32_t lane, uint32_t row) {
+    return __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(p, lane, row, 0));
+  }
+  static __device__ __forceinline__ void store(raw v, __amdgpu_buffer_rsrc_t p, uint32_t lane, uint32_t row) {
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v), p, lane, row, 0);
+  }
   static __device__ __forceinline__ f32x2 open(raw v) { return v; }
   static __device__ __forceinline__ raw close(f32x2 v) { return v; }
 };
@@ -222,12 +234,27 @@ __device__ __forceinline__ Where find_place(const RecLaunch& a) {
   return at;
 }
 
+// the rows of a run of a tensor, addressed by a uniform offset of its row and a lane's offset in it, 32 bits
+// each (a run's rows span less than 2^31 bytes: strides are below REC_MAX_STRIDE)
 template <class E>
-__device__ __forceinline__ void store_row(const RecLaunch& a, const Where& at, void* p, int j, f32x2 v) {
-  char* row = reinterpret_cast<char*>(reinterpret_cast<E*>(p) + ((int64_t)at.b * a.T + at.t0 + j) * a.D);
-  if (at.c < a.D)
-    *reinterpret_cast<typename Pair<E>::raw*>(row + (uint32_t)at.c * (uint32_t)sizeof(E)) = Pair<E>::close(v);
-}
+struct Rows {
+  __amdgpu_buffer_rsrc_t p;
+  uint32_t step;
+  __device__ __forceinline__ Rows(const RecLaunch& a, const Where& at, const void* t, int64_t stride) {
+    const int64_t row = (int64_t)at.b * a.T + (at.t0 < (int)a.T ? at.t0 : (int)a.T - 1);
+    step = (uint32_t)stride * (uint32_t)sizeof(E);
+    p = __builtin_amdgcn_make_buffer_rsrc(const_cast<E*>(reinterpret_cast<const E*>(t) + row * stride), 0, -1, 0x27000);
+  }
+  // row j; past the last token the last row, past the last channel the first ones
+  __device__ __forceinline__ typename Pair<E>::raw load(const RecLaunch& a, const Where& at, int j) const {
+    const int left = (int)a.T - 1 - at.t0, last = left > 0 ? left : 0;
+    return Pair<E>::load(p, (at.c < a.D ? (uint32_t)at.c : 0u) * (uint32_t)sizeof(E), (uint32_t)(j < last ? j : last) * step);
+  }
+  // row j, of a token that exists
+  __device__ __forceinline__ void store(const RecLaunch& a, const Where& at, int j, f32x2 v) const {
+    if (at.c < a.D) Pair<E>::store(Pair<E>::close(v), p, (uint32_t)at.c * (uint32_t)sizeof(E), (uint32_t)j * step);
+  }
+};
 
 __device__ __forceinline__ f32x2 state_in(const RecLaunch& a, const float* S, int64_t row, int c) {
   f32x2 h{0.f, 0.f};
@@ -287,11 +314,16 @@ struct Words {
 #pragma unroll
       for (int k = 0; k < 2; ++k) v[k] = __hip_atomic_load(p + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
+  __device__ __forceinline__ bool ready() const {
+    return (uint32_t)(v[0] >> 32) != NOT_YET && (uint32_t)(v[1] >> 32) != NOT_YET;
+  }
+  // while the words are not there one lane looks at its own: 64 lanes of all waiting waves would take as
+  // much of the memory's rate as the rows do
   __device__ __forceinline__ void wait(f32x2& P, f32x2& h) {
-    for (int i = 0; i < WAIT_ROUNDS; ++i) {
-      if (wave_all((uint32_t)(v[0] >> 32) != NOT_YET && (uint32_t)(v[1] >> 32) != NOT_YET)) break;
-      __builtin_amdgcn_s_sleep(1);
-      look();
+    for (int i = 0; i < WAIT_ROUNDS && !wave_all(ready()); ++i) {
+      __builtin_amdgcn_s_sleep(2);
+      if (lane_id() == 0) look();
+      if (wave_all(lane_id() != 0 || ready())) look();
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -402,38 +434,21 @@ template <class E, int RUN, bool GATE, bool BWD>
 struct Raw {
   typename Pair<E>::raw A[RUN], X[RUN], I[GATE ? RUN : 1], G[BWD ? RUN : 1];
 };
-// they are loaded token by token (backwards from the last one): rows past the last token and lanes past
-// the last channel load what lies inside instead.  Rows are uniform, a lane's offset in them 32 bits.
 template <class E, int RUN, bool GATE, bool BWD>
-struct Loader {
-  const char *A, *X, *I, *G;
-  uint32_t c;
-  int t;
-  __device__ __forceinline__ Loader(const RecLaunch& a, const Where& at) {
-    t = BWD ? at.t0 + RUN - 1 : at.t0;
-    const int64_t row = (int64_t)at.b * a.T + (t < (int)a.T ? t : (int)a.T - 1);
-    const int64_t size = sizeof(E);
-    A = reinterpret_cast<const char*>(a.A) + row * a.a_stride * size;
-    X = reinterpret_cast<const char*>(a.X) + row * a.x_stride * size;
-    I = reinterpret_cast<const char*>(a.I) + row * a.i_stride * size;
-    G = reinterpret_cast<const char*>(a.dH) + row * a.D * size;
-    c = (at.c < a.D ? (uint32_t)at.c : 0u) * (uint32_t)sizeof(E);
-  }
-  __device__ __forceinline__ void next(const RecLaunch& a, Raw<E, RUN, GATE, BWD>& r, int j) {
-    typedef typename Pair<E>::raw raw;
-    r.A[j] = *reinterpret_cast<const raw*>(A + c);
-    if constexpr (BWD) r.G[j] = *reinterpret_cast<const raw*>(G + c);
-    r.X[j] = *reinterpret_cast<const raw*>(X + c);
-    if constexpr (GATE) r.I[j] = *reinterpret_cast<const raw*>(I + c);
-    const bool move = BWD ? t < (int)a.T && t > 0 : t + 1 < (int)a.T;
-    t += BWD ? -1 : 1;
-    const int64_t size = BWD ? -(int64_t)sizeof(E) : (int64_t)sizeof(E);
-    A += move ? a.a_stride * size : 0;
-    X += move ? a.x_stride * size : 0;
-    if constexpr (GATE) I += move ? a.i_stride * size : 0;
-    if constexpr (BWD) G += move ? a.D * size : 0;
-  }
-};
+__device__ __forceinline__ void load_rows(const RecLaunch& a, const Where& at, Raw<E, RUN, GATE, BWD>& r) {
+  const Rows<E> A(a, at, a.A, a.a_stride), X(a, at, a.X, a.x_stride), I(a, at, GATE ? a.I : a.X, GATE ? a.i_stride : a.x_stride),
+      G(a, at, BWD ? a.dH : a.X, BWD ? a.D : a.x_stride);
+#pragma unroll
+  for (int j = 0; j < RUN; ++j) r.A[j] = A.load(a, at, j);
+  if constexpr (BWD)
+#pragma unroll
+    for (int j = 0; j < RUN; ++j) r.G[j] = G.load(a, at, j);
+#pragma unroll
+  for (int j = 0; j < RUN; ++j) r.X[j] = X.load(a, at, j);
+  if constexpr (GATE)
+#pragma unroll
+    for (int j = 0; j < RUN; ++j) r.I[j] = I.load(a, at, j);
+}
 
 // a, b and u = b s(I) X of every token of the run
 template <class E, int DECAY, int NORM, bool GATE, bool BWD, int RUN>
@@ -481,9 +496,7 @@ __global__ __launch_bounds__(RUNS* WAVE) __attribute__((amdgpu_waves_per_eu(4, 4
   __shared__ Link l;
   const Where at = find_place<RUN, false>(a);
   Raw<E, RUN, GATE, false> raw;
-  Loader<E, RUN, GATE, false> rows(a, at);
-#pragma unroll
-  for (int j = 0; j < RUN; ++j) rows.next(a, raw, j);
+  load_rows(a, at, raw);
   const Run<RUN> r = find_run<RUN>(a, at.t0, at.b);
   f32x2 dec[RUN], b[RUN], u[RUN];
   open_run<E, DECAY, NORM>(raw, channel_w(a, at.c), dec, b, u);
@@ -503,12 +516,13 @@ __global__ __launch_bounds__(RUNS* WAVE) __attribute__((amdgpu_waves_per_eu(4, 4
   if (at.t0 % GDN_REC_TILE == 0 && at.t0 < a.T)
     state_out(a, a.states, (int64_t)at.b * a.n_states + at.t0 / GDN_REC_TILE, at.c, goes_on ? h : f32x2{0.f, 0.f});
   if (!a.H) return;  // the states alone
+  const Rows<E> H(a, at, a.H, a.D);
 #pragma unroll
   for (int j = 0; j < RUN; ++j) {
     if (!(r.in >> j & 1)) continue;
     if (r.first >> j & 1) h = state_in(a, a.h0, r.seq_of(j), at.c);
     h = fma2(dec[j], h, u[j]);
-    store_row<E>(a, at, a.H, j, h);
+    H.store(a, at, j, h);
     if (r.last >> j & 1) state_out(a, a.h_out, r.seq_of(j), at.c, h);
   }
   empty_sequences(a, at, a.h0, a.h_out);
@@ -524,9 +538,7 @@ __global__ __launch_bounds__(RUNS* WAVE) __attribute__((amdgpu_waves_per_eu(4, 4
   const Where at = find_place<RUN, true>(a);
   const int run = RUNS - 1 - at.wave;  // in the chain's order
   Raw<E, RUN, GATE, true> raw;
-  Loader<E, RUN, GATE, true> rows(a, at);
-#pragma unroll
-  for (int j = RUN - 1; j >= 0; --j) rows.next(a, raw, j);
+  load_rows(a, at, raw);
   f32x2 h{0.f, 0.f};
   if (a.tiles > 1) h = state_in(a, a.states, (int64_t)at.b * a.n_states + at.tile * (BWD_TILE / GDN_REC_TILE), at.c);
   const Run<RUN> r = find_run<RUN>(a, at.t0, at.b);
@@ -576,6 +588,7 @@ __global__ __launch_bounds__(RUNS* WAVE) __attribute__((amdgpu_waves_per_eu(4, 4
     if constexpr (GATE) hide(raw.I[j]);
   }
   f32x2 e = l.before_run(run, tile_start(a, at, run, l));
+  const Rows<E> X(a, at, a.dX, a.D), A(a, at, a.dA, a.D), I(a, at, GATE ? a.dI : a.dX, a.D);
   f32x2 dw{0.f, 0.f};
 #pragma unroll
   for (int j = RUN - 1; j >= 0; --j) {
@@ -601,9 +614,9 @@ __global__ __launch_bounds__(RUNS* WAVE) __attribute__((amdgpu_waves_per_eu(4, 4
       if (r.first >> j & 1) state_out(a, a.dh0, r.seq_of(j), at.c, e);
     }
     if (at.t0 + j < a.T) {  // rows of no sequence: zeros
-      store_row<E>(a, at, a.dX, j, dX);
-      store_row<E>(a, at, a.dA, j, dA);
-      if constexpr (GATE) store_row<E>(a, at, a.dI, j, dI);
+      X.store(a, at, j, dX);
+      A.store(a, at, j, dA);
+      if constexpr (GATE) I.store(a, at, j, dI);
     }
   }
   empty_sequences(a, at, a.dh, a.dh0);
