@@ -306,9 +306,12 @@ __device__ __forceinline__ void publish(uint64_t* p, f32x2 P, f32x2 h) {
 // a lane's words of one entry, looked at until they are there.  Every lane of the wave calls look and wait;
 // lanes that are off (p NULL) wait for nothing.
 struct Words {
-  const uint64_t* p;
+  const uint64_t* p = nullptr;
   uint64_t v[2] = {0, 0};
-  __device__ __forceinline__ explicit Words(const uint64_t* at) : p(at) { look(); }
+  __device__ __forceinline__ void look(const uint64_t* at) {
+    p = at;
+    look();
+  }
   __device__ __forceinline__ void look() {
     if (p)
 #pragma unroll
@@ -364,70 +367,90 @@ struct Link {
   }
 };
 
-// The tile's start; all waves call it, after the barrier behind the runs' ends.  wave: the wave's run in the
-// chain's order.
-__device__ __forceinline__ f32x2 tile_start(const RecLaunch& a, const Where& at, int wave, Link& l) {
-  f32x2 x{0.f, 0.f};
-  if (a.tiles == 1) return x;
-  const int q = at.order, eight = q / EIGHT, block = eight / EIGHT, from = l.from, tiles = (int)a.tiles;
-  const bool on = at.c < a.D;
-  // words of this row, entry by entry [D]
-  uint64_t* ends = a.chain_tiles + (int64_t)at.b * tiles * a.D + at.c;
-  const int eights = tiles / EIGHT, blocks = eights / EIGHT;
-  uint64_t* eight_ends = a.chain_eights + (int64_t)at.b * eights * a.D + at.c;
-  uint64_t* states = a.chain_states + (int64_t)at.b * blocks * a.D + at.c;
+// A tile's place in its chain.  All waves make one, behind the barrier that follows the runs' ends (wave: the
+// wave's run in the chain's order): the tile's end is published, and the words that the tile's start
+// comes from are asked for, all at once.  start() waits for them; what stands between hides their way.
+struct Joint {
+  const RecLaunch& a;
+  Link& l;
+  int wave, q, from, tiles, tile0, tile1, eight0, eight1;
+  bool on, fresh;
+  int c;
+  int64_t row, row8, row64;  // the row's words: tile by tile, eight by eight, 64 by 64
   f32x2 P{1.f, 1.f}, h{0.f, 0.f};
-  bool fresh = false;
-  if (wave == 0) {
-    for (int k = 0; k < RUNS; ++k) {
-      h = l.run.behind(k, h, l.fresh[k] != 0);
-      P = mul2(P, l.run.P[k][lane_id()]);
-      fresh = fresh || l.fresh[k] != 0;
-    }
-    if (on && q + 1 < tiles) publish(ends + (int64_t)q * a.D, P, h);
+  Words near, far;
+
+  __device__ __forceinline__ uint64_t* tile_words(int k) const { return a.chain_tiles + (row + k) * a.D + c; }
+  __device__ __forceinline__ uint64_t* eight_words(int k) const { return a.chain_eights + (row8 + k) * a.D + c; }
+  __device__ __forceinline__ uint64_t* state_words(int k) const { return a.chain_states + (row64 + k) * a.D + c; }
+  // the slots of the tiles before this one in its eight, and of the eights before its own; the last wave
+  // takes the state before the 64
+  __device__ __forceinline__ bool one() const { return wave < EIGHT - 1 && tile0 + wave >= tile1 && tile0 + wave < q; }
+  __device__ __forceinline__ bool two() const {
+    return from < tile0 && wave < EIGHT - 1 && eight0 + wave >= eight1 && eight0 + wave < q / EIGHT;
   }
-  const int tile0 = eight * EIGHT, tile1 = from > tile0 ? from : tile0;
-  const int eight0 = block * EIGHT, eight1 = from / EIGHT > eight0 ? from / EIGHT : eight0;
-  const bool closes = q % EIGHT == EIGHT - 1 && q + 1 < tiles;  // the tile ends its eight, for others to use
-  if (from < q) {
-    // all words are asked for at once.  The wave behind the eights' takes the state.
-    const int kt = tile0 + wave, ke = eight0 + wave;
-    const bool one = wave < EIGHT - 1 && kt >= tile1 && kt < q;
-    const bool two = from < tile0 && wave < EIGHT - 1 && ke >= eight1 && ke < eight;
-    const bool three = wave == EIGHT - 1 && from < eight0 * EIGHT;
-    Words near(one && on ? ends + (int64_t)kt * a.D : nullptr);
-    Words far(on && two ? eight_ends + (int64_t)ke * a.D : on && three ? states + (int64_t)(block - 1) * a.D : nullptr);
-    f32x2 Pk, hk;
-    near.wait(Pk, hk);
-    if (one) l.tiles.put(wave, Pk, hk);
-    // the eight's end does not wait for what comes before the eight
-    if (closes) {
-      __syncthreads();
-      if (wave == 0) {
-        f32x2 y{0.f, 0.f}, Py{1.f, 1.f};  // Py is read only where no sequence starts in the eight
-        for (int k = tile1; k < q; ++k) {
-          y = l.tiles.behind(k - tile0, y, k == from);
-          Py = mul2(Py, l.tiles.P[k - tile0][lane_id()]);
-        }
-        if (on) publish(eight_ends + (int64_t)eight * a.D, mul2(Py, P), fresh ? h : fma2(P, y, h));
+  __device__ __forceinline__ bool three() const { return wave == EIGHT - 1 && from < eight0 * EIGHT; }
+
+  __device__ __forceinline__ Joint(const RecLaunch& args, const Where& at, int run, Link& link)
+      : a(args), l(link), wave(run), q(at.order), from(link.from), tiles((int)args.tiles), on(at.c < args.D), fresh(false), c(at.c) {
+    static_assert(RUNS == EIGHT, "a wave for every slot");
+    tile0 = q / EIGHT * EIGHT;
+    eight0 = q / (EIGHT * EIGHT) * EIGHT;
+    tile1 = from > tile0 ? from : tile0;
+    eight1 = from / EIGHT > eight0 ? from / EIGHT : eight0;
+    row = (int64_t)at.b * tiles;
+    row8 = (int64_t)at.b * (tiles / EIGHT);
+    row64 = (int64_t)at.b * (tiles / (EIGHT * EIGHT));
+    if (tiles == 1) return;
+    if (wave == 0) {
+      for (int k = 0; k < RUNS; ++k) {
+        h = l.run.behind(k, h, l.fresh[k] != 0);
+        P = mul2(P, l.run.P[k][lane_id()]);
+        fresh = fresh || l.fresh[k] != 0;
       }
+      if (on && q + 1 < tiles) publish(tile_words(q), P, h);
     }
-    far.wait(Pk, hk);
-    if (two) l.eights.put(wave, Pk, hk);
-    if (three) l.before[lane_id()] = hk;
-    __syncthreads();
-    if (from < eight0 * EIGHT) x = l.before[lane_id()];
-    if (from < tile0)
-      for (int k = eight1; k < eight; ++k) x = l.eights.behind(k - eight0, x, k == from / EIGHT);
-    for (int k = tile1; k < q; ++k) x = l.tiles.behind(k - tile0, x, k == from);
-  } else if (closes && wave == 0 && on) {
-    publish(eight_ends + (int64_t)eight * a.D, P, h);  // nothing comes from before: h alone is read
+    near.look(one() && on ? tile_words(tile0 + wave) : nullptr);
+    far.look(on && two() ? eight_words(eight0 + wave) : on && three() ? state_words(eight0 / EIGHT - 1) : nullptr);
   }
-  // the state behind 64 tiles
-  if (wave == 0 && q % (EIGHT * EIGHT) == EIGHT * EIGHT - 1 && q + 1 < tiles && on)
-    publish(states + (int64_t)block * a.D, P, fresh || from == q ? h : fma2(P, x, h));
-  return x;
-}
+
+  __device__ __forceinline__ f32x2 start() {
+    f32x2 x{0.f, 0.f};
+    if (tiles == 1) return x;
+    const bool closes = q % EIGHT == EIGHT - 1 && q + 1 < tiles;  // the tile ends its eight, for others to use
+    if (from < q) {
+      f32x2 Pk, hk;
+      near.wait(Pk, hk);
+      if (one()) l.tiles.put(wave, Pk, hk);
+      // the eight's end does not wait for what comes before the eight
+      if (closes) {
+        __syncthreads();
+        if (wave == 0) {
+          f32x2 y{0.f, 0.f}, Py{1.f, 1.f};  // Py is read only where no sequence starts in the eight
+          for (int k = tile1; k < q; ++k) {
+            y = l.tiles.behind(k - tile0, y, k == from);
+            Py = mul2(Py, l.tiles.P[k - tile0][lane_id()]);
+          }
+          if (on) publish(eight_words(q / EIGHT), mul2(Py, P), fresh ? h : fma2(P, y, h));
+        }
+      }
+      far.wait(Pk, hk);
+      if (two()) l.eights.put(wave, Pk, hk);
+      if (three()) l.before[lane_id()] = hk;
+      __syncthreads();
+      if (from < eight0 * EIGHT) x = l.before[lane_id()];
+      if (from < tile0)
+        for (int k = eight1; k < q / EIGHT; ++k) x = l.eights.behind(k - eight0, x, k == from / EIGHT);
+      for (int k = tile1; k < q; ++k) x = l.tiles.behind(k - tile0, x, k == from);
+    } else if (closes && wave == 0 && on) {
+      publish(eight_words(q / EIGHT), P, h);  // nothing comes from before: h alone is read
+    }
+    // the state behind 64 tiles
+    if (wave == 0 && q % (EIGHT * EIGHT) == EIGHT * EIGHT - 1 && q + 1 < tiles && on)
+      publish(state_words(eight0 / EIGHT), P, fresh || from == q ? h : fma2(P, x, h));
+    return x;
+  }
+};
 
 // the rows of a run, two channels a lane: A, X, I and backwards dH
 template <class E, int RUN, bool GATE, bool BWD>
@@ -450,26 +473,29 @@ __device__ __forceinline__ void load_rows(const RecLaunch& a, const Where& at, R
     for (int j = 0; j < RUN; ++j) r.I[j] = I.load(a, at, j);
 }
 
-// a, b and u = b s(I) X of every token of the run
-template <class E, int DECAY, int NORM, bool GATE, bool BWD, int RUN>
-__device__ __forceinline__ void open_run(const Raw<E, RUN, GATE, BWD>& raw, f32x2 w, f32x2 (&dec)[RUN],
-                                         f32x2 (&b)[RUN], f32x2 (&u)[RUN]) {
+// a and b of every token of the run
+template <class E, int DECAY, int NORM, int RUN>
+__device__ __forceinline__ void open_gates(const typename Pair<E>::raw (&A)[RUN], f32x2 w, f32x2 (&dec)[RUN], f32x2 (&b)[RUN]) {
 #pragma unroll
   for (int j = 0; j < RUN; ++j) {
-    const f32x2 Av = Pair<E>::open(raw.A[j]), x = Pair<E>::open(raw.X[j]);
+    const f32x2 Av = Pair<E>::open(A[j]);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const Gate<DECAY, NORM> g(Av[k], w[k]);
       dec[j][k] = g.a;
       b[j][k] = g.b;
-      u[j][k] = g.b * x[k];
-    }
-    if constexpr (GATE) {
-      const f32x2 i = Pair<E>::open(raw.I[j]);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) u[j][k] *= sigmoid(i[k]);
     }
   }
+}
+// u = b s(I) X of a token
+template <class E, bool GATE>
+__device__ __forceinline__ f32x2 input_of(typename Pair<E>::raw X, typename Pair<E>::raw I, f32x2 b) {
+  f32x2 u = mul2(b, Pair<E>::open(X));
+  if constexpr (GATE) {
+    const f32x2 i = Pair<E>::open(I);
+    u = mul2(u, f32x2{sigmoid(i[0]), sigmoid(i[1])});
+  }
+  return u;
 }
 
 // the run's end (P, h) from P = 1 and h
@@ -498,8 +524,10 @@ __global__ __launch_bounds__(RUNS* WAVE) __attribute__((amdgpu_waves_per_eu(4, 4
   Raw<E, RUN, GATE, false> raw;
   load_rows(a, at, raw);
   const Run<RUN> r = find_run<RUN>(a, at.t0, at.b);
-  f32x2 dec[RUN], b[RUN], u[RUN];
-  open_run<E, DECAY, NORM>(raw, channel_w(a, at.c), dec, b, u);
+  f32x2 dec[RUN], u[RUN];
+  open_gates<E, DECAY, NORM>(raw.A, channel_w(a, at.c), dec, u);
+#pragma unroll
+  for (int j = 0; j < RUN; ++j) u[j] = input_of<E, GATE>(raw.X[j], raw.I[GATE ? j : 0], u[j]);
   f32x2 P{1.f, 1.f}, h{0.f, 0.f};
   if (r.plain())
     walk<true>(a, at, r, dec, u, P, h);
@@ -512,7 +540,7 @@ __global__ __launch_bounds__(RUNS* WAVE) __attribute__((amdgpu_waves_per_eu(4, 4
     if (at.wave == 0) l.from = goes_on ? r.from / (RUN * RUNS) : at.order;
   }
   __syncthreads();
-  h = l.before_run(at.wave, tile_start(a, at, at.wave, l));
+  h = l.before_run(at.wave, Joint(a, at, at.wave, l).start());
   if (at.t0 % GDN_REC_TILE == 0 && at.t0 < a.T)
     state_out(a, a.states, (int64_t)at.b * a.n_states + at.t0 / GDN_REC_TILE, at.c, goes_on ? h : f32x2{0.f, 0.f});
   if (!a.H) return;  // the states alone
@@ -533,7 +561,7 @@ template <class E, int DECAY, int NORM, bool GATE>
 __global__ __launch_bounds__(RUNS* WAVE) __attribute__((amdgpu_waves_per_eu(4, 4))) void rec_bwd_kernel(RecLaunch a) {
   constexpr int RUN = BWD_TILE / RUNS;
   __shared__ Link l;
-  __shared__ Ends<RUNS> fwd;  // the runs' ends forwards
+  __shared__ f32x2 fwd[RUNS][WAVE];  // the runs' ends forwards
   __shared__ int starts[RUNS];
   const Where at = find_place<RUN, true>(a);
   const int run = RUNS - 1 - at.wave;  // in the chain's order
@@ -544,20 +572,17 @@ __global__ __launch_bounds__(RUNS* WAVE) __attribute__((amdgpu_waves_per_eu(4, 4
   const Run<RUN> r = find_run<RUN>(a, at.t0, at.b);
   const f32x2 w = channel_w(a, at.c);
   f32x2 dec[RUN], b[RUN], u[RUN];
-  open_run<E, DECAY, NORM>(raw, w, dec, b, u);
-  {
-    f32x2 P{1.f, 1.f}, x{0.f, 0.f}, e{0.f, 0.f};
-    walk<false>(a, at, r, dec, u, P, x);
-    fwd.put(at.wave, P, x);
+  open_gates<E, DECAY, NORM>(raw.A, w, dec, b);
+  f32x2 P{1.f, 1.f}, e{0.f, 0.f};
 #pragma unroll
-    for (int j = RUN - 1; j >= 0; --j) {
-      if (!(r.in >> j & 1)) continue;
-      if (r.last >> j & 1) e = state_in(a, a.dh, r.seq_of(j), at.c);
-      const f32x2 d = Pair<E>::open(raw.G[j]);
-      e = f32x2{dec[j][0] * (d[0] + e[0]), dec[j][1] * (d[1] + e[1])};
-    }
-    l.run.put(run, P, e);
+  for (int j = RUN - 1; j >= 0; --j) {
+    if (!(r.in >> j & 1)) continue;
+    if (r.last >> j & 1) e = state_in(a, a.dh, r.seq_of(j), at.c);
+    const f32x2 d = Pair<E>::open(raw.G[j]);
+    e = f32x2{dec[j][0] * (d[0] + e[0]), dec[j][1] * (d[1] + e[1])};
+    P = mul2(P, dec[j]);
   }
+  l.run.put(run, P, e);
   if (lane_id() == 0) {
     starts[at.wave] = r.first != 0;
     l.fresh[run] = r.last != 0;
@@ -569,7 +594,19 @@ __global__ __launch_bounds__(RUNS* WAVE) __attribute__((amdgpu_waves_per_eu(4, 4
     if (lane_id() == 0) l.from = goes_on ? (int)a.tiles - 1 - (to - 1) / (RUN * RUNS) : at.order;
   }
   __syncthreads();
-  for (int k = 0; k < at.wave; ++k) h = fwd.behind(k, h, starts[k] != 0);
+  Joint joint(a, at, run, l);
+  // the states, while the words are on their way
+#pragma unroll
+  for (int j = 0; j < RUN; ++j) u[j] = input_of<E, GATE>(raw.X[j], raw.I[GATE ? j : 0], b[j]);
+  f32x2 x{0.f, 0.f};
+  walk<false>(a, at, r, dec, u, P, x);
+  fwd[at.wave][lane_id()] = x;
+  __syncthreads();
+  // the runs' products are those of the chain's way
+  for (int k = 0; k < at.wave; ++k) {
+    const f32x2 y = fwd[k][lane_id()];
+    h = starts[k] != 0 ? y : fma2(l.run.P[RUNS - 1 - k][lane_id()], h, y);
+  }
   // u gives way to the states before the tokens
 #pragma unroll
   for (int j = 0; j < RUN; ++j) {
@@ -587,7 +624,7 @@ __global__ __launch_bounds__(RUNS* WAVE) __attribute__((amdgpu_waves_per_eu(4, 4
     hide(raw.G[j]);
     if constexpr (GATE) hide(raw.I[j]);
   }
-  f32x2 e = l.before_run(run, tile_start(a, at, run, l));
+  e = l.before_run(run, joint.start());
   const Rows<E> X(a, at, a.dX, a.D), A(a, at, a.dA, a.D), I(a, at, GATE ? a.dI : a.dX, a.D);
   f32x2 dw{0.f, 0.f};
 #pragma unroll
@@ -622,11 +659,11 @@ __global__ __launch_bounds__(RUNS* WAVE) __attribute__((amdgpu_waves_per_eu(4, 4
   empty_sequences(a, at, a.dh, a.dh0);
   if (DECAY != GDN_DECAY_POWER || !a.dw) return;
   __syncthreads();
-  fwd.P[at.wave][lane_id()] = dw;
+  fwd[at.wave][lane_id()] = dw;
   __syncthreads();
   if (at.wave != 0 || at.c >= a.D) return;
   dw = f32x2{0.f, 0.f};
-  for (int k = 0; k < RUNS; ++k) dw += fwd.P[k][lane_id()];
+  for (int k = 0; k < RUNS; ++k) dw += fwd[k][lane_id()];
   *reinterpret_cast<f32x2*>(a.part + ((int64_t)at.b * a.tiles + at.tile) * a.D + at.c) = dw;
 }
 
