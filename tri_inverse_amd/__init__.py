@@ -784,6 +784,7 @@ def gdn_residual_norm_bwd(dN, dR, R, Y, w_post=None, s=None, alpha: float = 1.0,
 
 # ---- queries and keys in front of the mixer, and the recurrence of every channel ------------------
 
+_F32, _F64, _INT32 = (torch.float32,), (torch.float64,), (torch.int32,)
 _QK_NORM = {"none": GDN_QK_NONE, "rms": GDN_QK_RMS, "l2": GDN_QK_L2}
 _PAIRS = {"halves": GDN_PAIRS_HALVES, "neighbours": GDN_PAIRS_NEIGHBOURS}
 _DECAY = {"power": GDN_DECAY_POWER, "sigmoid": GDN_DECAY_SIGMOID, "log": GDN_DECAY_LOG}
@@ -797,13 +798,17 @@ def _choice(value, name, table):
 
 
 def _token_rows(t, name, dtypes, shape, dev):
-    """A tensor [B, T, ...] whose tokens may lie at any one stride (a part of a wider projection), the
-    values of a token together; returns that stride."""
-    width = 1
-    for n in shape[2:]:
-        width *= n
-    if type(t) is torch.Tensor and t.shape == shape and t.dtype in dtypes and t.get_device() == dev.index and t.is_contiguous():
-        return width
+    """A tensor [B, T, D] or [B, T, heads, d] whose tokens may lie at any one stride (a part of a wider
+    projection), the values of a token together; returns that stride."""
+    width = shape[2] if len(shape) == 3 else shape[2] * shape[3]
+    if type(t) is torch.Tensor and t.shape == shape and t.dtype in dtypes and t.get_device() == dev.index:
+        if t.is_contiguous():
+            return width
+        st, T = t.stride(), shape[1]
+        step = st[1] if T > 1 else st[0]
+        if st[-1] == 1 and (len(st) == 3 or st[2] == shape[3]) and step >= width and (
+                T == 1 or shape[0] == 1 or st[0] == T * step):
+            return step
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA (HIP) tensor" % name)
     if t.dtype not in dtypes:
@@ -827,35 +832,40 @@ def _token_rows(t, name, dtypes, shape, dev):
 
 
 def _qk_args(Q, K, wq, wk, freqs, positions, norm, eps, pairs, axis):
-    """The gdn_qk_shape of a call after the inputs' checks; returns (shape, device, dtype)."""
+    """The gdn_qk_shape of a call after the inputs' checks; returns (shape, B, H_q, H_k, T, d, device, dtype)."""
     one = Q if Q is not None else K
     if not isinstance(one, torch.Tensor) or one.dim() != 4:
         raise ValueError("Q and K must be [B, T, heads, d], one of them at least given")
     B, T, _, d = one.shape
-    dev = one.device
-    sh = gdn_qk_shape()
-    if not one.is_cuda:
+    dev, dtype = one.device, one.dtype
+    if dev.type != "cuda":
         raise TypeError("Q and K must be CUDA (HIP) tensors")
+    Hq = Hk = qs = ks = 0
     if Q is not None:
-        sh.H_q, sh.q_stride = Q.shape[2], _token_rows(Q, "Q", _FLOAT, Q.shape, dev)
+        Hq, qs = Q.shape[2], _token_rows(Q, "Q", _FLOAT, Q.shape, dev)
     if K is not None:
         if K.dim() != 4:
             raise ValueError("K must be [B, T, heads, d]")
-        sh.H_k, sh.k_stride = K.shape[2], _token_rows(K, "K", (one.dtype,), (B, T, K.shape[2], d), dev)
-    for w, name, t in ((wq, "wq", Q), (wk, "wk", K)):
-        if w is not None:
-            if t is None:
-                raise ValueError("%s is given without its heads" % name)
-            _arg(w, name, (torch.float32,), (d,), dev)
-    axes = 1
+        Hk = K.shape[2]
+        ks = _token_rows(K, "K", _FLOAT if Q is None else (dtype,), (B, T, Hk, d), dev)
+    if wq is not None:
+        if Q is None:
+            raise ValueError("wq is given without its heads")
+        _arg(wq, "wq", _F32, (d,), dev)
+    if wk is not None:
+        if K is None:
+            raise ValueError("wk is given without its heads")
+        _arg(wk, "wk", _F32, (d,), dev)
+    axes, rot = 1, 0
     if freqs is None:
         if positions is not None or axis is not None:
             raise ValueError("positions and axis need freqs")
     else:
-        if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1 or 2 * freqs.numel() > d:
+        if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1 or 2 * freqs.shape[0] > d:
             raise ValueError("freqs must be [rotated values / 2], at most d / 2 of them")
-        n = freqs.numel()
-        _arg(freqs, "freqs", (torch.float64,), (n,), dev)
+        n = freqs.shape[0]
+        rot = 2 * n
+        _arg(freqs, "freqs", _F64, (n,), dev)
         if axis is not None:
             if len(axis) != n:
                 raise ValueError("axis must give an axis for each of the %d pairs" % n)
@@ -864,13 +874,13 @@ def _qk_args(Q, K, wq, wk, freqs, positions, norm, eps, pairs, axis):
             axes = positions.shape[0]
             if not 1 <= axes <= GDN_QK_MAX_AXES or min(axis, default=0) < 0 or max(axis, default=0) >= axes:
                 raise ValueError("axis must name one of the positions' 1 to %d axes, got %d of them" % (GDN_QK_MAX_AXES, axes))
-            ctypes.memmove(sh.axis, bytes(axis), n)
         if positions is not None:
-            _arg(positions, "positions", (torch.int32,), (B, T) if axis is None else (axes, B, T), dev)
-        sh.rot = 2 * n
-    sh.T, sh.B, sh.d, sh.dtype, sh.axes = T, B, d, _TORCH_DTYPE[one.dtype], axes
-    sh.norm, sh.pairs, sh.eps = _choice(norm, "norm", _QK_NORM), _choice(pairs, "pairs", _PAIRS), eps
-    return sh, dev, one.dtype
+            _arg(positions, "positions", _INT32, (B, T) if axis is None else (axes, B, T), dev)
+    sh = gdn_qk_shape(T, qs, ks, B, Hq, Hk, d, _TORCH_DTYPE[dtype], _choice(norm, "norm", _QK_NORM), eps, rot,
+                      _choice(pairs, "pairs", _PAIRS), axes)
+    if axis is not None:
+        ctypes.memmove(sh.axis, bytes(axis), len(axis))
+    return sh, B, Hq, Hk, T, d, dev, dtype
 
 
 def gdn_qk_norm_fwd(Q, K=None, wq=None, wk=None, freqs=None, positions=None, norm: str = "rms", eps: float = 1e-6,
@@ -884,11 +894,10 @@ def gdn_qk_norm_fwd(Q, K=None, wq=None, wk=None, freqs=None, positions=None, nor
     one position (None: no rotation); pairs "halves" (i, i + r/2) or "neighbours" (2i, 2i + 1).
     positions: int32 [B,T] (None: the token's index), or [axes,B,T] with axis, a sequence that names
     the axis of each pair.  Returns (Q_out, K_out)."""
-    sh, dev, dtype = _qk_args(Q, K, wq, wk, freqs, positions, norm, eps, pairs, axis)
-    B, T, d = sh.B, sh.T, sh.d
+    sh, B, Hq, Hk, T, d, dev, dtype = _qk_args(Q, K, wq, wk, freqs, positions, norm, eps, pairs, axis)
     with _scope(dev, stream):
-        Q_out = None if Q is None else _out(Q_out, "Q_out", (dtype,), (B, sh.H_q, T, d), dev, dtype)
-        K_out = None if K is None else _out(K_out, "K_out", (dtype,), (B, sh.H_k, T, d), dev, dtype)
+        Q_out = None if Q is None else _out(Q_out, "Q_out", (dtype,), (B, Hq, T, d), dev, dtype)
+        K_out = None if K is None else _out(K_out, "K_out", (dtype,), (B, Hk, T, d), dev, dtype)
         st = _lib.gdn_qk_norm_fwd(ctypes.byref(sh), _at(Q), _at(K), _at(wq), _at(wk), _at(freqs), _at(positions),
                                   _at(Q_out), _at(K_out), _current(dev))
     _check(st, "gdn_qk_norm_fwd")
@@ -899,17 +908,17 @@ def gdn_qk_norm_bwd(dQ_out, dK_out, Q, K=None, wq=None, wk=None, freqs=None, pos
                     eps: float = 1e-6, pairs: str = "halves", axis=None, workspace=None, stream=None):
     """Backward pass of gdn_qk_norm_fwd from dQ_out [B,H_q,T,d] and dK_out [B,H_k,T,d].  Returns (dQ
     [B,T,H_q,d], dK [B,T,H_k,d], dwq, dwk [d] fp32), each None without its tensor."""
-    sh, dev, dtype = _qk_args(Q, K, wq, wk, freqs, positions, norm, eps, pairs, axis)
-    B, T, d = sh.B, sh.T, sh.d
-    for t, name, x, H in ((dQ_out, "dQ_out", Q, sh.H_q), (dK_out, "dK_out", K, sh.H_k)):
+    sh, B, Hq, Hk, T, d, dev, dtype = _qk_args(Q, K, wq, wk, freqs, positions, norm, eps, pairs, axis)
+    for t, name, x, H in ((dQ_out, "dQ_out", Q, Hq), (dK_out, "dK_out", K, Hk)):
         if x is not None:
             _arg(t, name, (dtype,), (B, H, T, d), dev)
         elif t is not None:
             raise ValueError("%s is given without its heads" % name)
     with _scope(dev, stream):
-        dQ, dK = (None if t is None else torch.empty((B, T, H, d), device=dev, dtype=dtype)
-                  for t, H in ((Q, sh.H_q), (K, sh.H_k)))
-        dwq, dwk = (None if w is None else torch.empty((d,), device=dev, dtype=torch.float32) for w in (wq, wk))
+        dQ = None if Q is None else torch.empty((B, T, Hq, d), device=dev, dtype=dtype)
+        dK = None if K is None else torch.empty((B, T, Hk, d), device=dev, dtype=dtype)
+        dwq = None if wq is None else torch.empty_like(wq)
+        dwk = None if wk is None else torch.empty_like(wk)
         ws, ws_bytes = (None, 0) if dwq is dwk is None else _scratch(
             workspace, _lib.gdn_qk_norm_bwd_workspace_bytes(ctypes.byref(sh)), dev)
         st = _lib.gdn_qk_norm_bwd(ctypes.byref(sh), _at(dQ_out), _at(dK_out), _at(Q), _at(K), _at(wq), _at(wk),
@@ -923,29 +932,28 @@ def _rec_shape(X, A, I, w, offsets, decay, norm):
     """The gdn_rec_shape of a call after the inputs' checks; returns (shape, the states' shape, device)."""
     if not isinstance(X, torch.Tensor) or X.dim() != 3:
         raise ValueError("X must be [B, T, D]")
-    if not X.is_cuda:
+    shape, dev, dtype = X.shape, X.device, X.dtype
+    if dev.type != "cuda":
         raise TypeError("X must be a CUDA (HIP) tensor")
-    B, T, D = X.shape
-    dev, dtype = X.device, (X.dtype,)
-    xs = _token_rows(X, "X", _FLOAT, X.shape, dev)
-    as_ = _token_rows(A, "A", dtype, X.shape, dev)
-    is_ = D if I is None else _token_rows(I, "I", dtype, X.shape, dev)
+    B, T, D = shape
+    xs = _token_rows(X, "X", _FLOAT, shape, dev)
+    as_ = _token_rows(A, "A", (dtype,), shape, dev)
+    is_ = D if I is None else _token_rows(I, "I", (dtype,), shape, dev)
     kind = _choice(decay, "decay", _DECAY)
     if kind == GDN_DECAY_POWER:
-        _arg(w, "w", (torch.float32,), (D,), dev)
+        _arg(w, "w", _F32, (D,), dev)
     elif w is not None:
         raise ValueError('w belongs to decay "power"')
-    n = B
     if offsets is not None:
         if B != 1:
             raise ValueError("packed sequences lie in one row: B must be 1, got %d" % B)
         if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
             raise ValueError("offsets must be [sequences + 1], of one sequence at least")
-        n = offsets.numel() - 1
-        _arg(offsets, "offsets", (torch.int32,), (n + 1,), dev)
-    sh = gdn_rec_shape(T, _at(offsets), xs, as_, is_, n, D, kind, _choice(norm, "norm", _REC_NORM),
-                       _TORCH_DTYPE[X.dtype])
-    return sh, (n, D), dev
+        B = offsets.numel() - 1
+        _arg(offsets, "offsets", _INT32, (B + 1,), dev)
+    sh = gdn_rec_shape(T, None if offsets is None else offsets.data_ptr(), xs, as_, is_, B, D, kind,
+                       _choice(norm, "norm", _REC_NORM), _TORCH_DTYPE[dtype])
+    return sh, (B, D), dev
 
 
 def _plain_rec(B, T, D, decay, packed):
@@ -976,10 +984,10 @@ def gdn_rec_fwd(X, A, I=None, w=None, h0=None, offsets=None, decay: str = "power
     Returns (H [B,T,D], h_out [B or n,D] fp32, states for gdn_rec_bwd with want_states, else None)."""
     sh, state, dev = _rec_shape(X, A, I, w, offsets, decay, norm)
     if h0 is not None:
-        _arg(h0, "h0", (torch.float32,), state, dev)
+        _arg(h0, "h0", _F32, state, dev)
     with _scope(dev, stream):
-        H = _out(H, "H", (X.dtype,), X.shape, dev, X.dtype)
-        h_out = _out(h_out, "h_out", (torch.float32,), state, dev, torch.float32, h0)
+        H = _out(H, "H", (X.dtype,), X.shape, dev, X.dtype, X if X.is_contiguous() else None)
+        h_out = _out(h_out, "h_out", _F32, state, dev, torch.float32, h0)
         if h0 is not None and h_out.data_ptr() == h0.data_ptr() and h0.numel():
             raise ValueError("h_out must not be h0: a sequence's parts read the one while others write the other")
         states = None
@@ -1022,10 +1030,10 @@ def gdn_rec_step(X, A, I=None, w=None, h=None, decay: str = "power", norm: str =
     fp32 or None (zeros).  Pass h_out=h to update the state in place.  Returns (H [B,n,D], h_out)."""
     sh, state, dev = _rec_shape(X, A, I, w, None, decay, norm)
     if h is not None:
-        _arg(h, "h", (torch.float32,), state, dev)
+        _arg(h, "h", _F32, state, dev)
     with _scope(dev, stream):
-        H = _out(H, "H", (X.dtype,), X.shape, dev, X.dtype)
-        h_out = _out(h_out, "h_out", (torch.float32,), state, dev, torch.float32, h)
+        H = _out(H, "H", (X.dtype,), X.shape, dev, X.dtype, X if X.is_contiguous() else None)
+        h_out = _out(h_out, "h_out", _F32, state, dev, torch.float32, h)
         st = _lib.gdn_rec_step(ctypes.byref(sh), _at(X), _at(A), _at(I), _at(w), _at(h), _at(h_out), _at(H),
                                _current(dev))
     _check(st, "gdn_rec_step")
