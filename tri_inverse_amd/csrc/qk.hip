@@ -7,10 +7,10 @@
 // R(p) turns pair i by p f_i: the turns p f_i / 2 pi are formed in fp64 and only what they leave of
 // a quarter is rounded to fp32, so an angle is right to 2^-24 of a quarter turn at any position.
 //
-// Bound by bytes: each row is read once into registers and its result written.  A lane holds four
-// pairs of a row whole (two runs of 4 values, r/2 apart or next to each other), so that no value
-// crosses lanes but for the row's sum, and keeps its angles' cosines and sines for all heads of
-// its token that its workgroup takes.  Lanes of a wave take neighbouring tokens: what they write of a head is
+// Bound by bytes: each row is read once into registers and its result written, and a lane keeps its
+// angles' cosines and sines for all heads of its token that its workgroup takes; the next heads' rows are
+// on their way while it forms the last ones' results.  A lane's pairs are its own, so no value crosses
+// lanes but for the row's sum.  Lanes of a wave take neighbouring tokens: what they write of a head is
 // contiguous.  Gradients of the weights as in norm.hip: partial rows by workgroup, added in order.
 #include "gdn_device.hpp"
 #include "gdn_kernels.hpp"
@@ -18,23 +18,6 @@
 namespace gdn {
 
 namespace {
-
-__device__ __forceinline__ void load4(const __bf16* p, float* x) {
-  const bf16x4 v = *reinterpret_cast<const bf16x4*>(p);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) x[e] = (float)v[e];
-}
-__device__ __forceinline__ void load4(const float* p, float* x) {
-  const f32x4 v = *reinterpret_cast<const f32x4*>(p);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) x[e] = v[e];
-}
-__device__ __forceinline__ void store4(__bf16* p, const float* x) {
-  *reinterpret_cast<bf16x4*>(p) = pack4(f32x4{x[0], x[1], x[2], x[3]});
-}
-__device__ __forceinline__ void store4(float* p, const float* x) {
-  *reinterpret_cast<f32x4*>(p) = f32x4{x[0], x[1], x[2], x[3]};
-}
 
 // sum over aligned groups of LPR lanes, in every lane of the group
 template <int LPR>
@@ -73,117 +56,188 @@ __device__ __forceinline__ void cos_sin(double turns, float& c, float& s) {
   if (k >= 2) s = -s;
 }
 
-// a lane's place in a row: two runs of 4 values, and whether they are its pairs
+// a lane's place in a row, two runs of 4 values.  HALVES: its pairs are (run 0, run 1) value by value, the runs
+// half the rotated part apart, half the rest for the lanes behind it.  Otherwise pairs are neighbours in
+// a run: 8 neighbouring bf16 values, or fp32 runs half the row apart, so that lanes' runs lie next to each other.
+template <class E, bool HALVES>
 struct Place {
-  int at0, at1, pair;
-  bool on, turns;
+  static constexpr bool WIDE = sizeof(E) == 2 && !HALVES;
+  int at[2];
+  bool on;
+  __device__ __forceinline__ Place(const QkLaunch& a, int lane) {
+    on = 8 * lane < a.d;
+    if (!on) lane = 0;  // loads what lies inside
+    if constexpr (WIDE) {
+      at[0] = 8 * lane;
+      at[1] = 8 * lane + 4;
+    } else {
+      const bool in = !HALVES || 8 * lane < a.rot;
+      const int first = in ? 0 : a.rot, width = !HALVES ? a.d : in ? a.rot : a.d - a.rot;
+      at[0] = first + 4 * (lane - first / 8);
+      at[1] = at[0] + width / 2;
+    }
+  }
 };
-template <bool HALVES>
-__device__ __forceinline__ Place place(const QkLaunch& a, int lane) {
-  Place p;
-  p.on = 8 * lane < a.d;
-  p.turns = 8 * lane < a.rot;
-  p.pair = 4 * lane;
-  p.at0 = HALVES && p.turns ? 4 * lane : 8 * lane;
-  p.at1 = HALVES && p.turns ? a.rot / 2 + 4 * lane : 8 * lane + 4;
-  return p;
-}
 
+// cosines and sines of a lane's four pairs
 struct Turn {
   float c[4], s[4];
-};
-__device__ __forceinline__ Turn turn_of(const QkLaunch& a, const Place& p, uint32_t token, uint32_t tokens, uint32_t t) {
-  Turn r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r.c[i] = 1.f;
-    r.s[i] = 0.f;
-  }
-  if (p.on && p.turns)
+  // SPARE: one pair after the other, which takes fewer registers from the rows on their way
+  template <bool HALVES, bool SPARE, class P>
+  __device__ __forceinline__ void find(const QkLaunch& a, const P& p, uint32_t token, uint32_t tokens, uint32_t t) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const double pos =
-          a.positions ? (double)a.positions[(int64_t)a.axis[p.pair + i] * tokens + token] : (double)t;
-      cos_sin(pos * (a.freqs[p.pair + i] * 0.15915494309189535), r.c[i], r.s[i]);
+      const int v = HALVES ? p.at[0] + i : p.at[i / 2] + 2 * (i % 2);  // the pair's first value
+      c[i] = 1.f;
+      s[i] = 0.f;
+      if (v < a.rot) {
+        const int pair = HALVES ? v : v / 2;
+        const double pos = a.positions ? (double)a.positions[(int64_t)a.axis[pair] * tokens + token] : (double)t;
+        cos_sin(pos * (a.freqs[pair] * 0.15915494309189535), c[i], s[i]);
+      }
+      if constexpr (SPARE) __builtin_amdgcn_sched_barrier(0);
     }
-  return r;
-}
-// pairs in a lane: (x[i], x[4 + i]), or (x[2 i], x[2 i + 1])
-template <bool HALVES>
-__device__ __forceinline__ void turn(float (&x)[8], const Turn& r, float sign) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int p = HALVES ? i : 2 * i, q = HALVES ? 4 + i : 2 * i + 1;
-    const float s = sign * r.s[i], u = x[p], v = x[q];
-    x[p] = u * r.c[i] - v * s;
-    x[q] = v * r.c[i] + u * s;
   }
-}
+  template <bool HALVES, bool BACK>
+  __device__ __forceinline__ void turn(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int m = HALVES ? i : 2 * i, n = HALVES ? 4 + i : 2 * i + 1;
+      const float sn = BACK ? -s[i] : s[i], u = x[m], v = x[n];
+      x[m] = u * c[i] - v * sn;
+      x[n] = v * c[i] + u * sn;
+    }
+  }
+};
 
+// a lane's values of a row as they lie in memory
 template <class E>
-__device__ __forceinline__ void load_row(const E* p, const Place& at, bool on, float (&x)[8]) {
+struct Row;
+template <>
+struct Row<__bf16> {
+  u32x2 run[2];
+  template <bool WIDE>
+  __device__ __forceinline__ void load(const __bf16* p, const int (&at)[2]) {
+    if constexpr (WIDE) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(p + at[0]);
+      run[0] = u32x2{v[0], v[1]};
+      run[1] = u32x2{v[2], v[3]};
+    } else {
+      run[0] = *reinterpret_cast<const u32x2*>(p + at[0]);
+      run[1] = *reinterpret_cast<const u32x2*>(p + at[1]);
+    }
+  }
+  __device__ __forceinline__ void open(float (&x)[8]) const {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = 0.f;
-  if (on) {
-    load4(p + at.at0, x);
-    load4(p + at.at1, x + 4);
+    for (int i = 0; i < 2; ++i) {
+      const u32x2 w = run[i];
+      const f32x4 v = unpack4(__builtin_bit_cast(bf16x4, w));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[4 * i + e] = v[e];
+    }
+  }
+};
+template <>
+struct Row<float> {
+  f32x4 run[2];
+  template <bool WIDE>
+  __device__ __forceinline__ void load(const float* p, const int (&at)[2]) {
+    run[0] = *reinterpret_cast<const f32x4*>(p + at[0]);
+    run[1] = *reinterpret_cast<const f32x4*>(p + at[1]);
+  }
+  __device__ __forceinline__ void open(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[4 * i + e] = run[i][e];
+  }
+};
+// NT: stores of whole lines, past what the caches hold
+template <bool NT, class E, class P>
+__device__ __forceinline__ void store_row(E* p, const P& at, const float (&x)[8]) {
+  const f32x4 lo{x[0], x[1], x[2], x[3]}, hi{x[4], x[5], x[6], x[7]};
+  if constexpr (P::WIDE) {
+    store16<NT>(reinterpret_cast<u32x4*>(p + at.at[0]), __builtin_bit_cast(u32x4, pack8(lo, hi)));
+  } else if constexpr (sizeof(E) == 2) {
+    store16<NT>(reinterpret_cast<u32x2*>(p + at.at[0]), __builtin_bit_cast(u32x2, pack4(lo)));
+    store16<NT>(reinterpret_cast<u32x2*>(p + at.at[1]), __builtin_bit_cast(u32x2, pack4(hi)));
+  } else {
+    store16<NT>(reinterpret_cast<f32x4*>(p + at.at[0]), lo);
+    store16<NT>(reinterpret_cast<f32x4*>(p + at.at[1]), hi);
   }
 }
-template <class E>
-__device__ __forceinline__ void store_row(E* p, const Place& at, bool on, const float (&x)[8]) {
-  if (on) {
-    store4(p + at.at0, x);
-    store4(p + at.at1, x + 4);
-  }
-}
-__device__ __forceinline__ void load_weights(const float* w, const Place& at, float (&x)[8]) {
+__device__ __forceinline__ void load_weights(const float* w, const int (&at)[2], float (&x)[8]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = 1.f;
-  if (w && at.on) {
-    load4(w + at.at0, x);
-    load4(w + at.at1, x + 4);
-  }
+  for (int e = 0; e < 8; ++e) x[e] = w ? w[at[e / 4] + e % 4] : 1.f;
 }
 
 // 1 / n(x) of a row; 1 without a norm
 template <int LPR>
-__device__ __forceinline__ float row_rstd(const QkLaunch& a, const float (&x)[8]) {
+__device__ __forceinline__ float row_rstd(const QkLaunch& a, const float (&x)[8], bool on) {
   if (a.norm == GDN_QK_NONE) return 1.f;
   float ss = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-  ss = lanes_sum<LPR>(ss);
+  ss = lanes_sum<LPR>(on ? ss : 0.f);
   return 1.f / sqrtf((a.norm == GDN_QK_RMS ? ss / (float)a.d : ss) + a.eps);
 }
 
 }  // namespace
 
+// a row's token and place; a token past the last one stands for the last one, whose row it loads
+struct Token {
+  uint32_t token, b, t;
+  bool on;
+  __device__ __forceinline__ Token(const QkLaunch& a, uint32_t at, uint32_t tokens) {
+    on = at < tokens;
+    token = on ? at : tokens - 1;
+    b = token / (uint32_t)a.T;
+    t = token - b * (uint32_t)a.T;
+  }
+};
+
 // workgroup: 256 / LPR tokens, `per` heads of queries and keys from blockIdx.y * per on
-template <int LPR, class E, bool HALVES>
+template <int LPR, class E, bool HALVES, bool NT>
 __global__ __launch_bounds__(256) void qk_kernel(QkLaunch a, int per) {
-  const Place at = place<HALVES>(a, threadIdx.x % LPR);
+  typedef Place<E, HALVES> P;
+  constexpr int U = sizeof(E) == 2 ? 4 : 2;  // heads at a time
+  const P at(a, threadIdx.x % LPR);
   const uint32_t tokens = (uint32_t)(a.B * a.T);
-  const uint32_t token = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
-  const bool on = token < tokens && at.on;
-  const uint32_t b = token / (uint32_t)a.T, t = token - b * (uint32_t)a.T;
-  Turn r{};
-  if (token < tokens) r = turn_of(a, at, token, tokens, t);
+  const Token k(a, blockIdx.x * (256 / LPR) + threadIdx.x / LPR, tokens);
   const int first = blockIdx.y * per, last = min(first + per, a.Hq + a.Hk);
+  Turn angle;
+  bool found = false;
   auto heads = [&](int h0, int h1, int H, const void* in, int64_t stride, const float* weights, void* out) {
     if (h0 >= h1) return;
-    float w[8];
-    load_weights(weights, at, w);
-    const E* src = reinterpret_cast<const E*>(in) + (int64_t)token * stride;
-    E* dst = reinterpret_cast<E*>(out) + ((int64_t)b * H * a.T + t) * a.d;
-#pragma unroll 4
-    for (int h = h0; h < h1; ++h) {
-      float x[8];
-      load_row(src + (int64_t)h * a.d, at, on, x);
-      const float rstd = row_rstd<LPR>(a, x);
+    const E* src = reinterpret_cast<const E*>(in) + (int64_t)k.token * stride;
+    E* dst = reinterpret_cast<E*>(out) + ((int64_t)k.b * H * a.T + k.t) * a.d;
+    Row<E> row[U];
+    auto load = [&](int h) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= rstd * w[e];
-      turn<HALVES>(x, r, 1.f);
-      store_row(dst + (int64_t)h * a.T * a.d, at, on, x);
+      for (int u = 0; u < U; ++u)
+        row[u].template load<P::WIDE>(src + (int64_t)min(h + u, h1 - 1) * a.d, at.at);
+    };
+    load(h0);
+    float w[8];
+    load_weights(weights, at.at, w);
+    if (!found) angle.template find<HALVES, false>(a, at, k.token, tokens, k.t);
+    found = true;
+    for (int h = h0; h < h1; h += U) {
+      Row<E> now[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) now[u] = row[u];
+      if (h + U < h1) load(h + U);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (h + u >= h1) break;
+        float x[8];
+        now[u].open(x);
+        const float rstd = row_rstd<LPR>(a, x, at.on);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= rstd * w[e];
+        angle.template turn<HALVES, false>(x);
+        if (k.on && at.on) store_row<NT>(dst + (int64_t)(h + u) * a.T * a.d, at, x);
+      }
     }
   };
   heads(first, min(last, a.Hq), a.Hq, a.Q_in, a.q_stride, a.wq, a.Q);
@@ -191,53 +245,78 @@ __global__ __launch_bounds__(256) void qk_kernel(QkLaunch a, int per) {
 }
 
 // workgroups walk pieces of work: groups of tokens, and runs of `per` heads
-template <int LPR, class E, bool HALVES>
-__global__ __launch_bounds__(256) void qk_bwd_kernel(QkLaunch a, int per, uint32_t runs, uint32_t pieces, float* part) {
+template <int LPR, class E, bool HALVES, bool NT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4, 4))) void qk_bwd_kernel(QkLaunch a, int per, uint32_t runs, uint32_t pieces, float* part) {
+  typedef Place<E, HALVES> P;
+  constexpr int U = 1;
   __shared__ float sums[256 / LPR][8 * LPR];
-  const Place at = place<HALVES>(a, threadIdx.x % LPR);
+  const P at(a, threadIdx.x % LPR);
   const uint32_t tokens = (uint32_t)(a.B * a.T);
-  float w[2][8], dw[2][8];
-  load_weights(a.wq, at, w[0]);
-  load_weights(a.wk, at, w[1]);
+  float dw[2][8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.f;
   for (uint32_t piece = blockIdx.x; piece < pieces; piece += gridDim.x) {
-    const uint32_t group = piece / runs, token = group * (256 / LPR) + threadIdx.x / LPR;
+    const uint32_t group = piece / runs;
+    const Token k(a, group * (256 / LPR) + threadIdx.x / LPR, tokens);
     const int first = (int)(piece - group * runs) * per, last = min(first + per, a.Hq + a.Hk);
-    const bool row = token < tokens, on = row && at.on;
-    const uint32_t b = token / (uint32_t)a.T, t = token - b * (uint32_t)a.T;
-    Turn r{};
-    if (row) r = turn_of(a, at, token, tokens, t);
-    auto heads = [&](auto which, int h0, int h1, int H, const void* in, int64_t stride, const void* dy, void* dx) {
+    Turn angle;
+    bool found = false;
+    auto heads = [&](auto which, int h0, int h1, int H, const void* in, int64_t stride, const float* weights,
+                     const void* dy, void* dx) {
       constexpr int W = which.value;
-      const E* src = reinterpret_cast<const E*>(in) + (int64_t)token * stride;
-      const E* grad = reinterpret_cast<const E*>(dy) + ((int64_t)b * H * a.T + t) * a.d;
-      E* dst = reinterpret_cast<E*>(dx) + (int64_t)token * H * a.d;
-#pragma unroll 2
-      for (int h = h0; h < h1; ++h) {
-        float x[8], g[8];
-        load_row(src + (int64_t)h * a.d, at, on, x);
-        load_row(grad + (int64_t)h * a.T * a.d, at, on, g);
-        // past the last token the norm of zeros would be infinite where eps is 0, and dw not a number
-        const float rstd = row ? row_rstd<LPR>(a, x) : 0.f;
-        turn<HALVES>(g, r, -1.f);
-        float dot = 0.f;
+      if (h0 >= h1) return;
+      const E* src = reinterpret_cast<const E*>(in) + (int64_t)k.token * stride;
+      const E* grad = reinterpret_cast<const E*>(dy) + ((int64_t)k.b * H * a.T + k.t) * a.d;
+      E* dst = reinterpret_cast<E*>(dx) + (int64_t)k.token * H * a.d;
+      Row<E> rx[U], rg[U];
+      auto load = [&](int h) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] *= rstd;
-          dw[W][e] = fmaf(g[e], x[e], dw[W][e]);
-          g[e] *= w[W][e];
-          dot = fmaf(g[e], x[e], dot);
+        for (int u = 0; u < U; ++u) {
+          const int64_t i = min(h + u, h1 - 1);
+          rx[u].template load<P::WIDE>(src + i * a.d, at.at);
+          rg[u].template load<P::WIDE>(grad + i * a.T * a.d, at.at);
         }
-        dot = a.norm == GDN_QK_NONE ? 0.f : lanes_sum<LPR>(dot);
-        if (a.norm == GDN_QK_RMS) dot /= (float)a.d;
+      };
+      load(h0);
+      float w[8];
+      load_weights(weights, at.at, w);
+      if (!found) angle.template find<HALVES, true>(a, at, k.token, tokens, k.t);
+      found = true;
+      for (int h = h0; h < h1; h += U) {
+        Row<E> nx[U], ng[U];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = rstd * (g[e] - x[e] * dot);
-        store_row(dst + (int64_t)h * a.d, at, on, x);
+        for (int u = 0; u < U; ++u) {
+          nx[u] = rx[u];
+          ng[u] = rg[u];
+        }
+        if (h + U < h1) load(h + U);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (h + u >= h1) break;
+          float x[8], g[8];
+          nx[u].open(x);
+          ng[u].open(g);
+          // a token past the last one adds nothing to dw
+          const float rstd = k.on ? row_rstd<LPR>(a, x, at.on) : 0.f;
+          angle.template turn<HALVES, true>(g);
+          float dot = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            x[e] *= rstd;
+            dw[W][e] = fmaf(g[e], x[e], dw[W][e]);
+            g[e] *= w[e];
+            dot = fmaf(g[e], x[e], dot);
+          }
+          dot = a.norm == GDN_QK_NONE ? 0.f : lanes_sum<LPR>(at.on ? dot : 0.f);
+          if (a.norm == GDN_QK_RMS) dot /= (float)a.d;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = rstd * (g[e] - x[e] * dot);
+          if (k.on && at.on) store_row<NT>(dst + (int64_t)(h + u) * a.d, at, x);
+        }
       }
     };
-    heads(std::integral_constant<int, 0>{}, first, min(last, a.Hq), a.Hq, a.Q_in, a.q_stride, a.dQ, a.Q);
-    heads(std::integral_constant<int, 1>{}, max(first - a.Hq, 0), last - a.Hq, a.Hk, a.K_in, a.k_stride, a.dK, a.K);
+    heads(std::integral_constant<int, 0>{}, first, min(last, a.Hq), a.Hq, a.Q_in, a.q_stride, a.wq, a.dQ, a.Q);
+    heads(std::integral_constant<int, 1>{}, max(first - a.Hq, 0), last - a.Hq, a.Hk, a.K_in, a.k_stride, a.wk, a.dK, a.K);
   }
   if (!part) return;
 #pragma unroll
@@ -245,7 +324,7 @@ __global__ __launch_bounds__(256) void qk_bwd_kernel(QkLaunch a, int per, uint32
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (at.on) sums[threadIdx.x / LPR][(e < 4 ? at.at0 : at.at1 - 4) + e] = dw[which][e];
+      if (at.on) sums[threadIdx.x / LPR][at.at[e / 4] + e % 4] = dw[which][e];
     __syncthreads();
     for (int i = threadIdx.x; i < a.d; i += 256) {
       float s = 0.f;
@@ -261,10 +340,22 @@ namespace {
 
 int row_lanes(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 
+// Whether every store covers whole lines of 128 bytes; they then go past what the caches hold.  Of parts of
+// lines that costs more than it gives (4 x 8192 tokens of 32 heads of 128 bf16 values, 8 of them
+// turned: 129 us instead of 110; all turned: 100 instead of 105).
+bool whole_lines(const QkLaunch& p) {
+  const int size = p.bf16 ? 2 : 4;
+  if (!p.halves) return p.bf16 || p.d / 2 * size % 128 == 0;
+  return p.rot / 2 * size % 128 == 0 && (p.d - p.rot) / 2 * size % 128 == 0;
+}
+
 template <class F>
 int by_kind(const QkLaunch& p, F&& f) {
+  auto lines = [&](auto lpr, auto e, auto halves) {
+    return whole_lines(p) ? f(lpr, e, halves, std::true_type{}) : f(lpr, e, halves, std::false_type{});
+  };
   auto pairs = [&](auto lpr, auto e) {
-    return p.halves ? f(lpr, e, std::integral_constant<bool, true>{}) : f(lpr, e, std::integral_constant<bool, false>{});
+    return p.halves ? lines(lpr, e, std::true_type{}) : lines(lpr, e, std::false_type{});
   };
   auto type = [&](auto lpr) { return p.bf16 ? pairs(lpr, (__bf16*)nullptr) : pairs(lpr, (float*)nullptr); };
   switch (row_lanes(p.d)) {
@@ -299,9 +390,9 @@ int64_t bwd_groups(const QkLaunch& p) {
 size_t qk_bwd_workspace(const QkLaunch& p) { return (size_t)bwd_groups(p) * 2 * p.d * 4; }
 
 int launch_qk(const QkLaunch& p, hipStream_t s) {
-  return by_kind(p, [&](auto lpr, auto e, auto halves) {
+  return by_kind(p, [&](auto lpr, auto e, auto halves, auto nt) {
     const dim3 grid((unsigned)token_groups(p), (unsigned)head_runs(p)), block(256);
-    hipLaunchKernelGGL((qk_kernel<lpr.value, std::remove_pointer_t<decltype(e)>, halves.value>), grid, block, 0, s, p,
+    hipLaunchKernelGGL((qk_kernel<lpr.value, std::remove_pointer_t<decltype(e)>, halves.value, nt.value>), grid, block, 0, s, p,
                        heads_per_group(p));
     return 0;
   });
@@ -312,10 +403,14 @@ int launch_qk_bwd(const QkLaunch& p, void* workspace, hipStream_t s) {
   const bool rows = (int64_t)p.B * p.T > 0 && p.Hq + p.Hk > 0;
   const int64_t n = rows ? bwd_groups(p) : 0;
   if (rows)
-    by_kind(p, [&](auto lpr, auto e, auto halves) {
+    by_kind(p, [&](auto lpr, auto e, auto halves, auto nt) {
       const dim3 grid((unsigned)n), block(256);
       const int runs = head_runs(p);
-      hipLaunchKernelGGL((qk_bwd_kernel<lpr.value, std::remove_pointer_t<decltype(e)>, halves.value>), grid, block, 0, s,
+      typedef std::remove_pointer_t<decltype(e)> E;
+      // stores past the caches pay for fp32 (2 x 4096 tokens of 32 heads of 128: 84 us, through them 89), not for
+      // bf16 (4 x 4096 tokens: 94.4, through them 90.9)
+      constexpr bool past = nt.value && sizeof(E) == 4;
+      hipLaunchKernelGGL((qk_bwd_kernel<lpr.value, E, halves.value, past>), grid, block, 0, s,
                          p, heads_per_group(p), (uint32_t)runs, (uint32_t)(token_groups(p) * runs), part);
       return 0;
     });
