@@ -47,6 +47,9 @@ __device__ __forceinline__ void hide(V& v) {
   asm volatile("" : "+v"(v));
 }
 
+// outputs go past what the caches hold (the non-temporal bit): prefill 137.7 -> 132 us, training step 218 -> 211
+constexpr int PAST = 2;
+
 // two neighbouring channels as they lie in memory, and as fp32
 template <class E>
 struct Pair;
@@ -57,7 +60,7 @@ struct Pair<__bf16> {
     return __builtin_amdgcn_raw_buffer_load_b32(p, lane, row, 0);
   }
   static __device__ __forceinline__ void store(raw v, __amdgpu_buffer_rsrc_t p, uint32_t lane, uint32_t row) {
-    __builtin_amdgcn_raw_buffer_store_b32(v, p, lane, row, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(v, p, lane, row, PAST);
   }
   static __device__ __forceinline__ f32x2 open(raw v) {
     return f32x2{__builtin_bit_cast(float, v << 16), __builtin_bit_cast(float, v & 0xffff0000u)};
@@ -77,7 +80,7 @@ struct Pair<float> {
     return __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(p, lane, row, 0));
   }
   static __device__ __forceinline__ void store(raw v, __amdgpu_buffer_rsrc_t p, uint32_t lane, uint32_t row) {
-    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v), p, lane, row, 0);
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v), p, lane, row, PAST);
   }
   static __device__ __forceinline__ f32x2 open(raw v) { return v; }
   static __device__ __forceinline__ raw close(f32x2 v) { return v; }
