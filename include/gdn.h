@@ -435,7 +435,7 @@ typedef enum gdn_rec_norm { GDN_REC_NORM_SQRT = 0, GDN_REC_NORM_LINEAR = 1, GDN_
  * offsets != NULL: B packed sequences in T tokens, as in gdn_lin_shape, rows of the T tokens; rows of
  *   no sequence are not read into a result, H is not written there, and gradients there are zero.
  * X, A, I, H and their gradients in dtype (GDN_BF16 or GDN_F32); states [B][D] fp32.  D a multiple of
- * 8; at most 2^35 values in whole tiles of GDN_REC_TILE tokens and 128 channels.  Empty sequences and T == 0 return the given states unchanged (or zeros).  A log-decay of
+ * 8; fewer than 2^36 values, counted in whole tiles of GDN_REC_TILE tokens and 128 channels.  Empty sequences and T == 0 return the given states unchanged (or zeros).  A log-decay of
  * -inf forgets the state; where a = 1 the gradient of b = sqrt(1 - a^2) = 0 counts as 0. */
 typedef struct gdn_rec_shape {
   int64_t T;

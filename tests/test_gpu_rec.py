@@ -347,6 +347,59 @@ def test_many_tiles():
 
 
 @gpu
+@pytest.mark.parametrize("lens,first,tail", [([9000, 1, 0, 300, 8193, 5000, 64, 4096], 70, 40), ([1] * 700 + [0, 9001], 0, 0),
+                                             ([127, 8192, 1025, 63, 7777], 1, 0), ([20000], 500, 9000)],
+                         ids=["mixed", "ones", "odd", "one"])
+def test_packed_over_many_tiles(lens, first, tail):
+    """Sequences that start and end in any of the tiles that join by eights and by 64."""
+    say(f"recurrence packed over many tiles, {len(lens)} sequences")
+    T = first + sum(lens) + tail
+    x = {k: up(v) for k, v in ref.rec_inputs(T, 1, T, 24, "power", True, F32, n_state=len(lens), slow=True).items()}
+    how = dict(I=x["I"], w=x["w"], h0=x["h0"], offsets=offsets_of(lens, first))
+    H, h, st = tri.gdn_rec_fwd(x["X"], x["A"], want_states=True, **how)
+    g = tri.gdn_rec_bwd(x["X"], x["A"], x["dH"], dh=x["dh"], states=st, **how)
+    torch.cuda.synchronize()
+    inside = slice(first, first + sum(lens))
+    Hr, hr, EH, Eh, _ = ref.rec_forward(x, "power", "sqrt", x["h0"], lens, first)
+    close(H[:, inside], Hr[:, inside].cpu(), EH[:, inside].cpu(), "H")
+    close(h, hr.cpu(), Eh.cpu(), "h_out")
+    want, bound = ref.rec_backward(x, "power", "sqrt", x["h0"], x["dh"], lens, first)
+    for name, a, y, e in zip(("dX", "dA", "dI", "dw", "dh0"), g, want, bound):
+        close(a, y.cpu(), e.cpu(), name)
+
+
+@gpu
+def test_one_row_of_any_stride():
+    """One sequence of one token: its strides say nothing."""
+    say("recurrence, one row")
+    x = ref.rec_inputs(3, 1, 1, 24, "sigmoid", False, F32)
+    X, A = (torch.as_strided(up(x[k]), (1, 1, 24), (3, 5, 1)) for k in ("X", "A"))
+    H, h, _ = tri.gdn_rec_fwd(X, A, decay="sigmoid")
+    torch.cuda.synchronize()
+    Hr, hr, EH, Eh, _ = ref.rec_forward(x, "sigmoid", "sqrt")
+    close(H, Hr, EH, "H")
+    close(h, hr, Eh, "h_out")
+
+
+@gpu
+def test_one_workspace_for_calls_in_a_row():
+    """A workspace left by another call, of other sizes, changes nothing."""
+    say("recurrence, one workspace")
+    ws = torch.full((1 << 22,), 0xAB, device="cuda", dtype=torch.uint8)
+    for seed, (B, T, D, kind) in enumerate([(1, 2000, 264, "power"), (3, 500, 40, "log"), (2, 1300, 136, "sigmoid")]):
+        assert max(tri.gdn_rec_fwd_workspace_bytes(B, T, D), tri.gdn_rec_bwd_workspace_bytes(B, T, D, kind)) <= ws.numel()
+        x = {k: up(v) for k, v in ref.rec_inputs(seed, B, T, D, kind, True, BF).items()}
+        how = dict(I=x["I"], w=x["w"], h0=x["h0"], decay=kind)
+        one = tri.gdn_rec_fwd(x["X"], x["A"], want_states=True, workspace=ws, **how)
+        one += tri.gdn_rec_bwd(x["X"], x["A"], x["dH"], states=one[2], workspace=ws, **how)
+        one += tri.gdn_rec_bwd(x["X"], x["A"], x["dH"], workspace=ws, **how)
+        own = tri.gdn_rec_fwd(x["X"], x["A"], want_states=True, **how)
+        own += tri.gdn_rec_bwd(x["X"], x["A"], x["dH"], states=own[2], **how) * 2
+        torch.cuda.synchronize()
+        assert all(a is b is None or torch.equal(a, b) for a, b in zip(one, own))
+
+
+@gpu
 def test_python_refusals():
     X = torch.zeros((2, 5, 16), device="cuda")
     w, h = torch.ones(16, device="cuda"), torch.zeros((2, 16), device="cuda")

@@ -805,7 +805,7 @@ def _token_rows(t, name, dtypes, shape, dev):
         if t.is_contiguous():
             return width
         st, T = t.stride(), shape[1]
-        step = st[1] if T > 1 else st[0]
+        step = st[1] if T > 1 else st[0] if shape[0] > 1 else width
         if st[-1] == 1 and (len(st) == 3 or st[2] == shape[3]) and step >= width and (
                 T == 1 or shape[0] == 1 or st[0] == T * step):
             return step
