@@ -273,6 +273,26 @@ __device__ __forceinline__ void self_swap_f(float x, float& a, float& b) {
   b = __builtin_bit_cast(float, ub);
 }
 
+// sum over aligned groups of LPR lanes, in every lane of the group
+template <int LPR>
+__device__ __forceinline__ float group_sum(float x) {
+  static_assert(LPR == 4 || LPR == 8 || LPR == 16 || LPR == 32 || LPR == 64, "");
+  x += dpp_f<0xB1>(x);  // quad_perm 1,0,3,2
+  x += dpp_f<0x4E>(x);  // quad_perm 2,3,0,1
+  if constexpr (LPR >= 8) x += dpp_f<0x141>(x);  // row_half_mirror
+  if constexpr (LPR >= 16) x += dpp_f<0x140>(x);  // row_mirror
+  float a, b;
+  if constexpr (LPR >= 32) {
+    self_swap_f<16>(x, a, b);
+    x = a + b;
+  }
+  if constexpr (LPR >= 64) {
+    self_swap_f<32>(x, a, b);
+    x = a + b;
+  }
+  return x;
+}
+
 // reduce over the 16 lanes of each row (rotations by 8, 4, 2, 1), then over the rows
 template <typename F>
 __device__ __forceinline__ float wave_reduce(float v, F op) {

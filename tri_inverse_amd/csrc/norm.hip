@@ -52,26 +52,6 @@ __device__ __forceinline__ void fill8(float (&x)[8], float v) {
   for (int e = 0; e < 8; ++e) x[e] = v;
 }
 
-// sum over aligned groups of LPR lanes, in every lane of the group
-template <int LPR>
-__device__ __forceinline__ float group_sum(float x) {
-  static_assert(LPR == 4 || LPR == 8 || LPR == 16 || LPR == 32 || LPR == 64, "");
-  x += dpp_f<0xB1>(x);  // quad_perm 1,0,3,2
-  x += dpp_f<0x4E>(x);  // quad_perm 2,3,0,1
-  if constexpr (LPR >= 8) x += dpp_f<0x141>(x);  // row_half_mirror
-  if constexpr (LPR >= 16) x += dpp_f<0x140>(x);  // row_mirror
-  float a, b;
-  if constexpr (LPR >= 32) {
-    self_swap_f<16>(x, a, b);
-    x = a + b;
-  }
-  if constexpr (LPR >= 64) {
-    self_swap_f<32>(x, a, b);
-    x = a + b;
-  }
-  return x;
-}
-
 // act(z) and its derivative; 1 / (1 + e^-z) is 0 or 1 where e^-z overflows or vanishes.  What it
 // leaves of 1 is e^-z times itself for z >= 0, where the difference would cancel (17 % of the
 // sigmoid's derivative at z = 15, all of it from 17 on)

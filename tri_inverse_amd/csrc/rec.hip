@@ -15,18 +15,27 @@
 // join in LDS.  The tiles of a row and 128 channels form a chain, and the data is read once: a
 // workgroup publishes its tile's end (P, h), waits for those before it, and forms its outputs from the
 // registers it still holds.  Ends join by eights: a tile reads the ends of the tiles before it in its
-// eight, of the eights before its own in their eight, and the state before those 64 tiles, so a chain
-// has one step in a row for 64 tiles, whatever the order of the workgroups' progress the sums'
-// order is one, and the same call gives the same bits.
+// eight, of the eights before its own in their eight, and the state before those 64 tiles.  So a chain
+// has one step in a row for 64 tiles, and the order of the sums does not depend on the workgroups'
+// progress: the same call gives the same bits.
 //
 // Waiting: a word of a chain carries its value and, by not being NOT_YET, that it is there, in one
-// 64-bit (32-bit) store, so no fence is needed.  A workgroup takes its tile from its chain's counter,
+// 64-bit store, so no fence is needed.  A workgroup takes its tile from its chain's counter,
 // in the order of the workgroups' starts: whatever it waits for has been taken by a workgroup that is
 // already running, which itself waits only for earlier ones, so every wait ends.  A wait is bounded
 // all the same: past the bound it takes NaN for the state.
 //
-// Decays, states and sums are fp32; 1 - a is formed without cancelling (expm1), each output is
+// Decays, states and sums are fp32; 1 - a is formed without cancelling (a series near 0), each output is
 // rounded once.
+//
+// Measured (a copy of 1 GiB reaches 5.05 TB/s): 4 sequences of 8192 tokens, 2048 channels, bf16, 537 MB, 132
+// us, 4.1 TB/s.  With the stores through the caches 138, of which the chain 4, the gates' arithmetic 13,
+// both together 23.  One sequence of 65536 tokens, 1024 channels, 403 MB, 120 us, without the chain 91: of 8
+// chains alone a tile waits for the slowest of 64 that run beside it.  Training step of 4 x 4096 tokens,
+// 2048 channels, 738 MB, 210 us: forwards 70, backwards 135 (100 without chain and gates).
+// Tiles: 64 tokens forwards take 150 us for the first, 32 tokens 211 (each tile has its share of the
+// chain); 128 backwards spill, 260 us for the training step.  Workgroups that walk on along their chain
+// took 140 and, for the second, 142; three workgroups a CU, with half of u in LDS, 139 and 136.
 #include "gdn_device.hpp"
 #include "gdn_kernels.hpp"
 
@@ -99,10 +108,10 @@ __device__ __forceinline__ void sigmoid_rest(float z, float& s, float& rest) {
   rest = e * s;
 }
 
-// 1 - 2^(n gl), n = 1 or 2, p = 2^(n gl) known: below 1/4 in n g the series (its first term left out is below
-// 2^-24 of it), above it the difference, right to 2^-21
+// 1 - 2^(n gl), n = 1 or 2, given as `direct` from a: below 1/4 in n g the series (its first term left out is
+// below 2^-24 of it), above it the difference, right to 2^-21
 template <int N>
-__device__ __forceinline__ float rest_of(float gl, float p) {
+__device__ __forceinline__ float rest_of(float gl, float direct) {
   constexpr float x = N * LN2, x2 = x * x, x3 = x2 * x;
   float r = -x3 * x3 / 720.f;
   r = fmaf(r, gl, -x3 * x2 / 120.f);
@@ -110,7 +119,7 @@ __device__ __forceinline__ float rest_of(float gl, float p) {
   r = fmaf(r, gl, -x3 / 6.f);
   r = fmaf(r, gl, -x2 / 2.f);
   r = fmaf(r, gl, -x);
-  return fabsf(gl) < 0.25f * LOG2E / N ? r * gl : p;
+  return fabsf(gl) < 0.25f * LOG2E / N ? r * gl : direct;
 }
 
 // the decay of a token and the factor b of its input.  wl = -w log2 e.
