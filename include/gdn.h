@@ -436,7 +436,7 @@ typedef enum gdn_rec_norm { GDN_REC_NORM_SQRT = 0, GDN_REC_NORM_LINEAR = 1, GDN_
  *   no sequence are not read into a result, H is not written there, and gradients there are zero.
  * X, A, I, H and their gradients in dtype (GDN_BF16 or GDN_F32); states [B][D] fp32.  D a multiple of
  * 8; fewer than 2^36 values, counted in whole tiles of GDN_REC_TILE tokens and 128 channels.  Empty sequences and T == 0 return the given states unchanged (or zeros).  A log-decay of
- * -inf forgets the state; where a = 1 the gradient of b = sqrt(1 - a^2) = 0 counts as 0. */
+ * -inf forgets a finite state; where a = 1 the gradient of b = sqrt(1 - a^2) = 0 counts as 0. */
 typedef struct gdn_rec_shape {
   int64_t T;
   const int32_t* offsets;
@@ -462,7 +462,8 @@ gdn_status gdn_rec_fwd(const gdn_rec_shape* shape, const void* X, const void* A,
 /* Its backward pass: gradients of a loss from dH (as H) and dh (gradient of h_out, NULL = zeros): dX,
  * dA, dI (with I only) [B][T][D] in dtype, dw fp32 [D] and dh0 fp32 [B][D] (NULL = not wanted; dw with
  * GDN_DECAY_POWER only).  states as gdn_rec_fwd wrote them for the same inputs; NULL: they are formed
- * anew.  The same call gives the same bits. */
+ * anew.  The same call gives the same bits.  An infinity or a NaN in a row may reach all gradients of its
+ * sequence and channel: rows that pad a sequence must be finite here. */
 gdn_status gdn_rec_bwd(const gdn_rec_shape* shape, const void* X, const void* A, const void* I, const float* w,
                        const float* h0, const float* states, const void* dH, const float* dh, void* dX,
                        void* dA, void* dI, float* dw, float* dh0, void* workspace, size_t workspace_bytes,

@@ -288,7 +288,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4, 4))) voi
           nx[u].open(x);
           ng[u].open(g);
           // a token past the last one adds nothing to dw
-          const float rstd = k.on ? row_rstd<LPR>(a, x, at.on) : 0.f;
+          const float size = row_rstd<LPR>(a, x, at.on), rstd = k.on ? size : 0.f;
           angle.template turn<HALVES, true>(g);
           float dot = 0.f;
 #pragma unroll
