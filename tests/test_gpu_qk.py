@@ -8,6 +8,7 @@ rows in fp32 and fp64: 2^-17 of the sum of absolute values."""
 import ctypes
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -275,6 +276,29 @@ def test_python_refusals():
         go(torch.zeros((1, 1, 1, 48), device="cuda"))
     with pytest.raises(tri.GdnError):
         go(Q, freqs=f[:2])
+
+
+@gpu
+def test_more_pairs_than_a_row_has_axes_for():
+    # as many axes as pairs, twice what the shape has room for
+    Q, f = torch.zeros((1, 1, 1, 512), device="cuda"), torch.ones(256, device="cuda", dtype=torch.float64)
+    pos = torch.zeros((1, 1, 1), device="cuda", dtype=torch.int32)
+    with pytest.raises(ValueError):
+        tri.gdn_qk_norm_fwd(Q, freqs=f, positions=pos, axis=[0] * 256)
+    with pytest.raises(ValueError):
+        tri.gdn_qk_norm_fwd(Q[..., :256].contiguous(), freqs=f[:128], positions=[[[0]]], axis=[0] * 128)
+
+
+@gpu
+@pytest.mark.parametrize("kind", (tuple, bytes, np.array, torch.tensor))
+def test_axis_of_any_sequence(kind):
+    g = torch.Generator(device="cuda").manual_seed(3)
+    Q = torch.randn((1, 7, 2, 64), device="cuda", generator=g)
+    f = torch.rand(32, device="cuda", dtype=torch.float64, generator=g)
+    pos = torch.randint(0, 99, (3, 1, 7), device="cuda", dtype=torch.int32, generator=g)
+    axis = [(5 * i) % 3 for i in range(32)]
+    want = tri.gdn_qk_norm_fwd(Q, freqs=f, positions=pos, axis=axis)[0]
+    assert torch.equal(tri.gdn_qk_norm_fwd(Q, freqs=f, positions=pos, axis=kind(axis))[0], want)
 
 
 # ---- refusals of the C entry points, on the CPU ------------------------------------------------

@@ -864,12 +864,14 @@ def _qk_args(Q, K, wq, wk, freqs, positions, norm, eps, pairs, axis):
         if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1 or 2 * freqs.shape[0] > d:
             raise ValueError("freqs must be [rotated values / 2], at most d / 2 of them")
         n = freqs.shape[0]
+        if n > GDN_QK_MAX_PAIRS:
+            raise ValueError("freqs has %d pairs, more than %d" % (n, GDN_QK_MAX_PAIRS))
         rot = 2 * n
         _arg(freqs, "freqs", _F64, (n,), dev)
         if axis is not None:
             if len(axis) != n:
                 raise ValueError("axis must give an axis for each of the %d pairs" % n)
-            if positions is None or positions.dim() != 3:
+            if not isinstance(positions, torch.Tensor) or positions.dim() != 3:
                 raise ValueError("axis needs positions [axes, B, T]")
             axes = positions.shape[0]
             if not 1 <= axes <= GDN_QK_MAX_AXES or min(axis, default=0) < 0 or max(axis, default=0) >= axes:
@@ -879,7 +881,7 @@ def _qk_args(Q, K, wq, wk, freqs, positions, norm, eps, pairs, axis):
     sh = gdn_qk_shape(T, qs, ks, B, Hq, Hk, d, _TORCH_DTYPE[dtype], _choice(norm, "norm", _QK_NORM), eps, rot,
                       _choice(pairs, "pairs", _PAIRS), axes)
     if axis is not None:
-        ctypes.memmove(sh.axis, bytes(axis), len(axis))
+        ctypes.memmove(sh.axis, bytes(list(axis)), len(axis))  # an array's own bytes are not its values
     return sh, B, Hq, Hk, T, d, dev, dtype
 
 
