@@ -465,3 +465,11 @@ def test_c_refusals():
     assert q(lib.gdn_rec_fwd_workspace_bytes, D=60) == 0 and q(lib.gdn_rec_bwd_workspace_bytes, B=0) == 0
     assert q(lib.gdn_rec_bwd_workspace_bytes) > q(lib.gdn_rec_fwd_workspace_bytes)
     assert tri.gdn_rec_fwd_workspace_bytes(2, 200, 64) > 0 and tri.gdn_rec_bwd_workspace_bytes(2, 200, 64, packed=True) > 0
+
+
+def test_counts_past_32_bits():
+    for f in (tri.gdn_rec_fwd_workspace_bytes, tri.gdn_rec_bwd_workspace_bytes):
+        assert f((1 << 31) - 1, 1, 8) >= 0
+        for B in (1 << 31, (1 << 32) + 1):
+            with pytest.raises(ValueError):
+                f(B, 200, 64)

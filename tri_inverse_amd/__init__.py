@@ -930,6 +930,11 @@ def gdn_qk_norm_bwd(dQ_out, dK_out, Q, K=None, wq=None, wk=None, freqs=None, pos
     return dQ, dK, dwq, dwk
 
 
+def _rec_count(B):
+    if B >= 1 << 31:  # the library would count on from zero
+        raise ValueError("%d sequences, more than 2^31 - 1" % B)
+
+
 def _rec_shape(X, A, I, w, offsets, decay, norm):
     """The gdn_rec_shape of a call after the inputs' checks; returns (shape, the states' shape, device)."""
     if not isinstance(X, torch.Tensor) or X.dim() != 3:
@@ -953,12 +958,14 @@ def _rec_shape(X, A, I, w, offsets, decay, norm):
             raise ValueError("offsets must be [sequences + 1], of one sequence at least")
         B = offsets.numel() - 1
         _arg(offsets, "offsets", _INT32, (B + 1,), dev)
+    _rec_count(B)
     sh = gdn_rec_shape(T, None if offsets is None else offsets.data_ptr(), xs, as_, is_, B, D, kind,
                        _choice(norm, "norm", _REC_NORM), _TORCH_DTYPE[dtype])
     return sh, (B, D), dev
 
 
 def _plain_rec(B, T, D, decay, packed):
+    _rec_count(B)
     # of the offsets only their presence counts
     return gdn_rec_shape(int(T), 16 if packed else None, int(D), int(D), int(D), int(B), int(D),
                          _choice(decay, "decay", _DECAY), GDN_REC_NORM_SQRT, GDN_F32)
