@@ -101,9 +101,9 @@ __device__ __forceinline__ float rcp(float x) { return __builtin_amdgcn_rcpf(x);
 constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f;
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + exp2_of(-LOG2E * z)); }
-// sigmoid and what it leaves of 1, which a difference would cancel; 2^-126 and not 0 for far z < 0
+// sigmoid and what it leaves of 1, which a difference would cancel; 2^-126 and not 0 for far z < 0, NaN of NaN
 __device__ __forceinline__ void sigmoid_rest(float z, float& s, float& rest) {
-  const float e = exp2_of(fminf(-LOG2E * z, 126.f));
+  const float x = -LOG2E * z, e = exp2_of(x > 126.f ? 126.f : x);
   s = rcp(1.f + e);
   rest = e * s;
 }
