@@ -35,3 +35,36 @@ def test_gradients_of_nan_gates(decay):
         assert torch.isnan(g[0, 50, 1::4]).all(), name + " of a NaN in A"
         for c in (2, 3):
             assert torch.equal(g[..., c::4], y[..., c::4]), name
+
+
+@gpu
+@pytest.mark.parametrize("decay,norm,far", [("log", "none", 80), ("power", "linear", 80), ("sigmoid", "linear", 80),
+                                            ("power", "sqrt", 50), ("sigmoid", "sqrt", 50)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_far_gates_keep_their_digits(decay, norm, far, dtype):
+    """Sequences of one token, whose state is its input's part alone: small sigmoids, and what large ones leave of 1,
+    are right to the reference's bound, which does not grow with an fp32 gate.  X is scaled so that the outputs are large
+    beside the tolerance's constant; with sqrt(1 - a^2) the gates end where the bound's floor would count.
+
+    Of a bf16 gate z, rounded itself by 2^-9 |z| in e^-z, the product with log2 e is rounded to fp32: 2^-24 |z log2 e|, ln 2
+    of it in e^-z, and log2 e as it is held is off by 2^-26.3 |z| more in it: together below 2^-23 |z| = EPS |z| / 8."""
+    say(f"recurrence, gates up to {far}, {decay} {norm} {dtype}")
+    B, D = 70, 136
+    x = ref.rec_inputs(far, B, 1, D, decay, True, dtype)
+    gate = (15 + (far - 15) * torch.rand((B, 1, D), generator=torch.Generator().manual_seed(7))).to(dtype)
+    if decay == "log":
+        x["A"][:], x["I"] = -float("inf"), -gate
+    else:
+        x["A"], x["I"] = gate if decay == "sigmoid" else -gate, None
+    x["X"] = x["X"] * 2.0 ** 66
+    if dtype == F32:
+        check(x, decay, norm, h0=False, dh=False)
+    how = dict(I=up(x["I"]), w=up(x["w"]), decay=decay, norm=norm)
+    H, h, _ = tri.gdn_rec_fwd(up(x["X"]), up(x["A"]), **how)
+    H1, h1 = tri.gdn_rec_step(up(x["X"]), up(x["A"]), **how)
+    torch.cuda.synchronize()
+    Hr, hr, EH, Eh, _ = ref.rec_forward(x, decay, norm)
+    grow = 1 + gate.double() / 8 * (dtype == BF)
+    for y, z in ((H, h), (H1, h1)):
+        close(y, Hr, EH * grow, "H")
+        close(z, hr, Eh * grow[:, 0], "h_out")
