@@ -68,3 +68,50 @@ def test_far_gates_keep_their_digits(decay, norm, far, dtype):
     for y, z in ((H, h), (H1, h1)):
         close(y, Hr, EH * grow, "H")
         close(z, hr, Eh * grow[:, 0], "h_out")
+
+
+@gpu
+def test_many_short_and_empty_sequences():
+    """Sequences of none, one or two tokens: more of them than tokens."""
+    say("recurrence, 3000 short sequences")
+    lens = torch.randint(0, 3, (3000,), generator=torch.Generator().manual_seed(2))
+    lens[1000:2000] = 0
+    T = int(lens.sum()) + 30
+    check(ref.rec_inputs(1, 1, T, 24, "power", True, F32, n_state=3000), "power", "sqrt", lens=lens.tolist(), first=10)
+
+
+@gpu
+def test_time_of_empty_sequences():
+    """200000 sequences with 64 tokens among them: the states of the empty ones are copied by all waves of the call,
+    not by one wave one after the other (which took 0.54 us each; 0.25 allowed)."""
+    n, T, D = 200000, 64, 136
+    say("recurrence, 200000 sequences of 64 tokens")
+    some = torch.randperm(n, generator=torch.Generator().manual_seed(1))[:T].sort().values
+    lens = torch.zeros(n, dtype=torch.int64)
+    lens[some] = 1
+    off = cuda(torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)]).to(torch.int32))
+    x = {k: up(v) for k, v in ref.rec_inputs(3, 1, T, D, "power", True, F32).items()}
+    h0, dh = torch.randn((n, D), device="cuda"), torch.randn((n, D), device="cuda")
+
+    def both(h0, dh, off):
+        how = dict(I=x["I"], w=x["w"], h0=h0, offsets=off)
+        H, h, st = tri.gdn_rec_fwd(x["X"], x["A"], want_states=True, **how)
+        return (H, h) + tri.gdn_rec_bwd(x["X"], x["A"], x["dH"], dh=dh, states=st, **how)
+
+    some = cuda(some)
+    want = both(h0[some], dh[some], offsets_of([1] * T, 0))
+    got = both(h0, dh, off)
+    torch.cuda.synchronize()
+    empty = torch.ones(n, dtype=torch.bool, device="cuda")
+    empty[some] = False
+    assert torch.equal(got[1][empty], h0[empty]) and torch.equal(got[6][empty], dh[empty])
+    assert torch.equal(got[1][some], want[1]) and torch.equal(got[6][some], want[6])
+    for i in (0, 2, 3, 4, 5):
+        assert torch.equal(got[i], want[i]), i
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    both(h0, dh, off)
+    end.record()
+    torch.cuda.synchronize()
+    print("forward and backward: %.1f ms" % start.elapsed_time(end), flush=True)
+    assert start.elapsed_time(end) < 2 * n * 0.25e-3
