@@ -451,9 +451,10 @@ typedef struct gdn_rec_shape {
 size_t gdn_rec_fwd_workspace_bytes(const gdn_rec_shape* shape);
 size_t gdn_rec_bwd_workspace_bytes(const gdn_rec_shape* shape);
 
-/* H and h_out (NULL = not wanted) of whole sequences from h0 (NULL = zeros).  states: NULL, or fp32
- * [B][ceil(T / GDN_REC_TILE)][D] (packed: [ceil(T / GDN_REC_TILE)][D]), h before every GDN_REC_TILE-th token
- * (0 where that token does not continue a sequence), for the backward pass.  workspace as for
+/* H and h_out (NULL = not wanted) of whole sequences from h0 (NULL = zeros); h_out must not be h0
+ * (GDN_ERR_UNSUPPORTED).  states: NULL, or fp32 [B][ceil(T / GDN_REC_TILE)][D] (packed:
+ * [ceil(T / GDN_REC_TILE)][D]), h before every GDN_REC_TILE-th token (0 where that token does not continue a
+ * sequence), for the backward pass.  workspace as for
  * gdn_lin_chunk_fwd.  A row of H depends on no later token.  The same call gives the same bits. */
 gdn_status gdn_rec_fwd(const gdn_rec_shape* shape, const void* X, const void* A, const void* I, const float* w,
                        const float* h0, void* H, float* h_out, float* states, void* workspace,
@@ -461,8 +462,8 @@ gdn_status gdn_rec_fwd(const gdn_rec_shape* shape, const void* X, const void* A,
 
 /* Its backward pass: gradients of a loss from dH (as H) and dh (gradient of h_out, NULL = zeros): dX,
  * dA, dI (with I only) [B][T][D] in dtype, dw fp32 [D] and dh0 fp32 [B][D] (NULL = not wanted; dw with
- * GDN_DECAY_POWER only).  states as gdn_rec_fwd wrote them for the same inputs; NULL: they are formed
- * anew.  The same call gives the same bits.  An infinity or a NaN in a row may reach all gradients of its
+ * GDN_DECAY_POWER only); dh0 must not be dh (GDN_ERR_UNSUPPORTED).  states as gdn_rec_fwd wrote them for
+ * the same inputs; NULL: they are formed anew.  The same call gives the same bits.  An infinity or a NaN in a row may reach all gradients of its
  * sequence and channel: rows that pad a sequence must be finite here. */
 gdn_status gdn_rec_bwd(const gdn_rec_shape* shape, const void* X, const void* A, const void* I, const float* w,
                        const float* h0, const float* states, const void* dH, const float* dh, void* dX,

@@ -115,3 +115,18 @@ def test_time_of_empty_sequences():
     torch.cuda.synchronize()
     print("forward and backward: %.1f ms" % start.elapsed_time(end), flush=True)
     assert start.elapsed_time(end) < 2 * n * 0.25e-3
+
+
+def test_states_are_not_written_over():
+    """A state that some workgroups read while others write its place is refused; the step may update in place."""
+    lib, at = tri._lib, ctypes.byref(shape())
+    S, R = FAKE + 4096, FAKE + 8192
+
+    def fwd(h0, h_out):
+        return lib.gdn_rec_fwd(at, FAKE, FAKE, None, FAKE, h0, FAKE, h_out, None, None, 0, None)
+
+    def bwd(dh, dh0):
+        return lib.gdn_rec_bwd(at, FAKE, FAKE, None, FAKE, None, None, FAKE, dh, FAKE, FAKE, None, None, dh0, None, 0, None)
+
+    for f in (fwd, bwd):  # the workspace is looked at last
+        assert f(S, S) == 5 and f(S, R) == 6 and f(None, None) == 6

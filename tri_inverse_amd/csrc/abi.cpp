@@ -772,6 +772,7 @@ gdn_status gdn_rec_fwd(const gdn_rec_shape* s, const void* X, const void* A, con
   if (s->B == 0) return GDN_OK;  // no sequence, no row of H
   if (rec_rows(s) && (!X || !A || !H || (s->decay == GDN_DECAY_POWER && !w))) return GDN_ERR_NULL_POINTER;
   if (!all_aligned16({X, A, I, w, h0, H, h_out, states, s->offsets})) return GDN_ERR_BAD_ALIGNMENT;
+  if (h0 && h0 == h_out) return GDN_ERR_UNSUPPORTED;  // a sequence's first tokens read it when its last ones may have written
   gdn::RecLaunch p = rec_launch(s);
   if (!gdn::rec_grid_ok(p)) return GDN_ERR_UNSUPPORTED;
   st = check_workspace(gdn::rec_workspace(p, false), workspace, workspace_bytes);
@@ -797,6 +798,7 @@ gdn_status gdn_rec_bwd(const gdn_rec_shape* s, const void* X, const void* A, con
   if (rows && (!X || !A || !dH || !dX || !dA || (I && !dI) || (s->decay == GDN_DECAY_POWER && !w)))
     return GDN_ERR_NULL_POINTER;
   if (!all_aligned16({X, A, I, w, h0, states, dH, dh, dX, dA, dI, dw, dh0, s->offsets})) return GDN_ERR_BAD_ALIGNMENT;
+  if (dh0 && dh0 == dh) return GDN_ERR_UNSUPPORTED;
   gdn::RecLaunch p = rec_launch(s);
   if (!gdn::rec_grid_ok(p)) return GDN_ERR_UNSUPPORTED;
   st = check_workspace(rows ? gdn::rec_workspace(p, true) : 0, workspace, workspace_bytes);
