@@ -130,3 +130,19 @@ def test_states_are_not_written_over():
 
     for f in (fwd, bwd):  # the workspace is looked at last
         assert f(S, S) == 5 and f(S, R) == 6 and f(None, None) == 6
+
+
+@gpu
+def test_states_of_no_sequence():
+    """Packed rows that belong to no sequence: the states before every 64th token are zeros."""
+    say("recurrence, no sequence")
+    T, D = 130, 16
+    x = torch.ones((1, T, D), device="cuda")
+    off, states = torch.zeros(4, device="cuda", dtype=torch.int32), torch.full((1, 3, D), 7.0, device="cuda")
+    H = torch.full_like(x, 7.0)
+    sh = shape(T=T, D=D, B=0, decay=1, x_stride=D, a_stride=D, i_stride=D, offsets=off.data_ptr())
+    p = lambda t: t.data_ptr()  # noqa: E731
+    st = tri._lib.gdn_rec_fwd(ctypes.byref(sh), p(x), p(x), None, None, None, p(H), None, p(states), None, 0,
+                              torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0 and (states == 0).all() and (H == 7).all()

@@ -769,13 +769,13 @@ gdn_status gdn_rec_fwd(const gdn_rec_shape* s, const void* X, const void* A, con
                        void* stream) {
   gdn_status st = check_rec(s);
   if (st != GDN_OK) return st;
-  if (s->B == 0) return GDN_OK;  // no sequence, no row of H
-  if (rec_rows(s) && (!X || !A || !H || (s->decay == GDN_DECAY_POWER && !w))) return GDN_ERR_NULL_POINTER;
+  if (s->B == 0 && !(rec_rows(s) && states)) return GDN_OK;  // no sequence, no row of H
+  if (s->B > 0 && rec_rows(s) && (!X || !A || !H || (s->decay == GDN_DECAY_POWER && !w))) return GDN_ERR_NULL_POINTER;
   if (!all_aligned16({X, A, I, w, h0, H, h_out, states, s->offsets})) return GDN_ERR_BAD_ALIGNMENT;
   if (h0 && h0 == h_out) return GDN_ERR_UNSUPPORTED;  // a sequence's first tokens read it when its last ones may have written
   gdn::RecLaunch p = rec_launch(s);
   if (!gdn::rec_grid_ok(p)) return GDN_ERR_UNSUPPORTED;
-  st = check_workspace(gdn::rec_workspace(p, false), workspace, workspace_bytes);
+  st = check_workspace(s->B > 0 ? gdn::rec_workspace(p, false) : 0, workspace, workspace_bytes);
   if (st != GDN_OK) return st;
   p.X = X;
   p.A = A;

@@ -852,6 +852,10 @@ int launch_rec_fwd(const RecLaunch& p, void* workspace, hipStream_t s) {
     copy_states(p.h0, p.h_out, (int64_t)p.n_seq * p.D, s);
     return 0;
   }
+  if (p.n_seq == 0) {  // rows of no sequence: zeros before every token
+    copy_states(nullptr, p.states, p.n_states * p.D, s);
+    return 0;
+  }
   const RecLaunch q = chained(p, false, reinterpret_cast<char*>(workspace), s);
   return by_kind(p, [&](auto e, auto decay, auto norm, auto gate) {
     typedef std::remove_pointer_t<decltype(e)> E;
