@@ -4,8 +4,8 @@
 //   y = R(p) (n * w),  n = x * rstd,  rstd = (inv sum x^2 + eps)^-1/2,  inv = 1/d (RMS) or 1 (unit rows)
 // Backwards, with dn = R(-p) dy and u = dn * w:
 //   dw = sum_rows dn * n,   dx = rstd (u - n inv sum(u n))
-// R(p) turns pair i by p f_i: the turns p f_i / 2 pi are formed in fp64 and only what they leave of
-// a quarter is rounded to fp32, so an angle is right to 2^-24 of a quarter turn at any position.
+// R(p) turns pair i by p f_i: the turns p f_i / 2 pi are formed in fp64 with their remainders and only what they
+// leave of a quarter is rounded to fp32, so an angle is right to 2^-24 of a quarter turn at any position.
 //
 // Bound by bytes: each row is read once into registers and its result written, and a lane keeps its
 // angles' cosines and sines for all heads of its token that its workgroup takes; the next heads' rows are
@@ -25,10 +25,17 @@ namespace gdn {
 
 namespace {
 
-// cosine and sine of `turns` whole turns: to the nearest quarter in fp64, the rest (at most an eighth)
-// by the series, whose first terms left out are below 2^-28
-__device__ __forceinline__ void cos_sin(double turns, float& c, float& s) {
-  turns -= rint(turns);
+// cosine and sine of the angle pos freq.  1 / 2 pi in two parts and the remainders of the products keep what rounding
+// takes from far turns (without them 4.8 x 2^-24 of a quarter turn at 2^31); to the nearest quarter in fp64, the rest (at
+// most an eighth) by the series, whose first terms left out are below 2^-28
+__device__ __forceinline__ void cos_sin(double pos, double freq, float& c, float& s) {
+#pragma clang fp contract(off)  // the remainders are those of the products as rounded
+  constexpr double INV = 0x1.45f306dc9c883p-3, INV_REST = -0x1.6b01ec5417056p-57;
+  const double angle = pos * freq;
+  double turns = angle * INV;
+  const double rest = fma(fma(pos, freq, -angle), INV, fma(angle, INV_REST, fma(angle, INV, -turns)));
+  turns = (turns - rint(turns)) + rest;
+  turns -= rint(turns);  // past 2^52 turns the rest is more than one
   const double quarter = rint(4.0 * turns);
   const float x = (float)(fma(-0.25, quarter, turns) * 6.283185307179586);
   const float x2 = x * x;
@@ -84,7 +91,7 @@ struct Turn {
       if (v < a.rot) {
         const int pair = HALVES ? v : v / 2;
         const double pos = a.positions ? (double)a.positions[(int64_t)a.axis[pair] * tokens + token] : (double)t;
-        cos_sin(pos * (a.freqs[pair] * 0.15915494309189535), c[i], s[i]);
+        cos_sin(pos, a.freqs[pair], c[i], s[i]);
       }
       if constexpr (SPARE) __builtin_amdgcn_sched_barrier(0);
     }
