@@ -70,3 +70,39 @@ def test_angles_at_far_positions(pairs):
         worst = float((got - exact).abs().max()) * 2 ** 24
         print("%s: %.2f x 2^-24" % (name, worst), flush=True)
         assert worst <= 2.0, name
+
+
+@gpu
+def test_weight_gradients_over_many_equal_rows():
+    """2^26 equal rows: every addition to a sum of 32 bits rounds the same way, so a lane's own run of them has to be short.
+    n = (1 + eps)^-1/2, 0.45 x 2^-14 below 1, is lost from each addition to a sum between 512 and 1024."""
+    T, H, d, eps = 65536, 1024, 32, 0.9 * 2.0 ** -14
+    say("queries and keys, 2^26 equal rows")
+    Q = torch.ones((1, T, H, d), device="cuda", dtype=BF)
+    g = tri.gdn_qk_norm_bwd(Q.view(1, H, T, d), None, Q, None, torch.ones(d, device="cuda"), norm="rms", eps=eps)
+    torch.cuda.synchronize()
+    want = T * H / math.sqrt(1.0 + float(torch.tensor(eps, dtype=F32)))
+    worst = float((g[2].cpu().double() / want - 1).abs().max())
+    print("off by %.2f x 2^-17" % (worst * 2 ** 17), flush=True)
+    assert worst <= 2.0 ** -17
+
+
+@gpu
+def test_more_heads_than_a_piece_of_work_takes():
+    """130 query heads of 32768 tokens: three runs of heads, each gradient as without the other heads."""
+    say("queries and keys, 130 heads")
+    T, H, d = 32768, 130, 32
+    g = torch.Generator(device="cuda").manual_seed(4)
+    Q, dQ = (torch.randn(s, device="cuda", generator=g).to(BF) for s in ((1, T, H, d), (1, H, T, d)))
+    w = torch.ones(d, device="cuda")
+    how = dict(freqs=cuda(frequencies(16)), eps=1e-5)
+    dx, _, dw, _ = tri.gdn_qk_norm_bwd(dQ, None, Q, None, w, **how)
+    for s, e in ((0, 64), (60, 70), (128, 130)):
+        part = tri.gdn_qk_norm_bwd(dQ[:, s:e].contiguous(), None, Q[:, :, s:e], None, w, **how)
+        assert torch.equal(dx[:, :, s:e], part[0]), (s, e)
+    # the weights' gradients, of the values that are not turned
+    n = Q.double()
+    n = (n * (n.square().mean(-1, True) + 1e-5).rsqrt()).transpose(1, 2)[..., 16:]
+    n *= dQ[..., 16:].double()
+    torch.cuda.synchronize()
+    assert ((dw[16:].double() - n.sum((0, 1, 2))).abs() <= 2.0 ** -17 * n.abs().sum((0, 1, 2))).all()

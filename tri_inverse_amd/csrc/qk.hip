@@ -18,6 +18,8 @@
 // accesses and the pairs' other halves loaded too, 116 with them exchanged between lanes).  Backwards, 4
 // x 4096 tokens, 403 MB, 91 us, 4.4 TB/s, of which the column sum 4.6.  64 tokens of 32 and 16 heads, 64 of 128
 // values turned: 3.5 us, latency.
+#include <algorithm>
+
 #include "gdn_device.hpp"
 #include "gdn_kernels.hpp"
 
@@ -325,9 +327,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4, 4))) voi
       if (at.on) sums[threadIdx.x / LPR][at.at[e / 4] + e % 4] = dw[which][e];
     __syncthreads();
     for (int i = threadIdx.x; i < a.d; i += 256) {
-      float s = 0.f;
-      for (int k = 0; k < 256 / LPR; ++k) s += sums[k][i];
-      part[((int64_t)blockIdx.x * 2 + which) * a.d + i] = s;
+      double s = 0.0;
+      for (int k = 0; k < 256 / LPR; ++k) s += (double)sums[k][i];
+      part[((int64_t)blockIdx.x * 2 + which) * a.d + i] = (float)s;
     }
   }
 }
@@ -378,14 +380,25 @@ int head_runs(const QkLaunch& p) {
   const int per = heads_per_group(p);
   return (p.Hq + p.Hk + per - 1) / per;
 }
-int64_t bwd_groups(const QkLaunch& p) {
-  const int64_t n = token_groups(p) * head_runs(p);
-  return n < 1024 ? n : 1024;
-}
+// Backwards a lane adds at most 64 rows to each of its sums for a weight, in 32 bits; the sums go on in 64.  So a piece of
+// work has at most 64 heads, and there are more workgroups than 1024 where those would walk over more rows (16 x 8192
+// tokens of 16 and 16 heads of 128: 2048 workgroups, 642 us; 1024 of them, 128 rows to a sum, 635).
+constexpr int MOST_ROWS = 64;
+struct BwdWork {
+  int per, runs;
+  int64_t pieces, groups;
+  BwdWork(const QkLaunch& p) {
+    per = std::min(heads_per_group(p), MOST_ROWS);
+    runs = (p.Hq + p.Hk + per - 1) / per;
+    pieces = token_groups(p) * runs;
+    const int rows = std::min(per, std::max(p.Hq, p.Hk)), walk = MOST_ROWS / rows;  // of a piece; pieces in a row
+    groups = std::max(std::min<int64_t>(pieces, 1024), (pieces + walk - 1) / walk);
+  }
+};
 
 }  // namespace
 
-size_t qk_bwd_workspace(const QkLaunch& p) { return (size_t)bwd_groups(p) * 2 * p.d * 4; }
+size_t qk_bwd_workspace(const QkLaunch& p) { return (size_t)BwdWork(p).groups * 2 * p.d * 4; }
 
 int launch_qk(const QkLaunch& p, hipStream_t s) {
   return by_kind(p, [&](auto lpr, auto e, auto halves, auto nt) {
@@ -399,17 +412,18 @@ int launch_qk(const QkLaunch& p, hipStream_t s) {
 int launch_qk_bwd(const QkLaunch& p, void* workspace, hipStream_t s) {
   float* part = p.dwq || p.dwk ? reinterpret_cast<float*>(workspace) : nullptr;
   const bool rows = (int64_t)p.B * p.T > 0 && p.Hq + p.Hk > 0;
-  const int64_t n = rows ? bwd_groups(p) : 0;
+  int64_t n = 0;
   if (rows)
     by_kind(p, [&](auto lpr, auto e, auto halves, auto nt) {
+      const BwdWork w(p);
+      n = w.groups;
       const dim3 grid((unsigned)n), block(256);
-      const int runs = head_runs(p);
       typedef std::remove_pointer_t<decltype(e)> E;
       // stores past the caches pay for fp32 (2 x 4096 tokens of 32 heads of 128: 84 us, through them 89), not for
       // bf16 (4 x 4096 tokens: 94.4, through them 90.9)
       constexpr bool past = nt.value && sizeof(E) == 4;
       hipLaunchKernelGGL((qk_bwd_kernel<lpr.value, E, halves.value, past>), grid, block, 0, s,
-                         p, heads_per_group(p), (uint32_t)runs, (uint32_t)(token_groups(p) * runs), part);
+                         p, w.per, (uint32_t)w.runs, (uint32_t)w.pieces, part);
       return 0;
     });
   if (p.dwq || p.dwk) launch_column_sum(part, n, p.d, 2, p.dwq, p.dwk, s);  // no rows: zeros
