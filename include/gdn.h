@@ -430,13 +430,18 @@ typedef enum gdn_rec_norm { GDN_REC_NORM_SQRT = 0, GDN_REC_NORM_LINEAR = 1, GDN_
 
 /* Per sequence and channel, tokens in order, state h fp32:
  *   h_t = a_t h_{t-1} + b_t s(I_t) X_t        (I NULL: b_t X_t)
+ * b_t counts for the first token of a sequence as for any other.
  * offsets == NULL: B sequences of T tokens each; X, A, I [B][T] rows of D values, x_stride,
  *   a_stride, i_stride values apart (parts of wider projections; multiples of 8, at most 2^24), H [B][T][D].
  * offsets != NULL: B packed sequences in T tokens, as in gdn_lin_shape, rows of the T tokens; rows of
  *   no sequence are not read into a result, H is not written there, and gradients there are zero.
  * X, A, I, H and their gradients in dtype (GDN_BF16 or GDN_F32); states [B][D] fp32.  D a multiple of
- * 8; fewer than 2^36 values, counted in whole tiles of GDN_REC_TILE tokens and 128 channels.  Empty sequences and T == 0 return the given states unchanged (or zeros).  A log-decay of
- * -inf forgets a finite state; where a = 1 the gradient of b = sqrt(1 - a^2) = 0 counts as 0. */
+ * 8; fewer than 2^36 values, counted in whole tiles of GDN_REC_TILE tokens and 128 channels.  Empty
+ * sequences and T == 0 return the given states unchanged (or zeros).  A log-decay of -inf forgets a finite
+ * state; where a = 1 the gradient of b = sqrt(1 - a^2) = 0 counts as 0.
+ * Within a call of gdn_rec_fwd or gdn_rec_bwd workgroups wait for those of earlier tokens (backwards of later
+ * ones), which run already.  A wait is bounded all the same: after some seconds without what it waits
+ * for the results behind it are NaN, and the status, returned before, is GDN_OK. */
 typedef struct gdn_rec_shape {
   int64_t T;
   const int32_t* offsets;

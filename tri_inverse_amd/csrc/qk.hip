@@ -16,7 +16,7 @@
 // Measured (a copy of 1 GiB reaches 5.05 TB/s): 4 x 8192 tokens, 16 and 16 heads of 128, bf16, all turned, 537
 // MB, 100 us, 5.4 TB/s (115 with every head's loads behind the last one's results; 145 with 16-byte
 // accesses and the pairs' other halves loaded too, 116 with them exchanged between lanes).  Backwards, 4
-// x 4096 tokens, 403 MB, 91 us, 4.4 TB/s, of which the column sum 4.6.  64 tokens of 32 and 16 heads, 64 of 128
+// x 4096 tokens, 403 MB, 91 us, 4.4 TB/s, of which the kernel 87, 4.6 TB/s, the column sum 4.6.  64 tokens of 32 and 16 heads, 64 of 128
 // values turned: 3.5 us, latency.
 #include <algorithm>
 

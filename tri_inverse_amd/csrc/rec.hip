@@ -28,11 +28,11 @@
 // Decays, states and sums are fp32; 1 - a is formed without cancelling (a series near 0), each output is
 // rounded once.
 //
-// Measured (a copy of 1 GiB reaches 5.05 TB/s): 4 sequences of 8192 tokens, 2048 channels, bf16, 537 MB, 132
-// us, 4.1 TB/s.  With the stores through the caches 138, of which the chain 4, the gates' arithmetic 13,
+// Measured (a copy of 1 GiB reaches 5.05 TB/s): 4 sequences of 8192 tokens, 2048 channels, bf16, 537 MB, 130
+// us, 4.1 TB/s.  With the stores through the caches it took 138, of which the chain 4, the gates' arithmetic 13,
 // both together 23.  One sequence of 65536 tokens, 1024 channels, 403 MB, 120 us, without the chain 91: of 8
 // chains alone a tile waits for the slowest of 64 that run beside it.  Training step of 4 x 4096 tokens,
-// 2048 channels, 738 MB, 210 us: forwards 70, backwards 135 (100 without chain and gates).
+// 2048 channels, 738 MB, 208 us: the kernels 69 forwards and 139 backwards in a profile (100 without chain and gates).
 // Tiles: 64 tokens forwards take 150 us for the first, 32 tokens 211 (each tile has its share of the
 // chain); 128 backwards spill, 260 us for the training step.  Workgroups that walk on along their chain
 // took 140 and, for the second, 142; three workgroups a CU, with half of u in LDS, 139 and 136.
@@ -56,7 +56,9 @@ __device__ __forceinline__ void hide(V& v) {
   asm volatile("" : "+v"(v));
 }
 
-// outputs go past what the caches hold (the non-temporal bit): prefill 137.7 -> 132 us, training step 218 -> 211
+// outputs go past what the caches hold (the non-temporal bit): prefill 137.7 -> 132 us, training step 218 -> 211; also where
+// rows end inside lines: training steps of 4 x 4096 tokens of 520 and 776 channels 90 -> 84 and 117 -> 111, forwards alone
+// 2 % less to 2 % more
 constexpr int PAST = 2;
 
 // two neighbouring channels as they lie in memory, and as fp32
