@@ -8,8 +8,9 @@ T written as fp32.  value = 64x64 blocks per second.
 The same JSON line also carries the other inverse variants of that workload, the
 chunk-wise prefill forward (B=4, H=16, seq 8192, d_k = d_v = 128, C = 64) in tokens per
 second with its roofline, the forward-substitution comparison, the decode step, the WY
-chunk-size sweep, the fp8 prefill at seq 32768, the oracle's CPU baseline and the
-accuracy report.
+chunk-size sweep, the fp8 prefill at seq 32768, the oracle's CPU baseline and of the
+accuracy report each relative error (--report FILE writes the whole of it).  Figures beside
+the headline's have five significant digits, so that the line stays near 12 KB.
 
 Inputs are seeded synthetic tensors (see synth/), resident in HBM before timing.
 Eight input/output buffer sets are rotated so that successive launches do not hit
@@ -17,7 +18,8 @@ the 256 MB Infinity Cache.  Kernel durations come from HIP events recorded on th
 stream the kernels are launched on.
 
 Usage: python bench.py [--gpus 1] [--steps K] [--warmup W] [--no-cpu]
-                       [--only all|c3|fs|decode|c2|c4] [--profile-launches n --only LEG]
+                       [--only all|c3|fs|decode|c2|c4] [--report FILE]
+                       [--profile-launches n --only LEG]
 (the headline always runs; --only limits the other legs)
 """
 from __future__ import annotations
@@ -626,6 +628,22 @@ def cpu_baseline_and_accuracy(torch, tri, synth):
     return cpu, acc
 
 
+def rel_only(report):
+    """The report with each comparison's relF alone."""
+    if not isinstance(report, dict):
+        return report
+    return report["relF"] if "relF" in report else {k: rel_only(v) for k, v in report.items()}
+
+
+def rounded(x):
+    """Floats of nested lists and dicts to five significant digits."""
+    if isinstance(x, float):
+        return float("%.5g" % x)
+    if isinstance(x, dict):
+        return {k: rounded(v) for k, v in x.items()}
+    return [rounded(v) for v in x] if isinstance(x, list) else x
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -633,6 +651,7 @@ def main():
     ap.add_argument("--warmup", type=int, default=10)
     ap.add_argument("--no-cpu", action="store_true")
     ap.add_argument("--only", default="all")
+    ap.add_argument("--report", help="file for the whole accuracy report (JSON)")
     ap.add_argument("--profile-launches", type=int, default=0,
                     help="profiling mode: run the launch --only names (default the headline) "
                          "this many times plus a 256 MiB device copy (counter calibration), "
@@ -725,8 +744,13 @@ def main():
                                             ("neumann", 3, False, "fp8")],
                                            3, 1, n_sets=1, stats=True)
     if not args.no_cpu:
-        out["cpu_baseline"], out["accuracy"] = cpu_baseline_and_accuracy(torch, tri, synth)
-    print(json.dumps(out))
+        out["cpu_baseline"], accuracy = cpu_baseline_and_accuracy(torch, tri, synth)
+        out["accuracy"] = rel_only(accuracy)
+        if args.report:
+            with open(args.report, "w") as f:
+                json.dump(accuracy, f, indent=1)
+    head = {k: out[k] for k in ("value", "ms_per_step")}
+    print(json.dumps({**rounded(out), **head}, separators=(",", ":")), flush=True)
 
 
 if __name__ == "__main__":
